@@ -22,7 +22,8 @@
  *     plan array of mot_routed_gemm_noalloc.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream of the current
  *     device). Every pointer must belong to the stream's device (the device guard of
- *     [PR-503]'s RMSNorm launcher commit); the launch runs on that device.
+ *     [PR-503]'s RMSNorm launcher commit); the launch runs on that device. While a stream is
+ *     being captured into a graph, its device must be the current one.
  *   - Calls are asynchronous on `stream`. A nonzero return is a host-detected error: no
  *     kernel was launched and no output was written (fail closed: [RFC-435] §3 Numerical
  *     contract). Errors found on the device (a modality other than 0/1, a position
@@ -43,7 +44,7 @@
 extern "C" {
 #endif
 
-#define MOT_ABI_VERSION 4
+#define MOT_ABI_VERSION 5
 
 /* host-detected status codes (return values) */
 #define MOT_OK            0
@@ -64,6 +65,7 @@ extern "C" {
 #define MOT_DEV_BAD_POSITION  0x8u  /* a RoPE position outside [0, P) (clamped to 0) */
 #define MOT_DEV_BAD_SEQUENCE  0x10u /* an attention sequence descriptor out of range */
 #define MOT_DEV_BAD_TIME      0x20u /* SDE step times outside 0 <= t_next < t_i <= 1 */
+#define MOT_DEV_BAD_PAGE      0x40u /* a cache slot, a page index or a sequence length out of range */
 
 /* epilogues of mot_routed_gemm */
 #define MOT_EPI_CAST   0  /* out = bf16(acc) */
@@ -79,6 +81,10 @@ extern "C" {
 #define MOT_SET_UND  1
 #define MOT_SET_GEN  2
 #define MOT_SET_BOTH 3
+
+/* element types of a paged key-value cache */
+#define MOT_KV_BF16 0
+#define MOT_KV_E4M3 1  /* 8-bit floats (4 exponent, 3 fraction bits, largest value 448) with scales */
 
 /* largest packed batch the library accepts */
 #define MOT_MAX_TOKENS (1 << 24)
@@ -295,6 +301,78 @@ int mot_rope_table_fill_host_fp32(double theta, int D, int P, float* host_cs);
  */
 int mot_joint_attention(const mot_bf16* qkv, int64_t T, int Hq, int Hkv, int D, const int32_t* seqs,
                         int n_seq, float scale, void* ws, size_t ws_bytes, mot_bf16* out, void* stream);
+
+/*
+ * Paged key-value cache ([RFC-435] §1 Motivation item 2: latent tokens query the prompt KV at every
+ * step; §2 Reference hazards: cached prefill. The pages fix no cache layout). The caller owns the
+ * pages; the three calls below write, read back and attend over
+ *   k_cache, v_cache  [n_pages][Hkv][page][D]   bf16 (MOT_KV_BF16) or e4m3 (MOT_KV_E4M3).
+ *   scales            [n_pages][Hkv][page][2]   fp32, e4m3 only (ignored for bf16): K's and V's scale
+ *                     of each token and head; a cached vector stands for code * scale.
+ * Slot s is token s % page of page s / page. Geometry of all three: D in {64, 128}; Hq, Hkv in
+ * 1 .. 1024, Hq a multiple of Hkv; page a multiple of 16, 16 <= page <= 1024; n_pages >= 1 and
+ * n_pages * Hkv * page < 2^31, else MOT_ERR_GEOMETRY; any other kv_type is MOT_ERR_ARG. All pointers
+ * 16-byte aligned device memory of the stream's device. ws has at least 64 bytes whose error word
+ * receives MOT_DEV_BAD_PAGE (it is OR-ed into, never cleared: start from a zeroed or planned one).
+ */
+
+/*
+ * mot_kv_cache_write -- the K and V columns of fused QKV rows into cache slots.
+ *   qkv    [T][(Hq + 2 Hkv) D] bf16   rows of mot_routed_qkv_norm_rope's output (q, k, v heads).
+ *   slots  [T] int32                  each row's slot, or -1: the row is not written. Any other value
+ *                                     outside [0, n_pages * page) sets MOT_DEV_BAD_PAGE and the row is
+ *                                     not written. The slots >= 0 of one call are distinct.
+ * MOT_KV_BF16 copies the values. MOT_KV_E4M3, per vector x of D values: scale = 2^e with the smallest
+ * e >= -64 that has max|x| <= 448 * 2^e, code = e4m3(x / scale) to nearest even (x / scale is exact
+ * unless it leaves fp32's range at the bottom); a vector that holds an infinity or a NaN gets the
+ * scale NaN, so that it reads as NaN. Slots that no row names keep their contents.
+ */
+int mot_kv_cache_write(const mot_bf16* qkv, int64_t T, int Hq, int Hkv, int D, const int32_t* slots, int kv_type,
+                       int64_t n_pages, int page, void* k_cache, void* v_cache, float* scales, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/*
+ * mot_kv_cache_read -- cached vectors back into the K and V columns of fused QKV rows, for
+ * mot_joint_attention over a cached prefix.
+ *   slots  [T] int32                  each row's slot (a slot may be read into several rows), or -1:
+ *                                     the row is left as it is; other values outside the cache set
+ *                                     MOT_DEV_BAD_PAGE and leave the row as it is.
+ *   qkv    [T][(Hq + 2 Hkv) D] bf16   out: the K and V columns of the rows; the q columns are kept.
+ * MOT_KV_BF16 copies; MOT_KV_E4M3 gives bf16(code * scale), exact within bf16's range.
+ */
+int mot_kv_cache_read(const void* k_cache, const void* v_cache, const float* scales, int kv_type, int64_t n_pages,
+                      int page, const int32_t* slots, int64_t T, int Hq, int Hkv, int D, mot_bf16* qkv, void* ws,
+                      size_t ws_bytes, void* stream);
+
+/*
+ * mot_paged_decode_workspace_bytes -- workspace bytes of mot_paged_decode_attention for R rows whose
+ * page tables have max_pages entries: the 64-byte header (its error word) and the partial results of
+ * split sequences. 0 for a geometry that the call rejects.
+ */
+size_t mot_paged_decode_workspace_bytes(int64_t R, int Hq, int Hkv, int D, int max_pages, int page);
+
+/*
+ * mot_paged_decode_attention -- attention of one new token a row over its cached keys.
+ *   qkv    [R][(Hq + 2 Hkv) D] bf16   the rows' fused QKV; only the q heads are read (write the row's
+ *                                     K and V into the cache first: mot_kv_cache_write).
+ *   table  [R][max_pages] int32       row r's keys j = 0 .. lens[r] - 1 are token j % page of page
+ *                                     table[r][j / page]; entries past the length are not read.
+ *   lens   [R] int32                  keys of each row, 0 <= lens[r] <= max_pages * page: 0 gives a row
+ *                                     of zeros (an idle slot of the batch); a value out of range sets
+ *                                     MOT_DEV_BAD_PAGE and the row is not written. A page index outside
+ *                                     [0, n_pages) among the entries read sets MOT_DEV_BAD_PAGE and
+ *                                     leaves the row's output undefined.
+ *   scale  softmax scale (1 / sqrt(D) for the standard attention), > 0.
+ *   ws     at least mot_paged_decode_workspace_bytes(R, Hq, Hkv, D, max_pages, page) bytes; everything
+ *          after its first 64 bytes is scratch that the call overwrites (so not a routing plan in use).
+ *   out    [R][Hq D] bf16             out.
+ * Rows of one sequence (several new tokens) are several rows with equal page tables and their own
+ * lengths. Geometry: 1 <= R <= MOT_MAX_TOKENS, R * Hq < 2^31, max_pages >= 1, max_pages * page <= 2^30.
+ */
+int mot_paged_decode_attention(const mot_bf16* qkv, int64_t R, int Hq, int Hkv, int D, const int32_t* table,
+                               const int32_t* lens, int max_pages, int kv_type, int64_t n_pages, int page,
+                               const void* k_cache, const void* v_cache, const float* scales, float scale, void* ws,
+                               size_t ws_bytes, mot_bf16* out, void* stream);
 
 /*
  * mot_routed_gemm_dx -- input gradient of the routed GEMM out = a W[mod]^T through both

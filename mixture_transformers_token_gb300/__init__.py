@@ -30,9 +30,11 @@ __all__ = [
     "mot_selftest_wait_timeout",
     "DEV_BAD_TIME", "mot_flow_workspace_bytes", "mot_flow_schedule_host", "mot_cfg_combine_renorm",
     "mot_flow_sde_step", "mot_flow_cfg_sde_step", "mot_flow_noise",
+    "DEV_BAD_PAGE", "KV_BF16", "KV_E4M3", "mot_kv_cache_write", "mot_kv_cache_read",
+    "mot_paged_decode_workspace_bytes", "mot_paged_decode_attention",
 ]
 
-ABI_VERSION = 4
+ABI_VERSION = 5
 EPI_CAST = 0
 EPI_SWIGLU = 1
 A_PLAN_ORDER = 0x100
@@ -44,6 +46,8 @@ DEV_PLAN_MISMATCH = 0x4
 DEV_BAD_POSITION = 0x8
 DEV_BAD_SEQUENCE = 0x10
 DEV_BAD_TIME = 0x20
+DEV_BAD_PAGE = 0x40
+KV_BF16, KV_E4M3 = 0, 1  # element types of a paged key-value cache
 NOALLOC_MAX_TOKENS = 65536
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -85,6 +89,13 @@ _SIGNATURES = {
     "mot_flow_cfg_sde_step": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i64, _c_p, _c_p, _c_sz,
                                      _c_p, _c_p, _c_p]),
     "mot_flow_noise": (_c_i, [_c_p, ctypes.c_uint64, _c_i, _c_i64, _c_p, _c_p]),
+    "mot_kv_cache_write": (_c_i, [_c_p, _c_i64, _c_i, _c_i, _c_i, _c_p, _c_i, _c_i64, _c_i, _c_p, _c_p, _c_p, _c_p,
+                                  _c_sz, _c_p]),
+    "mot_kv_cache_read": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i64, _c_i, _c_p, _c_i64, _c_i, _c_i, _c_i, _c_p, _c_p,
+                                 _c_sz, _c_p]),
+    "mot_paged_decode_workspace_bytes": (_c_sz, [_c_i64, _c_i, _c_i, _c_i, _c_i, _c_i]),
+    "mot_paged_decode_attention": (_c_i, [_c_p, _c_i64, _c_i, _c_i, _c_i, _c_p, _c_p, _c_i, _c_i, _c_i64, _c_i, _c_p,
+                                          _c_p, _c_p, _c_f, _c_p, _c_sz, _c_p, _c_p]),
     "mot_device_status": (_c_i, [_c_p, ctypes.POINTER(ctypes.c_uint32), _c_p]),
 }
 
@@ -379,6 +390,91 @@ def mot_joint_attention(qkv, seqs, Hq: int, Hkv: int, D: int, ws, scale: float |
     _check("mot_joint_attention", _lib().mot_joint_attention(
         qkv.data_ptr(), T, Hq, Hkv, D, seqs.data_ptr(), seqs.shape[0], sc, ws.data_ptr(), ws.numel(),
         out.data_ptr(), _stream(qkv, stream)))
+    return out
+
+
+def _kv_cache(k_cache, v_cache, scales):
+    """Checks a cache's tensors: (kv_type, n_pages, Hkv, page, D, the scales' pointer or None)."""
+    e4m3 = k_cache.dtype == torch.float8_e4m3fn
+    dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    _dev(k_cache, "k_cache", dtype, 4)
+    _dev(v_cache, "v_cache", dtype, 4)
+    shape = k_cache.shape
+    if v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    n_pages, Hkv, page, D = shape
+    if not e4m3:
+        return KV_BF16, n_pages, Hkv, page, D, None
+    if scales is None:
+        raise ValueError("an e4m3 cache needs its scales")
+    sp = _dev(scales, "scales", torch.float32, 4)
+    if tuple(scales.shape) != (n_pages, Hkv, page, 2):
+        raise ValueError(f"scales must be [{n_pages}, {Hkv}, {page}, 2]")
+    return KV_E4M3, n_pages, Hkv, page, D, sp
+
+
+def mot_kv_cache_write(qkv, slots, k_cache, v_cache, Hq: int, ws, scales=None, stream=None) -> None:
+    """Writes the K and V columns of the fused QKV rows [T][(Hq + 2 Hkv) D] into the cache's slots
+    (int32 [T], -1: skip the row). The cache [n_pages][Hkv][page][D] is bf16, or float8_e4m3fn with
+    fp32 `scales` [n_pages][Hkv][page][2]. `ws` (>= 64 bytes) receives device errors."""
+    kt, n_pages, Hkv, page, D, sp = _kv_cache(k_cache, v_cache, scales)
+    T, N = qkv.shape
+    _dev(qkv, "qkv", torch.bfloat16, 2)
+    _dev(slots, "slots", torch.int32, 1)
+    _dev(ws, "ws", torch.uint8, 1)
+    if N != (Hq + 2 * Hkv) * D or slots.shape[0] != T:
+        raise ValueError(f"qkv must be [T, {(Hq + 2 * Hkv) * D}] and slots [T]")
+    _check("mot_kv_cache_write", _lib().mot_kv_cache_write(
+        qkv.data_ptr(), T, Hq, Hkv, D, slots.data_ptr(), kt, n_pages, page, k_cache.data_ptr(), v_cache.data_ptr(),
+        sp, ws.data_ptr(), ws.numel(), _stream(qkv, stream)))
+
+
+def mot_kv_cache_read(k_cache, v_cache, slots, qkv, Hq: int, ws, scales=None, stream=None):
+    """Reads cached vectors back into the K and V columns of the fused QKV rows `qkv` (the q columns
+    and rows with slot -1 are kept). Arguments as mot_kv_cache_write; returns qkv."""
+    kt, n_pages, Hkv, page, D, sp = _kv_cache(k_cache, v_cache, scales)
+    T, N = qkv.shape
+    _dev(qkv, "qkv", torch.bfloat16, 2)
+    _dev(slots, "slots", torch.int32, 1)
+    _dev(ws, "ws", torch.uint8, 1)
+    if N != (Hq + 2 * Hkv) * D or slots.shape[0] != T:
+        raise ValueError(f"qkv must be [T, {(Hq + 2 * Hkv) * D}] and slots [T]")
+    _check("mot_kv_cache_read", _lib().mot_kv_cache_read(
+        k_cache.data_ptr(), v_cache.data_ptr(), sp, kt, n_pages, page, slots.data_ptr(), T, Hq, Hkv, D,
+        qkv.data_ptr(), ws.data_ptr(), ws.numel(), _stream(qkv, stream)))
+    return qkv
+
+
+def mot_paged_decode_workspace_bytes(R: int, Hq: int, Hkv: int, D: int, max_pages: int, page: int) -> int:
+    return int(_lib().mot_paged_decode_workspace_bytes(R, Hq, Hkv, D, max_pages, page))
+
+
+def mot_paged_decode_attention(qkv, table, lens, k_cache, v_cache, Hq: int, ws, scales=None, scale: float | None = None,
+                               out=None, stream=None):
+    """Attention of one new token a row over its pages: the q heads of the fused QKV rows [R][(Hq + 2
+    Hkv) D], page table int32 [R][max_pages], lens int32 [R] (0: a row of zeros), the cache as for
+    mot_kv_cache_write. `ws` (>= mot_paged_decode_workspace_bytes) is scratch after its 64-byte header.
+    Returns out [R][Hq D] bf16."""
+    kt, n_pages, Hkv, page, D, sp = _kv_cache(k_cache, v_cache, scales)
+    R, N = qkv.shape
+    _dev(qkv, "qkv", torch.bfloat16, 2)
+    _dev(table, "table", torch.int32, 2)
+    _dev(lens, "lens", torch.int32, 1)
+    _dev(ws, "ws", torch.uint8, 1)
+    if N != (Hq + 2 * Hkv) * D:
+        raise ValueError(f"qkv must be [R, {(Hq + 2 * Hkv) * D}]")
+    if table.shape[0] != R or lens.shape[0] != R:
+        raise ValueError("table must be [R, max_pages] and lens [R]")
+    if out is None:
+        out = torch.empty((R, Hq * D), dtype=torch.bfloat16, device=qkv.device)
+    _dev(out, "out", torch.bfloat16, 2)
+    if out.shape[0] != R or out.shape[1] != Hq * D:
+        raise ValueError(f"out must be [{R}, {Hq * D}]")
+    sc = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    _check("mot_paged_decode_attention", _lib().mot_paged_decode_attention(
+        qkv.data_ptr(), R, Hq, Hkv, D, table.data_ptr(), lens.data_ptr(), table.shape[1], kt, n_pages, page,
+        k_cache.data_ptr(), v_cache.data_ptr(), sp, sc, ws.data_ptr(), ws.numel(), out.data_ptr(),
+        _stream(qkv, stream)))
     return out
 
 

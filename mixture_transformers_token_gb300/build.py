@@ -24,7 +24,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmot.so")
 
 SOURCES = ["mot_route_norm.cu", "mot_gemm.cu", "mot_misc.cu", "mot_backward.cu", "mot_attention.cu",
-           "mot_flow.cu"]
+           "mot_flow.cu", "mot_kvcache.cu", "mot_decode.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # --fmad=false: no scalar multiply and add are contracted into a fused multiply-add, which the
 # numerical contract forbids (the kernels write their arithmetic with explicitly rounded operations;

@@ -637,6 +637,81 @@ def g_joint_attention(qkv, seqs, Hq: int, Hkv: int, D: int, scale: float | None 
 
 
 # ---------------------------------------------------------------------------
+# Paged key-value cache: the e4m3 form of a vector and single-token attention over pages
+# ---------------------------------------------------------------------------
+#
+# [RFC-435] §1 Motivation item 2 and §2 Reference hazards name the cached prompt KV; the pages fix
+# neither a cache layout nor a quantised form. Both are this library's: K and V pages
+# [n_pages][Hkv][page][D], e4m3 vectors with power-of-two scales [n_pages][Hkv][page][2].
+
+KV_MIN_SCALE_EXP = -64
+
+
+def e4m3_values() -> np.ndarray:
+    """The 127 finite non-negative values of the 8-bit float with 4 exponent and 3 fraction bits (bias
+    7, no infinities, the all-ones pattern is NaN), by code."""
+    c = np.arange(127)
+    e, f = c >> 3, c & 7
+    return np.where(e == 0, f * 2.0 ** -9, (8 + f) * np.ldexp(1.0, e - 10))
+
+
+def e4m3_round(x) -> np.ndarray:
+    """x rounded to the nearest e4m3 value (ties to the even code), |x| <= 448; NaN stays NaN."""
+    x = np.asarray(x, np.float64)
+    v = e4m3_values()
+    a = np.abs(np.where(np.isnan(x), 0.0, x))
+    if np.any(a > 448.0):
+        raise ValueError("outside e4m3's range")
+    hi = np.minimum(np.searchsorted(v, a), 126)
+    lo = np.maximum(hi - 1, 0)
+    up, down = v[hi] - a, a - v[lo]
+    code = np.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+    code = np.where(v[hi] == a, hi, code)
+    return np.where(np.isnan(x), np.nan, np.copysign(v[code], x))
+
+
+def kv_quantise(x) -> tuple[np.ndarray, np.ndarray]:
+    """Vectors [..., D] (exact bf16 values in float64) to (e4m3 values, scales [...]): the scale is the
+    smallest power of two 2^e, e >= -64, with max|x| <= 448 * 2^e, NaN for a vector with a value that is
+    not finite."""
+    x = np.asarray(x, np.float64)
+    a = np.max(np.abs(x), axis=-1)
+    fine = np.isfinite(a)
+    e = np.full(a.shape, KV_MIN_SCALE_EXP)
+    for k in range(KV_MIN_SCALE_EXP, 121):  # the first exponent that holds the vector
+        e = np.where(fine & (np.where(fine, a, 0.0) > np.ldexp(448.0, k)), k + 1, e)
+    scale = np.where(fine, np.ldexp(1.0, e), np.nan)
+    with np.errstate(invalid="ignore"):
+        y = x / scale[..., None]
+    return e4m3_round(y), scale
+
+
+def g_paged_decode(q, k_rows, v_rows, Hq: int, Hkv: int, scale: float | None = None):
+    """Single-token attention in float64. q [R][Hq][D]; k_rows, v_rows: for each row its cached keys and
+    values [len][Hkv][D]. Query head h reads KV head h // (Hq / Hkv); a row without keys gives zeros.
+    Returns out_pre [R][Hq][D], p_abs_v (the sums of p |v| that bound an output's rounding), and per (row,
+    head) s_abs, the largest sum |q||k| scale, and s_max, the largest |score|."""
+    q = np.asarray(q, np.float64)
+    R, _, D = q.shape
+    sc = 1.0 / np.sqrt(D) if scale is None else float(scale)
+    out, pav = np.zeros((R, Hq, D)), np.zeros((R, Hq, D))
+    s_abs, s_max = np.zeros((R, Hq)), np.zeros((R, Hq))
+    for r in range(R):
+        if len(k_rows[r]) == 0:
+            continue
+        for h in range(Hq):
+            k = np.asarray(k_rows[r], np.float64)[:, h // (Hq // Hkv)]
+            v = np.asarray(v_rows[r], np.float64)[:, h // (Hq // Hkv)]
+            s = (k @ q[r, h]) * sc
+            p = np.exp(s - np.max(s))
+            p = p / np.sum(p)
+            out[r, h], pav[r, h] = p @ v, p @ np.abs(v)
+            s_abs[r, h] = np.max(np.abs(k) @ np.abs(q[r, h])) * sc
+            s_max[r, h] = np.max(np.abs(s))
+    return {"out_pre": out, "p_abs_v": pav, "s_abs": s_abs, "s_max": s_max}
+
+
+# ---------------------------------------------------------------------------
 # Flow-matching sampler pieces: schedule, three-branch renormalised CFG, SDE step and logp
 # ---------------------------------------------------------------------------
 #
