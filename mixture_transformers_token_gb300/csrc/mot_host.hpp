@@ -17,9 +17,14 @@ constexpr int kMaxDevices = 64;
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Device that owns `stream` (the current device for the legacy default stream).
+// Device that owns `stream` (the current device for the legacy default stream). Asking a stream that
+// is being captured for its device would invalidate the capture, so the current device is taken
+// there too; the pointers' check then refuses a stream of another device.
 inline int stream_device(cudaStream_t s, int* dev) {
-  if (s == nullptr) return cudaGetDevice(dev) == cudaSuccess ? MOT_OK : MOT_ERR_CUDA;
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (s != nullptr && cudaStreamIsCapturing(s, &capture) != cudaSuccess) return MOT_ERR_CUDA;
+  if (s == nullptr || capture != cudaStreamCaptureStatusNone)
+    return cudaGetDevice(dev) == cudaSuccess ? MOT_OK : MOT_ERR_CUDA;
   return cudaStreamGetDevice(s, dev) == cudaSuccess ? MOT_OK : MOT_ERR_CUDA;
 }
 
