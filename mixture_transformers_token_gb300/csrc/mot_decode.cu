@@ -1,10 +1,38 @@
-// Attention of single new tokens over a paged key-value cache.
+// Attention of single new tokens over a paged key-value cache, split over the keys and joined.
 //
 // Sources: [RFC][BAGEL-7B-MoT][CUDA/ROCm] WS1/WS2 kernel roadmap and integration plan #435 (§1
 // Motivation item 2: queries over the cached prompt KV; §3 Numerical contract: fixed accumulation
 // order, a row's bits do not depend on the pack). The attention is the textbook scaled dot-product
 // softmax with grouped KV heads.
+//
+// Splitting. A row's keys are cut into ranges of span(len) keys, a function of the row's own length
+// and the head geometry alone, so a row's bits do not depend on the batch. The span is the shortest
+// multiple of a CTA's round (8 warps x TOK keys) that cuts one row into at most as many (range, KV
+// head) items as there are SMs: a single long row then fills the machine in one wave, and each long
+// row of a batch gives every SM about one item. A persistent CTA per SM takes every 152nd item.
+//
+// Arithmetic of an item (a key range of one KV head, up to 8 of its query heads): warp w of 8 takes
+// the range's tiles w, w + 8, ... of TOK keys. Per tile S = Q K^T with mma.sync (m16n8k16: the heads
+// are the 16 rows, half of them empty), x = S c in powers of two, then w = 2^(x - ref) where the
+// reference starts as the tile's maximum less 6 and moves only when a tile's maximum exceeds it by
+// more than 14 (so w <= 2^14, and the largest w is at least 2^6); sums of w in fp32 per lane;
+// O^T += V^T W^T (m16n8k16: 16 dims x 8 heads). The 8 warps' (ref, sum, O) are joined in warp order,
+// the ranges' in a fixed order by join_kernel. Every fp32 operation is rounded on its own.
+// bf16 cache: w goes into the product as two bf16 (w and what its rounding leaves), so the weights
+// keep 16 bits: one bf16 each would put an error the size of the output's own rounding beside it.
+// e4m3 cache: codes become halves (exact), the query is scaled by a power of two into the halves'
+// range (exact but for elements below 2^-24 of the largest), and a weight is a half. A token's V scale
+// belongs into its weight, so the reference follows x + log2(scale): the halves' range is then spent on
+// what the products contribute, however the scales differ.
+//
+// What bounds it: HBM. A key costs 4 G flop per 4 bytes, far below the tensor cores' rate even on
+// mma.sync (tcgen05's smallest M is 64 rows; here there are at most 8), so the design is about bytes in
+// flight: every warp owns a ring of STAGES tiles in shared memory, filled by its own TMA copies
+// (16-key boxes, hardware swizzle, so ldmatrix reads are free of bank conflicts), 24 KB a warp and
+// 192 KB an SM, several times the 54 KB an SM needs to cover HBM's latency at full rate. No producer warp and no
+// barrier between warps inside a range: a ring runs on into the next item's tiles.
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "mot_kvcache.cuh"
@@ -13,104 +41,631 @@ namespace mot {
 namespace decode {
 
 constexpr int WARPS = 8;
+constexpr int THREADS = 32 * WARPS;
+constexpr int HEADS = 8;      // query heads of an item
+constexpr int SPLIT_ITEMS = 152;  // items that one row is cut into, at most: one for each SM
+constexpr float kAbove = 14.0f, kBelow = 6.0f;  // the reference's slack, powers of two
+
+template <int D, bool E4M3>
+struct Cfg {
+  static constexpr int ROW = D * (E4M3 ? 1 : 2);            // bytes of a cached vector
+  static constexpr int TOK = ROW == 256 ? 16 : 32;          // keys of a tile: 4 KB of K (2 KB at 64-byte rows)
+  static constexpr int KT = TOK * ROW;                      // bytes of a tile's K
+  static constexpr int BOX = ROW < 128 ? ROW : 128;         // bytes of a TMA box's row, the swizzle's width
+  static constexpr int HALVES = ROW / BOX;                  // boxes across a row
+  static constexpr int SC = E4M3 ? TOK * 8 : 0;             // bytes of a tile's scales
+  static constexpr int STAGES = KT == 2048 ? 6 : 3;
+  static constexpr int ROUND = WARPS * TOK;                 // keys a CTA takes at a time
+  static constexpr int MIN_SPAN = 256;                      // shortest range
+  static constexpr uint32_t TILES = 0;                      // [WARPS][STAGES][K tile, V tile]
+  static constexpr uint32_t SCALES = TILES + WARPS * STAGES * 2 * KT;
+  static constexpr uint32_t ML = SCALES + WARPS * STAGES * SC;        // [2][WARPS][HEADS] float
+  static constexpr uint32_t SLOT = ML + 2 * WARPS * HEADS * 4;        // [WARPS] where a warp's O lies
+  static constexpr uint32_t BARS = SLOT + WARPS * 4;
+  static constexpr uint32_t ABORT = BARS + WARPS * STAGES * 8;
+  static constexpr size_t BYTES = 1024 + size_t(ABORT) + 16;
+  static_assert(HEADS * D * 4 <= KT, "a warp's O fits into a tile's K");
+};
 
 struct Args {
   const uint16_t* qkv;   // [R][(Hq + 2 Hkv) D]
   const int32_t* table;  // [R][max_pages]
   const int32_t* lens;   // [R]
-  const uint8_t* k;
-  const uint8_t* v;
   const float* scales;
   int64_t n_pages;
-  int max_pages, page;
-  int Hq, Hkv;
-  float c;  // scale * log2(e)
-  uint16_t* out;  // [R][Hq D]
+  int R, max_pages, page;
+  int Hq, Hkv, G;        // G = Hq / Hkv
+  int HC;                // groups of up to 8 heads that share a KV head
+  int max_split;         // ranges of a row that the workspace has room for
+  float c;               // scale * log2(e)
+  float2* ml;            // [R][max_split][Hq] (reference, sum) of a range
+  float* part;           // [R][max_split][Hq][D]
+  uint16_t* out;         // [R][Hq D]
   uint32_t* err;
 };
 
+// Keys of a row's ranges, and how many there are (an empty row has one empty range, which writes its
+// zeros). `round` and `min_span` are those of Cfg.
+__host__ __device__ inline int span_of(int len, int round, int min_span, int heads) {
+  const int most = SPLIT_ITEMS / heads > 1 ? SPLIT_ITEMS / heads : 1;
+  const int each = (len + most - 1) / most;
+  const int span = (each + round - 1) / round * round;
+  return span > min_span ? span : min_span;
+}
+__host__ __device__ inline int splits_of(int len, int span) { return len == 0 ? 1 : (len + span - 1) / span; }
+
+// ---------------------------------------------------------------------------
+// small wrappers
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool HALF>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  if (HALF)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(r) : "r"(a), "r"(sel));
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// items
+// ---------------------------------------------------------------------------
+struct Item {
+  int row, g, hc, split, n_split;
+  int t0, t1;  // keys [t0, t1) of the row
+};
+
+// Finds items in ascending order; warp-uniform results. The lanes hold 32 rows' lengths at a time.
 template <int D, bool E4M3>
-__device__ __forceinline__ void load_vec(const uint8_t* base, int64_t row, int lane, float (&x)[D / 32]) {
-  if (E4M3) {
-    const uint8_t* p = base + row * D + lane * (D / 32);
-#pragma unroll
-    for (int i = 0; i < D / 32; i += 2) {
-      const float2 f = kv::h2_to_f2(kv::e4m3x2_to_h2(*reinterpret_cast<const uint16_t*>(p + i)));
-      x[i] = f.x;
-      x[i + 1] = f.y;
+struct Walk {
+  int64_t base;  // items of the rows before rb
+  int rb, len, n, incl;
+
+  __device__ void load(const Args& a, bool report) {
+    const int lane = threadIdx.x & 31, row = rb + lane;
+    len = 0;
+    n = 0;
+    if (row < a.R) {
+      len = a.lens[row];
+      if (len < 0 || len > int64_t(a.max_pages) * a.page) {
+        if (report) atomicOr(a.err, MOT_DEV_BAD_PAGE);
+      } else {
+        const int heads = a.Hkv * a.HC;
+        n = splits_of(len, span_of(len, Cfg<D, E4M3>::ROUND, Cfg<D, E4M3>::MIN_SPAN, heads)) * heads;
+      }
     }
-  } else {
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + row * D + lane * (D / 32);
+    incl = n;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) x[i] = bf_to_f(p[i]);
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += o;
+    }
+  }
+  __device__ void init(const Args& a, bool report) {
+    base = 0;
+    rb = 0;
+    load(a, report);
+  }
+  __device__ bool find(const Args& a, int64_t it, Item& m, bool report) {
+    for (;;) {
+      const int total = __shfl_sync(0xffffffffu, incl, 31);
+      if (it < base + total) break;
+      if (rb + 32 >= a.R) return false;
+      base += total;
+      rb += 32;
+      load(a, report);
+    }
+    const int k = int(it - base);
+    const int l = __ffs(__ballot_sync(0xffffffffu, k < incl)) - 1;
+    const int local = k - (__shfl_sync(0xffffffffu, incl, l) - __shfl_sync(0xffffffffu, n, l));
+    const int nk = __shfl_sync(0xffffffffu, len, l), heads = a.Hkv * a.HC;
+    const int span = span_of(nk, Cfg<D, E4M3>::ROUND, Cfg<D, E4M3>::MIN_SPAN, heads);
+    m.row = rb + l;
+    m.split = local / heads;
+    const int hh = local - m.split * heads;
+    m.g = hh / a.HC;
+    m.hc = hh - m.g * a.HC;
+    m.n_split = splits_of(nk, span);
+    m.t0 = m.split * span;
+    m.t1 = m.t0 + span < nk ? m.t0 + span : nk;
+    return true;
+  }
+};
+
+// Shared-memory offset of the 16-byte chunk c of row r in a tile (the TMA's swizzle).
+template <int D, bool E4M3>
+__device__ __forceinline__ uint32_t chunk(int r, int c) {
+  using C = Cfg<D, E4M3>;
+  if (C::BOX == 64) return uint32_t(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+  // boxes of 16 rows, one behind the other per 16 keys: [16-key block][half][16 rows][128 bytes]
+  return uint32_t(((r >> 4) * C::HALVES + (c >> 3)) * 2048 + (r & 15) * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(THREADS, 1)
+    decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Args a) {
+  using C = Cfg<D, E4M3>;
+  constexpr int TOK = C::TOK, NT = TOK / 8, KS = D / 16, STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
+  uint8_t* ring = smem + C::TILES + warp * STAGES * 2 * C::KT;
+  uint8_t* ring_sc = smem + C::SCALES + warp * STAGES * C::SC;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BARS) + warp * STAGES;
+  float* s_ref = reinterpret_cast<float*>(smem + C::ML);
+  float* s_sum = s_ref + WARPS * HEADS;
+  uint32_t* s_slot = reinterpret_cast<uint32_t*>(smem + C::SLOT);
+  volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(smem + C::ABORT);
+
+  if (lane == 0) {
+    for (int i = 0; i < STAGES; ++i) mbar_init(smem_u32(&full[i]), 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 0) {
+    *abort_flag = 0u;
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- the warp's stream of tiles: the cursor `p` is the next tile to be copied, the table entry of
+  // lane i's 16 keys already on its way ----
+  const bool report = blockIdx.x == 0 && warp == 0;
+  Walk<D, E4M3> walk;
+  walk.init(a, report);
+  Walk<D, E4M3> pwalk = walk;
+  Item p;
+  int64_t pit = blockIdx.x;
+  int ptile = 0;        // first key of the tile
+  int ppage = 0;        // lane i < TOK / 16: the page of the tile's keys 16 i ..
+  int issued = 0, taken = 0;
+  bool ok = true;  // no wait of this warp has given up
+  bool pmore = pwalk.find(a, pit, p, false);
+  if (pmore) ptile = p.t0 + warp * TOK;
+
+  auto seek = [&]() {  // moves p to the next tile that exists and starts its table lookup
+    while (pmore && ptile >= p.t1) {
+      pit += gridDim.x;
+      pmore = pwalk.find(a, pit, p, false);
+      if (pmore) ptile = p.t0 + warp * TOK;
+    }
+    if (pmore && lane < TOK / 16 && ptile + 16 * lane < p.t1)
+      ppage = __ldg(a.table + int64_t(p.row) * a.max_pages + (ptile + 16 * lane) / a.page);
+  };
+  auto issue = [&]() {  // copies the tile at p into the next slot and moves on
+    if (!pmore || !ok) return;
+    const int st = issued % STAGES;
+    const uint32_t bar = smem_u32(&full[st]);
+    const int blocks = (min(TOK, p.t1 - ptile) + 15) / 16;
+    if (lane == 0) mbar_arrive_expect_tx(bar, blocks * (16 * (2 * C::ROW + (E4M3 ? 8 : 0))));
+    __syncwarp();
+    if (lane < blocks) {
+      int pg = ppage;
+      if (pg < 0 || pg >= a.n_pages) {
+        atomicOr(a.err, MOT_DEV_BAD_PAGE);
+        pg = 0;
+      }
+      const int key = ptile + 16 * lane;
+      const int y = (pg * a.Hkv + p.g) * a.page + key % a.page;
+      const uint32_t dst = smem_u32(ring + st * 2 * C::KT) + lane * (16 * C::ROW);
+#pragma unroll
+      for (int h = 0; h < C::HALVES; ++h) tma_load_2d(dst + h * 2048, &tm_k, h * (C::BOX / (E4M3 ? 1 : 2)), y, bar);
+#pragma unroll
+      for (int h = 0; h < C::HALVES; ++h)
+        tma_load_2d(dst + C::KT + h * 2048, &tm_v, h * (C::BOX / (E4M3 ? 1 : 2)), y, bar);
+      if (E4M3) bulk_load(smem_u32(ring_sc + st * C::SC) + lane * 128, a.scales + 2 * int64_t(y), 128, bar);
+    }
+    ++issued;
+    ptile += C::ROUND;
+    seek();
+  };
+  seek();
+  for (int i = 0; i < STAGES; ++i) issue();
+
+  Item m;
+  for (int64_t it = blockIdx.x; walk.find(a, it, m, report); it += gridDim.x) {
+    // ---- the query fragments: head g8 of the group in row g8, rows 8 .. 15 empty ----
+    const int h0 = m.g * a.G + m.hc * HEADS;                      // first query head
+    const int nh = min(HEADS, a.G - m.hc * HEADS);                // heads of this item
+    uint32_t q[KS][2];
+    const uint16_t* qrow = a.qkv + (int64_t(m.row) * (a.Hq + 2 * a.Hkv) + h0 + g8) * D;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      // element pairs of columns 2 t and 2 t + 8 of the k-step: dims 16 s + 2 t and + 8 (bf16), or, as an
+      // e4m3 lane holds 4 consecutive dims, 16 s + 4 t and + 2
+      const int d0 = 16 * s + (E4M3 ? 4 * t4 : 2 * t4), d1 = d0 + (E4M3 ? 2 : 8);
+      q[s][0] = g8 < nh ? *reinterpret_cast<const uint32_t*>(qrow + d0) : 0u;
+      q[s][1] = g8 < nh ? *reinterpret_cast<const uint32_t*>(qrow + d1) : 0u;
+    }
+    float c = a.c;
+    if (E4M3) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          top = max(top, max((q[s][i] << 16) & 0x7FFFFFFFu, q[s][i] & 0x7FFF0000u));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      int e = 14 - (int(top >> 23) - 127);   // 2^e takes the largest element into [2^14, 2^15)
+      e = min(e, 100);
+      const float f = __uint_as_float(uint32_t(e + 127) << 23);
+      c = __fmul_rn(c, __uint_as_float(uint32_t(127 - e) << 23));
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) q[s][i] = pack_h2(__fmul_rn(bf_lo(q[s][i]), f), __fmul_rn(bf_hi(q[s][i]), f));
+    }
+
+    float o[D / 16][4];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+    float ref = -INFINITY, sum = 0.0f;
+    int slot = -1;  // the slot of the item's last tile, held back: O passes through it
+
+    for (int tile = m.t0 + warp * TOK; tile < m.t1; tile += C::ROUND) {
+      if (slot >= 0) issue();  // into the slot that the tile before has left
+      const int st = taken % STAGES;
+      slot = st;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[st]), uint32_t(taken / STAGES) & 1u, abort_flag,
+                                                     a.err));
+      if (!ok) continue;
+      ++taken;
+      uint8_t* kt = ring + st * 2 * C::KT;
+      const uint32_t kb = smem_u32(kt), vb = kb + C::KT;
+      const int nv = min(TOK, m.t1 - tile);  // keys of the tile
+      if (nv < TOK) {
+        // rows of V behind the last key: whatever the page holds there (or the slot, where no page was
+        // copied) must not meet a weight of zero as a NaN
+        for (int i = lane; i < (TOK - nv) * (C::ROW / 16); i += 32)
+          *reinterpret_cast<uint4*>(kt + C::KT + chunk<D, E4M3>(nv + i / (C::ROW / 16), i % (C::ROW / 16))) =
+              make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();  // before a later copy into the slot
+        __syncwarp();
+      }
+
+      // ---- S = Q K^T: lane has head g8, keys 8 j + 2 t4 and + 1 ----
+      float x[NT][4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[j][i] = 0.0f;
+      if constexpr (E4M3) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          uint32_t r[4];
+          ldsm4(r, kb + chunk<D, E4M3>(lane, s));
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            mma16816<true>(x[j], q[s][0], 0u, q[s][1], 0u, kv::e4m3x2_to_h2(r[j] & 0xFFFFu),
+                           kv::e4m3x2_to_h2(r[j] >> 16));
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int b = 0; b < TOK / 16; ++b) {
+            uint32_t r[4];
+            ldsm4(r, kb + chunk<D, E4M3>(16 * b + (lane >> 4) * 8 + (lane & 7), 2 * s + ((lane >> 3) & 1)));
+            mma16816<false>(x[2 * b], q[s][0], 0u, q[s][1], 0u, r[0], r[1]);
+            mma16816<false>(x[2 * b + 1], q[s][0], 0u, q[s][1], 0u, r[2], r[3]);
+          }
+      }
+
+      // ---- weights ----
+      float tmax = -INFINITY;
+      float inv[NT][2], fac[NT][2];  // e4m3: 2^-e and s / 2^e of each key's V scale s, e its exponent
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if constexpr (E4M3) {
+          const float4 sc = *reinterpret_cast<const float4*>(ring_sc + st * C::SC + (8 * j + 2 * t4) * 8);
+          const float ks[2] = {sc.x, sc.z}, vs[2] = {sc.y, sc.w};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t b = __float_as_uint(vs[i]);
+            const int e = int(b >> 23) - 127;
+            inv[j][i] = __uint_as_float(uint32_t(127 - e) << 23);
+            fac[j][i] = __uint_as_float((b & 0x007FFFFFu) | 0x3F800000u);
+            // a scale that is not finite makes the key's weight NaN
+            const float ev = __fadd_rn(float(e), __fmul_rn(vs[i], 0.0f));
+            x[j][i] = __fadd_rn(__fmul_rn(__fmul_rn(x[j][i], c), ks[i]), ev);
+          }
+        } else {
+          x[j][0] = __fmul_rn(x[j][0], c);
+          x[j][1] = __fmul_rn(x[j][1], c);
+        }
+        if (nv < TOK) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (8 * j + 2 * t4 + i >= nv) {
+              x[j][i] = -INFINITY;
+              if constexpr (E4M3) inv[j][i] = fac[j][i] = 0.0f;  // whatever the scale's place holds
+            }
+        }
+        tmax = fmaxf(tmax, fmaxf(x[j][0], x[j][1]));
+      }
+      tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
+      tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
+      const bool moves = tmax > __fadd_rn(ref, kAbove);  // also from -inf
+      if (__any_sync(0xffffffffu, moves)) {
+        const float next = moves ? __fsub_rn(tmax, kBelow) : ref;
+        const float alpha = moves ? (ref == -INFINITY ? 0.0f : exp2f(__fsub_rn(ref, next))) : 1.0f;
+        ref = next;
+        sum = __fmul_rn(sum, alpha);
+        const float al0 = __shfl_sync(0xffffffffu, alpha, 8 * t4), al1 = __shfl_sync(0xffffffffu, alpha, 8 * t4 + 4);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          o[i][0] = __fmul_rn(o[i][0], al0);
+          o[i][1] = __fmul_rn(o[i][1], al1);
+          o[i][2] = __fmul_rn(o[i][2], al0);
+          o[i][3] = __fmul_rn(o[i][3], al1);
+        }
+      }
+      const float nref = ref == -INFINITY ? 0.0f : -ref;  // no key with a weight yet: every x is -inf
+      uint32_t w[NT], wl[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        float w0 = exp2f(__fadd_rn(x[j][0], nref)), w1 = exp2f(__fadd_rn(x[j][1], nref));
+        if constexpr (E4M3) {
+          sum = __fadd_rn(sum, __fadd_rn(__fmul_rn(w0, inv[j][0]), __fmul_rn(w1, inv[j][1])));
+          w[j] = pack_h2(__fmul_rn(w0, fac[j][0]), __fmul_rn(w1, fac[j][1]));
+        } else {
+          sum = __fadd_rn(sum, __fadd_rn(w0, w1));
+          w[j] = pack_bf2(w0, w1);
+          wl[j] = pack_bf2(__fsub_rn(w0, bf_lo(w[j])), __fsub_rn(w1, bf_hi(w[j])));
+        }
+      }
+
+      // ---- O^T += V^T W^T: lane has dims g8 and g8 + 8 (e4m3: 2 g8 and 2 g8 + 1) of 16, heads 2 t4, + 1 ----
+      if constexpr (E4M3) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          uint32_t r[4];
+          ldsm4t(r, vb + chunk<D, E4M3>(lane, s));  // pairs of dims of keys 2 t, 2 t + 1 in each 8-key group
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r[i] = prmt(r[i], 0x3120);
+#pragma unroll
+          for (int b = 0; b < TOK / 16; ++b)
+            mma16816<true>(o[s], kv::e4m3x2_to_h2(r[2 * b] & 0xFFFFu), kv::e4m3x2_to_h2(r[2 * b] >> 16),
+                           kv::e4m3x2_to_h2(r[2 * b + 1] & 0xFFFFu), kv::e4m3x2_to_h2(r[2 * b + 1] >> 16), w[2 * b],
+                           w[2 * b + 1]);
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int b = 0; b < TOK / 16; ++b) {
+            uint32_t r[4];
+            ldsm4t(r, vb + chunk<D, E4M3>(16 * b + (lane >> 4) * 8 + (lane & 7), 2 * s + ((lane >> 3) & 1)));
+            mma16816<false>(o[s], r[0], r[1], r[2], r[3], w[2 * b], w[2 * b + 1]);
+            mma16816<false>(o[s], r[0], r[1], r[2], r[3], wl[2 * b], wl[2 * b + 1]);
+          }
+      }
+      __syncwarp();  // every lane has read the slot
+    }
+
+    // ---- the warps' results are joined in warp order; O passes through the last tile's slot ----
+    sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 1));
+    sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 2));
+    if (t4 == 0) {
+      s_ref[warp * HEADS + g8] = ref;
+      s_sum[warp * HEADS + g8] = sum;
+    }
+    if (slot >= 0 && ok) {
+      // [head][dim ^ 8 (head / 2)]: the four lanes of a group fall into different banks
+      float* ob = reinterpret_cast<float*>(ring + slot * 2 * C::KT);
+      const int sw = 8 * t4;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float* ho = ob + (2 * t4 + j) * D;
+          if (E4M3) {
+            *reinterpret_cast<float2*>(ho + ((16 * i + 2 * g8) ^ sw)) = make_float2(o[i][j], o[i][j + 2]);
+          } else {
+            ho[(16 * i + g8) ^ sw] = o[i][j];
+            ho[(16 * i + g8 + 8) ^ sw] = o[i][j + 2];
+          }
+        }
+    }
+    if (lane == 0) s_slot[warp] = slot < 0 ? 0u : uint32_t(C::TILES + (warp * STAGES + slot) * 2 * C::KT);
+    __syncthreads();
+    if (warp < nh && *abort_flag == 0u) {  // warp k joins head k, D / 32 dims a lane
+      constexpr int E = D / 32;
+      float refs[WARPS], top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < WARPS; ++k) {
+        refs[k] = s_ref[k * HEADS + warp];
+        top = fmaxf(top, refs[k]);
+      }
+      float total = 0.0f, acc[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) acc[i] = 0.0f;
+      const int d = (E * lane) ^ (8 * (warp >> 1));
+#pragma unroll
+      for (int k = 0; k < WARPS; ++k) {
+        // a warp without tiles has -inf here; one whose scores are all -inf has a sum of zero, or NaN
+        if (refs[k] == -INFINITY) {
+          total = __fadd_rn(total, s_sum[k * HEADS + warp]);
+          continue;
+        }
+        const float f = exp2f(__fsub_rn(refs[k], top));
+        total = __fadd_rn(total, __fmul_rn(s_sum[k * HEADS + warp], f));
+        const float* src = reinterpret_cast<const float*>(smem + s_slot[k]) + warp * D + d;
+        float v[E];
+        if constexpr (E == 4) {
+          const float4 u = *reinterpret_cast<const float4*>(src);
+          v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+        } else {
+          const float2 u = *reinterpret_cast<const float2*>(src);
+          v[0] = u.x; v[1] = u.y;
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = __fadd_rn(acc[i], __fmul_rn(v[i], f));
+      }
+      const int head = h0 + warp;
+      if (m.n_split == 1) {
+        const float r = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+        uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (int64_t(m.row) * a.Hq + head) * D) + lane * (E / 2);
+#pragma unroll
+        for (int i = 0; i < E; i += 2) dst[i / 2] = pack_bf2(__fmul_rn(acc[i], r), __fmul_rn(acc[i + 1], r));
+      } else {
+        const int64_t at = (int64_t(m.row) * a.max_split + m.split) * a.Hq + head;
+        float* dst = a.part + at * D + E * lane;
+        if constexpr (E == 4) *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        else *reinterpret_cast<float2*>(dst) = make_float2(acc[0], acc[1]);
+        if (lane == 0) a.ml[at] = make_float2(top, total);
+      }
+    }
+    fence_proxy_async_smem();  // the slots go back to the copies
+    __syncthreads();
+    if (slot >= 0) issue();
+  }
+  // after a wait that gave up: every copy has landed before the CTA can exit
+  for (; taken < issued; ++taken) mbar_drain(smem_u32(&full[taken % STAGES]), uint32_t(taken / STAGES) & 1u);
+}
+
+// Joins the ranges of one (row, head): the references' maximum, each range's factor, then the ranges
+// w, w + 8, ... by warp w in ascending order and the 8 warps' sums in order. Rows of one range were
+// written by decode_kernel.
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(256) join_kernel(const Args a) {
+  constexpr int E = D / 32;
+  __shared__ float s_f[SPLIT_ITEMS], s_top[WARPS], s_tot[WARPS];
+  __shared__ float s_acc[WARPS][D];
+  pdl_wait();
+  const int row = int(blockIdx.x / a.Hq), head = int(blockIdx.x % a.Hq);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int len = a.lens[row];
+  if (len <= 0 || len > int64_t(a.max_pages) * a.page) return;
+  const int n = splits_of(len, span_of(len, Cfg<D, E4M3>::ROUND, Cfg<D, E4M3>::MIN_SPAN, a.Hkv * a.HC));
+  if (n <= 1) return;
+  const int64_t at0 = int64_t(row) * a.max_split * a.Hq + head;
+  const float2 ml = threadIdx.x < n ? a.ml[at0 + int64_t(threadIdx.x) * a.Hq] : make_float2(-INFINITY, 0.0f);
+  float top = ml.x;
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  if (lane == 0) s_top[warp] = top;
+  __syncthreads();
+  top = s_top[0];
+#pragma unroll
+  for (int k = 1; k < WARPS; ++k) top = fmaxf(top, s_top[k]);
+  const float f = ml.x == -INFINITY ? 0.0f : exp2f(__fsub_rn(ml.x, top));
+  if (threadIdx.x < n) s_f[threadIdx.x] = f;
+  float tot = ml.x == -INFINITY ? ml.y : __fmul_rn(ml.y, f);
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) tot = __fadd_rn(tot, __shfl_xor_sync(0xffffffffu, tot, off));
+  if (lane == 0) s_tot[warp] = tot;
+  __syncthreads();
+  float acc[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) acc[i] = 0.0f;
+#pragma unroll 4
+  for (int s = warp; s < n; s += WARPS) {
+    const float* src = a.part + (at0 + int64_t(s) * a.Hq) * D + E * lane;
+    float v[E];
+    if constexpr (E == 4) {
+      const float4 u = *reinterpret_cast<const float4*>(src);
+      v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+    } else {
+      const float2 u = *reinterpret_cast<const float2*>(src);
+      v[0] = u.x; v[1] = u.y;
+    }
+    const float fs = s_f[s];
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[i] = __fadd_rn(acc[i], __fmul_rn(v[i], fs));
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) s_acc[warp][E * lane + i] = acc[i];
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float total = s_tot[0], v = s_acc[0][threadIdx.x];
+#pragma unroll
+    for (int k = 1; k < WARPS; ++k) {
+      total = __fadd_rn(total, s_tot[k]);
+      v = __fadd_rn(v, s_acc[k][threadIdx.x]);
+    }
+    const float r = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+    a.out[(int64_t(row) * a.Hq + head) * D + threadIdx.x] = f_to_bf(__fmul_rn(v, r));
   }
 }
 
-// One CTA per (row, query head); each warp takes every eighth key with its own running maximum and
-// sum, the warps' results are joined in order.
+// Ranges that a row can have when its table holds max_len keys.
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(32 * WARPS) decode_kernel(const Args a) {
-  constexpr int E = D / 32;
-  __shared__ float sm[WARPS], sl[WARPS], so[WARPS][D];
-  const int64_t row = blockIdx.x / a.Hq;
-  const int h = int(blockIdx.x % a.Hq), g = h / (a.Hq / a.Hkv);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int len = a.lens[row];
-  if (len < 0 || len > int64_t(a.max_pages) * a.page) {
-    if (threadIdx.x == 0) atomicOr(a.err, MOT_DEV_BAD_PAGE);
-    return;
-  }
-  float q[E], o[E];
-  const uint16_t* qp = a.qkv + (row * (a.Hq + 2 * a.Hkv) + h) * D + lane * E;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    q[i] = bf_to_f(qp[i]);
-    o[i] = 0.0f;
-  }
-  float m = -INFINITY, l = 0.0f;
-  for (int j = warp; j < len; j += WARPS) {
-    int p = a.table[row * a.max_pages + j / a.page];
-    if (p < 0 || p >= a.n_pages) {
-      if (lane == 0) atomicOr(a.err, MOT_DEV_BAD_PAGE);
-      p = 0;
-    }
-    const int64_t r = (int64_t(p) * a.Hkv + g) * a.page + j % a.page;
-    float x[E], s = 0.0f;
-    load_vec<D, E4M3>(a.k, r, lane, x);
-#pragma unroll
-    for (int i = 0; i < E; ++i) s = __fadd_rn(s, __fmul_rn(q[i], x[i]));
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
-    if (E4M3) s = __fmul_rn(s, a.scales[2 * r]);
-    s = __fmul_rn(s, a.c);
-    const float mn = s > m || isnan(s) ? s : m;
-    const float alpha = m == -INFINITY ? 0.0f : exp2f(__fsub_rn(m, mn));
-    float w = mn == -INFINITY ? 0.0f : exp2f(__fsub_rn(s, mn));
-    m = mn;
-    l = __fadd_rn(__fmul_rn(l, alpha), w);
-    load_vec<D, E4M3>(a.v, r, lane, x);
-    if (E4M3) w = __fmul_rn(w, a.scales[2 * r + 1]);
-#pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = __fadd_rn(__fmul_rn(o[i], alpha), __fmul_rn(w, x[i]));
-  }
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < E; ++i) so[warp][lane * E + i] = o[i];
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float top = sm[0];
-    for (int w = 1; w < WARPS; ++w) top = sm[w] > top || isnan(sm[w]) ? sm[w] : top;
-    float sum = 0.0f, acc = 0.0f;
-    for (int w = 0; w < WARPS; ++w) {
-      const float f = sm[w] == -INFINITY ? 0.0f : exp2f(__fsub_rn(sm[w], top));
-      sum = __fadd_rn(sum, __fmul_rn(sl[w], f));
-      acc = __fadd_rn(acc, __fmul_rn(so[w][threadIdx.x], f));
-    }
-    a.out[(row * a.Hq + h) * D + threadIdx.x] = f_to_bf(sum == 0.0f ? 0.0f : __fdiv_rn(acc, sum));
-  }
+inline int max_split(int64_t max_len, int heads) {
+  const int most = SPLIT_ITEMS / heads > 1 ? SPLIT_ITEMS / heads : 1;
+  const int64_t n = (max_len + Cfg<D, E4M3>::MIN_SPAN - 1) / Cfg<D, E4M3>::MIN_SPAN;
+  return n < most ? int(n) : most;
+}
+
+// 2D map of the cache's vectors [rows][D] in boxes of 16 rows.
+inline bool cache_map(CUtensorMap* m, const void* base, int D, bool e4m3, int64_t rows) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (enc == nullptr) return false;
+  const int bytes = D * (e4m3 ? 1 : 2), box_bytes = bytes < 128 ? bytes : 128;
+  cuuint64_t dims[2] = {cuuint64_t(D), cuuint64_t(rows)};
+  cuuint64_t strides[1] = {cuuint64_t(bytes)};
+  cuuint32_t box[2] = {cuuint32_t(e4m3 ? box_bytes : box_bytes / 2), 16};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool E4M3>
+static int launch(Args a, const void* k, const void* v, int dev, cudaStream_t s) {
+  using C = Cfg<D, E4M3>;
+  const int heads = a.Hkv * a.HC;
+  a.max_split = max_split<D, E4M3>(int64_t(a.max_pages) * a.page, heads);
+  a.part = reinterpret_cast<float*>(a.ml + (int64_t(a.R) * a.max_split * a.Hq + 1) / 2 * 2);
+  CUtensorMap tm_k, tm_v;
+  const int64_t rows = a.n_pages * a.Hkv * a.page;
+  if (!cache_map(&tm_k, k, D, E4M3, rows) || !cache_map(&tm_v, v, D, E4M3, rows)) return MOT_ERR_CUDA;
+  if (cudaFuncSetAttribute(decode_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::BYTES)) !=
+      cudaSuccess)
+    return MOT_ERR_CUDA;
+  const int64_t items = int64_t(a.R) * a.max_split * heads;
+  const unsigned grid = unsigned(items < sm_count(dev) ? items : sm_count(dev));
+  if (launch_dependent(decode_kernel<D, E4M3>, dim3(grid), dim3(THREADS), C::BYTES, s, tm_k, tm_v, a) != cudaSuccess)
+    return MOT_ERR_CUDA;
+  if (a.max_split > 1 &&
+      launch_dependent(join_kernel<D, E4M3>, dim3(unsigned(int64_t(a.R) * a.Hq)), dim3(256), 0, s, a) != cudaSuccess)
+    return MOT_ERR_CUDA;
+  return MOT_OK;
 }
 
 }  // namespace decode
@@ -121,7 +676,13 @@ using namespace mot;
 extern "C" size_t mot_paged_decode_workspace_bytes(int64_t R, int Hq, int Hkv, int D, int max_pages, int page) {
   if (kv::check_shape(Hq, Hkv, D, MOT_KV_BF16, 1, page) != MOT_OK) return 0;
   if (R < 1 || R > MOT_MAX_TOKENS || max_pages < 1 || int64_t(max_pages) * page > (int64_t(1) << 30)) return 0;
-  return sizeof(PlanHeader);
+  if (R * Hq > (int64_t(1) << 31) - 1) return 0;
+  const int G = Hq / Hkv, heads = Hkv * ((G + decode::HEADS - 1) / decode::HEADS);
+  const int64_t n = D == 64 ? decode::max_split<64, false>(int64_t(max_pages) * page, heads)
+                            : decode::max_split<128, false>(int64_t(max_pages) * page, heads);
+  // a (reference, sum) pair and D floats for each range of each (row, head), unless no row is split
+  const int64_t parts = n > 1 ? R * n * Hq : 0;
+  return sizeof(PlanHeader) + size_t((parts * 8 + 15) / 16 * 16) + size_t(parts) * D * 4;
 }
 
 extern "C" int mot_paged_decode_attention(const mot_bf16* qkv, int64_t R, int Hq, int Hkv, int D, const int32_t* table,
@@ -133,7 +694,7 @@ extern "C" int mot_paged_decode_attention(const mot_bf16* qkv, int64_t R, int Hq
   int st = kv::check_shape(Hq, Hkv, D, kv_type, n_pages, page);
   if (st != MOT_OK) return st;
   const size_t need = mot_paged_decode_workspace_bytes(R, Hq, Hkv, D, max_pages, page);
-  if (need == 0 || R * Hq > (int64_t(1) << 31) - 1) return MOT_ERR_GEOMETRY;
+  if (need == 0) return MOT_ERR_GEOMETRY;
   if (!(scale > 0.0f) || !(scale < 3.0e38f)) return MOT_ERR_ARG;
   if (!aligned16(qkv) || !aligned16(table) || !aligned16(lens) || !aligned16(k_cache) || !aligned16(v_cache) ||
       !aligned16(ws) || !aligned16(out) || (e4m3 && !aligned16(scales)))
@@ -149,21 +710,21 @@ extern "C" int mot_paged_decode_attention(const mot_bf16* qkv, int64_t R, int Hq
   a.qkv = qkv;
   a.table = table;
   a.lens = lens;
-  a.k = static_cast<const uint8_t*>(k_cache);
-  a.v = static_cast<const uint8_t*>(v_cache);
   a.scales = scales;
   a.n_pages = n_pages;
+  a.R = int(R);
   a.max_pages = max_pages;
   a.page = page;
   a.Hq = Hq;
   a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.HC = (a.G + decode::HEADS - 1) / decode::HEADS;
   a.c = scale * 1.4426950408889634f;
+  a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + sizeof(PlanHeader));
   a.out = out;
   a.err = &static_cast<PlanHeader*>(ws)->error;
-  const unsigned grid = unsigned(R * Hq);
-  if (D == 64 && e4m3) decode::decode_kernel<64, true><<<grid, 32 * decode::WARPS, 0, s>>>(a);
-  else if (D == 64) decode::decode_kernel<64, false><<<grid, 32 * decode::WARPS, 0, s>>>(a);
-  else if (e4m3) decode::decode_kernel<128, true><<<grid, 32 * decode::WARPS, 0, s>>>(a);
-  else decode::decode_kernel<128, false><<<grid, 32 * decode::WARPS, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MOT_OK : MOT_ERR_CUDA;
+  if (D == 64) return e4m3 ? decode::launch<64, true>(a, k_cache, v_cache, dev, s)
+                           : decode::launch<64, false>(a, k_cache, v_cache, dev, s);
+  return e4m3 ? decode::launch<128, true>(a, k_cache, v_cache, dev, s)
+              : decode::launch<128, false>(a, k_cache, v_cache, dev, s);
 }
