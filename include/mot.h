@@ -367,7 +367,7 @@ size_t mot_paged_decode_workspace_bytes(int64_t R, int Hq, int Hkv, int D, int m
  *          after its first 64 bytes is scratch that the call overwrites (so not a routing plan in use).
  *   out    [R][Hq D] bf16             out.
  * Rows of one sequence (several new tokens) are several rows with equal page tables and their own
- * lengths. Geometry: 1 <= R <= MOT_MAX_TOKENS, R * Hq < 2^31, max_pages >= 1, max_pages * page <= 2^30.
+ * lengths. Geometry: 1 <= R <= MOT_MAX_TOKENS, R * (Hq + 2 Hkv) < 2^31, max_pages >= 1, max_pages * page <= 2^30.
  */
 int mot_paged_decode_attention(const mot_bf16* qkv, int64_t R, int Hq, int Hkv, int D, const int32_t* table,
                                const int32_t* lens, int max_pages, int kv_type, int64_t n_pages, int page,

@@ -27,10 +27,13 @@
 //
 // What bounds it: HBM. A key costs 4 G flop per 4 bytes, far below the tensor cores' rate even on
 // mma.sync (tcgen05's smallest M is 64 rows; here there are at most 8), so the design is about bytes in
-// flight: every warp owns a ring of STAGES tiles in shared memory, filled by its own TMA copies
-// (16-key boxes, hardware swizzle, so ldmatrix reads are free of bank conflicts), 24 KB a warp and
-// 192 KB an SM, several times the 54 KB an SM needs to cover HBM's latency at full rate. No producer warp and no
-// barrier between warps inside a range: a ring runs on into the next item's tiles.
+// flight: every consumer warp owns a ring of STAGES tiles in shared memory (24 KB a warp, 192 KB an SM,
+// several times the 54 KB an SM needs to cover HBM's latency at full rate) and meets the others only
+// where an item ends. A producer warp walks the items, looks the pages up one round ahead (a lane for
+// each 16 keys), and fills the rings with TMA copies (16-key boxes, hardware swizzle, so ldmatrix reads
+// are free of bank conflicts) and a ring of item descriptors with the queries, running on into the next
+// items while the consumers join one. With every warp walking and copying for itself, the lookups'
+// latencies stood in the consumers' way: 45 us instead of the figure below on 256 rows of 100 to 300 keys.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -40,8 +43,11 @@
 namespace mot {
 namespace decode {
 
-constexpr int WARPS = 8;
-constexpr int THREADS = 32 * WARPS;
+constexpr int WARPS = 8;                  // consumers
+constexpr int PRODUCERS = 4;              // warps 8 .. 11, two consumers each
+constexpr int THREADS = 32 * (WARPS + PRODUCERS);
+constexpr int ITEMS = 4;                  // item descriptors in flight
+constexpr int WINDOW = 256;               // rows whose item counts the producer holds at a time
 constexpr int HEADS = 8;      // query heads of an item
 constexpr int SPLIT_ITEMS = 152;  // items that one row is cut into, at most: one for each SM
 constexpr float kAbove = 14.0f, kBelow = 6.0f;  // the reference's slack, powers of two
@@ -59,12 +65,28 @@ struct Cfg {
   static constexpr int MIN_SPAN = 256;                      // shortest range
   static constexpr uint32_t TILES = 0;                      // [WARPS][STAGES][K tile, V tile]
   static constexpr uint32_t SCALES = TILES + WARPS * STAGES * 2 * KT;
-  static constexpr uint32_t ML = SCALES + WARPS * STAGES * SC;        // [2][WARPS][HEADS] float
+  static constexpr uint32_t Q = SCALES + WARPS * STAGES * SC;         // [ITEMS][HEADS][D] bf16
+  static constexpr uint32_t DESC = Q + ITEMS * HEADS * D * 2;         // [ITEMS] Item
+  static constexpr uint32_t ML = DESC + ITEMS * 32;                   // [2][WARPS][HEADS] float
   static constexpr uint32_t SLOT = ML + 2 * WARPS * HEADS * 4;        // [WARPS] where a warp's O lies
-  static constexpr uint32_t BARS = SLOT + WARPS * 4;
-  static constexpr uint32_t ABORT = BARS + WARPS * STAGES * 8;
+  static constexpr uint32_t ROWS = SLOT + WARPS * 4;                  // [PRODUCERS][3][WINDOW]: items up to a row, its length, span
+  static constexpr uint32_t BARS = ROWS + PRODUCERS * 3 * WINDOW * 4;             // full, empty [WARPS][STAGES] each
+  static constexpr uint32_t IBARS = BARS + 2 * WARPS * STAGES * 8;    // full, empty [ITEMS] each, join [2]
+  static constexpr uint32_t ABORT = IBARS + (2 * ITEMS + 2) * 8;
   static constexpr size_t BYTES = 1024 + size_t(ABORT) + 16;
   static_assert(HEADS * D * 4 <= KT, "a warp's O fits into a tile's K");
+};
+
+// Division by a number known to the host. m = floor(2^32 / d) makes the high half of n m either the
+// quotient or one less, for every n < 2^32.
+struct Div {
+  uint32_t d, m;
+  Div() = default;
+  explicit Div(uint32_t by) : d(by), m(uint32_t((uint64_t(1) << 32) / by - (by == 1 ? 1 : 0))) {}
+  __device__ __forceinline__ uint32_t of(uint32_t n) const {
+    const uint32_t q = __umulhi(n, m);
+    return n - q * d >= d ? q + 1 : q;
+  }
 };
 
 struct Args {
@@ -77,6 +99,8 @@ struct Args {
   int Hq, Hkv, G;        // G = Hq / Hkv
   int HC;                // groups of up to 8 heads that share a KV head
   int max_split;         // ranges of a row that the workspace has room for
+  int box;               // keys of a copy: 16, or 32 where a tile's 32 lie in one page
+  Div by_page, by_heads, by_hc;  // page, Hkv * HC, HC
   float c;               // scale * log2(e)
   float2* ml;            // [R][max_split][Hq] (reference, sum) of a range
   float* part;           // [R][max_split][Hq][D]
@@ -136,65 +160,100 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t sel) {
   return r;
 }
 
+// Rows y .. of an array of vectors, whole: vectors of 256 bytes as two halves of 128, one behind the other
+// (a 3D map whose third dimension is the half), the others as one box.
+template <int HALVES>
+__device__ __forceinline__ void tma_load_vectors(uint32_t dst, const void* tmap, int32_t y, uint32_t bar) {
+  if (HALVES == 1) {
+    tma_load_2d(dst, tmap, 0, y, bar);
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(tmap), "r"(0), "r"(y), "r"(0), "r"(bar)
+        : "memory");
+  }
+}
+
 // ---------------------------------------------------------------------------
 // items
 // ---------------------------------------------------------------------------
 struct Item {
-  int row, g, hc, split, n_split;
-  int t0, t1;  // keys [t0, t1) of the row
+  int row, g, hc, split;
+  int t0, t1;    // keys [t0, t1) of the row
+  int split_up;  // the row has more than one range
+  int pad;
 };
+static_assert(sizeof(Item) == 32, "a descriptor is 32 bytes");
 
-// Finds items in ascending order; warp-uniform results. The lanes hold 32 rows' lengths at a time.
+// Finds items in ascending order; used by the producer warp, warp-uniform results. The item counts of
+// WINDOW rows at a time lie in shared memory, summed up.
 template <int D, bool E4M3>
 struct Walk {
-  int64_t base;  // items of the rows before rb
-  int rb, len, n, incl;
+  int64_t base;  // items of the rows before the window
+  int w0, nw;    // the window's first row and its rows
+  int hint;      // no row of the window before this one holds an item still to come
+  int* upto;     // items of the window's rows up to and with row i
+  int* lens;
+  int* spans;
 
-  __device__ void load(const Args& a, bool report) {
-    const int lane = threadIdx.x & 31, row = rb + lane;
-    len = 0;
-    n = 0;
-    if (row < a.R) {
-      len = a.lens[row];
-      if (len < 0 || len > int64_t(a.max_pages) * a.page) {
-        if (report) atomicOr(a.err, MOT_DEV_BAD_PAGE);
-      } else {
-        const int heads = a.Hkv * a.HC;
-        n = splits_of(len, span_of(len, Cfg<D, E4M3>::ROUND, Cfg<D, E4M3>::MIN_SPAN, heads)) * heads;
+  __device__ void load(const Args& a) {
+    const int lane = threadIdx.x & 31, heads = a.Hkv * a.HC;
+    nw = min(WINDOW, a.R - w0);
+    hint = 0;
+    __syncwarp();
+    for (int i = lane; i < nw; i += 32) lens[i] = a.lens[w0 + i];
+    __syncwarp();
+    int sum = 0;
+    for (int i0 = 0; i0 < nw; i0 += 32) {
+      int n = 0;
+      if (i0 + lane < nw) {
+        const int len = lens[i0 + lane];
+        if (len < 0 || len > int64_t(a.max_pages) * a.page) {
+          if (blockIdx.x == 0 && threadIdx.x / 32 == WARPS) atomicOr(a.err, MOT_DEV_BAD_PAGE);
+        } else {
+          const int span = span_of(len, Cfg<D, E4M3>::ROUND, Cfg<D, E4M3>::MIN_SPAN, heads);
+          n = splits_of(len, span) * heads;
+          spans[i0 + lane] = span;
+        }
       }
-    }
-    incl = n;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += o;
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, n, off);
+        if (lane >= off) n += o;
+      }
+      if (i0 + lane < nw) upto[i0 + lane] = sum + n;
+      sum += __shfl_sync(0xffffffffu, n, 31);
     }
+    __syncwarp();
   }
-  __device__ void init(const Args& a, bool report) {
+  __device__ void init(const Args& a, int* rows) {
     base = 0;
-    rb = 0;
-    load(a, report);
+    w0 = 0;
+    upto = rows;
+    lens = rows + WINDOW;
+    spans = lens + WINDOW;
+    load(a);
   }
-  __device__ bool find(const Args& a, int64_t it, Item& m, bool report) {
-    for (;;) {
-      const int total = __shfl_sync(0xffffffffu, incl, 31);
-      if (it < base + total) break;
-      if (rb + 32 >= a.R) return false;
-      base += total;
-      rb += 32;
-      load(a, report);
+  __device__ bool find(const Args& a, int64_t it, Item& m) {
+    while (it >= base + upto[nw - 1]) {
+      if (w0 + nw >= a.R) return false;
+      base += upto[nw - 1];
+      w0 += nw;
+      load(a);
     }
-    const int k = int(it - base);
-    const int l = __ffs(__ballot_sync(0xffffffffu, k < incl)) - 1;
-    const int local = k - (__shfl_sync(0xffffffffu, incl, l) - __shfl_sync(0xffffffffu, n, l));
-    const int nk = __shfl_sync(0xffffffffu, len, l), heads = a.Hkv * a.HC;
-    const int span = span_of(nk, Cfg<D, E4M3>::ROUND, Cfg<D, E4M3>::MIN_SPAN, heads);
-    m.row = rb + l;
-    m.split = local / heads;
-    const int hh = local - m.split * heads;
-    m.g = hh / a.HC;
+    const int lane = threadIdx.x & 31, k = int(it - base);
+    uint32_t hit;
+    while ((hit = __ballot_sync(0xffffffffu, hint + lane < nw && upto[min(hint + lane, nw - 1)] > k)) == 0u) hint += 32;
+    hint += __ffs(hit) - 1;
+    const int first = hint > 0 ? upto[hint - 1] : 0, span = spans[hint], nk = lens[hint];
+    const int local = k - first;
+    m.row = w0 + hint;
+    m.split = int(a.by_heads.of(local));
+    const int hh = local - m.split * int(a.by_heads.d);
+    m.g = int(a.by_hc.of(hh));
     m.hc = hh - m.g * a.HC;
-    m.n_split = splits_of(nk, span);
+    m.split_up = (upto[hint] - first) > int(a.by_heads.d);
     m.t0 = m.split * span;
     m.t1 = m.t0 + span < nk ? m.t0 + span : nk;
     return true;
@@ -212,110 +271,196 @@ __device__ __forceinline__ uint32_t chunk(int r, int c) {
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(THREADS, 1)
-    decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Args a) {
+    decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ CUtensorMap tm_q, const Args a) {
   using C = Cfg<D, E4M3>;
   constexpr int TOK = C::TOK, NT = TOK / 8, KS = D / 16, STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
-  uint8_t* ring = smem + C::TILES + warp * STAGES * 2 * C::KT;
-  uint8_t* ring_sc = smem + C::SCALES + warp * STAGES * C::SC;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BARS) + warp * STAGES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BARS);   // [WARPS][STAGES] full, then empty
+  uint64_t* ifull = reinterpret_cast<uint64_t*>(smem + C::IBARS);
+  uint64_t* iempty = ifull + ITEMS;
+  uint64_t* join = iempty + ITEMS;  // the warps' results are there; they have been read
+  Item* desc = reinterpret_cast<Item*>(smem + C::DESC);
   float* s_ref = reinterpret_cast<float*>(smem + C::ML);
   float* s_sum = s_ref + WARPS * HEADS;
   uint32_t* s_slot = reinterpret_cast<uint32_t*>(smem + C::SLOT);
   volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(smem + C::ABORT);
 
-  if (lane == 0) {
-    for (int i = 0; i < STAGES; ++i) mbar_init(smem_u32(&full[i]), 1);
-    fence_mbar_init();
-  }
   if (threadIdx.x == 0) {
+    for (int i = 0; i < 2 * WARPS * STAGES; ++i) mbar_init(smem_u32(&bars[i]), 1);
+    for (int i = 0; i < ITEMS; ++i) {
+      mbar_init(smem_u32(&ifull[i]), 1);
+      mbar_init(smem_u32(&iempty[i]), WARPS);
+    }
+    mbar_init(smem_u32(&join[0]), WARPS);
+    mbar_init(smem_u32(&join[1]), WARPS);
+    fence_mbar_init();
     *abort_flag = 0u;
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_q);
   }
   __syncthreads();
   pdl_wait();
   pdl_trigger();
 
-  // ---- the warp's stream of tiles: the cursor `p` is the next tile to be copied, the table entry of
-  // lane i's 16 keys already on its way ----
-  const bool report = blockIdx.x == 0 && warp == 0;
-  Walk<D, E4M3> walk;
-  walk.init(a, report);
-  Walk<D, E4M3> pwalk = walk;
-  Item p;
-  int64_t pit = blockIdx.x;
-  int ptile = 0;        // first key of the tile
-  int ppage = 0;        // lane i < TOK / 16: the page of the tile's keys 16 i ..
-  int issued = 0, taken = 0;
-  bool ok = true;  // no wait of this warp has given up
-  bool pmore = pwalk.find(a, pit, p, false);
-  if (pmore) ptile = p.t0 + warp * TOK;
-
-  auto seek = [&]() {  // moves p to the next tile that exists and starts its table lookup
-    while (pmore && ptile >= p.t1) {
-      pit += gridDim.x;
-      pmore = pwalk.find(a, pit, p, false);
-      if (pmore) ptile = p.t0 + warp * TOK;
-    }
-    if (pmore && lane < TOK / 16 && ptile + 16 * lane < p.t1)
-      ppage = __ldg(a.table + int64_t(p.row) * a.max_pages + (ptile + 16 * lane) / a.page);
-  };
-  auto issue = [&]() {  // copies the tile at p into the next slot and moves on
-    if (!pmore || !ok) return;
-    const int st = issued % STAGES;
-    const uint32_t bar = smem_u32(&full[st]);
-    const int blocks = (min(TOK, p.t1 - ptile) + 15) / 16;
-    if (lane == 0) mbar_arrive_expect_tx(bar, blocks * (16 * (2 * C::ROW + (E4M3 ? 8 : 0))));
-    __syncwarp();
-    if (lane < blocks) {
-      int pg = ppage;
-      if (pg < 0 || pg >= a.n_pages) {
-        atomicOr(a.err, MOT_DEV_BAD_PAGE);
-        pg = 0;
+  if (warp >= WARPS) {
+    // ---------------- producers: a lane for each copy's keys of the two tiles that a warp copies ----------------
+    const int pw = warp - WARPS;
+    const int per = TOK / a.box;  // copies of a tile: 1 or 2
+    const int cw = (WARPS / PRODUCERS) * pw + (per == 2 ? lane >> 1 : lane), sub = per == 2 ? lane & 1 : 0;
+    const bool works = lane < (WARPS / PRODUCERS) * per;  // whose tile, which copy of it
+    uint64_t* full = bars + cw * STAGES;
+    uint64_t* empty = full + WARPS * STAGES;
+    uint8_t* ring = smem + C::TILES + cw * STAGES * 2 * C::KT;
+    uint8_t* ring_sc = smem + C::SCALES + cw * STAGES * C::SC;
+    Walk<D, E4M3> walk;
+    walk.init(a, reinterpret_cast<int*>(smem + C::ROWS) + pw * 3 * WINDOW);
+    int issued = 0, items = 0;  // tiles of warp cw, items
+    bool ok = true;
+    int64_t it = blockIdx.x;
+    Item m{}, nx{};
+    bool more = walk.find(a, it, m);
+    int r0 = m.t0;  // the round's first key
+    auto lookup = [&](const Item& w, int first) {  // the page of this lane's keys
+      const int key = first + cw * TOK + a.box * sub;
+      return works && key < w.t1 ? __ldg(a.table + int64_t(w.row) * a.max_pages + a.by_page.of(key)) : 0;
+    };
+    int pg = more ? lookup(m, r0) : 0;
+    while (more) {
+      // the round after this one, its lookup on the way while this one's copies go out
+      bool nmore = true;
+      int n0 = r0 + C::ROUND;
+      nx = m;
+      if (n0 >= m.t1) {
+        it += gridDim.x;
+        nmore = walk.find(a, it, nx);
+        n0 = nx.t0;
       }
-      const int key = ptile + 16 * lane;
-      const int y = (pg * a.Hkv + p.g) * a.page + key % a.page;
-      const uint32_t dst = smem_u32(ring + st * 2 * C::KT) + lane * (16 * C::ROW);
-#pragma unroll
-      for (int h = 0; h < C::HALVES; ++h) tma_load_2d(dst + h * 2048, &tm_k, h * (C::BOX / (E4M3 ? 1 : 2)), y, bar);
-#pragma unroll
-      for (int h = 0; h < C::HALVES; ++h)
-        tma_load_2d(dst + C::KT + h * 2048, &tm_v, h * (C::BOX / (E4M3 ? 1 : 2)), y, bar);
-      if (E4M3) bulk_load(smem_u32(ring_sc + st * C::SC) + lane * 128, a.scales + 2 * int64_t(y), 128, bar);
-    }
-    ++issued;
-    ptile += C::ROUND;
-    seek();
-  };
-  seek();
-  for (int i = 0; i < STAGES; ++i) issue();
+      const int npg = nmore ? lookup(nx, n0) : 0;
 
-  Item m;
-  for (int64_t it = blockIdx.x; walk.find(a, it, m, report); it += gridDim.x) {
+      if (pw == 0 && r0 == m.t0) {
+        // a new item: its descriptor and its queries
+        const int is = items % ITEMS;
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&iempty[is]), (uint32_t(items / ITEMS) & 1u) ^ 1u, abort_flag,
+                                               a.err));
+        if (!ok) break;
+        if (lane == 0) {
+          desc[is] = m;
+          const int h0 = m.g * a.G + m.hc * HEADS;
+          // 8 heads whatever the group has: the rows behind are not used
+          mbar_arrive_expect_tx(smem_u32(&ifull[is]), HEADS * D * 2);
+          tma_load_vectors<D / 64>(smem_u32(smem + C::Q + is * HEADS * D * 2), &tm_q,
+                                   m.row * (a.Hq + 2 * a.Hkv) + h0, smem_u32(&ifull[is]));
+        }
+        ++items;
+        __syncwarp();
+      }
+      const int tile = r0 + cw * TOK;
+      if (works && tile < m.t1) {
+        const int st = issued % STAGES;
+        const uint32_t bar = smem_u32(&full[st]);
+        ok = mbar_wait(smem_u32(&empty[st]), (uint32_t(issued / STAGES) & 1u) ^ 1u, abort_flag, a.err);
+        if (ok) {
+          const int copies = m.t1 - tile > a.box ? per : 1;
+          if (sub == 0) mbar_arrive_expect_tx(bar, copies * a.box * (2 * C::ROW + (E4M3 ? 8 : 0)));
+          if (sub < copies) {
+            int page = pg;
+            if (page < 0 || page >= a.n_pages) {
+              atomicOr(a.err, MOT_DEV_BAD_PAGE);
+              page = 0;
+            }
+            const int key = tile + a.box * sub;
+            const int y = (page * a.Hkv + m.g) * a.page + (key - int(a.by_page.of(key)) * a.page);
+            const uint32_t dst = smem_u32(ring + st * 2 * C::KT) + sub * (16 * C::ROW);
+            tma_load_vectors<C::HALVES>(dst, &tm_k, y, bar);
+            if (E4M3) bulk_load(smem_u32(ring_sc + st * C::SC) + sub * 128, a.scales + 2 * int64_t(y), a.box * 8, bar);
+            tma_load_vectors<C::HALVES>(dst + C::KT, &tm_v, y, bar);
+          }
+          ++issued;
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      more = nmore;
+      m = nx;
+      r0 = n0;
+      pg = npg;
+    }
+    if (ok && pw == 0) {
+      // no more items
+      const int is = items % ITEMS;
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&iempty[is]), (uint32_t(items / ITEMS) & 1u) ^ 1u, abort_flag,
+                                             a.err));
+      if (ok) {
+        if (lane == 0) {
+          desc[is].row = -1;
+          mbar_arrive(smem_u32(&ifull[is]));
+        }
+        ++items;
+      }
+    }
+    // every copy has landed before the CTA can exit: the last phase of each slot
+    if (works)
+      for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+        mbar_drain(smem_u32(&full[i % STAGES]), uint32_t(i / STAGES) & 1u);
+    for (int i = items > ITEMS ? items - ITEMS : 0; i < items; ++i)
+      mbar_drain(smem_u32(&ifull[i % ITEMS]), uint32_t(i / ITEMS) & 1u);
+    return;
+  }
+
+  // ---------------- consumers ----------------
+  uint64_t* full = bars + warp * STAGES;
+  uint64_t* empty = full + WARPS * STAGES;
+  uint8_t* ring = smem + C::TILES + warp * STAGES * 2 * C::KT;
+  uint8_t* ring_sc = smem + C::SCALES + warp * STAGES * C::SC;
+  int taken = 0;
+  for (int item = 0;; ++item) {
+    const int is = item % ITEMS;
+    const uint32_t phase = uint32_t(item) & 1u;  // of the join barriers
+    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&ifull[is]), uint32_t(item / ITEMS) & 1u, abort_flag, a.err))) return;
+    const Item m = desc[is];
+    if (m.row < 0) return;
     // ---- the query fragments: head g8 of the group in row g8, rows 8 .. 15 empty ----
     const int h0 = m.g * a.G + m.hc * HEADS;                      // first query head
     const int nh = min(HEADS, a.G - m.hc * HEADS);                // heads of this item
+    // element pairs of columns 2 t and 2 t + 8 of a k-step: dims 16 s + 2 t and + 8 (bf16), or, as an e4m3
+    // lane holds 4 consecutive dims, 16 s + 4 t and + 2
     uint32_t q[KS][2];
-    const uint16_t* qrow = a.qkv + (int64_t(m.row) * (a.Hq + 2 * a.Hkv) + h0 + g8) * D;
+    const uint32_t qb = smem_u32(smem + C::Q + is * HEADS * D * 2);  // [half][8 heads][128 bytes], swizzled
+    if constexpr (E4M3) {
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      // element pairs of columns 2 t and 2 t + 8 of the k-step: dims 16 s + 2 t and + 8 (bf16), or, as an
-      // e4m3 lane holds 4 consecutive dims, 16 s + 4 t and + 2
-      const int d0 = 16 * s + (E4M3 ? 4 * t4 : 2 * t4), d1 = d0 + (E4M3 ? 2 : 8);
-      q[s][0] = g8 < nh ? *reinterpret_cast<const uint32_t*>(qrow + d0) : 0u;
-      q[s][1] = g8 < nh ? *reinterpret_cast<const uint32_t*>(qrow + d1) : 0u;
+      for (int s = 0; s < KS; ++s)
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                     : "=r"(q[s][0]), "=r"(q[s][1])
+                     : "r"(qb + (s >> 2) * 1024 + g8 * 128 + ((((2 * s + (t4 >> 1)) & 7) ^ g8) << 4) + 8 * (t4 & 1))
+                     : "memory");
+    } else {
+#pragma unroll
+      for (int s = 0; s < KS; s += 2) {
+        uint32_t r[4];
+        const int ch = 2 * s + (lane >> 3);
+        ldsm4(r, qb + (ch >> 3) * 1024 + (lane & 7) * 128 + (((ch & 7) ^ (lane & 7)) << 4));
+        q[s][0] = r[0]; q[s][1] = r[1];
+        q[s + 1][0] = r[2]; q[s + 1][1] = r[3];
+      }
     }
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) q[s][i] = g8 < nh ? q[s][i] : 0u;
     float c = a.c;
     if (E4M3) {
-      uint32_t top = 0;
+      // the largest magnitude by its bits, two at a time (infinities above, NaNs above them)
+      uint32_t top2[2] = {0u, 0u};
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          top = max(top, max((q[s][i] << 16) & 0x7FFFFFFFu, q[s][i] & 0x7FFF0000u));
+        for (int i = 0; i < 2; ++i) top2[i] = __vmaxu2(top2[i], q[s][i] & 0x7FFF7FFFu);
+      top2[0] = __vmaxu2(top2[0], top2[1]);
+      uint32_t top = max(top2[0] << 16, top2[0] & 0xFFFF0000u);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       int e = 14 - (int(top >> 23) - 127);   // 2^e takes the largest element into [2^14, 2^15)
@@ -337,12 +482,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     int slot = -1;  // the slot of the item's last tile, held back: O passes through it
 
     for (int tile = m.t0 + warp * TOK; tile < m.t1; tile += C::ROUND) {
-      if (slot >= 0) issue();  // into the slot that the tile before has left
+      if (slot >= 0 && lane == 0) mbar_arrive(smem_u32(&empty[slot]));  // the tile before has been read
       const int st = taken % STAGES;
       slot = st;
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[st]), uint32_t(taken / STAGES) & 1u, abort_flag,
-                                                     a.err));
-      if (!ok) continue;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[st]), uint32_t(taken / STAGES) & 1u, abort_flag, a.err)))
+        return;
       ++taken;
       uint8_t* kt = ring + st * 2 * C::KT;
       const uint32_t kb = smem_u32(kt), vb = kb + C::KT;
@@ -484,7 +628,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       s_ref[warp * HEADS + g8] = ref;
       s_sum[warp * HEADS + g8] = sum;
     }
-    if (slot >= 0 && ok) {
+    if (slot >= 0) {
       // [head][dim ^ 8 (head / 2)]: the four lanes of a group fall into different banks
       float* ob = reinterpret_cast<float*>(ring + slot * 2 * C::KT);
       const int sw = 8 * t4;
@@ -502,42 +646,43 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     }
     if (lane == 0) s_slot[warp] = slot < 0 ? 0u : uint32_t(C::TILES + (warp * STAGES + slot) * 2 * C::KT);
-    __syncthreads();
-    if (warp < nh && *abort_flag == 0u) {  // warp k joins head k, D / 32 dims a lane
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&join[0]));
+    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&join[0]), phase, abort_flag, a.err))) return;
+    if (warp < nh) {  // warp k joins head k, D / 32 dims a lane
       constexpr int E = D / 32;
-      float refs[WARPS], top = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < WARPS; ++k) {
-        refs[k] = s_ref[k * HEADS + warp];
-        top = fmaxf(top, refs[k]);
-      }
-      float total = 0.0f, acc[E];
-#pragma unroll
-      for (int i = 0; i < E; ++i) acc[i] = 0.0f;
+      float refs[WARPS], sums[WARPS], v[WARPS][E], top = -INFINITY;
       const int d = (E * lane) ^ (8 * (warp >> 1));
 #pragma unroll
       for (int k = 0; k < WARPS; ++k) {
-        // a warp without tiles has -inf here; one whose scores are all -inf has a sum of zero, or NaN
-        if (refs[k] == -INFINITY) {
-          total = __fadd_rn(total, s_sum[k * HEADS + warp]);
-          continue;
-        }
-        const float f = exp2f(__fsub_rn(refs[k], top));
-        total = __fadd_rn(total, __fmul_rn(s_sum[k * HEADS + warp], f));
+        refs[k] = s_ref[k * HEADS + warp];
+        sums[k] = s_sum[k * HEADS + warp];
         const float* src = reinterpret_cast<const float*>(smem + s_slot[k]) + warp * D + d;
-        float v[E];
         if constexpr (E == 4) {
           const float4 u = *reinterpret_cast<const float4*>(src);
-          v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+          v[k][0] = u.x; v[k][1] = u.y; v[k][2] = u.z; v[k][3] = u.w;
         } else {
           const float2 u = *reinterpret_cast<const float2*>(src);
-          v[0] = u.x; v[1] = u.y;
+          v[k][0] = u.x; v[k][1] = u.y;
         }
+      }
 #pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = __fadd_rn(acc[i], __fmul_rn(v[i], f));
+      for (int k = 0; k < WARPS; ++k) top = fmaxf(top, refs[k]);
+      float total = 0.0f, acc[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) acc[i] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < WARPS; ++k) {
+        // a warp without tiles has -inf here and no O (what was read is dropped); one whose scores are all
+        // -inf, or NaN, has a sum of zero, or NaN
+        const bool none = refs[k] == -INFINITY;
+        const float f = none ? 1.0f : exp2f(__fsub_rn(refs[k], top));
+        total = __fadd_rn(total, __fmul_rn(sums[k], f));
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = __fadd_rn(acc[i], none ? 0.0f : __fmul_rn(v[k][i], f));
       }
       const int head = h0 + warp;
-      if (m.n_split == 1) {
+      if (!m.split_up) {
         const float r = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
         uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (int64_t(m.row) * a.Hq + head) * D) + lane * (E / 2);
 #pragma unroll
@@ -551,11 +696,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     fence_proxy_async_smem();  // the slots go back to the copies
-    __syncthreads();
-    if (slot >= 0) issue();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(smem_u32(&join[1]));
+      mbar_arrive(smem_u32(&iempty[is]));
+    }
+    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&join[1]), phase, abort_flag, a.err))) return;
+    if (slot >= 0 && lane == 0) mbar_arrive(smem_u32(&empty[slot]));
   }
-  // after a wait that gave up: every copy has landed before the CTA can exit
-  for (; taken < issued; ++taken) mbar_drain(smem_u32(&full[taken % STAGES]), uint32_t(taken / STAGES) & 1u);
 }
 
 // Joins the ranges of one (row, head): the references' maximum, each range's factor, then the ranges
@@ -631,17 +779,17 @@ inline int max_split(int64_t max_len, int heads) {
   return n < most ? int(n) : most;
 }
 
-// 2D map of the cache's vectors [rows][D] in boxes of 16 rows.
-inline bool cache_map(CUtensorMap* m, const void* base, int D, bool e4m3, int64_t rows) {
+// Map of vectors [rows][D] in boxes of box_rows whole vectors, for tma_load_vectors.
+inline bool vector_map(CUtensorMap* m, const void* base, int D, bool e4m3, int64_t rows, uint32_t box_rows) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return false;
-  const int bytes = D * (e4m3 ? 1 : 2), box_bytes = bytes < 128 ? bytes : 128;
-  cuuint64_t dims[2] = {cuuint64_t(D), cuuint64_t(rows)};
-  cuuint64_t strides[1] = {cuuint64_t(bytes)};
-  cuuint32_t box[2] = {cuuint32_t(e4m3 ? box_bytes : box_bytes / 2), 16};
-  cuuint32_t estr[2] = {1, 1};
-  return enc(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
-             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  const int size = e4m3 ? 1 : 2, bytes = D * size, box_bytes = bytes < 128 ? bytes : 128;
+  cuuint64_t dims[3] = {cuuint64_t(box_bytes / size), cuuint64_t(rows), 2};
+  cuuint64_t strides[2] = {cuuint64_t(bytes), 128};
+  cuuint32_t box[3] = {cuuint32_t(box_bytes / size), box_rows, 2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, bytes == 256 ? 3 : 2,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -652,15 +800,22 @@ static int launch(Args a, const void* k, const void* v, int dev, cudaStream_t s)
   const int heads = a.Hkv * a.HC;
   a.max_split = max_split<D, E4M3>(int64_t(a.max_pages) * a.page, heads);
   a.part = reinterpret_cast<float*>(a.ml + (int64_t(a.R) * a.max_split * a.Hq + 1) / 2 * 2);
-  CUtensorMap tm_k, tm_v;
+  CUtensorMap tm_k, tm_v, tm_q;
   const int64_t rows = a.n_pages * a.Hkv * a.page;
-  if (!cache_map(&tm_k, k, D, E4M3, rows) || !cache_map(&tm_v, v, D, E4M3, rows)) return MOT_ERR_CUDA;
+  a.box = C::TOK == 32 && a.page % 32 == 0 ? 32 : 16;
+  a.by_page = Div(a.page);
+  a.by_heads = Div(heads);
+  a.by_hc = Div(a.HC);
+  if (!vector_map(&tm_k, k, D, E4M3, rows, a.box) || !vector_map(&tm_v, v, D, E4M3, rows, a.box) ||
+      !vector_map(&tm_q, a.qkv, D, false, int64_t(a.R) * (a.Hq + 2 * a.Hkv), HEADS))
+    return MOT_ERR_CUDA;
   if (cudaFuncSetAttribute(decode_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::BYTES)) !=
       cudaSuccess)
     return MOT_ERR_CUDA;
   const int64_t items = int64_t(a.R) * a.max_split * heads;
   const unsigned grid = unsigned(items < sm_count(dev) ? items : sm_count(dev));
-  if (launch_dependent(decode_kernel<D, E4M3>, dim3(grid), dim3(THREADS), C::BYTES, s, tm_k, tm_v, a) != cudaSuccess)
+  if (launch_dependent(decode_kernel<D, E4M3>, dim3(grid), dim3(THREADS), C::BYTES, s, tm_k, tm_v, tm_q, a) !=
+      cudaSuccess)
     return MOT_ERR_CUDA;
   if (a.max_split > 1 &&
       launch_dependent(join_kernel<D, E4M3>, dim3(unsigned(int64_t(a.R) * a.Hq)), dim3(256), 0, s, a) != cudaSuccess)
@@ -676,7 +831,7 @@ using namespace mot;
 extern "C" size_t mot_paged_decode_workspace_bytes(int64_t R, int Hq, int Hkv, int D, int max_pages, int page) {
   if (kv::check_shape(Hq, Hkv, D, MOT_KV_BF16, 1, page) != MOT_OK) return 0;
   if (R < 1 || R > MOT_MAX_TOKENS || max_pages < 1 || int64_t(max_pages) * page > (int64_t(1) << 30)) return 0;
-  if (R * Hq > (int64_t(1) << 31) - 1) return 0;
+  if (R * (Hq + 2 * Hkv) > (int64_t(1) << 31) - 1) return 0;  // head vectors have 32-bit TMA coordinates
   const int G = Hq / Hkv, heads = Hkv * ((G + decode::HEADS - 1) / decode::HEADS);
   const int64_t n = D == 64 ? decode::max_split<64, false>(int64_t(max_pages) * page, heads)
                             : decode::max_split<128, false>(int64_t(max_pages) * page, heads);
