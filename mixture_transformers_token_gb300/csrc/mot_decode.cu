@@ -45,7 +45,10 @@ namespace decode {
 
 constexpr int WARPS = 8;                  // consumers
 constexpr int PRODUCERS = 4;              // warps 8 .. 11, two consumers each
-constexpr int THREADS = 32 * (WARPS + PRODUCERS);
+constexpr int JOINERS = 4;                // warps 12 .. 15, two heads each
+constexpr int THREADS = 32 * (WARPS + PRODUCERS + JOINERS);
+// Registers of a thread: 128 at launch, then 168, 72 and 104 (256 * 168 + 128 * 72 + 128 * 104 = 512 * 128).
+constexpr int CONSUMER_REGS = 168, PRODUCER_REGS = 72, JOINER_REGS = 104;
 constexpr int ITEMS = 4;                  // item descriptors in flight
 constexpr int WINDOW = 256;               // rows whose item counts the producer holds at a time
 constexpr int HEADS = 8;      // query heads of an item
@@ -62,17 +65,17 @@ struct Cfg {
   static constexpr int SC = E4M3 ? TOK * 8 : 0;             // bytes of a tile's scales
   static constexpr int STAGES = KT == 2048 ? 6 : 3;
   static constexpr int ROUND = WARPS * TOK;                 // keys a CTA takes at a time
-  static constexpr int MIN_SPAN = 256;                      // shortest range
+  static constexpr int MIN_SPAN = 2 * ROUND;                // shortest range
   static constexpr uint32_t TILES = 0;                      // [WARPS][STAGES][K tile, V tile]
   static constexpr uint32_t SCALES = TILES + WARPS * STAGES * 2 * KT;
   static constexpr uint32_t Q = SCALES + WARPS * STAGES * SC;         // [ITEMS][HEADS][D] bf16
   static constexpr uint32_t DESC = Q + ITEMS * HEADS * D * 2;         // [ITEMS] Item
-  static constexpr uint32_t ML = DESC + ITEMS * 32;                   // [2][WARPS][HEADS] float
-  static constexpr uint32_t SLOT = ML + 2 * WARPS * HEADS * 4;        // [WARPS] where a warp's O lies
-  static constexpr uint32_t ROWS = SLOT + WARPS * 4;                  // [PRODUCERS][3][WINDOW]: items up to a row, its length, span
+  static constexpr uint32_t ML = DESC + ITEMS * 32;                   // [2][2][WARPS][HEADS] float
+  static constexpr uint32_t SLOT = ML + 4 * WARPS * HEADS * 4;        // [2][WARPS] the slot that holds a warp's O
+  static constexpr uint32_t ROWS = SLOT + 2 * WARPS * 4;                  // [PRODUCERS][3][WINDOW]: items up to a row, its length, span
   static constexpr uint32_t BARS = ROWS + PRODUCERS * 3 * WINDOW * 4;             // full, empty [WARPS][STAGES] each
-  static constexpr uint32_t IBARS = BARS + 2 * WARPS * STAGES * 8;    // full, empty [ITEMS] each, join [2]
-  static constexpr uint32_t ABORT = IBARS + (2 * ITEMS + 2) * 8;
+  static constexpr uint32_t IBARS = BARS + 2 * WARPS * STAGES * 8;    // full, empty [ITEMS] each, jfull, jread [2] each
+  static constexpr uint32_t ABORT = IBARS + (2 * ITEMS + 4) * 8;
   static constexpr size_t BYTES = 1024 + size_t(ABORT) + 16;
   static_assert(HEADS * D * 4 <= KT, "a warp's O fits into a tile's K");
 };
@@ -281,22 +284,26 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BARS);   // [WARPS][STAGES] full, then empty
   uint64_t* ifull = reinterpret_cast<uint64_t*>(smem + C::IBARS);
   uint64_t* iempty = ifull + ITEMS;
-  uint64_t* join = iempty + ITEMS;  // the warps' results are there; they have been read
+  uint64_t* jfull = iempty + ITEMS;  // the consumers' results of an item are there (by the item's parity)
+  uint64_t* jread = jfull + 2;       // and have been read
   Item* desc = reinterpret_cast<Item*>(smem + C::DESC);
   float* s_ref = reinterpret_cast<float*>(smem + C::ML);
-  float* s_sum = s_ref + WARPS * HEADS;
-  uint32_t* s_slot = reinterpret_cast<uint32_t*>(smem + C::SLOT);
+  float* s_sum = s_ref + 2 * WARPS * HEADS;
+  int* s_slot = reinterpret_cast<int*>(smem + C::SLOT);
   volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(smem + C::ABORT);
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2 * WARPS * STAGES; ++i) mbar_init(smem_u32(&bars[i]), 1);
-    for (int i = 0; i < ITEMS; ++i) {
-      mbar_init(smem_u32(&ifull[i]), 1);
-      mbar_init(smem_u32(&iempty[i]), WARPS);
-    }
-    mbar_init(smem_u32(&join[0]), WARPS);
-    mbar_init(smem_u32(&join[1]), WARPS);
-    fence_mbar_init();
+  {
+    // a barrier a thread
+    const int i = int(threadIdx.x), n = 2 * WARPS * STAGES;
+    if (i < n) mbar_init(smem_u32(&bars[i]), 1);
+    else if (i < n + ITEMS) mbar_init(smem_u32(&ifull[i - n]), 1);
+    else if (i < n + 2 * ITEMS) mbar_init(smem_u32(&iempty[i - n - ITEMS]), WARPS + JOINERS);
+    else if (i < n + 2 * ITEMS + 2) mbar_init(smem_u32(&jfull[i - n - 2 * ITEMS]), WARPS);
+    else if (i < n + 2 * ITEMS + 4) mbar_init(smem_u32(&jread[i - n - 2 * ITEMS - 2]), JOINERS);
+    if (i < n + 2 * ITEMS + 4) fence_mbar_init();
+    static_assert(n + 2 * ITEMS + 4 < THREADS, "a thread for each barrier");
+  }
+  if (threadIdx.x == THREADS - 1) {
     *abort_flag = 0u;
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -306,7 +313,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   pdl_wait();
   pdl_trigger();
 
-  if (warp >= WARPS) {
+  if (warp >= WARPS && warp < WARPS + PRODUCERS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PRODUCER_REGS));
     // ---------------- producers: a lane for each copy's keys of the two tiles that a warp copies ----------------
     const int pw = warp - WARPS;
     const int per = TOK / a.box;  // copies of a tile: 1 or 2
@@ -411,6 +419,83 @@ __global__ void __launch_bounds__(THREADS, 1)
     return;
   }
 
+  if (warp >= WARPS + PRODUCERS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(JOINER_REGS));
+    // ---------------- joiners: warp w takes heads w and w + 4, the consumers' results in warp order ----------------
+    constexpr int E = D / 32;  // dims of a lane
+    const int jw = warp - WARPS - PRODUCERS;
+    for (int item = 0;; ++item) {
+      const int is = item % ITEMS, par = item & 1;
+      const uint32_t phase = uint32_t(item / 2) & 1u;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&ifull[is]), uint32_t(item / ITEMS) & 1u, abort_flag, a.err)))
+        return;
+      const Item m = desc[is];
+      if (m.row < 0) return;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&jfull[par]), phase, abort_flag, a.err))) return;
+      const int nh = min(HEADS, a.G - m.hc * HEADS);
+#pragma unroll 1
+      for (int hd = jw; hd < nh; hd += JOINERS) {
+        float refs[WARPS], sums[WARPS], v[WARPS][E], top = -INFINITY;
+        const int d = (E * lane) ^ (8 * (hd >> 1));
+#pragma unroll
+        for (int k = 0; k < WARPS; ++k) {
+          refs[k] = s_ref[(par * WARPS + k) * HEADS + hd];
+          sums[k] = s_sum[(par * WARPS + k) * HEADS + hd];
+          const int st = max(s_slot[par * WARPS + k], 0);
+          const float* src = reinterpret_cast<const float*>(smem + C::TILES + (k * STAGES + st) * 2 * C::KT) + hd * D + d;
+          if constexpr (E == 4) {
+            const float4 u = *reinterpret_cast<const float4*>(src);
+            v[k][0] = u.x; v[k][1] = u.y; v[k][2] = u.z; v[k][3] = u.w;
+          } else {
+            const float2 u = *reinterpret_cast<const float2*>(src);
+            v[k][0] = u.x; v[k][1] = u.y;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < WARPS; ++k) top = fmaxf(top, refs[k]);
+        float total = 0.0f, acc[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < WARPS; ++k) {
+          // a warp without tiles has -inf here and no O (what was read is dropped); one whose scores are all
+          // -inf, or NaN, has a sum of zero, or NaN
+          const bool none = refs[k] == -INFINITY;
+          const float f = none ? 1.0f : exp2f(__fsub_rn(refs[k], top));
+          total = __fadd_rn(total, __fmul_rn(sums[k], f));
+#pragma unroll
+          for (int i = 0; i < E; ++i) acc[i] = __fadd_rn(acc[i], none ? 0.0f : __fmul_rn(v[k][i], f));
+        }
+        const int head = m.g * a.G + m.hc * HEADS + hd;
+        if (!m.split_up) {
+          const float r = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+          uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (int64_t(m.row) * a.Hq + head) * D) + lane * (E / 2);
+#pragma unroll
+          for (int i = 0; i < E; i += 2) dst[i / 2] = pack_bf2(__fmul_rn(acc[i], r), __fmul_rn(acc[i + 1], r));
+        } else {
+          const int64_t at = (int64_t(m.row) * a.max_split + m.split) * a.Hq + head;
+          float* dst = a.part + at * D + E * lane;
+          if constexpr (E == 4) *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+          else *reinterpret_cast<float2*>(dst) = make_float2(acc[0], acc[1]);
+          if (lane == 0) a.ml[at] = make_float2(top, total);
+        }
+      }
+      const int st = lane < WARPS ? s_slot[par * WARPS + lane] : -1;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&jread[par]));
+        mbar_arrive(smem_u32(&iempty[is]));
+      }
+      if (jw == 0) {
+        // the slots that O came in go back to the copies when every joiner has read them
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&jread[par]), phase, abort_flag, a.err))) return;
+        fence_proxy_async_smem();
+        if (st >= 0) mbar_arrive(smem_u32(&bars[(WARPS + lane) * STAGES + st]));
+      }
+    }
+  }
+
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(CONSUMER_REGS));
   // ---------------- consumers ----------------
   uint64_t* full = bars + warp * STAGES;
   uint64_t* empty = full + WARPS * STAGES;
@@ -419,12 +504,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   int taken = 0;
   for (int item = 0;; ++item) {
     const int is = item % ITEMS;
-    const uint32_t phase = uint32_t(item) & 1u;  // of the join barriers
+    const int par = item & 1;
     if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&ifull[is]), uint32_t(item / ITEMS) & 1u, abort_flag, a.err))) return;
     const Item m = desc[is];
     if (m.row < 0) return;
     // ---- the query fragments: head g8 of the group in row g8, rows 8 .. 15 empty ----
-    const int h0 = m.g * a.G + m.hc * HEADS;                      // first query head
     const int nh = min(HEADS, a.G - m.hc * HEADS);                // heads of this item
     // element pairs of columns 2 t and 2 t + 8 of a k-step: dims 16 s + 2 t and + 8 (bf16), or, as an e4m3
     // lane holds 4 consecutive dims, 16 s + 4 t and + 2
@@ -621,12 +705,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();  // every lane has read the slot
     }
 
-    // ---- the warps' results are joined in warp order; O passes through the last tile's slot ----
+    // ---- the joiners take it from here: O passes to them through the last tile's slot ----
     sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 1));
     sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 2));
+    // the item before last has left its place
+    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&jread[par]), (uint32_t(item / 2) & 1u) ^ 1u, abort_flag, a.err)))
+      return;
     if (t4 == 0) {
-      s_ref[warp * HEADS + g8] = ref;
-      s_sum[warp * HEADS + g8] = sum;
+      s_ref[(par * WARPS + warp) * HEADS + g8] = ref;
+      s_sum[(par * WARPS + warp) * HEADS + g8] = sum;
     }
     if (slot >= 0) {
       // [head][dim ^ 8 (head / 2)]: the four lanes of a group fall into different banks
@@ -645,129 +732,125 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
     }
-    if (lane == 0) s_slot[warp] = slot < 0 ? 0u : uint32_t(C::TILES + (warp * STAGES + slot) * 2 * C::KT);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&join[0]));
-    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&join[0]), phase, abort_flag, a.err))) return;
-    if (warp < nh) {  // warp k joins head k, D / 32 dims a lane
-      constexpr int E = D / 32;
-      float refs[WARPS], sums[WARPS], v[WARPS][E], top = -INFINITY;
-      const int d = (E * lane) ^ (8 * (warp >> 1));
-#pragma unroll
-      for (int k = 0; k < WARPS; ++k) {
-        refs[k] = s_ref[k * HEADS + warp];
-        sums[k] = s_sum[k * HEADS + warp];
-        const float* src = reinterpret_cast<const float*>(smem + s_slot[k]) + warp * D + d;
-        if constexpr (E == 4) {
-          const float4 u = *reinterpret_cast<const float4*>(src);
-          v[k][0] = u.x; v[k][1] = u.y; v[k][2] = u.z; v[k][3] = u.w;
-        } else {
-          const float2 u = *reinterpret_cast<const float2*>(src);
-          v[k][0] = u.x; v[k][1] = u.y;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < WARPS; ++k) top = fmaxf(top, refs[k]);
-      float total = 0.0f, acc[E];
-#pragma unroll
-      for (int i = 0; i < E; ++i) acc[i] = 0.0f;
-#pragma unroll
-      for (int k = 0; k < WARPS; ++k) {
-        // a warp without tiles has -inf here and no O (what was read is dropped); one whose scores are all
-        // -inf, or NaN, has a sum of zero, or NaN
-        const bool none = refs[k] == -INFINITY;
-        const float f = none ? 1.0f : exp2f(__fsub_rn(refs[k], top));
-        total = __fadd_rn(total, __fmul_rn(sums[k], f));
-#pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = __fadd_rn(acc[i], none ? 0.0f : __fmul_rn(v[k][i], f));
-      }
-      const int head = h0 + warp;
-      if (!m.split_up) {
-        const float r = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
-        uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (int64_t(m.row) * a.Hq + head) * D) + lane * (E / 2);
-#pragma unroll
-        for (int i = 0; i < E; i += 2) dst[i / 2] = pack_bf2(__fmul_rn(acc[i], r), __fmul_rn(acc[i + 1], r));
-      } else {
-        const int64_t at = (int64_t(m.row) * a.max_split + m.split) * a.Hq + head;
-        float* dst = a.part + at * D + E * lane;
-        if constexpr (E == 4) *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        else *reinterpret_cast<float2*>(dst) = make_float2(acc[0], acc[1]);
-        if (lane == 0) a.ml[at] = make_float2(top, total);
-      }
-    }
-    fence_proxy_async_smem();  // the slots go back to the copies
+    if (lane == 0) s_slot[par * WARPS + warp] = slot;
+    fence_proxy_async_smem();  // the slot goes back to the copies through the joiners
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(smem_u32(&join[1]));
+      mbar_arrive(smem_u32(&jfull[par]));
       mbar_arrive(smem_u32(&iempty[is]));
     }
-    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&join[1]), phase, abort_flag, a.err))) return;
-    if (slot >= 0 && lane == 0) mbar_arrive(smem_u32(&empty[slot]));
   }
 }
 
-// Joins the ranges of one (row, head): the references' maximum, each range's factor, then the ranges
-// w, w + 8, ... by warp w in ascending order and the 8 warps' sums in order. Rows of one range were
-// written by decode_kernel.
-template <int D, bool E4M3>
+// Joins the ranges of a (row, head): out = (sum of f_s O_s) / (sum of f_s l_s), f_s the factor of range s
+// under the largest reference. The order is fixed: the l of 32 ranges at a time by a butterfly, these
+// sums in order; the O of the ranges s, s + 8, ... in order, then the eight sums in order. A row of up to
+// 32 ranges is a warp's work, its eight sums in registers (kWide false); beyond that a CTA takes a (row,
+// head), a warp each sum, with the same bits. Rows of one range were written by decode_kernel. A CTA a
+// (row, head) in every case spent 23 us on 7168 heads of 9 ranges, most of it on starting CTAs.
+constexpr int NARROW = 32;
+
+template <int D, bool E4M3, bool kWide>
 __global__ void __launch_bounds__(256) join_kernel(const Args a) {
   constexpr int E = D / 32;
-  __shared__ float s_f[SPLIT_ITEMS], s_top[WARPS], s_tot[WARPS];
-  __shared__ float s_acc[WARPS][D];
+  __shared__ float s_acc[kWide ? 8 : 1][D];
   pdl_wait();
-  const int row = int(blockIdx.x / a.Hq), head = int(blockIdx.x % a.Hq);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t rh = kWide ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * 8 + warp;
+  if (rh >= int64_t(a.R) * a.Hq) return;
+  const int row = int(rh / a.Hq), head = int(rh - int64_t(row) * a.Hq);
   const int len = a.lens[row];
   if (len <= 0 || len > int64_t(a.max_pages) * a.page) return;
   const int n = splits_of(len, span_of(len, Cfg<D, E4M3>::ROUND, Cfg<D, E4M3>::MIN_SPAN, a.Hkv * a.HC));
   if (n <= 1) return;
   const int64_t at0 = int64_t(row) * a.max_split * a.Hq + head;
-  const float2 ml = threadIdx.x < n ? a.ml[at0 + int64_t(threadIdx.x) * a.Hq] : make_float2(-INFINITY, 0.0f);
-  float top = ml.x;
+  constexpr int NL = kWide ? (SPLIT_ITEMS + 31) / 32 : 1;  // ranges of a lane: 32 i + lane
+  float f[NL], l[NL], top = -INFINITY;
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  if (lane == 0) s_top[warp] = top;
-  __syncthreads();
-  top = s_top[0];
-#pragma unroll
-  for (int k = 1; k < WARPS; ++k) top = fmaxf(top, s_top[k]);
-  const float f = ml.x == -INFINITY ? 0.0f : exp2f(__fsub_rn(ml.x, top));
-  if (threadIdx.x < n) s_f[threadIdx.x] = f;
-  float tot = ml.x == -INFINITY ? ml.y : __fmul_rn(ml.y, f);
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) tot = __fadd_rn(tot, __shfl_xor_sync(0xffffffffu, tot, off));
-  if (lane == 0) s_tot[warp] = tot;
-  __syncthreads();
-  float acc[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) acc[i] = 0.0f;
-#pragma unroll 4
-  for (int s = warp; s < n; s += WARPS) {
-    const float* src = a.part + (at0 + int64_t(s) * a.Hq) * D + E * lane;
-    float v[E];
-    if constexpr (E == 4) {
-      const float4 u = *reinterpret_cast<const float4*>(src);
-      v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-    } else {
-      const float2 u = *reinterpret_cast<const float2*>(src);
-      v[0] = u.x; v[1] = u.y;
-    }
-    const float fs = s_f[s];
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = __fadd_rn(acc[i], __fmul_rn(v[i], fs));
+  for (int i = 0; i < NL; ++i) {
+    const float2 ml = 32 * i + lane < n ? __ldcg(a.ml + at0 + int64_t(32 * i + lane) * a.Hq) : make_float2(-INFINITY, 0.0f);
+    f[i] = ml.x;
+    l[i] = ml.y;
+    top = fmaxf(top, ml.x);
   }
 #pragma unroll
-  for (int i = 0; i < E; ++i) s_acc[warp][E * lane + i] = acc[i];
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float total = s_tot[0], v = s_acc[0][threadIdx.x];
+  for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  float total = 0.0f;
 #pragma unroll
-    for (int k = 1; k < WARPS; ++k) {
-      total = __fadd_rn(total, s_tot[k]);
-      v = __fadd_rn(v, s_acc[k][threadIdx.x]);
+  for (int i = 0; i < NL; ++i) {
+    // a range without a weight has -inf here, and a sum of zero (or NaN: kept)
+    const bool none = f[i] == -INFINITY;
+    f[i] = none ? 0.0f : exp2f(__fsub_rn(f[i], top));
+    float t = none ? l[i] : __fmul_rn(l[i], f[i]);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) t = __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, off));
+    total = __fadd_rn(total, t);
+  }
+  const float r = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+  constexpr int K = kWide ? 1 : 8;  // sums that this warp forms
+  float acc[K][E];
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[k][i] = 0.0f;
+  const float* base = a.part + at0 * D + E * lane;
+  // K or 4 ranges' vectors on their way at a time; a range that does not exist adds zero
+  auto load = [&](float (&v)[E], int s) {
+    const float* src = base + int64_t(s) * a.Hq * D;
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = 0.0f;
+    if (s < n) {
+      if constexpr (E == 4) {
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(src));
+        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+      } else {
+        const float2 u = __ldcg(reinterpret_cast<const float2*>(src));
+        v[0] = u.x; v[1] = u.y;
+      }
     }
-    const float r = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
-    a.out[(int64_t(row) * a.Hq + head) * D + threadIdx.x] = f_to_bf(__fmul_rn(v, r));
+  };
+  if constexpr (kWide) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      if (32 * i >= n) break;
+      float v[4][E];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) load(v[u], 32 * i + 8 * u + warp);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float fs = __shfl_sync(0xffffffffu, f[i], 8 * u + warp);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[0][e] = __fadd_rn(acc[0][e], __fmul_rn(v[u][e], fs));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) s_acc[warp][E * lane + i] = acc[0][i];
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float v = s_acc[0][threadIdx.x];
+#pragma unroll
+      for (int k = 1; k < 8; ++k) v = __fadd_rn(v, s_acc[k][threadIdx.x]);
+      a.out[rh * D + threadIdx.x] = f_to_bf(__fmul_rn(v, r));
+    }
+  } else {
+    for (int s0 = 0; s0 < n; s0 += 8) {
+      float v[8][E];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) load(v[k], s0 + k);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float fs = __shfl_sync(0xffffffffu, f[0], (s0 + k) & 31);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[k][e] = __fadd_rn(acc[k][e], __fmul_rn(v[k][e], fs));
+      }
+    }
+#pragma unroll
+    for (int k = 1; k < 8; ++k)
+#pragma unroll
+      for (int i = 0; i < E; ++i) acc[0][i] = __fadd_rn(acc[0][i], acc[k][i]);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + rh * D) + lane * (E / 2);
+#pragma unroll
+    for (int i = 0; i < E; i += 2) dst[i / 2] = pack_bf2(__fmul_rn(acc[0][i], r), __fmul_rn(acc[0][i + 1], r));
   }
 }
 
@@ -817,9 +900,14 @@ static int launch(Args a, const void* k, const void* v, int dev, cudaStream_t s)
   if (launch_dependent(decode_kernel<D, E4M3>, dim3(grid), dim3(THREADS), C::BYTES, s, tm_k, tm_v, tm_q, a) !=
       cudaSuccess)
     return MOT_ERR_CUDA;
-  if (a.max_split > 1 &&
-      launch_dependent(join_kernel<D, E4M3>, dim3(unsigned(int64_t(a.R) * a.Hq)), dim3(256), 0, s, a) != cudaSuccess)
-    return MOT_ERR_CUDA;
+  if (a.max_split > 1) {
+    const int64_t heads_total = int64_t(a.R) * a.Hq;
+    const cudaError_t e =
+        a.max_split > NARROW
+            ? launch_dependent(join_kernel<D, E4M3, true>, dim3(unsigned(heads_total)), dim3(256), 0, s, a)
+            : launch_dependent(join_kernel<D, E4M3, false>, dim3(unsigned((heads_total + 7) / 8)), dim3(256), 0, s, a);
+    if (e != cudaSuccess) return MOT_ERR_CUDA;
+  }
   return MOT_OK;
 }
 
