@@ -47,8 +47,12 @@ constexpr int WARPS = 8;                  // consumers
 constexpr int PRODUCERS = 4;              // warps 8 .. 11, two consumers each
 constexpr int JOINERS = 4;                // warps 12 .. 15, two heads each
 constexpr int THREADS = 32 * (WARPS + PRODUCERS + JOINERS);
-// Registers of a thread: 128 at launch, then 168, 72 and 104 (256 * 168 + 128 * 72 + 128 * 104 = 512 * 128).
-constexpr int CONSUMER_REGS = 168, PRODUCER_REGS = 72, JOINER_REGS = 104;
+// Registers of a thread: at launch, then of each kind of warp. The consumers' share waits for what the
+// others give up, so the sum has to be the launch's; the host checks the compiled kernel's count.
+constexpr int LAUNCH_REGS = 128, CONSUMER_REGS = 168, PRODUCER_REGS = 72, JOINER_REGS = 104;
+static_assert(WARPS * CONSUMER_REGS + PRODUCERS * PRODUCER_REGS + JOINERS * JOINER_REGS ==
+                  (WARPS + PRODUCERS + JOINERS) * LAUNCH_REGS,
+              "register split");
 constexpr int ITEMS = 4;                  // item descriptors in flight
 constexpr int WINDOW = 256;               // rows whose item counts the producer holds at a time
 constexpr int HEADS = 8;      // query heads of an item
@@ -65,7 +69,7 @@ struct Cfg {
   static constexpr int SC = E4M3 ? TOK * 8 : 0;             // bytes of a tile's scales
   static constexpr int STAGES = KT == 2048 ? 6 : 3;
   static constexpr int ROUND = WARPS * TOK;                 // keys a CTA takes at a time
-  static constexpr int MIN_SPAN = 2 * ROUND;                // shortest range
+  static constexpr int MIN_SPAN = 512;                      // shortest range
   static constexpr uint32_t TILES = 0;                      // [WARPS][STAGES][K tile, V tile]
   static constexpr uint32_t SCALES = TILES + WARPS * STAGES * 2 * KT;
   static constexpr uint32_t Q = SCALES + WARPS * STAGES * SC;         // [ITEMS][HEADS][D] bf16
@@ -743,114 +747,124 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // Joins the ranges of a (row, head): out = (sum of f_s O_s) / (sum of f_s l_s), f_s the factor of range s
-// under the largest reference. The order is fixed: the l of 32 ranges at a time by a butterfly, these
-// sums in order; the O of the ranges s, s + 8, ... in order, then the eight sums in order. A row of up to
-// 32 ranges is a warp's work, its eight sums in registers (kWide false); beyond that a CTA takes a (row,
-// head), a warp each sum, with the same bits. Rows of one range were written by decode_kernel. A CTA a
-// (row, head) in every case spent 23 us on 7168 heads of 9 ranges, most of it on starting CTAs.
+// under the largest reference. The order is fixed: the f l of 32 ranges at a time by a butterfly, these
+// sums in order; the f O of the ranges s, s + 8, ... in order from zero, then the eight sums in order.
+// Rows of up to NARROW ranges are a warp's work for each 64 dims (kWide false: the eight sums in its
+// registers); where a row may have more, a CTA takes a (row, head) and a warp each sum, with the same bits.
+// Rows of one range were written by decode_kernel. A CTA a (row, head) in every case spent 23 us on 7168
+// heads of 9 ranges, most of it on starting CTAs.
 constexpr int NARROW = 32;
+constexpr int NARROW_WARPS = 4;
+
+// L consecutive floats of a range's vector, zeros for a range that does not exist.
+template <int L>
+__device__ __forceinline__ void load_part(float (&v)[L], const float* src, bool there) {
+#pragma unroll
+  for (int i = 0; i < L; ++i) v[i] = 0.0f;
+  if (there) {
+    if constexpr (L == 4) {
+      const float4 u = __ldcg(reinterpret_cast<const float4*>(src));
+      v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+    } else {
+      const float2 u = __ldcg(reinterpret_cast<const float2*>(src));
+      v[0] = u.x; v[1] = u.y;
+    }
+  }
+}
 
 template <int D, bool E4M3, bool kWide>
-__global__ void __launch_bounds__(256) join_kernel(const Args a) {
-  constexpr int E = D / 32;
-  __shared__ float s_acc[kWide ? 8 : 1][D];
-  pdl_wait();
+__global__ void __launch_bounds__(kWide ? 256 : 32 * NARROW_WARPS) join_kernel(const Args a) {
+  constexpr int L = kWide ? D / 32 : 2;               // dims of a lane
+  constexpr int PER = kWide ? 1 : D / 64;             // warps of a (row, head)
+  constexpr int NL = kWide ? (SPLIT_ITEMS + 31) / 32 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t rh = kWide ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * 8 + warp;
-  if (rh >= int64_t(a.R) * a.Hq) return;
-  const int row = int(rh / a.Hq), head = int(rh - int64_t(row) * a.Hq);
-  const int len = a.lens[row];
-  if (len <= 0 || len > int64_t(a.max_pages) * a.page) return;
-  const int n = splits_of(len, span_of(len, Cfg<D, E4M3>::ROUND, Cfg<D, E4M3>::MIN_SPAN, a.Hkv * a.HC));
+  const uint32_t unit = kWide ? blockIdx.x : blockIdx.x * NARROW_WARPS + warp, rh = unit / PER;
+  const int row = int(rh / uint32_t(a.Hq)), head = int(rh - uint32_t(row) * uint32_t(a.Hq));
+  // the lengths are the call's inputs: there before decode_kernel began
+  const int len = row < a.R ? a.lens[row] : 0;
+  int n = 0;
+  if (len > 0 && len <= int64_t(a.max_pages) * a.page)
+    n = splits_of(len, span_of(len, Cfg<D, E4M3>::ROUND, Cfg<D, E4M3>::MIN_SPAN, a.Hkv * a.HC));
+  pdl_wait();
   if (n <= 1) return;
   const int64_t at0 = int64_t(row) * a.max_split * a.Hq + head;
-  constexpr int NL = kWide ? (SPLIT_ITEMS + 31) / 32 : 1;  // ranges of a lane: 32 i + lane
-  float f[NL], l[NL], top = -INFINITY;
+  float f[NL], total = 0.0f, top = -INFINITY;
+  {
+    float2 ml[NL];
 #pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    const float2 ml = 32 * i + lane < n ? __ldcg(a.ml + at0 + int64_t(32 * i + lane) * a.Hq) : make_float2(-INFINITY, 0.0f);
-    f[i] = ml.x;
-    l[i] = ml.y;
-    top = fmaxf(top, ml.x);
-  }
+    for (int i = 0; i < NL; ++i) {
+      const int s = 32 * i + lane;
+      ml[i] = s < n ? __ldcg(a.ml + at0 + int64_t(s) * a.Hq) : make_float2(-INFINITY, 0.0f);
+    }
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  float total = 0.0f;
+    for (int i = 0; i < NL; ++i) top = fmaxf(top, ml[i].x);
 #pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    // a range without a weight has -inf here, and a sum of zero (or NaN: kept)
-    const bool none = f[i] == -INFINITY;
-    f[i] = none ? 0.0f : exp2f(__fsub_rn(f[i], top));
-    float t = none ? l[i] : __fmul_rn(l[i], f[i]);
+    for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) t = __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, off));
-    total = __fadd_rn(total, t);
+    for (int i = 0; i < NL; ++i) {
+      // a range without a weight has -inf here, and a sum of zero (or NaN: kept)
+      const bool none = ml[i].x == -INFINITY;
+      f[i] = none ? 0.0f : exp2f(__fsub_rn(ml[i].x, top));
+      float t = none ? ml[i].y : __fmul_rn(ml[i].y, f[i]);
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) t = __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, off));
+      total = __fadd_rn(total, t);
+    }
   }
   const float r = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
-  constexpr int K = kWide ? 1 : 8;  // sums that this warp forms
-  float acc[K][E];
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[k][i] = 0.0f;
-  const float* base = a.part + at0 * D + E * lane;
-  // K or 4 ranges' vectors on their way at a time; a range that does not exist adds zero
-  auto load = [&](float (&v)[E], int s) {
-    const float* src = base + int64_t(s) * a.Hq * D;
-#pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = 0.0f;
-    if (s < n) {
-      if constexpr (E == 4) {
-        const float4 u = __ldcg(reinterpret_cast<const float4*>(src));
-        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-      } else {
-        const float2 u = __ldcg(reinterpret_cast<const float2*>(src));
-        v[0] = u.x; v[1] = u.y;
-      }
-    }
-  };
+  const int64_t step = int64_t(a.Hq) * D;
+  const float* base = a.part + at0 * D + (kWide ? 0 : 64 * (unit - rh * PER)) + L * lane;
   if constexpr (kWide) {
+    __shared__ float s_acc[8][D];
+    float acc[L];
+#pragma unroll
+    for (int e = 0; e < L; ++e) acc[e] = 0.0f;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       if (32 * i >= n) break;
-      float v[4][E];
+      float v[4][L];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) load(v[u], 32 * i + 8 * u + warp);
+      for (int u = 0; u < 4; ++u) load_part(v[u], base + (32 * i + 8 * u + warp) * step, 32 * i + 8 * u + warp < n);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const float fs = __shfl_sync(0xffffffffu, f[i], 8 * u + warp);
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[0][e] = __fadd_rn(acc[0][e], __fmul_rn(v[u][e], fs));
+        for (int e = 0; e < L; ++e) acc[e] = __fadd_rn(acc[e], __fmul_rn(v[u][e], fs));
       }
     }
 #pragma unroll
-    for (int i = 0; i < E; ++i) s_acc[warp][E * lane + i] = acc[0][i];
+    for (int e = 0; e < L; ++e) s_acc[warp][L * lane + e] = acc[e];
     __syncthreads();
     if (threadIdx.x < D) {
       float v = s_acc[0][threadIdx.x];
 #pragma unroll
       for (int k = 1; k < 8; ++k) v = __fadd_rn(v, s_acc[k][threadIdx.x]);
-      a.out[rh * D + threadIdx.x] = f_to_bf(__fmul_rn(v, r));
+      a.out[int64_t(rh) * D + threadIdx.x] = f_to_bf(__fmul_rn(v, r));
     }
   } else {
-    for (int s0 = 0; s0 < n; s0 += 8) {
-      float v[8][E];
+    float acc[8][L];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) load(v[k], s0 + k);
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int e = 0; e < L; ++e) acc[k][e] = 0.0f;
+#pragma unroll 1
+    for (int s0 = 0; s0 < n; s0 += 8) {
+      float v[8][L];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) load_part(v[k], base + (s0 + k) * step, s0 + k < n);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float fs = __shfl_sync(0xffffffffu, f[0], (s0 + k) & 31);
+        const float fs = __shfl_sync(0xffffffffu, f[0], s0 + k);
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[k][e] = __fadd_rn(acc[k][e], __fmul_rn(v[k][e], fs));
+        for (int e = 0; e < L; ++e) acc[k][e] = __fadd_rn(acc[k][e], __fmul_rn(v[k][e], fs));
       }
     }
 #pragma unroll
     for (int k = 1; k < 8; ++k)
 #pragma unroll
-      for (int i = 0; i < E; ++i) acc[0][i] = __fadd_rn(acc[0][i], acc[k][i]);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + rh * D) + lane * (E / 2);
-#pragma unroll
-    for (int i = 0; i < E; i += 2) dst[i / 2] = pack_bf2(__fmul_rn(acc[0][i], r), __fmul_rn(acc[0][i + 1], r));
+      for (int e = 0; e < L; ++e) acc[0][e] = __fadd_rn(acc[0][e], acc[k][e]);
+    reinterpret_cast<uint32_t*>(a.out + int64_t(rh) * D)[32 * (unit - rh * PER) + lane] =
+        pack_bf2(__fmul_rn(acc[0][0], r), __fmul_rn(acc[0][1], r));
   }
 }
 
@@ -895,17 +909,25 @@ static int launch(Args a, const void* k, const void* v, int dev, cudaStream_t s)
   if (cudaFuncSetAttribute(decode_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::BYTES)) !=
       cudaSuccess)
     return MOT_ERR_CUDA;
+  static std::atomic<int> regs{0};
+  if (regs.load() == 0) {
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, decode_kernel<D, E4M3>) != cudaSuccess) return MOT_ERR_CUDA;
+    regs.store(attr.numRegs);
+  }
+  if (regs.load() != LAUNCH_REGS) return MOT_ERR_CUDA;
   const int64_t items = int64_t(a.R) * a.max_split * heads;
   const unsigned grid = unsigned(items < sm_count(dev) ? items : sm_count(dev));
   if (launch_dependent(decode_kernel<D, E4M3>, dim3(grid), dim3(THREADS), C::BYTES, s, tm_k, tm_v, tm_q, a) !=
       cudaSuccess)
     return MOT_ERR_CUDA;
   if (a.max_split > 1) {
-    const int64_t heads_total = int64_t(a.R) * a.Hq;
+    const int64_t heads_total = int64_t(a.R) * a.Hq, warps = heads_total * (D / 64);
     const cudaError_t e =
         a.max_split > NARROW
             ? launch_dependent(join_kernel<D, E4M3, true>, dim3(unsigned(heads_total)), dim3(256), 0, s, a)
-            : launch_dependent(join_kernel<D, E4M3, false>, dim3(unsigned((heads_total + 7) / 8)), dim3(256), 0, s, a);
+            : launch_dependent(join_kernel<D, E4M3, false>, dim3(unsigned((warps + NARROW_WARPS - 1) / NARROW_WARPS)),
+                               dim3(32 * NARROW_WARPS), 0, s, a);
     if (e != cudaSuccess) return MOT_ERR_CUDA;
   }
   return MOT_OK;
