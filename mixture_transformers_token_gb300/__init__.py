@@ -140,6 +140,9 @@ def _check(fn: str, status: int) -> None:
 
 
 def _dev(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int | None = None) -> int:
+    # the common case first: a call checks up to eight tensors
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and ndim == t.dim():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -153,8 +156,14 @@ def _dev(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int | None = None
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (2 us less a call), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(t: torch.Tensor, stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(t.get_device())
         stream = torch.cuda.current_stream(t.device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -394,54 +403,53 @@ def mot_joint_attention(qkv, seqs, Hq: int, Hkv: int, D: int, ws, scale: float |
 
 
 def _kv_cache(k_cache, v_cache, scales):
-    """Checks a cache's tensors: (kv_type, n_pages, Hkv, page, D, the scales' pointer or None)."""
-    e4m3 = k_cache.dtype == torch.float8_e4m3fn
+    """Checks a cache's tensors: (kv_type, n_pages, Hkv, page, D, the three pointers; no scales: None)."""
+    e4m3 = k_cache.dtype is torch.float8_e4m3fn
     dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
-    _dev(k_cache, "k_cache", dtype, 4)
-    _dev(v_cache, "v_cache", dtype, 4)
+    kp = _dev(k_cache, "k_cache", dtype, 4)
+    vp = _dev(v_cache, "v_cache", dtype, 4)
     shape = k_cache.shape
     if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have the same shape")
     n_pages, Hkv, page, D = shape
     if not e4m3:
-        return KV_BF16, n_pages, Hkv, page, D, None
+        return KV_BF16, n_pages, Hkv, page, D, kp, vp, None
     if scales is None:
         raise ValueError("an e4m3 cache needs its scales")
     sp = _dev(scales, "scales", torch.float32, 4)
-    if tuple(scales.shape) != (n_pages, Hkv, page, 2):
+    if scales.shape != (n_pages, Hkv, page, 2):
         raise ValueError(f"scales must be [{n_pages}, {Hkv}, {page}, 2]")
-    return KV_E4M3, n_pages, Hkv, page, D, sp
+    return KV_E4M3, n_pages, Hkv, page, D, kp, vp, sp
+
+
+def _kv_rows(qkv, slots, Hq: int, Hkv: int, D: int):
+    T, N = qkv.shape
+    qp = _dev(qkv, "qkv", torch.bfloat16, 2)
+    lp = _dev(slots, "slots", torch.int32, 1)
+    if N != (Hq + 2 * Hkv) * D or slots.shape[0] != T:
+        raise ValueError(f"qkv must be [T, {(Hq + 2 * Hkv) * D}] and slots [T]")
+    return T, qp, lp
 
 
 def mot_kv_cache_write(qkv, slots, k_cache, v_cache, Hq: int, ws, scales=None, stream=None) -> None:
     """Writes the K and V columns of the fused QKV rows [T][(Hq + 2 Hkv) D] into the cache's slots
     (int32 [T], -1: skip the row). The cache [n_pages][Hkv][page][D] is bf16, or float8_e4m3fn with
     fp32 `scales` [n_pages][Hkv][page][2]. `ws` (>= 64 bytes) receives device errors."""
-    kt, n_pages, Hkv, page, D, sp = _kv_cache(k_cache, v_cache, scales)
-    T, N = qkv.shape
-    _dev(qkv, "qkv", torch.bfloat16, 2)
-    _dev(slots, "slots", torch.int32, 1)
-    _dev(ws, "ws", torch.uint8, 1)
-    if N != (Hq + 2 * Hkv) * D or slots.shape[0] != T:
-        raise ValueError(f"qkv must be [T, {(Hq + 2 * Hkv) * D}] and slots [T]")
+    kt, n_pages, Hkv, page, D, kp, vp, sp = _kv_cache(k_cache, v_cache, scales)
+    T, qp, lp = _kv_rows(qkv, slots, Hq, Hkv, D)
+    wp = _dev(ws, "ws", torch.uint8, 1)
     _check("mot_kv_cache_write", _lib().mot_kv_cache_write(
-        qkv.data_ptr(), T, Hq, Hkv, D, slots.data_ptr(), kt, n_pages, page, k_cache.data_ptr(), v_cache.data_ptr(),
-        sp, ws.data_ptr(), ws.numel(), _stream(qkv, stream)))
+        qp, T, Hq, Hkv, D, lp, kt, n_pages, page, kp, vp, sp, wp, ws.numel(), _stream(qkv, stream)))
 
 
 def mot_kv_cache_read(k_cache, v_cache, slots, qkv, Hq: int, ws, scales=None, stream=None):
     """Reads cached vectors back into the K and V columns of the fused QKV rows `qkv` (the q columns
     and rows with slot -1 are kept). Arguments as mot_kv_cache_write; returns qkv."""
-    kt, n_pages, Hkv, page, D, sp = _kv_cache(k_cache, v_cache, scales)
-    T, N = qkv.shape
-    _dev(qkv, "qkv", torch.bfloat16, 2)
-    _dev(slots, "slots", torch.int32, 1)
-    _dev(ws, "ws", torch.uint8, 1)
-    if N != (Hq + 2 * Hkv) * D or slots.shape[0] != T:
-        raise ValueError(f"qkv must be [T, {(Hq + 2 * Hkv) * D}] and slots [T]")
+    kt, n_pages, Hkv, page, D, kp, vp, sp = _kv_cache(k_cache, v_cache, scales)
+    T, qp, lp = _kv_rows(qkv, slots, Hq, Hkv, D)
+    wp = _dev(ws, "ws", torch.uint8, 1)
     _check("mot_kv_cache_read", _lib().mot_kv_cache_read(
-        k_cache.data_ptr(), v_cache.data_ptr(), sp, kt, n_pages, page, slots.data_ptr(), T, Hq, Hkv, D,
-        qkv.data_ptr(), ws.data_ptr(), ws.numel(), _stream(qkv, stream)))
+        kp, vp, sp, kt, n_pages, page, lp, T, Hq, Hkv, D, qp, wp, ws.numel(), _stream(qkv, stream)))
     return qkv
 
 
@@ -455,25 +463,25 @@ def mot_paged_decode_attention(qkv, table, lens, k_cache, v_cache, Hq: int, ws, 
     Hkv) D], page table int32 [R][max_pages], lens int32 [R] (0: a row of zeros), the cache as for
     mot_kv_cache_write. `ws` (>= mot_paged_decode_workspace_bytes) is scratch after its 64-byte header.
     Returns out [R][Hq D] bf16."""
-    kt, n_pages, Hkv, page, D, sp = _kv_cache(k_cache, v_cache, scales)
+    kt, n_pages, Hkv, page, D, kp, vp, sp = _kv_cache(k_cache, v_cache, scales)
     R, N = qkv.shape
-    _dev(qkv, "qkv", torch.bfloat16, 2)
-    _dev(table, "table", torch.int32, 2)
-    _dev(lens, "lens", torch.int32, 1)
-    _dev(ws, "ws", torch.uint8, 1)
+    qp = _dev(qkv, "qkv", torch.bfloat16, 2)
+    tp = _dev(table, "table", torch.int32, 2)
+    lp = _dev(lens, "lens", torch.int32, 1)
+    wp = _dev(ws, "ws", torch.uint8, 1)
     if N != (Hq + 2 * Hkv) * D:
         raise ValueError(f"qkv must be [R, {(Hq + 2 * Hkv) * D}]")
+    max_pages = table.shape[1]
     if table.shape[0] != R or lens.shape[0] != R:
         raise ValueError("table must be [R, max_pages] and lens [R]")
     if out is None:
         out = torch.empty((R, Hq * D), dtype=torch.bfloat16, device=qkv.device)
-    _dev(out, "out", torch.bfloat16, 2)
-    if out.shape[0] != R or out.shape[1] != Hq * D:
+    op = _dev(out, "out", torch.bfloat16, 2)
+    if out.shape != (R, Hq * D):
         raise ValueError(f"out must be [{R}, {Hq * D}]")
     sc = 1.0 / math.sqrt(D) if scale is None else float(scale)
     _check("mot_paged_decode_attention", _lib().mot_paged_decode_attention(
-        qkv.data_ptr(), R, Hq, Hkv, D, table.data_ptr(), lens.data_ptr(), table.shape[1], kt, n_pages, page,
-        k_cache.data_ptr(), v_cache.data_ptr(), sp, sc, ws.data_ptr(), ws.numel(), out.data_ptr(),
+        qp, R, Hq, Hkv, D, tp, lp, max_pages, kt, n_pages, page, kp, vp, sp, sc, wp, ws.numel(), op,
         _stream(qkv, stream)))
     return out
 
