@@ -84,18 +84,6 @@ struct Cfg {
   static_assert(HEADS * D * 4 <= KT, "a warp's O fits into a tile's K");
 };
 
-// Division by a number known to the host. m = floor(2^32 / d) makes the high half of n m either the
-// quotient or one less, for every n < 2^32.
-struct Div {
-  uint32_t d, m;
-  Div() = default;
-  explicit Div(uint32_t by) : d(by), m(uint32_t((uint64_t(1) << 32) / by - (by == 1 ? 1 : 0))) {}
-  __device__ __forceinline__ uint32_t of(uint32_t n) const {
-    const uint32_t q = __umulhi(n, m);
-    return n - q * d >= d ? q + 1 : q;
-  }
-};
-
 struct Args {
   const uint16_t* qkv;   // [R][(Hq + 2 Hkv) D]
   const int32_t* table;  // [R][max_pages]
@@ -107,7 +95,7 @@ struct Args {
   int HC;                // groups of up to 8 heads that share a KV head
   int max_split;         // ranges of a row that the workspace has room for
   int box;               // keys of a copy: 16, or 32 where a tile's 32 lie in one page
-  Div by_page, by_heads, by_hc;  // page, Hkv * HC, HC
+  kv::Div by_page, by_heads, by_hc;  // page, Hkv * HC, HC
   float c;               // scale * log2(e)
   float2* ml;            // [R][max_split][Hq] (reference, sum) of a range
   float* part;           // [R][max_split][Hq][D]
@@ -900,9 +888,9 @@ static int launch(Args a, const void* k, const void* v, int dev, cudaStream_t s)
   CUtensorMap tm_k, tm_v, tm_q;
   const int64_t rows = a.n_pages * a.Hkv * a.page;
   a.box = C::TOK == 32 && a.page % 32 == 0 ? 32 : 16;
-  a.by_page = Div(a.page);
-  a.by_heads = Div(heads);
-  a.by_hc = Div(a.HC);
+  a.by_page = kv::Div(a.page);
+  a.by_heads = kv::Div(heads);
+  a.by_hc = kv::Div(a.HC);
   if (!vector_map(&tm_k, k, D, E4M3, rows, a.box) || !vector_map(&tm_v, v, D, E4M3, rows, a.box) ||
       !vector_map(&tm_q, a.qkv, D, false, int64_t(a.R) * (a.Hq + 2 * a.Hkv), HEADS))
     return MOT_ERR_CUDA;

@@ -55,17 +55,22 @@ __device__ __forceinline__ float e4m3_scale(float a) {
   return __uint_as_float(uint32_t(e + 127) << 23);
 }
 
-// 1 / scale for a scale that e4m3_scale made (exact; NaN for NaN).
-__device__ __forceinline__ float inverse_scale(float scale) { return __fdiv_rn(1.0f, scale); }
+// 1 / scale for a scale that e4m3_scale made: 2^-e by its bits (NaN for NaN).
+__device__ __forceinline__ float inverse_scale(float scale) {
+  const uint32_t b = __float_as_uint(scale);
+  return b >= 0x7F800000u ? scale : __uint_as_float(0x7F000000u - b);
+}
 
-struct Cache {
-  const void* k;
-  const void* v;
-  const float* scales;  // e4m3 only
-  int64_t n_pages;
-  int page;
-  int Hkv, D;
-  bool e4m3;
+// Division by a number known to the host. m = floor(2^32 / d) makes the high half of n m either the
+// quotient or one less, for every n < 2^32.
+struct Div {
+  uint32_t d, m;
+  Div() = default;
+  explicit Div(uint32_t by) : d(by), m(uint32_t((uint64_t(1) << 32) / by - (by == 1 ? 1 : 0))) {}
+  __device__ __forceinline__ uint32_t of(uint32_t n) const {
+    const uint32_t q = __umulhi(n, m);
+    return n - q * d >= d ? q + 1 : q;
+  }
 };
 
 // Checks of the cache's shape that need no CUDA call.
