@@ -20,8 +20,7 @@
 // the ranges' in a fixed order by join_kernel. Every fp32 operation is rounded on its own.
 // bf16 cache: w goes into the product as two bf16 (w and what its rounding leaves), so the weights
 // keep 16 bits: one bf16 each would put an error the size of the output's own rounding beside it.
-// e4m3 cache: codes become halves (exact), the query is scaled by a power of two into the halves'
-// range (exact but for elements below 2^-24 of the largest), and a weight is a half. A token's V scale
+// e4m3 cache: codes become halves (exact), the query too, scaled by a power of two, and a weight is a half. A token's V scale
 // belongs into its weight, so the reference follows x + log2(scale): the halves' range is then spent on
 // what the products contribute, however the scales differ.
 //
@@ -49,7 +48,7 @@ constexpr int JOINERS = 4;                // warps 12 .. 15, two heads each
 constexpr int THREADS = 32 * (WARPS + PRODUCERS + JOINERS);
 // Registers of a thread: at launch, then of each kind of warp. The consumers' share waits for what the
 // others give up, so the sum has to be the launch's; the host checks the compiled kernel's count.
-constexpr int LAUNCH_REGS = 128, CONSUMER_REGS = 168, PRODUCER_REGS = 72, JOINER_REGS = 104;
+constexpr int LAUNCH_REGS = 128, CONSUMER_REGS = 160, PRODUCER_REGS = 80, JOINER_REGS = 112;
 static_assert(WARPS * CONSUMER_REGS + PRODUCERS * PRODUCER_REGS + JOINERS * JOINER_REGS ==
                   (WARPS + PRODUCERS + JOINERS) * LAUNCH_REGS,
               "register split");
@@ -73,13 +72,15 @@ struct Cfg {
   static constexpr uint32_t TILES = 0;                      // [WARPS][STAGES][K tile, V tile]
   static constexpr uint32_t SCALES = TILES + WARPS * STAGES * 2 * KT;
   static constexpr uint32_t Q = SCALES + WARPS * STAGES * SC;         // [ITEMS][HEADS][D] bf16
-  static constexpr uint32_t DESC = Q + ITEMS * HEADS * D * 2;         // [ITEMS] Item
+  static constexpr uint32_t ZERO = Q + ITEMS * HEADS * D * 2;         // [HEADS][D] float: the O of a warp without tiles
+  static constexpr uint32_t DESC = ZERO + HEADS * D * 4;              // [ITEMS] Item
   static constexpr uint32_t ML = DESC + ITEMS * 32;                   // [2][2][WARPS][HEADS] float
-  static constexpr uint32_t SLOT = ML + 4 * WARPS * HEADS * 4;        // [2][WARPS] the slot that holds a warp's O
+  static constexpr uint32_t QC = ML + 4 * WARPS * HEADS * 4;          // [ITEMS][HEADS] float: c over the query's scale
+  static constexpr uint32_t SLOT = QC + ITEMS * HEADS * 4;        // [2][WARPS] the slot that holds a warp's O
   static constexpr uint32_t ROWS = SLOT + 2 * WARPS * 4;                  // [PRODUCERS][3][WINDOW]: items up to a row, its length, span
   static constexpr uint32_t BARS = ROWS + PRODUCERS * 3 * WINDOW * 4;             // full, empty [WARPS][STAGES] each
-  static constexpr uint32_t IBARS = BARS + 2 * WARPS * STAGES * 8;    // full, empty [ITEMS] each, jfull, jread [2] each
-  static constexpr uint32_t ABORT = IBARS + (2 * ITEMS + 4) * 8;
+  static constexpr uint32_t IBARS = BARS + 2 * WARPS * STAGES * 8;    // full, empty, qready [ITEMS] each, jfull, jread [2] each
+  static constexpr uint32_t ABORT = IBARS + (3 * ITEMS + 4) * 8;
   static constexpr size_t BYTES = 1024 + size_t(ABORT) + 16;
   static_assert(HEADS * D * 4 <= KT, "a warp's O fits into a tile's K");
 };
@@ -276,11 +277,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BARS);   // [WARPS][STAGES] full, then empty
   uint64_t* ifull = reinterpret_cast<uint64_t*>(smem + C::IBARS);
   uint64_t* iempty = ifull + ITEMS;
-  uint64_t* jfull = iempty + ITEMS;  // the consumers' results of an item are there (by the item's parity)
+  uint64_t* qready = iempty + ITEMS;  // e4m3: the queries are halves now
+  uint64_t* jfull = qready + ITEMS;  // the consumers' results of an item are there (by the item's parity)
   uint64_t* jread = jfull + 2;       // and have been read
   Item* desc = reinterpret_cast<Item*>(smem + C::DESC);
   float* s_ref = reinterpret_cast<float*>(smem + C::ML);
   float* s_sum = s_ref + 2 * WARPS * HEADS;
+  float* s_qc = reinterpret_cast<float*>(smem + C::QC);
   int* s_slot = reinterpret_cast<int*>(smem + C::SLOT);
   volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(smem + C::ABORT);
 
@@ -290,11 +293,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (i < n) mbar_init(smem_u32(&bars[i]), 1);
     else if (i < n + ITEMS) mbar_init(smem_u32(&ifull[i - n]), 1);
     else if (i < n + 2 * ITEMS) mbar_init(smem_u32(&iempty[i - n - ITEMS]), WARPS + JOINERS);
-    else if (i < n + 2 * ITEMS + 2) mbar_init(smem_u32(&jfull[i - n - 2 * ITEMS]), WARPS);
-    else if (i < n + 2 * ITEMS + 4) mbar_init(smem_u32(&jread[i - n - 2 * ITEMS - 2]), JOINERS);
-    if (i < n + 2 * ITEMS + 4) fence_mbar_init();
-    static_assert(n + 2 * ITEMS + 4 < THREADS, "a thread for each barrier");
+    else if (i < n + 3 * ITEMS) mbar_init(smem_u32(&qready[i - n - 2 * ITEMS]), JOINERS);
+    else if (i < n + 3 * ITEMS + 2) mbar_init(smem_u32(&jfull[i - n - 3 * ITEMS]), WARPS);
+    else if (i < n + 3 * ITEMS + 4) mbar_init(smem_u32(&jread[i - n - 3 * ITEMS - 2]), JOINERS);
+    if (i < n + 3 * ITEMS + 4) fence_mbar_init();
+    static_assert(n + 3 * ITEMS + 4 < THREADS, "a thread for each barrier");
   }
+  for (int i = int(threadIdx.x); i < HEADS * D / 4; i += THREADS)
+    reinterpret_cast<float4*>(smem + C::ZERO)[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (threadIdx.x == THREADS - 1) {
     *abort_flag = 0u;
     tma_prefetch_desc(&tm_k);
@@ -413,9 +419,52 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp >= WARPS + PRODUCERS) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(JOINER_REGS));
-    // ---------------- joiners: warp w takes heads w and w + 4, the consumers' results in warp order ----------------
-    constexpr int E = D / 32;  // dims of a lane
-    const int jw = warp - WARPS - PRODUCERS;
+    // ---------------- joiners: half a warp a head, the consumers' results in warp order ----------------
+    // The two heads of a warp share every instruction: this code runs once an item, from cold instruction
+    // caches, so its length is its time (a head after the other it took 3400 cycles an item, and the
+    // joiners were what bounded the e4m3 cache).
+    static_assert(HEADS == 2 * JOINERS, "a joiner's halves");
+    constexpr int P = D / 64;  // pieces of 4 dims of a lane: 64 i + 4 l16
+    const int jw = warp - WARPS - PRODUCERS, l16 = lane & 15, hd = 2 * jw + (lane >> 4);
+    // e4m3: the queries of item i become halves, each head scaled by a power of two that takes its largest
+    // element into [2^14, 2^15) (exact but for elements below 2^-24 of it); false after a wait that gave up
+    auto convert = [&](int i) -> bool {
+      const int is = i % ITEMS;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&ifull[is]), uint32_t(i / ITEMS) & 1u, abort_flag, a.err)))
+        return false;
+      if (desc[is].row >= 0) {
+        // in place: [half][8 heads][128 bytes] with the 128-byte swizzle, 16 bytes of a vector a lane (D = 64: 8)
+        const uint32_t byte = (D / 16) * l16 * 2;
+        uint32_t* at = reinterpret_cast<uint32_t*>(smem + C::Q + is * HEADS * D * 2 + (byte >> 7) * 1024 + hd * 128 +
+                                                   ((((byte >> 4) & 7) ^ hd) << 4) + (byte & 15));
+        uint32_t w[D / 32], top2 = 0;
+        if constexpr (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4*>(at);
+          w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(at);
+          w[0] = u.x; w[1] = u.y;
+        }
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+          top2 = __vmaxu2(top2, w[k] & 0x7FFF7FFFu);  // magnitudes by their bits: infinities above, then NaNs
+        uint32_t top = max(top2 << 16, top2 & 0xFFFF0000u);
+#pragma unroll
+        for (int off = 8; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const int e = min(14 - (int(top >> 23) - 127), 100);
+        const float f = __uint_as_float(uint32_t(e + 127) << 23);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) w[k] = pack_h2(__fmul_rn(bf_lo(w[k]), f), __fmul_rn(bf_hi(w[k]), f));
+        if constexpr (D == 128) *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+        else *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+        if (l16 == 0) s_qc[is * HEADS + hd] = __fmul_rn(a.c, __uint_as_float(uint32_t(127 - e) << 23));
+      }
+      fence_proxy_async_smem();  // the place goes back to the copies
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&qready[is]));
+      return true;
+    };
+    if (E4M3 && !convert(0)) return;
     for (int item = 0;; ++item) {
       const int is = item % ITEMS, par = item & 1;
       const uint32_t phase = uint32_t(item / 2) & 1u;
@@ -423,56 +472,59 @@ __global__ void __launch_bounds__(THREADS, 1)
         return;
       const Item m = desc[is];
       if (m.row < 0) return;
+      if (E4M3 && !convert(item + 1)) return;
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&jfull[par]), phase, abort_flag, a.err))) return;
       const int nh = min(HEADS, a.G - m.hc * HEADS);
-#pragma unroll 1
-      for (int hd = jw; hd < nh; hd += JOINERS) {
-        float refs[WARPS], sums[WARPS], v[WARPS][E], top = -INFINITY;
-        const int d = (E * lane) ^ (8 * (hd >> 1));
+      const int st = lane < WARPS ? s_slot[par * WARPS + lane] : -1;
+      const uint32_t off = st >= 0 ? C::TILES + ((lane & 7) * STAGES + st) * 2 * C::KT : C::ZERO;
+      float4 v[WARPS][P];
 #pragma unroll
-        for (int k = 0; k < WARPS; ++k) {
-          refs[k] = s_ref[(par * WARPS + k) * HEADS + hd];
-          sums[k] = s_sum[(par * WARPS + k) * HEADS + hd];
-          const int st = max(s_slot[par * WARPS + k], 0);
-          const float* src = reinterpret_cast<const float*>(smem + C::TILES + (k * STAGES + st) * 2 * C::KT) + hd * D + d;
-          if constexpr (E == 4) {
-            const float4 u = *reinterpret_cast<const float4*>(src);
-            v[k][0] = u.x; v[k][1] = u.y; v[k][2] = u.z; v[k][3] = u.w;
-          } else {
-            const float2 u = *reinterpret_cast<const float2*>(src);
-            v[k][0] = u.x; v[k][1] = u.y;
-          }
+      for (int k = 0; k < WARPS; ++k) {
+        const float* src = reinterpret_cast<const float*>(smem + __shfl_sync(0xffffffffu, off, k)) + hd * D;
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[k][i] = *reinterpret_cast<const float4*>(src + ((64 * i + 4 * l16) ^ (8 * (hd >> 1))));
+      }
+      // lane k of 8 has warp k's reference and sum: one exponential each, the factors go round by shuffles
+      const float ref = s_ref[(par * WARPS + (lane & 7)) * HEADS + hd], sum = s_sum[(par * WARPS + (lane & 7)) * HEADS + hd];
+      float top = ref;
+#pragma unroll
+      for (int o = 4; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // a warp without tiles has -inf here, and zeros; one whose scores are all -inf (or NaN) a sum of zero (or NaN)
+      const bool none = ref == -INFINITY;
+      const float f = none ? 0.0f : exp2f(__fsub_rn(ref, top));
+      float total = none ? sum : __fmul_rn(sum, f);
+#pragma unroll
+      for (int o = 4; o >= 1; o >>= 1) total = __fadd_rn(total, __shfl_xor_sync(0xffffffffu, total, o));
+      float acc[P][4] = {};
+#pragma unroll
+      for (int k = 0; k < WARPS; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, (lane & 16) + k);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          acc[i][0] = __fadd_rn(acc[i][0], __fmul_rn(v[k][i].x, fk));
+          acc[i][1] = __fadd_rn(acc[i][1], __fmul_rn(v[k][i].y, fk));
+          acc[i][2] = __fadd_rn(acc[i][2], __fmul_rn(v[k][i].z, fk));
+          acc[i][3] = __fadd_rn(acc[i][3], __fmul_rn(v[k][i].w, fk));
         }
-#pragma unroll
-        for (int k = 0; k < WARPS; ++k) top = fmaxf(top, refs[k]);
-        float total = 0.0f, acc[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < WARPS; ++k) {
-          // a warp without tiles has -inf here and no O (what was read is dropped); one whose scores are all
-          // -inf, or NaN, has a sum of zero, or NaN
-          const bool none = refs[k] == -INFINITY;
-          const float f = none ? 1.0f : exp2f(__fsub_rn(refs[k], top));
-          total = __fadd_rn(total, __fmul_rn(sums[k], f));
-#pragma unroll
-          for (int i = 0; i < E; ++i) acc[i] = __fadd_rn(acc[i], none ? 0.0f : __fmul_rn(v[k][i], f));
-        }
+      }
+      if (hd < nh) {
         const int head = m.g * a.G + m.hc * HEADS + hd;
         if (!m.split_up) {
           const float r = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
-          uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (int64_t(m.row) * a.Hq + head) * D) + lane * (E / 2);
+          uint16_t* dst = a.out + (int64_t(m.row) * a.Hq + head) * D + 4 * l16;
 #pragma unroll
-          for (int i = 0; i < E; i += 2) dst[i / 2] = pack_bf2(__fmul_rn(acc[i], r), __fmul_rn(acc[i + 1], r));
+          for (int i = 0; i < P; ++i)
+            *reinterpret_cast<uint2*>(dst + 64 * i) = make_uint2(pack_bf2(__fmul_rn(acc[i][0], r), __fmul_rn(acc[i][1], r)),
+                                                                 pack_bf2(__fmul_rn(acc[i][2], r), __fmul_rn(acc[i][3], r)));
         } else {
           const int64_t at = (int64_t(m.row) * a.max_split + m.split) * a.Hq + head;
-          float* dst = a.part + at * D + E * lane;
-          if constexpr (E == 4) *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-          else *reinterpret_cast<float2*>(dst) = make_float2(acc[0], acc[1]);
-          if (lane == 0) a.ml[at] = make_float2(top, total);
+          float* dst = a.part + at * D + 4 * l16;
+#pragma unroll
+          for (int i = 0; i < P; ++i)
+            *reinterpret_cast<float4*>(dst + 64 * i) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+          if (l16 == 0) a.ml[at] = make_float2(top, total);
         }
       }
-      const int st = lane < WARPS ? s_slot[par * WARPS + lane] : -1;
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(smem_u32(&jread[par]));
@@ -497,7 +549,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   for (int item = 0;; ++item) {
     const int is = item % ITEMS;
     const int par = item & 1;
-    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&ifull[is]), uint32_t(item / ITEMS) & 1u, abort_flag, a.err))) return;
+    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(E4M3 ? &qready[is] : &ifull[is]), uint32_t(item / ITEMS) & 1u,
+                                           abort_flag, a.err)))
+      return;
     const Item m = desc[is];
     if (m.row < 0) return;
     // ---- the query fragments: head g8 of the group in row g8, rows 8 .. 15 empty ----
@@ -527,27 +581,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int s = 0; s < KS; ++s)
 #pragma unroll
       for (int i = 0; i < 2; ++i) q[s][i] = g8 < nh ? q[s][i] : 0u;
-    float c = a.c;
-    if (E4M3) {
-      // the largest magnitude by its bits, two at a time (infinities above, NaNs above them)
-      uint32_t top2[2] = {0u, 0u};
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) top2[i] = __vmaxu2(top2[i], q[s][i] & 0x7FFF7FFFu);
-      top2[0] = __vmaxu2(top2[0], top2[1]);
-      uint32_t top = max(top2[0] << 16, top2[0] & 0xFFFF0000u);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      int e = 14 - (int(top >> 23) - 127);   // 2^e takes the largest element into [2^14, 2^15)
-      e = min(e, 100);
-      const float f = __uint_as_float(uint32_t(e + 127) << 23);
-      c = __fmul_rn(c, __uint_as_float(uint32_t(127 - e) << 23));
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) q[s][i] = pack_h2(__fmul_rn(bf_lo(q[s][i]), f), __fmul_rn(bf_hi(q[s][i]), f));
-    }
+    const float c = E4M3 ? s_qc[is * HEADS + g8] : a.c;
 
     float o[D / 16][4];
 #pragma unroll
@@ -616,11 +650,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t b = __float_as_uint(vs[i]);
-            const int e = int(b >> 23) - 127;
-            inv[j][i] = __uint_as_float(uint32_t(127 - e) << 23);
-            fac[j][i] = __uint_as_float((b & 0x007FFFFFu) | 0x3F800000u);
-            // a scale that is not finite makes the key's weight NaN
-            const float ev = __fadd_rn(float(e), __fmul_rn(vs[i], 0.0f));
+            const float ev = __fsub_rn(__uint_as_float((b >> 23) | 0x4B000000u), 8388735.0f);  // 2^23 + 127
+            inv[j][i] = __uint_as_float(0x7F000000u - (b & 0x7F800000u));
+            fac[j][i] = __fmul_rn(vs[i], inv[j][i]);  // NaN for a scale of NaN
             x[j][i] = __fadd_rn(__fmul_rn(__fmul_rn(x[j][i], c), ks[i]), ev);
           }
         } else {
