@@ -157,18 +157,32 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t sel) {
 }
 
 // Rows y .. of an array of vectors, whole: vectors of 256 bytes as two halves of 128, one behind the other
-// (a 3D map whose third dimension is the half), the others as one box.
+// (a 3D map whose third dimension is the half), the others as one box. `policy`: an L2 cache policy.
 template <int HALVES>
-__device__ __forceinline__ void tma_load_vectors(uint32_t dst, const void* tmap, int32_t y, uint32_t bar) {
-  if (HALVES == 1) {
-    tma_load_2d(dst, tmap, 0, y, bar);
-  } else {
+__device__ __forceinline__ void tma_load_vectors(uint32_t dst, const void* tmap, int32_t y, uint32_t bar,
+                                                 uint64_t policy) {
+  if (HALVES == 1)
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(dst),
-        "l"(tmap), "r"(0), "r"(y), "r"(0), "r"(bar)
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
+        "{%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(tmap), "r"(0), "r"(y), "r"(bar), "l"(policy)
         : "memory");
-  }
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
+        "{%2, %3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(tmap), "r"(0), "r"(y), "r"(0), "r"(bar), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ uint64_t policy_evict_first() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
 }
 
 // ---------------------------------------------------------------------------
@@ -324,6 +338,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t* ring_sc = smem + C::SCALES + cw * STAGES * C::SC;
     Walk<D, E4M3> walk;
     walk.init(a, reinterpret_cast<int*>(smem + C::ROWS) + pw * 3 * WINDOW);
+    // K and V pass through once (unless several groups of heads share them): they leave L2 first, and the
+    // partial results, the page tables and the kernels' own instructions stay
+    const uint64_t keep = policy_evict_normal(), stream = a.HC == 1 ? policy_evict_first() : keep;
     int issued = 0, items = 0;  // tiles of warp cw, items
     bool ok = true;
     int64_t it = blockIdx.x;
@@ -359,7 +376,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           // 8 heads whatever the group has: the rows behind are not used
           mbar_arrive_expect_tx(smem_u32(&ifull[is]), HEADS * D * 2);
           tma_load_vectors<D / 64>(smem_u32(smem + C::Q + is * HEADS * D * 2), &tm_q,
-                                   m.row * (a.Hq + 2 * a.Hkv) + h0, smem_u32(&ifull[is]));
+                                   m.row * (a.Hq + 2 * a.Hkv) + h0, smem_u32(&ifull[is]), keep);
         }
         ++items;
         __syncwarp();
@@ -381,9 +398,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int key = tile + a.box * sub;
             const int y = (page * a.Hkv + m.g) * a.page + (key - int(a.by_page.of(key)) * a.page);
             const uint32_t dst = smem_u32(ring + st * 2 * C::KT) + sub * (16 * C::ROW);
-            tma_load_vectors<C::HALVES>(dst, &tm_k, y, bar);
+            tma_load_vectors<C::HALVES>(dst, &tm_k, y, bar, stream);
             if (E4M3) bulk_load(smem_u32(ring_sc + st * C::SC) + sub * 128, a.scales + 2 * int64_t(y), a.box * 8, bar);
-            tma_load_vectors<C::HALVES>(dst + C::KT, &tm_v, y, bar);
+            tma_load_vectors<C::HALVES>(dst + C::KT, &tm_v, y, bar, stream);
           }
           ++issued;
         }
