@@ -813,7 +813,6 @@ template <int D, bool E4M3, bool kWide>
 __global__ void __launch_bounds__(kWide ? 256 : 32 * NARROW_WARPS) join_kernel(const Args a) {
   constexpr int L = kWide ? D / 32 : 2;               // dims of a lane
   constexpr int PER = kWide ? 1 : D / 64;             // warps of a (row, head)
-  constexpr int NL = kWide ? (SPLIT_ITEMS + 31) / 32 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t unit = kWide ? blockIdx.x : blockIdx.x * NARROW_WARPS + warp, rh = unit / PER;
   const int row = int(rh / uint32_t(a.Hq)), head = int(rh - uint32_t(row) * uint32_t(a.Hq));
@@ -825,28 +824,32 @@ __global__ void __launch_bounds__(kWide ? 256 : 32 * NARROW_WARPS) join_kernel(c
   pdl_wait();
   if (n <= 1) return;
   const int64_t at0 = int64_t(row) * a.max_split * a.Hq + head;
-  float f[NL], total = 0.0f, top = -INFINITY;
-  {
-    float2 ml[NL];
+  // thread (narrow: lane) s has range s
+  const int mine = kWide ? int(threadIdx.x) : lane;
+  const float2 ml = mine < n ? __ldcg(a.ml + at0 + int64_t(mine) * a.Hq) : make_float2(-INFINITY, 0.0f);
+  float top = ml.x;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int s = 32 * i + lane;
-      ml[i] = s < n ? __ldcg(a.ml + at0 + int64_t(s) * a.Hq) : make_float2(-INFINITY, 0.0f);
-    }
+  for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  __shared__ float s_top[8], s_total[8], s_f[kWide ? 256 : 1];
+  if constexpr (kWide) {
+    if (lane == 0) s_top[warp] = top;
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NL; ++i) top = fmaxf(top, ml[i].x);
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, s_top[k]);
+  }
+  // a range without a weight has -inf here, and a sum of zero (or NaN: kept)
+  const bool none = ml.x == -INFINITY;
+  const float f = none ? 0.0f : exp2f(__fsub_rn(ml.x, top));
+  float total = none ? ml.y : __fmul_rn(ml.y, f);
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  for (int off = 16; off >= 1; off >>= 1) total = __fadd_rn(total, __shfl_xor_sync(0xffffffffu, total, off));
+  if constexpr (kWide) {
+    s_f[threadIdx.x] = f;
+    if (lane == 0) s_total[warp] = total;
+    __syncthreads();
+    total = s_total[0];
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      // a range without a weight has -inf here, and a sum of zero (or NaN: kept)
-      const bool none = ml[i].x == -INFINITY;
-      f[i] = none ? 0.0f : exp2f(__fsub_rn(ml[i].x, top));
-      float t = none ? ml[i].y : __fmul_rn(ml[i].y, f[i]);
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) t = __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, off));
-      total = __fadd_rn(total, t);
-    }
+    for (int k = 1; k < 8; ++k) total = __fadd_rn(total, s_total[k]);
   }
   const float r = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
   const int64_t step = int64_t(a.Hq) * D;
@@ -856,15 +859,14 @@ __global__ void __launch_bounds__(kWide ? 256 : 32 * NARROW_WARPS) join_kernel(c
     float acc[L];
 #pragma unroll
     for (int e = 0; e < L; ++e) acc[e] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      if (32 * i >= n) break;
+#pragma unroll 1
+    for (int s0 = warp; s0 < n; s0 += 32) {
       float v[4][L];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) load_part(v[u], base + (32 * i + 8 * u + warp) * step, 32 * i + 8 * u + warp < n);
+      for (int u = 0; u < 4; ++u) load_part(v[u], base + (s0 + 8 * u) * step, s0 + 8 * u < n);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float fs = __shfl_sync(0xffffffffu, f[i], 8 * u + warp);
+        const float fs = s_f[s0 + 8 * u];  // zero behind the last range
 #pragma unroll
         for (int e = 0; e < L; ++e) acc[e] = __fadd_rn(acc[e], __fmul_rn(v[u][e], fs));
       }
@@ -891,7 +893,7 @@ __global__ void __launch_bounds__(kWide ? 256 : 32 * NARROW_WARPS) join_kernel(c
       for (int k = 0; k < 8; ++k) load_part(v[k], base + (s0 + k) * step, s0 + k < n);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float fs = __shfl_sync(0xffffffffu, f[0], s0 + k);
+        const float fs = __shfl_sync(0xffffffffu, f, s0 + k);
 #pragma unroll
         for (int e = 0; e < L; ++e) acc[k][e] = __fadd_rn(acc[k][e], __fmul_rn(v[k][e], fs));
       }
