@@ -150,6 +150,12 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// The transposed 8 x 8 matrix of 16-bit elements whose row g lane (g, t) holds columns 2 t, 2 t + 1 of.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t sel) {
   uint32_t r;
   asm("prmt.b32 %0, %1, %1, %2;" : "=r"(r) : "r"(a), "r"(sel));
@@ -284,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_q, const Args a) {
   using C = Cfg<D, E4M3>;
-  constexpr int TOK = C::TOK, NT = TOK / 8, KS = D / 16, STAGES = C::STAGES;
+  constexpr int TOK = C::TOK, NB = TOK / 16, KS = D / 16, STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
@@ -598,14 +604,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int s = 0; s < KS; ++s)
 #pragma unroll
       for (int i = 0; i < 2; ++i) q[s][i] = g8 < nh ? q[s][i] : 0u;
-    const float c = E4M3 ? s_qc[is * HEADS + g8] : a.c;
+    float c[2] = {a.c, a.c};
+    if constexpr (E4M3) {
+      c[0] = s_qc[is * HEADS + 2 * t4];
+      c[1] = s_qc[is * HEADS + 2 * t4 + 1];
+    }
 
     float o[D / 16][4];
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
-    float ref = -INFINITY, sum = 0.0f;
+    float ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f};  // of heads 2 t4 and 2 t4 + 1
     int slot = -1;  // the slot of the item's last tile, held back: O passes through it
 
     for (int tile = m.t0 + warp * TOK; tile < m.t1; tile += C::ROUND) {
@@ -628,95 +638,102 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
       }
 
-      // ---- S = Q K^T: lane has head g8, keys 8 j + 2 t4 and + 1 ----
-      float x[NT][4];
+      // ---- S^T = K Q^T: lane has keys 16 b + 8 i + g8, heads 2 t4 and 2 t4 + 1 (x[b][2 i], x[b][2 i + 1]) ----
+      float x[NB][4];
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[j][i] = 0.0f;
+        for (int i = 0; i < 4; ++i) x[b][i] = 0.0f;
       if constexpr (E4M3) {
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-          uint32_t r[4];
+          uint32_t r[4];  // 4 dims of a key in each group of 8 keys
           ldsm4(r, kb + chunk<D, E4M3>(lane, s));
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
-            mma16816<true>(x[j], q[s][0], 0u, q[s][1], 0u, kv::e4m3x2_to_h2(r[j] & 0xFFFFu),
-                           kv::e4m3x2_to_h2(r[j] >> 16));
+          for (int b = 0; b < NB; ++b)
+            mma16816<true>(x[b], kv::e4m3x2_to_h2(r[2 * b] & 0xFFFFu), kv::e4m3x2_to_h2(r[2 * b + 1] & 0xFFFFu),
+                           kv::e4m3x2_to_h2(r[2 * b] >> 16), kv::e4m3x2_to_h2(r[2 * b + 1] >> 16), q[s][0], q[s][1]);
         }
       } else {
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
-          for (int b = 0; b < TOK / 16; ++b) {
+          for (int b = 0; b < NB; ++b) {
             uint32_t r[4];
             ldsm4(r, kb + chunk<D, E4M3>(16 * b + (lane >> 4) * 8 + (lane & 7), 2 * s + ((lane >> 3) & 1)));
-            mma16816<false>(x[2 * b], q[s][0], 0u, q[s][1], 0u, r[0], r[1]);
-            mma16816<false>(x[2 * b + 1], q[s][0], 0u, q[s][1], 0u, r[2], r[3]);
+            mma16816<false>(x[b], r[0], r[2], r[1], r[3], q[s][0], q[s][1]);
           }
       }
 
       // ---- weights ----
-      float tmax = -INFINITY;
-      float inv[NT][2], fac[NT][2];  // e4m3: 2^-e and s / 2^e of each key's V scale s, e its exponent
+      float inv[NB][2], fac[NB][2];  // e4m3: 2^-e and s / 2^e of each key's V scale s, e its exponent
+      float tmax[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        if constexpr (E4M3) {
-          const float4 sc = *reinterpret_cast<const float4*>(ring_sc + st * C::SC + (8 * j + 2 * t4) * 8);
-          const float ks[2] = {sc.x, sc.z}, vs[2] = {sc.y, sc.w};
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t b = __float_as_uint(vs[i]);
-            const float ev = __fsub_rn(__uint_as_float((b >> 23) | 0x4B000000u), 8388735.0f);  // 2^23 + 127
-            inv[j][i] = __uint_as_float(0x7F000000u - (b & 0x7F800000u));
-            fac[j][i] = __fmul_rn(vs[i], inv[j][i]);  // NaN for a scale of NaN
-            x[j][i] = __fadd_rn(__fmul_rn(__fmul_rn(x[j][i], c), ks[i]), ev);
+        for (int i = 0; i < 2; ++i) {
+          const int key = 16 * b + 8 * i + g8;
+          if constexpr (E4M3) {
+            const float2 sc = *reinterpret_cast<const float2*>(ring_sc + st * C::SC + key * 8);  // K's, V's
+            const uint32_t u = __float_as_uint(sc.y);
+            const float ev = __fsub_rn(__uint_as_float((u >> 23) | 0x4B000000u), 8388735.0f);  // 2^23 + 127
+            inv[b][i] = __uint_as_float(0x7F000000u - (u & 0x7F800000u));
+            fac[b][i] = __fmul_rn(sc.y, inv[b][i]);  // NaN for a scale of NaN
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              x[b][2 * i + h] = __fadd_rn(__fmul_rn(__fmul_rn(x[b][2 * i + h], c[h]), sc.x), ev);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) x[b][2 * i + h] = __fmul_rn(x[b][2 * i + h], c[h]);
           }
-        } else {
-          x[j][0] = __fmul_rn(x[j][0], c);
-          x[j][1] = __fmul_rn(x[j][1], c);
-        }
-        if (nv < TOK) {
+          if (nv < TOK && key >= nv) {
+            x[b][2 * i] = x[b][2 * i + 1] = -INFINITY;
+            if constexpr (E4M3) inv[b][i] = fac[b][i] = 0.0f;  // whatever the scale's place holds
+          }
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (8 * j + 2 * t4 + i >= nv) {
-              x[j][i] = -INFINITY;
-              if constexpr (E4M3) inv[j][i] = fac[j][i] = 0.0f;  // whatever the scale's place holds
-            }
+          for (int h = 0; h < 2; ++h) tmax[h] = fmaxf(tmax[h], x[b][2 * i + h]);
         }
-        tmax = fmaxf(tmax, fmaxf(x[j][0], x[j][1]));
-      }
-      tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
-      tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
-      const bool moves = tmax > __fadd_rn(ref, kAbove);  // also from -inf
-      if (__any_sync(0xffffffffu, moves)) {
-        const float next = moves ? __fsub_rn(tmax, kBelow) : ref;
-        const float alpha = moves ? (ref == -INFINITY ? 0.0f : exp2f(__fsub_rn(ref, next))) : 1.0f;
-        ref = next;
-        sum = __fmul_rn(sum, alpha);
-        const float al0 = __shfl_sync(0xffffffffu, alpha, 8 * t4), al1 = __shfl_sync(0xffffffffu, alpha, 8 * t4 + 4);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          o[i][0] = __fmul_rn(o[i][0], al0);
-          o[i][1] = __fmul_rn(o[i][1], al1);
-          o[i][2] = __fmul_rn(o[i][2], al0);
-          o[i][3] = __fmul_rn(o[i][3], al1);
-        }
-      }
-      const float nref = ref == -INFINITY ? 0.0f : -ref;  // no key with a weight yet: every x is -inf
-      uint32_t w[NT], wl[NT];
+      for (int off = 4; off <= 16; off <<= 1)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        float w0 = exp2f(__fadd_rn(x[j][0], nref)), w1 = exp2f(__fadd_rn(x[j][1], nref));
-        if constexpr (E4M3) {
-          sum = __fadd_rn(sum, __fadd_rn(__fmul_rn(w0, inv[j][0]), __fmul_rn(w1, inv[j][1])));
-          w[j] = pack_h2(__fmul_rn(w0, fac[j][0]), __fmul_rn(w1, fac[j][1]));
-        } else {
-          sum = __fadd_rn(sum, __fadd_rn(w0, w1));
-          w[j] = pack_bf2(w0, w1);
-          wl[j] = pack_bf2(__fsub_rn(w0, bf_lo(w[j])), __fsub_rn(w1, bf_hi(w[j])));
+        for (int h = 0; h < 2; ++h) tmax[h] = fmaxf(tmax[h], __shfl_xor_sync(0xffffffffu, tmax[h], off));
+      const bool moves0 = tmax[0] > __fadd_rn(ref[0], kAbove), moves1 = tmax[1] > __fadd_rn(ref[1], kAbove);  // also from -inf
+      if (__any_sync(0xffffffffu, moves0 || moves1)) {
+        const bool moves[2] = {moves0, moves1};
+        float alpha[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float next = moves[h] ? __fsub_rn(tmax[h], kBelow) : ref[h];
+          alpha[h] = moves[h] ? (ref[h] == -INFINITY ? 0.0f : exp2f(__fsub_rn(ref[h], next))) : 1.0f;
+          ref[h] = next;
+          sum[h] = __fmul_rn(sum[h], alpha[h]);
         }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[i][k] = __fmul_rn(o[i][k], alpha[k & 1]);
       }
+      // no key with a weight yet: every x is -inf
+      const float nref[2] = {ref[0] == -INFINITY ? 0.0f : -ref[0], ref[1] == -INFINITY ? 0.0f : -ref[1]};
+      // w[2 b + i]: head g8, keys 16 b + 8 i + 2 t4 and + 1 (the transposed 8 x 8 of the lanes' weights)
+      uint32_t w[2 * NB], wl[2 * NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float w0 = exp2f(__fadd_rn(x[b][2 * i], nref[0])), w1 = exp2f(__fadd_rn(x[b][2 * i + 1], nref[1]));
+          if constexpr (E4M3) {
+            sum[0] = __fadd_rn(sum[0], __fmul_rn(w0, inv[b][i]));
+            sum[1] = __fadd_rn(sum[1], __fmul_rn(w1, inv[b][i]));
+            w[2 * b + i] = transpose8(pack_h2(__fmul_rn(w0, fac[b][i]), __fmul_rn(w1, fac[b][i])));
+          } else {
+            sum[0] = __fadd_rn(sum[0], w0);
+            sum[1] = __fadd_rn(sum[1], w1);
+            const uint32_t hi = pack_bf2(w0, w1);
+            w[2 * b + i] = transpose8(hi);
+            wl[2 * b + i] = transpose8(pack_bf2(__fsub_rn(w0, bf_lo(hi)), __fsub_rn(w1, bf_hi(hi))));
+          }
+        }
 
       // ---- O^T += V^T W^T: lane has dims g8 and g8 + 8 (e4m3: 2 g8 and 2 g8 + 1) of 16, heads 2 t4, + 1 ----
       if constexpr (E4M3) {
@@ -727,7 +744,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) r[i] = prmt(r[i], 0x3120);
 #pragma unroll
-          for (int b = 0; b < TOK / 16; ++b)
+          for (int b = 0; b < NB; ++b)
             mma16816<true>(o[s], kv::e4m3x2_to_h2(r[2 * b] & 0xFFFFu), kv::e4m3x2_to_h2(r[2 * b] >> 16),
                            kv::e4m3x2_to_h2(r[2 * b + 1] & 0xFFFFu), kv::e4m3x2_to_h2(r[2 * b + 1] >> 16), w[2 * b],
                            w[2 * b + 1]);
@@ -736,7 +753,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
-          for (int b = 0; b < TOK / 16; ++b) {
+          for (int b = 0; b < NB; ++b) {
             uint32_t r[4];
             ldsm4t(r, vb + chunk<D, E4M3>(16 * b + (lane >> 4) * 8 + (lane & 7), 2 * s + ((lane >> 3) & 1)));
             mma16816<false>(o[s], r[0], r[1], r[2], r[3], w[2 * b], w[2 * b + 1]);
@@ -747,14 +764,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 
     // ---- the joiners take it from here: O passes to them through the last tile's slot ----
-    sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 1));
-    sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 2));
+#pragma unroll
+    for (int off = 4; off <= 16; off <<= 1)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) sum[h] = __fadd_rn(sum[h], __shfl_xor_sync(0xffffffffu, sum[h], off));
     // the item before last has left its place
     if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&jread[par]), (uint32_t(item / 2) & 1u) ^ 1u, abort_flag, a.err)))
       return;
-    if (t4 == 0) {
-      s_ref[(par * WARPS + warp) * HEADS + g8] = ref;
-      s_sum[(par * WARPS + warp) * HEADS + g8] = sum;
+    if (g8 == 0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        s_ref[(par * WARPS + warp) * HEADS + 2 * t4 + h] = ref[h];
+        s_sum[(par * WARPS + warp) * HEADS + 2 * t4 + h] = sum[h];
+      }
     }
     if (slot >= 0) {
       // [head][dim ^ 8 (head / 2)]: the four lanes of a group fall into different banks
