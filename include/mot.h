@@ -32,7 +32,8 @@
  *     Outputs are defined only when both are clean.
  *   - Numerics ([RFC-435] §3): fixed fp32 accumulation and reduction order, no split-K,
  *     stream-K or atomics in any reduction, no TF32 or fast math, round-to-nearest-even
- *     casts only at the points each entry point declares.
+ *     casts only at the points each entry point declares. (mot_paged_decode_attention alone cuts
+ *     a long sum, over a row's keys: at borders of the row's own, joined in a fixed order.)
  */
 #ifndef MOT_H
 #define MOT_H
@@ -366,8 +367,15 @@ size_t mot_paged_decode_workspace_bytes(int64_t R, int Hq, int Hkv, int D, int m
  *   ws     at least mot_paged_decode_workspace_bytes(R, Hq, Hkv, D, max_pages, page) bytes; everything
  *          after its first 64 bytes is scratch that the call overwrites (so not a routing plan in use).
  *   out    [R][Hq D] bf16             out.
+ * Query head h reads KV head h / (Hq / Hkv); S = q . k in fp32 on the tensor cores, the weights 2^x of
+ * x = S scale log2 e against a running reference in fp32, their sums in fp32; a weight enters its
+ * product with v as two bf16 (MOT_KV_BF16: 16 significant bits) or as a half together with v's scale
+ * (MOT_KV_E4M3: 11); out = bf16(O / sum). A row's keys are cut into ranges at borders that its own
+ * length and the head geometry alone set, and the ranges are joined in a fixed order, so a row's bits
+ * depend neither on the other rows nor on where its pages lie. scales may be any
+ * numbers from 2^-64 to 2^126 (MOT_KV_E4M3; NaN makes what its head sees NaN).
  * Rows of one sequence (several new tokens) are several rows with equal page tables and their own
- * lengths. Geometry: 1 <= R <= MOT_MAX_TOKENS, R * (Hq + 2 Hkv) < 2^31, max_pages >= 1, max_pages * page <= 2^30.
+ * lengths. The call's tensors do not overlap. Geometry: 1 <= R <= MOT_MAX_TOKENS, R * (Hq + 2 Hkv) < 2^31, max_pages >= 1, max_pages * page <= 2^30.
  */
 int mot_paged_decode_attention(const mot_bf16* qkv, int64_t R, int Hq, int Hkv, int D, const int32_t* table,
                                const int32_t* lens, int max_pages, int kv_type, int64_t n_pages, int page,

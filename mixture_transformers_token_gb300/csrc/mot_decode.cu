@@ -7,32 +7,42 @@
 //
 // Splitting. A row's keys are cut into ranges of span(len) keys, a function of the row's own length
 // and the head geometry alone, so a row's bits do not depend on the batch. The span is the shortest
-// multiple of a CTA's round (8 warps x TOK keys) that cuts one row into at most as many (range, KV
-// head) items as there are SMs: a single long row then fills the machine in one wave, and each long
-// row of a batch gives every SM about one item. A persistent CTA per SM takes every 152nd item.
+// multiple of a CTA's round (8 warps x TOK keys), 512 keys at least, that cuts one row into no more
+// (range, KV head) items than there are SMs: a single long row then fills the machine in one wave, and
+// each long row of a batch gives every SM about one item. Of the shortest spans 256, 512, 768 and 1024,
+// 512 was taken over 20 batches: 1024 is 12 % faster on 12 rows of 2000 keys and 2 % on 64 of up to
+// 8192, but 24 % slower on one row of 4000; 256 is 9 % faster there and 28 % slower on 256 e4m3
+// rows of up to 4096. A persistent CTA per SM takes every 152nd item.
 //
 // Arithmetic of an item (a key range of one KV head, up to 8 of its query heads): warp w of 8 takes
-// the range's tiles w, w + 8, ... of TOK keys. Per tile S = Q K^T with mma.sync (m16n8k16: the heads
-// are the 16 rows, half of them empty), x = S c in powers of two, then w = 2^(x - ref) where the
-// reference starts as the tile's maximum less 6 and moves only when a tile's maximum exceeds it by
-// more than 14 (so w <= 2^14, and the largest w is at least 2^6); sums of w in fp32 per lane;
-// O^T += V^T W^T (m16n8k16: 16 dims x 8 heads). The 8 warps' (ref, sum, O) are joined in warp order,
-// the ranges' in a fixed order by join_kernel. Every fp32 operation is rounded on its own.
+// the range's tiles w, w + 8, ... of TOK keys. Per tile S^T = K Q^T with mma.sync (m16n8k16: 16 keys x
+// 8 heads), x = S c in powers of two, then w = 2^(x - ref) where a head's reference starts as the
+// tile's maximum less 6 and moves only when a tile's maximum exceeds it by more than 14 (so w <= 2^14,
+// and the largest w is at least 2^6); sums of w in fp32 per lane; O^T += V^T W^T (m16n8k16: 16 dims x 8
+// heads), the weights turned by movmatrix. The 8 warps' (ref, sum, O) are joined in a fixed order, the
+// ranges' in a fixed order by join_kernel. Every fp32 operation is rounded on its own.
 // bf16 cache: w goes into the product as two bf16 (w and what its rounding leaves), so the weights
 // keep 16 bits: one bf16 each would put an error the size of the output's own rounding beside it.
-// e4m3 cache: codes become halves (exact), the query too, scaled by a power of two, and a weight is a half. A token's V scale
-// belongs into its weight, so the reference follows x + log2(scale): the halves' range is then spent on
-// what the products contribute, however the scales differ.
+// e4m3 cache: codes become halves (exact), the query too, scaled by a power of two that takes its largest
+// element into [2^14, 2^15) (exact but for elements below 2^-24 of it), and a weight is a half. A token's
+// V scale belongs into its weight, so the reference follows x + log2(scale): the halves' range is then
+// spent on what the products contribute, however the scales differ.
 //
 // What bounds it: HBM. A key costs 4 G flop per 4 bytes, far below the tensor cores' rate even on
-// mma.sync (tcgen05's smallest M is 64 rows; here there are at most 8), so the design is about bytes in
-// flight: every consumer warp owns a ring of STAGES tiles in shared memory (24 KB a warp, 192 KB an SM,
-// several times the 54 KB an SM needs to cover HBM's latency at full rate) and meets the others only
-// where an item ends. A producer warp walks the items, looks the pages up one round ahead (a lane for
-// each 16 keys), and fills the rings with TMA copies (16-key boxes, hardware swizzle, so ldmatrix reads
-// are free of bank conflicts) and a ring of item descriptors with the queries, running on into the next
-// items while the consumers join one. With every warp walking and copying for itself, the lookups'
-// latencies stood in the consumers' way: 45 us instead of the figure below on 256 rows of 100 to 300 keys.
+// mma.sync (tcgen05's smallest M is 64 rows; here there are 8 heads, and a tile's 16 to 32 keys), so the
+// design is about bytes in flight: every consumer warp owns a ring of STAGES tiles in shared memory (24 KB
+// a warp, 192 KB an SM, several times the 54 KB an SM needs to cover HBM's latency at full rate), and what
+// is not a tile's arithmetic is done by other warps. Four producer warps walk the items, look the pages up
+// one round ahead and fill the rings with TMA copies (16 or 32 keys, hardware swizzle, so ldmatrix reads are
+// free of bank conflicts; they leave L2 first); the first also sends the items' descriptors and queries.
+// Four joiner warps turn e4m3 queries into halves an item ahead, and join the consumers' results while
+// these run on. What each step brought, on 64 ragged bf16 rows of up to 8192 keys and 256 e4m3 rows of up
+// to 4096 (28 / 4 heads of 128; floors 93 and 90 us at the copy's rate): every warp walking and copying for
+// itself 157 and 294 us; producers 111 and 219; joiners, one warp a head in narrow joins, spans of
+// 512 110 and 130; queries by the joiners, two heads a joiner 107 and 118; the L2 policy 103 and 116;
+// K Q^T 103 and 115 (6.2 and 5.3 TB/s). One e4m3 row of 131072 keys takes 28 us (floor 20), one bf16
+// row of 500 7. The e4m3 cache is bound by its consumers' instructions: 128 conversions and 32 products a
+// tile that brings 8 KB.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
