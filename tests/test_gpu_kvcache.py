@@ -3,7 +3,7 @@
 The written cache and the rows read back are compared bit for bit. A decoded output is compared with
 the fp64 golden under a bound that counts each rounding:
   scores    the dot product's fp32 accumulation, at most 2 D 2^-24 sum|q||k| scale; the score times
-            scale log2 e (and, in an e4m3 cache, a power of two), rounded twice: 2^-23 |s|. An error d
+            scale log2 e and a scale, rounded thrice: 2^-22 |s|. An error d
             of a score changes its weight by the factor e^d, and the sum of the weights by as much.
   weights   2^-20 for exp2f and the rescaling of a handful of running maxima; a weight's own rounding
             before its product with v: 2^-11 (a half, e4m3 cache) or 2^-16 (two bf16, bf16 cache).
@@ -461,6 +461,86 @@ def test_offsets_beyond_32_bits(kv):
             q, s = O.kv_quantise(a)
             a = q * s[..., None]
         np.testing.assert_array_equal(c, a)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_decode_many_rows(kv):
+    # more rows than the walk holds at a time, more items a CTA than descriptors in flight; bad rows between
+    r = W.rng_for(7, 607)
+    lens = [int(n) for n in r.integers(0, 1400, 300)]
+    lens[255], lens[256], lens[299] = 1399, 0, 1
+    b = Batch(lens, 8, 4, 64, kv, 16, seed=101)
+    out = b.run()
+    b.check(out, b.golden(), "300 rows")
+    bad = b.lens_t.clone()
+    at = torch.tensor([0, 31, 32, 100, 255, 256, 299], device=DEV)
+    bad[at] = torch.tensor([-1, 2 ** 31 - 1, -2 ** 31, 10 ** 6, -1, -5, 2 ** 30], dtype=torch.int32, device=DEV)
+    ws, keep = b.ws(), torch.full_like(out, 2.0)
+    got = mot.mot_paged_decode_attention(b.q, b.table, bad, b.k, b.v, 8, ws, scales=b.scales, out=keep.clone())
+    assert mot.mot_device_status(ws) == mot.DEV_BAD_PAGE
+    fine = torch.ones(300, dtype=torch.bool, device=DEV)
+    fine[at] = False
+    assert torch.equal(got[fine], out[fine]) and torch.equal(got[~fine], keep[~fine])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_decode_row_bits_do_not_depend_on_the_table_width(kv):
+    # a table that could hold a row of more than 32 ranges takes the other form of the join
+    b = Batch([6000, 300, 13000], 7, 1, 128, kv, 16, seed=111)
+    want = b.run()
+    b.table = torch.cat([b.table, torch.full((3, 2000), -1, dtype=torch.int32, device=DEV)], 1).contiguous()
+    assert_bitwise(b.run(), want, "wide table")
+    b.check(want, b.golden(), "two forms of the join")
+
+
+def test_decode_scales_that_are_no_powers_of_two():
+    b = Batch([333, 40, 1], 14, 2, 128, "e4m3", 16, seed=121)
+    r = W.rng_for(8, 608)
+    f = torch.from_numpy(np.exp2(r.uniform(-6, 6, tuple(b.scales.shape))).astype(np.float32)).to(DEV)
+    b.scales *= f
+    n_pages, Hkv, page, _ = b.scales.shape
+    k, v = (_values(t, b.scales[..., i]) for i, t in enumerate((b.k, b.v)))
+    tab = b.table.cpu().numpy()
+    rows = [[tab[i, j // page] * page + j % page for j in range(n)] for i, n in enumerate(b.lens)]
+    q = f64(b.q)[:, : b.Hq * b.D].reshape(len(b.lens), b.Hq, b.D)
+    g = O.g_paged_decode(q, [k[x] for x in rows], [v[x] for x in rows], b.Hq, b.Hkv)
+    b.check(b.run(), g, "scales")
+
+
+def test_decode_on_two_streams_at_once():
+    a, b = Batch([3000, 50, 700], 28, 4, 128, "e4m3", 32, seed=131), Batch([900] * 9, 4, 2, 64, "bf16", 16, seed=132)
+    want_a, want_b = a.run(), b.run()
+    wa, wb, oa, ob = a.ws(), b.ws(), torch.empty_like(want_a), torch.empty_like(want_b)
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        mot.mot_paged_decode_attention(a.q, a.table, a.lens_t, a.k, a.v, a.Hq, wa, scales=a.scales, out=oa, stream=sa)
+        mot.mot_paged_decode_attention(b.q, b.table, b.lens_t, b.k, b.v, b.Hq, wb, out=ob, stream=sb)
+    torch.cuda.synchronize()
+    assert torch.equal(oa, want_a) and torch.equal(ob, want_b)
+    assert mot.mot_device_status(wa) == 0 and mot.mot_device_status(wb) == 0
+
+
+def test_write_and_read_in_a_captured_graph():
+    Hq, Hkv, D, page, T = 4, 2, 64, 16, 40
+    x = _qkv(T, Hq, Hkv, D, 141).to(DEV)
+    slots = torch.from_numpy(_slots(T, 64, 142)).to(DEV)
+    k, v, sc = _empty_cache(4, Hkv, page, D, "e4m3")
+    ws, y = _ws(), torch.zeros_like(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mot.mot_kv_cache_write(x, slots, k, v, Hq, ws, scales=sc)
+        mot.mot_kv_cache_read(k, v, slots, y, Hq, ws, scales=sc)
+    for seed in (143, 144):
+        x.copy_(_qkv(T, Hq, Hkv, D, seed).to(DEV))
+        slots.copy_(torch.from_numpy(_slots(T, 64, seed)).to(DEV))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(_kv(x, Hq, Hkv, D), _kv(y, Hq, Hkv, D)):
+            q, s = O.kv_quantise(a)
+            np.testing.assert_array_equal(b, q * s[..., None])
+    assert mot.mot_device_status(ws) == 0
 
 
 # ---------------------------------------------------------------------------
