@@ -854,6 +854,7 @@ __global__ void __launch_bounds__(kWide ? 256 : 32 * NARROW_WARPS) join_kernel(c
   if (len > 0 && len <= int64_t(a.max_pages) * a.page)
     n = splits_of(len, span_of(len, Cfg<D, E4M3>::ROUND, Cfg<D, E4M3>::MIN_SPAN, a.Hkv * a.HC));
   pdl_wait();
+  pdl_trigger();  // what comes next may start up under this grid
   if (n <= 1) return;
   const int64_t at0 = int64_t(row) * a.max_split * a.Hq + head;
   // thread (narrow: lane) s has range s

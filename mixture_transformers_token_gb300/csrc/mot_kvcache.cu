@@ -196,7 +196,7 @@ static int move(bool write, uint16_t* qkv, int64_t T, int Hq, int Hkv, int D, co
   a.by_page = Div(uint32_t(page));
   a.err = &static_cast<PlanHeader*>(ws)->error;
   const int64_t groups = THREADS / (D / (8 * PIECES)), vectors = T * Hkv * 2;
-  const int64_t want = (vectors + groups - 1) / groups, most = int64_t(8) * sm_count(dev);
+  const int64_t want = (vectors + groups - 1) / groups, most = int64_t(16) * sm_count(dev);
   const unsigned grid = unsigned(want < most ? want : most);
   a.step_row = int(int64_t(grid) * groups / (2 * Hkv));
   a.step_j = int(int64_t(grid) * groups % (2 * Hkv));
