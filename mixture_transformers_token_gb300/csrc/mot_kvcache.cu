@@ -8,7 +8,7 @@
 // D bf16, two 16-byte pieces a lane, K's group beside V's of the same token and head. HBM bounds them. A group
 // walks its vectors by additions: a 64-bit division a vector cost as much as the quantiser. On 36864
 // rows of 4 heads of 128 in e4m3 (115 MB to read and write, 16.9 us at the copy's rate) the write takes
-// 19.2 us and the read 20.7; with one piece a lane (twice the shuffles, address sums and groups) they took
+// 18.8 us and the read 20.7; with one piece a lane (twice the shuffles, address sums and groups) they took
 // 28.3 and 25.3, with two vectors of one piece in flight 25.9 and 22.2.
 
 #include <cuda_runtime.h>
