@@ -313,7 +313,8 @@ int mot_joint_attention(const mot_bf16* qkv, int64_t T, int Hq, int Hkv, int D, 
  * Slot s is token s % page of page s / page. Geometry of all three: D in {64, 128}; Hq, Hkv in
  * 1 .. 1024, Hq a multiple of Hkv; page a multiple of 16, 16 <= page <= 1024; n_pages >= 1 and
  * n_pages * Hkv * page < 2^31, else MOT_ERR_GEOMETRY; any other kv_type is MOT_ERR_ARG. All pointers
- * 16-byte aligned device memory of the stream's device. ws has at least 64 bytes whose error word
+ * are device memory of the stream's device, 16-byte aligned, int32 arrays (slots, table, lens: parts of
+ * longer ones serve) 4-byte aligned. ws has at least 64 bytes whose error word
  * receives MOT_DEV_BAD_PAGE (it is OR-ed into, never cleared: start from a zeroed or planned one).
  */
 

@@ -1033,7 +1033,7 @@ extern "C" int mot_paged_decode_attention(const mot_bf16* qkv, int64_t R, int Hq
   const size_t need = mot_paged_decode_workspace_bytes(R, Hq, Hkv, D, max_pages, page);
   if (need == 0) return MOT_ERR_GEOMETRY;
   if (!(scale > 0.0f) || !(scale < 3.0e38f)) return MOT_ERR_ARG;
-  if (!aligned16(qkv) || !aligned16(table) || !aligned16(lens) || !aligned16(k_cache) || !aligned16(v_cache) ||
+  if (!aligned16(qkv) || !kv::aligned4(table) || !kv::aligned4(lens) || !aligned16(k_cache) || !aligned16(v_cache) ||
       !aligned16(ws) || !aligned16(out) || (e4m3 && !aligned16(scales)))
     return MOT_ERR_ALIGN;
   if (ws_bytes < need) return MOT_ERR_WORKSPACE;

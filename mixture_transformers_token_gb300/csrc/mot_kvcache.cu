@@ -172,7 +172,7 @@ static int move(bool write, uint16_t* qkv, int64_t T, int Hq, int Hkv, int D, co
   int st = check_shape(Hq, Hkv, D, kv_type, n_pages, page);
   if (st != MOT_OK) return st;
   if (T < 1 || T > MOT_MAX_TOKENS) return MOT_ERR_GEOMETRY;
-  if (!aligned16(qkv) || !aligned16(slots) || !aligned16(k) || !aligned16(v) || !aligned16(ws) ||
+  if (!aligned16(qkv) || !aligned4(slots) || !aligned16(k) || !aligned16(v) || !aligned16(ws) ||
       (e4m3 && !aligned16(scales)))
     return MOT_ERR_ALIGN;
   if (ws_bytes < sizeof(PlanHeader)) return MOT_ERR_WORKSPACE;

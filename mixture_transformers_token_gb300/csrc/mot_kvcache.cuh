@@ -73,6 +73,8 @@ struct Div {
   }
 };
 
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 // Checks of the cache's shape that need no CUDA call.
 inline int check_shape(int Hq, int Hkv, int D, int kv_type, int64_t n_pages, int page) {
   if (kv_type != MOT_KV_BF16 && kv_type != MOT_KV_E4M3) return MOT_ERR_ARG;

@@ -493,6 +493,24 @@ def test_decode_row_bits_do_not_depend_on_the_table_width(kv):
     b.check(want, b.golden(), "two forms of the join")
 
 
+def test_parts_of_longer_index_arrays():
+    # slots, tables and lengths that start inside longer tensors, on 4-byte boundaries
+    b = Batch([70, 33, 200, 16, 90], 4, 2, 64, "e4m3", 16, seed=115)
+    want = b.run()
+    width = b.table.shape[1]
+    lens = torch.cat([torch.zeros(3, dtype=torch.int32, device=DEV), b.lens_t])[3:]
+    table = torch.cat([torch.full((1,), -5, dtype=torch.int32, device=DEV), b.table.reshape(-1)])[1:].reshape(5, width)
+    assert lens.data_ptr() % 16 and table.data_ptr() % 16
+    ws = b.ws()
+    got = mot.mot_paged_decode_attention(b.q, table, lens, b.k, b.v, 4, ws, scales=b.scales)
+    assert mot.mot_device_status(ws) == 0
+    assert_bitwise(got, want, "shifted arrays")
+    slots = torch.arange(9, dtype=torch.int32, device=DEV)
+    y = mot.mot_kv_cache_read(b.k, b.v, slots[1:], b.q.new_zeros((8, b.q.shape[1])), 4, ws, scales=b.scales)
+    z = mot.mot_kv_cache_read(b.k, b.v, slots[1:].clone(), b.q.new_zeros((8, b.q.shape[1])), 4, ws, scales=b.scales)
+    assert_bitwise(y, z, "shifted slots")
+
+
 def test_decode_scales_that_are_no_powers_of_two():
     b = Batch([333, 40, 1], 14, 2, 128, "e4m3", 16, seed=121)
     r = W.rng_for(8, 608)

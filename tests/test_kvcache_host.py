@@ -109,9 +109,12 @@ def test_decode_rejects(lib):
     write, read, f = _cache_calls(lib)
     for name in ("table", "lens", "out"):
         assert f(**{name: None}) == MOT_ERR_NULL, name
-        assert f(**{name: MIS}) == MOT_ERR_ALIGN, name
-    for name in (write, read):
-        assert name(slots=None) == MOT_ERR_NULL and name(slots=MIS) == MOT_ERR_ALIGN
+        assert f(**{name: MIS + 2}) == MOT_ERR_ALIGN, name
+    assert f(out=MIS) == MOT_ERR_ALIGN
+    for call in (write, read):
+        assert call(slots=None) == MOT_ERR_NULL and call(slots=MIS + 2) == MOT_ERR_ALIGN
+        assert call(slots=MIS + 4) not in (0, MOT_ERR_ALIGN)     # an int32 array may start anywhere
+    assert f(table=MIS + 4, lens=MIS) not in (0, MOT_ERR_ALIGN)
     assert f(mp=0) == MOT_ERR_GEOMETRY
     assert f(mp=(1 << 26) + 1) == MOT_ERR_GEOMETRY            # more than 2^30 keys a row
     assert f(T=1 << 22, Hq=1024, Hkv=1024) == MOT_ERR_GEOMETRY  # R * Hq
