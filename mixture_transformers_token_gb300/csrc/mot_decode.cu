@@ -703,18 +703,19 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) tmax[h] = fmaxf(tmax[h], x[b][2 * i + h]);
         }
+      // a head's tile maximum is above its reference's slack (also from -inf) if a lane's is: only then do the
+      // lanes exchange them
+      if (__any_sync(0xffffffffu, tmax[0] > __fadd_rn(ref[0], kAbove) || tmax[1] > __fadd_rn(ref[1], kAbove))) {
 #pragma unroll
-      for (int off = 4; off <= 16; off <<= 1)
+        for (int off = 4; off <= 16; off <<= 1)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) tmax[h] = fmaxf(tmax[h], __shfl_xor_sync(0xffffffffu, tmax[h], off));
-      const bool moves0 = tmax[0] > __fadd_rn(ref[0], kAbove), moves1 = tmax[1] > __fadd_rn(ref[1], kAbove);  // also from -inf
-      if (__any_sync(0xffffffffu, moves0 || moves1)) {
-        const bool moves[2] = {moves0, moves1};
+          for (int h = 0; h < 2; ++h) tmax[h] = fmaxf(tmax[h], __shfl_xor_sync(0xffffffffu, tmax[h], off));
         float alpha[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float next = moves[h] ? __fsub_rn(tmax[h], kBelow) : ref[h];
-          alpha[h] = moves[h] ? (ref[h] == -INFINITY ? 0.0f : exp2f(__fsub_rn(ref[h], next))) : 1.0f;
+          const bool moves = tmax[h] > __fadd_rn(ref[h], kAbove);
+          const float next = moves ? __fsub_rn(tmax[h], kBelow) : ref[h];
+          alpha[h] = moves ? (ref[h] == -INFINITY ? 0.0f : exp2f(__fsub_rn(ref[h], next))) : 1.0f;
           ref[h] = next;
           sum[h] = __fmul_rn(sum[h], alpha[h]);
         }
