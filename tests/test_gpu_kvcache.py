@@ -357,6 +357,29 @@ def test_decode_row_bits_do_not_depend_on_the_batch(kv):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,Hq,Hkv,D,page", [(5003, 24, 2, 128, 16), (4100, 20, 1, 64, 48), (2051, 64, 4, 64, 32),
+                                             (3500, 33, 1, 128, 16)])
+def test_decode_groups_of_more_than_eight_heads(n, Hq, Hkv, D, page, kv):
+    lens = [n, 0, 700, 33, 1, n // 2, 512, 17] * 3
+    b = Batch(lens, Hq, Hkv, D, kv, page, seed=n, spread=2)
+    want = b.run()
+    b.check(want, b.golden(), f"{Hq}/{Hkv} heads")
+    assert_bitwise(b.run([0, 5, 2]), want[[0, 5, 2]], "a part of the batch")
+    c = Batch([900, 33, 1], Hq, Hkv, D, kv, page, seed=n + 1, q_gain=40.0)
+    c.check(c.run(), c.golden(), "a sharp softmax")
+    # one head's NaN, in the first and in the second eight, and in the last head
+    clean = f64(c.run()).reshape(3, Hq, D)
+    for head in (3, 8, Hq - 1):
+        was = c.q[0, head * D + 5].clone()
+        c.q[0, head * D + 5] = float("nan")
+        got = f64(c.run()).reshape(3, Hq, D)
+        others = [h for h in range(Hq) if h != head]
+        assert np.isnan(got[0, head]).all() and np.array_equal(got[0, others], clean[0, others])
+        assert np.array_equal(got[1:], clean[1:])
+        c.q[0, head * D + 5] = was
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_decode_nan_and_infinity_stay_in_their_rows(kv):
     Hq, Hkv, D, page = 4, 2, 64, 16
     b = Batch([40, 50, 60, 20], Hq, Hkv, D, kv, page, seed=41)
