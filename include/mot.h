@@ -376,7 +376,10 @@ size_t mot_paged_decode_workspace_bytes(int64_t R, int Hq, int Hkv, int D, int m
  * depend neither on the other rows nor on where its pages lie. scales may be any
  * numbers from 2^-64 to 2^126 (MOT_KV_E4M3; NaN makes what its head sees NaN).
  * Rows of one sequence (several new tokens) are several rows with equal page tables and their own
- * lengths. The call's tensors do not overlap. Geometry: 1 <= R <= MOT_MAX_TOKENS, R * (Hq + 2 Hkv) < 2^31, max_pages >= 1, max_pages * page <= 2^30.
+ * lengths. The call's tensors do not overlap; calls that may run at the same time (other streams, graphs)
+ * have workspaces of their own. Geometry: 1 <= R <= MOT_MAX_TOKENS, R * (Hq + 2 Hkv) < 2^31, max_pages >= 1,
+ * max_pages * page <= 2^24 (the longest range, a row's whole length where there are many KV heads, then
+ * takes a fraction of the second after which a wait is given up).
  */
 int mot_paged_decode_attention(const mot_bf16* qkv, int64_t R, int Hq, int Hkv, int D, const int32_t* table,
                                const int32_t* lens, int max_pages, int kv_type, int64_t n_pages, int page,

@@ -1016,7 +1016,9 @@ using namespace mot;
 
 extern "C" size_t mot_paged_decode_workspace_bytes(int64_t R, int Hq, int Hkv, int D, int max_pages, int page) {
   if (kv::check_shape(Hq, Hkv, D, MOT_KV_BF16, 1, page) != MOT_OK) return 0;
-  if (R < 1 || R > MOT_MAX_TOKENS || max_pages < 1 || int64_t(max_pages) * page > (int64_t(1) << 30)) return 0;
+  // with more than 76 (KV head, group of 8 heads) pairs a row is one range, which the joiners wait for: 2^24
+  // keys take about 0.2 s (1.6 us a round of 128 at HBM's rate), against the 1 s after which a wait is given up
+  if (R < 1 || R > MOT_MAX_TOKENS || max_pages < 1 || int64_t(max_pages) * page > (int64_t(1) << 24)) return 0;
   if (R * (Hq + 2 * Hkv) > (int64_t(1) << 31) - 1) return 0;  // head vectors have 32-bit TMA coordinates
   const int G = Hq / Hkv, heads = Hkv * ((G + decode::HEADS - 1) / decode::HEADS);
   const int64_t n = D == 64 ? decode::max_split<64, false>(int64_t(max_pages) * page, heads)

@@ -116,7 +116,9 @@ def test_decode_rejects(lib):
         assert call(slots=MIS + 4) not in (0, MOT_ERR_ALIGN)     # an int32 array may start anywhere
     assert f(table=MIS + 4, lens=MIS) not in (0, MOT_ERR_ALIGN)
     assert f(mp=0) == MOT_ERR_GEOMETRY
-    assert f(mp=(1 << 26) + 1) == MOT_ERR_GEOMETRY            # more than 2^30 keys a row
+    assert f(mp=(1 << 26) + 1) == MOT_ERR_GEOMETRY
+    assert f(mp=(1 << 20) + 1) == MOT_ERR_GEOMETRY            # more than 2^24 keys a row
+    assert f(mp=1 << 20, T=1) not in (0, MOT_ERR_GEOMETRY)
     assert f(T=1 << 22, Hq=1024, Hkv=1024) == MOT_ERR_GEOMETRY  # R * Hq
     for scale in (0.0, -1.0, float("nan"), float("inf")):
         assert f(scale=scale) == MOT_ERR_ARG
