@@ -424,6 +424,24 @@ def test_decode_reports_bad_lengths_and_pages():
             assert torch.equal(out[[0, 2, 3]], clean[[0, 2, 3]])
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_decode_batches_that_begin_or_consist_of_bad_lengths(kv):
+    # more rows than a producer's window holds, so that whole windows have no work
+    good = [40, 700, 0, 16]
+    b = Batch(good, 4, 2, 64, kv, 16, seed=52)
+    want = b.run()
+    n = 600
+    pick = torch.cat([torch.zeros(n, dtype=torch.int64), torch.arange(4)]).to(DEV)
+    q, t, lens = b.q[pick].contiguous(), b.table[pick].contiguous(), b.lens_t[pick].contiguous()
+    lens[:n] = -1
+    for rows in (slice(0, n + 4), slice(0, n), slice(0, 1)):
+        ws = b.ws(n + 4)
+        out = torch.full((len(lens[rows]), 4 * 64), -3.0, dtype=torch.bfloat16, device=DEV)
+        mot.mot_paged_decode_attention(q[rows], t[rows], lens[rows], b.k, b.v, 4, ws, scales=b.scales, out=out)
+        assert mot.mot_device_status(ws) == mot.DEV_BAD_PAGE
+        assert (out[:n] == -3).all() and torch.equal(out[n:], want[: len(out) - len(out[:n])])
+
+
 def test_decode_leaves_what_lies_around_its_outputs():
     b = Batch([70, 700, 3], 7, 1, 64, "bf16", 16, seed=61)
     want = b.run()
