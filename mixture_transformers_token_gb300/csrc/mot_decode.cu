@@ -109,7 +109,7 @@ struct Args {
   int HC;                // groups of up to 8 heads that share a KV head
   int max_split;         // ranges of a row that the workspace has room for
   int box;               // keys of a copy: 16, or 32 where a tile's 32 lie in one page
-  kv::Div by_page, by_heads, by_hc;  // page, Hkv * HC, HC
+  kv::Div by_page, by_heads, by_hc, by_most;  // page, Hkv * HC, HC, most ranges of a row
   float c;               // scale * log2(e)
   float2* ml;            // [R][max_split][Hq] (reference, sum) of a range
   float* part;           // [R][max_split][Hq][D]
@@ -117,15 +117,21 @@ struct Args {
   uint32_t* err;
 };
 
-// Keys of a row's ranges, and how many there are (an empty row has one empty range, which writes its
-// zeros). `round` and `min_span` are those of Cfg.
-__host__ __device__ inline int span_of(int len, int round, int min_span, int heads) {
-  const int most = SPLIT_ITEMS / heads > 1 ? SPLIT_ITEMS / heads : 1;
-  const int each = (len + most - 1) / most;
-  const int span = (each + round - 1) / round * round;
-  return span > min_span ? span : min_span;
+// Ranges that one row is cut into, at most.
+inline int most_of(int heads) { return SPLIT_ITEMS / heads > 1 ? SPLIT_ITEMS / heads : 1; }
+
+// How many ranges a row of len keys has, and their keys (an empty row has one empty range, which writes its
+// zeros). C: the Cfg.
+template <typename C>
+__device__ __forceinline__ int ranges_of(const Args& a, int len, int& span) {
+  const int each = int(a.by_most.of(uint32_t(len) + a.by_most.d - 1));
+  span = (each + C::ROUND - 1) / C::ROUND * C::ROUND;
+  if (span <= C::MIN_SPAN) {
+    span = C::MIN_SPAN;
+    return len == 0 ? 1 : (len + C::MIN_SPAN - 1) / C::MIN_SPAN;
+  }
+  return (len + span - 1) / span;
 }
-__host__ __device__ inline int splits_of(int len, int span) { return len == 0 ? 1 : (len + span - 1) / span; }
 
 // ---------------------------------------------------------------------------
 // small wrappers
@@ -219,6 +225,7 @@ static_assert(sizeof(Item) == 32, "a descriptor is 32 bytes");
 // WINDOW rows at a time lie in shared memory, summed up.
 template <int D, bool E4M3>
 struct Walk {
+  using C = Cfg<D, E4M3>;
   int64_t base;  // items of the rows before the window
   int w0, nw;    // the window's first row and its rows
   int hint;      // no row of the window before this one holds an item still to come
@@ -230,30 +237,36 @@ struct Walk {
     const int lane = threadIdx.x & 31, heads = a.Hkv * a.HC;
     nw = min(WINDOW, a.R - w0);
     hint = 0;
-    __syncwarp();
-    for (int i = lane; i < nw; i += 32) lens[i] = a.lens[w0 + i];
-    __syncwarp();
-    int sum = 0;
-    for (int i0 = 0; i0 < nw; i0 += 32) {
-      int n = 0;
-      if (i0 + lane < nw) {
-        const int len = lens[i0 + lane];
-        if (len < 0 || len > int64_t(a.max_pages) * a.page) {
-          if (blockIdx.x == 0 && threadIdx.x / 32 == WARPS) atomicOr(a.err, MOT_DEV_BAD_PAGE);
-        } else {
-          const int span = span_of(len, Cfg<D, E4M3>::ROUND, Cfg<D, E4M3>::MIN_SPAN, heads);
-          n = splits_of(len, span) * heads;
-          spans[i0 + lane] = span;
-        }
-      }
+    // all loads on their way at once, then a lane takes neighbouring rows: one exchange sums up the lanes'
+    int len[WINDOW / 32];
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, n, off);
-        if (lane >= off) n += o;
+    for (int k = 0; k < WINDOW / 32; ++k) len[k] = 32 * k + lane < nw ? a.lens[w0 + 32 * k + lane] : 0;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < WINDOW / 32; ++k)
+      if (32 * k + lane < nw) lens[32 * k + lane] = len[k];
+    __syncwarp();
+    const int each = (nw + 31) / 32, first = min(lane * each, nw), last = min(first + each, nw);
+    int mine = 0;
+    for (int i = first; i < last; ++i) {
+      const int n = lens[i];
+      if (n < 0 || n > int64_t(a.max_pages) * a.page) {
+        if (blockIdx.x == 0 && threadIdx.x / 32 == WARPS) atomicOr(a.err, MOT_DEV_BAD_PAGE);
+      } else {
+        int span;
+        mine += ranges_of<C>(a, n, span) * heads;
+        spans[i] = span;
       }
-      if (i0 + lane < nw) upto[i0 + lane] = sum + n;
-      sum += __shfl_sync(0xffffffffu, n, 31);
+      upto[i] = mine;
     }
+    int before = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, before, off);
+      if (lane >= off) before += o;
+    }
+    before -= mine;
+    for (int i = first; i < last; ++i) upto[i] += before;
     __syncwarp();
   }
   __device__ void init(const Args& a, int* rows) {
@@ -854,16 +867,18 @@ __global__ void __launch_bounds__(kWide ? 256 : 32 * NARROW_WARPS) join_kernel(c
   const int row = int(rh / uint32_t(a.Hq)), head = int(rh - uint32_t(row) * uint32_t(a.Hq));
   // the lengths are the call's inputs: there before decode_kernel began
   const int len = row < a.R ? a.lens[row] : 0;
-  int n = 0;
-  if (len > 0 && len <= int64_t(a.max_pages) * a.page)
-    n = splits_of(len, span_of(len, Cfg<D, E4M3>::ROUND, Cfg<D, E4M3>::MIN_SPAN, a.Hkv * a.HC));
-  pdl_wait();
-  pdl_trigger();  // what comes next may start up under this grid
-  if (n <= 1) return;
   const int64_t at0 = int64_t(row) * a.max_split * a.Hq + head;
   // thread (narrow: lane) s has range s
   const int mine = kWide ? int(threadIdx.x) : lane;
-  const float2 ml = mine < n ? __ldcg(a.ml + at0 + int64_t(mine) * a.Hq) : make_float2(-INFINITY, 0.0f);
+  pdl_wait();
+  pdl_trigger();  // what comes next may start up under this grid
+  // on its way beside the length: the workspace has the place whether the row has the range or not
+  float2 ml = make_float2(-INFINITY, 0.0f);
+  if (row < a.R && mine < a.max_split) ml = __ldcg(a.ml + at0 + int64_t(mine) * a.Hq);
+  int n = 0, span;
+  if (len > 0 && len <= int64_t(a.max_pages) * a.page) n = ranges_of<Cfg<D, E4M3>>(a, len, span);
+  if (n <= 1) return;
+  if (mine >= n) ml = make_float2(-INFINITY, 0.0f);
   float top = ml.x;
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -947,7 +962,7 @@ __global__ void __launch_bounds__(kWide ? 256 : 32 * NARROW_WARPS) join_kernel(c
 // Ranges that a row can have when its table holds max_len keys.
 template <int D, bool E4M3>
 inline int max_split(int64_t max_len, int heads) {
-  const int most = SPLIT_ITEMS / heads > 1 ? SPLIT_ITEMS / heads : 1;
+  const int most = most_of(heads);
   const int64_t n = (max_len + Cfg<D, E4M3>::MIN_SPAN - 1) / Cfg<D, E4M3>::MIN_SPAN;
   return n < most ? int(n) : most;
 }
@@ -979,6 +994,7 @@ static int launch(Args a, const void* k, const void* v, int dev, cudaStream_t s)
   a.by_page = kv::Div(a.page);
   a.by_heads = kv::Div(heads);
   a.by_hc = kv::Div(a.HC);
+  a.by_most = kv::Div(most_of(heads));
   if (!vector_map(&tm_k, k, D, E4M3, rows, a.box) || !vector_map(&tm_v, v, D, E4M3, rows, a.box) ||
       !vector_map(&tm_q, a.qkv, D, false, int64_t(a.R) * (a.Hq + 2 * a.Hkv), HEADS))
     return MOT_ERR_CUDA;
