@@ -41,7 +41,7 @@
 // itself 157 and 294 us; producers 111 and 219; joiners, one warp a head in narrow joins, spans of
 // 512 110 and 130; queries by the joiners, two heads a joiner 107 and 118; the L2 policy 103 and 116;
 // K Q^T 103 and 115; maxima exchanged only when a reference moves 102 and 113 (6.2 and 5.4 TB/s). One e4m3
-// row of 131072 keys takes 28 us (floor 20), one bf16 row of 500 7. A KV head's query heads beyond 8 are
+// row of 131072 keys takes 27 us (floor 20), one bf16 row of 500 7. A KV head's query heads beyond 8 are
 // items of their own, which read the tiles again through L2: 64 rows of up to 4096 keys of 2 KV heads take
 // 35 and 23 us with 8 heads each, 50 and 37 with 16; items of 16 heads took 41 and 34 there, but 9.6 us
 // instead of 6.9 on one row of 500 and up to 13 % more on 12 to 40 rows. The e4m3 cache is bound by its consumers' instructions: 128 conversions and 32 products a
@@ -213,7 +213,7 @@ __device__ __forceinline__ uint64_t policy_evict_normal() {
 // ---------------------------------------------------------------------------
 // items
 // ---------------------------------------------------------------------------
-struct Item {
+struct alignas(16) Item {
   int row, g, hc, split;
   int t0, t1;    // keys [t0, t1) of the row
   int split_up;  // the row has more than one range
@@ -726,19 +726,25 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int off = 4; off <= 16; off <<= 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) tmax[h] = fmaxf(tmax[h], __shfl_xor_sync(0xffffffffu, tmax[h], off));
-        float alpha[2];
+        if (tile == m.t0 + warp * TOK) {
+          // the item's first tile: nothing to scale yet
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bool moves = tmax[h] > __fadd_rn(ref[h], kAbove);
-          const float next = moves ? __fsub_rn(tmax[h], kBelow) : ref[h];
-          alpha[h] = moves ? (ref[h] == -INFINITY ? 0.0f : exp2f(__fsub_rn(ref[h], next))) : 1.0f;
-          ref[h] = next;
-          sum[h] = __fmul_rn(sum[h], alpha[h]);
+          for (int h = 0; h < 2; ++h) ref[h] = __fsub_rn(tmax[h], kBelow);
+        } else {
+          float alpha[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const bool moves = tmax[h] > __fadd_rn(ref[h], kAbove);
+            const float next = moves ? __fsub_rn(tmax[h], kBelow) : ref[h];
+            alpha[h] = moves ? (ref[h] == -INFINITY ? 0.0f : exp2f(__fsub_rn(ref[h], next))) : 1.0f;
+            ref[h] = next;
+            sum[h] = __fmul_rn(sum[h], alpha[h]);
+          }
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[i][k] = __fmul_rn(o[i][k], alpha[k & 1]);
         }
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[i][k] = __fmul_rn(o[i][k], alpha[k & 1]);
       }
       // no key with a weight yet: every x is -inf
       const float nref[2] = {ref[0] == -INFINITY ? 0.0f : -ref[0], ref[1] == -INFINITY ? 0.0f : -ref[1]};
@@ -835,12 +841,22 @@ __global__ void __launch_bounds__(THREADS, 1)
 // Joins the ranges of a (row, head): out = (sum of f_s O_s) / (sum of f_s l_s), f_s the factor of range s
 // under the largest reference. The order is fixed: the f l of 32 ranges at a time by a butterfly, these
 // sums in order; the f O of the ranges s, s + 8, ... in order from zero, then the eight sums in order.
-// Rows of up to NARROW ranges are a warp's work for each 64 dims (kWide false: the eight sums in its
-// registers); where a row may have more, a CTA takes a (row, head) and a warp each sum, with the same bits.
-// Rows of one range were written by decode_kernel. A CTA a (row, head) in every case spent 23 us on 7168
-// heads of 9 ranges, most of it on starting CTAs.
-constexpr int NARROW = 32;
+// Two forms with the same bits: a warp for each 64 dims of a (row, head), the eight sums in its registers, or
+// (kWide) a CTA a (row, head) and a warp each sum, which reads all ranges at once but starts more threads.
+// Rows of one range were written by decode_kernel.
 constexpr int NARROW_WARPS = 4;
+constexpr int MOST_WIDE = 256;  // ranges that the wide form can take
+
+// Which form: the wide one pays while its CTAs are few for the ranges that there are to read one after the
+// other. Wide against narrow: a bf16 row of 20000 keys over 8 KV heads twice (19 ranges at most, 64 heads) 29.5
+// against 31.6 us, 20 e4m3 rows of up to 14000 (28, 560) 39.6 and 43.4, 16 of up to 8000 (16, 448) 19.0 and 20.5,
+// 42 of these (16, 1176) 40.8 and 40.6, 40 of up to 5000 (10, 1120) 28.4 and 27.5, 33 of up to 1500 (3, 132)
+// 8.0 and 7.5. Tables are often wider than their rows, so more than 16 ranges move the border no further: 64
+// e4m3 rows of up to 700 with a table for 131072 (38, 1792) take 17.5 us with the wide form and 16.0 with the
+// narrow one.
+inline bool wide_join(int64_t heads, int max_split, int sms) {
+  return max_split > 4 && heads <= int64_t(sms) * (max_split < 16 ? max_split : 16) / 2;
+}
 
 // L consecutive floats of a range's vector, zeros for a range that does not exist.
 template <int L>
@@ -859,7 +875,7 @@ __device__ __forceinline__ void load_part(float (&v)[L], const float* src, bool 
 }
 
 template <int D, bool E4M3, bool kWide>
-__global__ void __launch_bounds__(kWide ? 256 : 32 * NARROW_WARPS) join_kernel(const Args a) {
+__global__ void __launch_bounds__(kWide ? MOST_WIDE : 32 * NARROW_WARPS) join_kernel(const Args a) {
   constexpr int L = kWide ? D / 32 : 2;               // dims of a lane
   constexpr int PER = kWide ? 1 : D / 64;             // warps of a (row, head)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -879,22 +895,40 @@ __global__ void __launch_bounds__(kWide ? 256 : 32 * NARROW_WARPS) join_kernel(c
   if (len > 0 && len <= int64_t(a.max_pages) * a.page) n = ranges_of<Cfg<D, E4M3>>(a, len, span);
   if (n <= 1) return;
   if (mine >= n) ml = make_float2(-INFINITY, 0.0f);
+  // O of NV ranges at a time; kWide: of the ranges warp, warp + 8, ..., the first on their way while the factors
+  // are made (one bf16 row of 32768 keys 18.0 -> 16.3 us, with 4 at a time 16.9; the narrow form gains nothing)
+  constexpr int NV = 8;
+  const int64_t step = int64_t(a.Hq) * D;
+  const float* base = a.part + at0 * D + (kWide ? 0 : 64 * (unit - rh * PER)) + L * lane;
+  float v[NV][L];
+  if constexpr (kWide) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) load_part(v[k], base + (warp + 8 * k) * step, warp + 8 * k < n);
+  }
   float top = ml.x;
+  if constexpr (!kWide)
+    for (int s = lane + 32; s < n; s += 32) top = fmaxf(top, __ldcg(a.ml + at0 + int64_t(s) * a.Hq).x);
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  __shared__ float s_top[8], s_total[8], s_f[kWide ? 256 : 1];
+  __shared__ float s_top[8], s_total[8], s_f[kWide ? MOST_WIDE : 1];
   if constexpr (kWide) {
     if (lane == 0) s_top[warp] = top;
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 8; ++k) top = fmaxf(top, s_top[k]);
   }
-  // a range without a weight has -inf here, and a sum of zero (or NaN: kept)
-  const bool none = ml.x == -INFINITY;
-  const float f = none ? 0.0f : exp2f(__fsub_rn(ml.x, top));
-  float total = none ? ml.y : __fmul_rn(ml.y, f);
+  // the factor of this thread's range and 32 ranges' sum; a range without a weight has -inf here, and a sum of
+  // zero (or NaN: kept)
+  float f, total;
+  auto factor = [&]() {
+    const bool none = ml.x == -INFINITY;
+    f = none ? 0.0f : exp2f(__fsub_rn(ml.x, top));
+    float sum = none ? ml.y : __fmul_rn(ml.y, f);
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) total = __fadd_rn(total, __shfl_xor_sync(0xffffffffu, total, off));
+    for (int off = 16; off >= 1; off >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, off));
+    return sum;
+  };
+  total = factor();
   if constexpr (kWide) {
     s_f[threadIdx.x] = f;
     if (lane == 0) s_total[warp] = total;
@@ -902,22 +936,19 @@ __global__ void __launch_bounds__(kWide ? 256 : 32 * NARROW_WARPS) join_kernel(c
     total = s_total[0];
 #pragma unroll
     for (int k = 1; k < 8; ++k) total = __fadd_rn(total, s_total[k]);
-  }
-  const float r = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
-  const int64_t step = int64_t(a.Hq) * D;
-  const float* base = a.part + at0 * D + (kWide ? 0 : 64 * (unit - rh * PER)) + L * lane;
-  if constexpr (kWide) {
+    const float r = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
     __shared__ float s_acc[8][D];
     float acc[L];
 #pragma unroll
     for (int e = 0; e < L; ++e) acc[e] = 0.0f;
 #pragma unroll 1
-    for (int s0 = warp; s0 < n; s0 += 32) {
-      float v[4][L];
+    for (int s0 = warp; s0 < n; s0 += 8 * NV) {
+      if (s0 != warp) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) load_part(v[u], base + (s0 + 8 * u) * step, s0 + 8 * u < n);
+        for (int u = 0; u < NV; ++u) load_part(v[u], base + (s0 + 8 * u) * step, s0 + 8 * u < n);
+      }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < NV; ++u) {
         const float fs = s_f[s0 + 8 * u];  // zero behind the last range
 #pragma unroll
         for (int e = 0; e < L; ++e) acc[e] = __fadd_rn(acc[e], __fmul_rn(v[u][e], fs));
@@ -940,12 +971,15 @@ __global__ void __launch_bounds__(kWide ? 256 : 32 * NARROW_WARPS) join_kernel(c
       for (int e = 0; e < L; ++e) acc[k][e] = 0.0f;
 #pragma unroll 1
     for (int s0 = 0; s0 < n; s0 += 8) {
-      float v[8][L];
+      if (s0 > 0 && s0 % 32 == 0) {
+        ml = s0 + lane < n ? __ldcg(a.ml + at0 + int64_t(s0 + lane) * a.Hq) : make_float2(-INFINITY, 0.0f);
+        total = __fadd_rn(total, factor());
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) load_part(v[k], base + (s0 + k) * step, s0 + k < n);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float fs = __shfl_sync(0xffffffffu, f, s0 + k);
+        const float fs = __shfl_sync(0xffffffffu, f, (s0 + k) % 32);
 #pragma unroll
         for (int e = 0; e < L; ++e) acc[k][e] = __fadd_rn(acc[k][e], __fmul_rn(v[k][e], fs));
       }
@@ -954,6 +988,7 @@ __global__ void __launch_bounds__(kWide ? 256 : 32 * NARROW_WARPS) join_kernel(c
     for (int k = 1; k < 8; ++k)
 #pragma unroll
       for (int e = 0; e < L; ++e) acc[0][e] = __fadd_rn(acc[0][e], acc[k][e]);
+    const float r = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
     reinterpret_cast<uint32_t*>(a.out + int64_t(rh) * D)[32 * (unit - rh * PER) + lane] =
         pack_bf2(__fmul_rn(acc[0][0], r), __fmul_rn(acc[0][1], r));
   }
@@ -962,6 +997,7 @@ __global__ void __launch_bounds__(kWide ? 256 : 32 * NARROW_WARPS) join_kernel(c
 // Ranges that a row can have when its table holds max_len keys.
 template <int D, bool E4M3>
 inline int max_split(int64_t max_len, int heads) {
+  static_assert(SPLIT_ITEMS <= MOST_WIDE, "a thread of the wide join for each range");
   const int most = most_of(heads);
   const int64_t n = (max_len + Cfg<D, E4M3>::MIN_SPAN - 1) / Cfg<D, E4M3>::MIN_SPAN;
   return n < most ? int(n) : most;
@@ -1016,8 +1052,8 @@ static int launch(Args a, const void* k, const void* v, int dev, cudaStream_t s)
   if (a.max_split > 1) {
     const int64_t heads_total = int64_t(a.R) * a.Hq, warps = heads_total * (D / 64);
     const cudaError_t e =
-        a.max_split > NARROW
-            ? launch_dependent(join_kernel<D, E4M3, true>, dim3(unsigned(heads_total)), dim3(256), 0, s, a)
+        wide_join(heads_total, a.max_split, sm_count(dev))
+            ? launch_dependent(join_kernel<D, E4M3, true>, dim3(unsigned(heads_total)), dim3(MOST_WIDE), 0, s, a)
             : launch_dependent(join_kernel<D, E4M3, false>, dim3(unsigned((warps + NARROW_WARPS - 1) / NARROW_WARPS)),
                                dim3(32 * NARROW_WARPS), 0, s, a);
     if (e != cudaSuccess) return MOT_ERR_CUDA;

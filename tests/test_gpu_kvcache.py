@@ -525,13 +525,19 @@ def test_decode_many_rows(kv):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
-def test_decode_row_bits_do_not_depend_on_the_table_width(kv):
-    # a table that could hold a row of more than 32 ranges takes the other form of the join
-    b = Batch([6000, 300, 13000], 7, 1, 128, kv, 16, seed=111)
+def test_decode_row_bits_do_not_depend_on_the_table_width_or_the_join(kv):
+    # few rows take one form of the join, many the other (also with more than 32 ranges); so do narrow tables
+    b = Batch([6000, 300, 40000, 1500], 7, 1, 128, kv, 16, seed=111)
     want = b.run()
-    b.table = torch.cat([b.table, torch.full((3, 2000), -1, dtype=torch.int32, device=DEV)], 1).contiguous()
+    b.check(want, b.golden(), "few rows")
+    rows = [0, 1, 2, 3] * 90
+    assert_bitwise(b.run(rows), want[torch.tensor(rows, device=DEV)], "many rows")
+    short = b.table
+    b.table = torch.cat([b.table, torch.full((4, 3000), -1, dtype=torch.int32, device=DEV)], 1).contiguous()
     assert_bitwise(b.run(), want, "wide table")
-    b.check(want, b.golden(), "two forms of the join")
+    assert_bitwise(b.run(rows), want[torch.tensor(rows, device=DEV)], "wide table, many rows")
+    b.table = short[:, : 1500 // 16 + 1].contiguous()
+    assert_bitwise(b.run([3, 1]), want[[3, 1]], "narrow table")
 
 
 def test_parts_of_longer_index_arrays():
