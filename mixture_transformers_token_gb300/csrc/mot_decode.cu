@@ -40,12 +40,15 @@
 // to 4096 (28 / 4 heads of 128; floors 93 and 90 us at the copy's rate): every warp walking and copying for
 // itself 157 and 294 us; producers 111 and 219; joiners, one warp a head in narrow joins, spans of
 // 512 110 and 130; queries by the joiners, two heads a joiner 107 and 118; the L2 policy 103 and 116;
-// K Q^T 103 and 115; maxima exchanged only when a reference moves 102 and 113 (6.2 and 5.4 TB/s). One e4m3
+// K Q^T 103 and 115; maxima exchanged only when a reference moves 103 and 114; a walk that loads its lengths
+// at once and a join whose loads do not wait for one another 102 and 109 (6.2 and 5.6 TB/s). One e4m3
 // row of 131072 keys takes 27 us (floor 20), one bf16 row of 500 7. A KV head's query heads beyond 8 are
 // items of their own, which read the tiles again through L2: 64 rows of up to 4096 keys of 2 KV heads take
 // 35 and 23 us with 8 heads each, 50 and 37 with 16; items of 16 heads took 41 and 34 there, but 9.6 us
-// instead of 6.9 on one row of 500 and up to 13 % more on 12 to 40 rows. The e4m3 cache is bound by its consumers' instructions: 128 conversions and 32 products a
-// tile that brings 8 KB.
+// instead of 6.9 on one row of 500 and up to 13 % more on 12 to 40 rows. What is above the floors now: the
+// start (lengths, page table, first tiles one after the other: 3 us), the join (2 us, 5 on 256 rows) and the last
+// CTAs' rest. With the products and weights left out, the 256 e4m3 rows take 3 us less and the 64 bf16 rows
+// the same; only rows of one or two tiles a warp wait for arithmetic (256 e4m3 rows of up to 300: 21 us, floor 9).
 
 #include <cuda.h>
 #include <cuda_runtime.h>
