@@ -92,10 +92,12 @@ struct Cfg {
   static constexpr uint32_t DESC = ZERO + HEADS * D * 4;              // [ITEMS] Item
   static constexpr uint32_t ML = DESC + ITEMS * 32;                   // [2][2][WARPS][HEADS] float
   static constexpr uint32_t QC = ML + 4 * WARPS * HEADS * 4;          // [ITEMS][HEADS] float: c over the query's scale
-  static constexpr uint32_t SLOT = QC + ITEMS * HEADS * 4;        // [2][WARPS] the slot that holds a warp's O
-  static constexpr uint32_t ROWS = SLOT + 2 * WARPS * 4;                  // [PRODUCERS][3][WINDOW]: items up to a row, its length, span
-  static constexpr uint32_t BARS = ROWS + PRODUCERS * 3 * WINDOW * 4;             // full, empty [WARPS][STAGES] each
-  static constexpr uint32_t IBARS = BARS + 2 * WARPS * STAGES * 8;    // full, empty, qready [ITEMS] each, jfull, jread [2] each
+  static constexpr uint32_t SLOT = QC + ITEMS * HEADS * 4;            // [2][WARPS] the slot that holds a warp's O
+  // [PRODUCERS][3][WINDOW]: items up to a row, its length, its span
+  static constexpr uint32_t ROWS = SLOT + 2 * WARPS * 4;
+  static constexpr uint32_t BARS = ROWS + PRODUCERS * 3 * WINDOW * 4; // full, empty [WARPS][STAGES] each
+  // full, empty, qready [ITEMS] each, jfull, jread [2] each
+  static constexpr uint32_t IBARS = BARS + 2 * WARPS * STAGES * 8;
   static constexpr uint32_t ABORT = IBARS + (3 * ITEMS + 4) * 8;
   static constexpr size_t BYTES = 1024 + size_t(ABORT) + 16;
   static_assert(HEADS * D * 4 <= KT, "a warp's O fits into a tile's K");
