@@ -374,7 +374,9 @@ size_t mot_paged_decode_workspace_bytes(int64_t R, int Hq, int Hkv, int D, int m
  * (MOT_KV_E4M3: 11); out = bf16(O / sum). A row's keys are cut into ranges at borders that its own
  * length and the head geometry alone set, and the ranges are joined in a fixed order, so a row's bits
  * depend neither on the other rows nor on where its pages lie. scales may be any
- * numbers from 2^-64 to 2^126 (MOT_KV_E4M3; NaN makes what its head sees NaN).
+ * numbers from 2^-64 to 2^126 (MOT_KV_E4M3; NaN makes what its head sees NaN), however far apart: every key
+ * keeps its part of the weights' sum. A product of a weight and v's scale below 2^-30 of the head's largest may
+ * count as zero. V scales of 2^17 and more make their row take up to five times as long.
  * Rows of one sequence (several new tokens) are several rows with equal page tables and their own
  * lengths. The call's tensors do not overlap; calls that may run at the same time (other streams, graphs)
  * have workspaces of their own. Geometry: 1 <= R <= MOT_MAX_TOKENS, R * (Hq + 2 Hkv) < 2^31, max_pages >= 1,

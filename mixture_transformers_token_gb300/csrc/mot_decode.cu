@@ -26,7 +26,11 @@
 // e4m3 cache: codes become halves (exact), the query too, scaled by a power of two that takes its largest
 // element into [2^14, 2^15) (exact but for elements below 2^-24 of it), and a weight is a half. A token's
 // V scale belongs into its weight, so the reference follows x + log2(scale): the halves' range is then
-// spent on what the products contribute, however the scales differ.
+// spent on what the products contribute, however the scales differ. The sums take the same exponential over
+// the scale. That is in range while the scales are 2^-64 to 2^17: a key whose score leads, with the smallest
+// scale (a zero vector has it) beside the largest, is at 2^-80 of the largest product. Beside a scale of 2^17
+// and more it could fall below fp32's range and out of the sum, so a warp that has met one takes its sums from
+// the scores alone, in a second pass over its keys (loud_sums).
 //
 // What bounds it: HBM. A key costs 4 G flop per 4 bytes, far below the tensor cores' rate even on
 // mma.sync (tcgen05's smallest M is 64 rows; here there are 8 heads, and a tile's 16 to 32 keys), so the
@@ -73,6 +77,7 @@ constexpr int WINDOW = 256;               // rows whose item counts the producer
 constexpr int HEADS = 8;      // query heads of an item
 constexpr int SPLIT_ITEMS = 152;  // items that one row is cut into, at most: one for each SM
 constexpr float kAbove = 14.0f, kBelow = 6.0f;  // the reference's slack, powers of two
+constexpr float kLoud = 0x1p-17f;  // one over the V scales from which on loud_sums has the sums
 
 template <int D, bool E4M3>
 struct Cfg {
@@ -108,6 +113,7 @@ struct Args {
   const int32_t* table;  // [R][max_pages]
   const int32_t* lens;   // [R]
   const float* scales;
+  const uint8_t* k;      // K as the copies take it
   int64_t n_pages;
   int R, max_pages, page;
   int Hq, Hkv, G;        // G = Hq / Hkv
@@ -316,10 +322,91 @@ __device__ __forceinline__ uint32_t chunk(int r, int c) {
   return uint32_t(((r >> 4) * C::HALVES + (c >> 3)) * 2048 + (r & 15) * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
+// The sums of a warp's weights in an item of an e4m3 cache from the scores alone: for each head the sum of
+// 2^score. A lane takes a tile's key; K comes from memory again, the queries (halves, [half][8 heads][128 bytes],
+// swizzled) and their factors from shared memory. refs, sums and o (the warp's references, sums and O, [HEADS][D])
+// become e, the sum over 2^e, in [1/2, 1), and O under 2^e: then O is the warp's own output times that number, so in
+// range wherever the values are. It is code beside the loop, for values that no model has, because there a second
+// exponential a weight, or a vote a tile, cost every row time (256 rows of up to 4096 keys 113.3 or 111.4 instead of
+// 109.9 us, 256 of up to 300 23.4 or 22.2 instead of 20.6); beside it these take 110.2 and 21.2. Loud rows take up to
+// five times theirs (568 us a call instead of 121; 6.1 us a round of 256 keys, so 0.4 s a range of 2^24 keys).
+template <int D>
+__device__ __noinline__ void loud_sums(const Args& a, int row, int g, int t0, int t1, const uint8_t* q,
+                                       const float* qc, float* refs, float* sums, float* o) {
+  using C = Cfg<D, true>;
+  static_assert(C::TOK == 32, "a lane for each key of a tile");
+  const int lane = threadIdx.x & 31;
+  float top[HEADS], sum[HEADS];  // a lane's references, moved as the tiles' are, and sums
+#pragma unroll
+  for (int h = 0; h < HEADS; ++h) {
+    top[h] = -INFINITY;
+    sum[h] = 0.0f;
+  }
+#pragma unroll 1
+  for (int key = t0 + lane; key < t1; key += C::ROUND) {
+    const int nth = a.by_page.of(key), at = key - nth * a.page;
+    int page = a.table[int64_t(row) * a.max_pages + nth];
+    if (page < 0 || page >= a.n_pages) page = 0;  // reported where it was copied
+    const int64_t y = (int64_t(page) * a.Hkv + g) * a.page + at;
+    const float scale = a.scales[2 * y];
+    const uint2* codes = reinterpret_cast<const uint2*>(a.k + y * D);
+    uint2 u = codes[0];
+    float x[HEADS] = {};
+#pragma unroll 1
+    for (int c = 0; c < D / 8; ++c) {
+      const float2 k[4] = {kv::h2_to_f2(kv::e4m3x2_to_h2(u.x & 0xFFFFu)), kv::h2_to_f2(kv::e4m3x2_to_h2(u.x >> 16)),
+                           kv::h2_to_f2(kv::e4m3x2_to_h2(u.y & 0xFFFFu)), kv::h2_to_f2(kv::e4m3x2_to_h2(u.y >> 16))};
+      if (c + 1 < D / 8) u = codes[c + 1];
+#pragma unroll
+      for (int h = 0; h < HEADS; ++h) {
+        const uint4 w = *reinterpret_cast<const uint4*>(q + (c >> 3) * 1024 + h * 128 + (((c & 7) ^ h) << 4));
+        const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = kv::h2_to_f2(e[i]);  // a half times a code is exact: one rounding an addition
+          x[h] = __fmaf_rn(k[i].y, f.y, __fmaf_rn(k[i].x, f.x, x[h]));
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < HEADS; ++h) {
+      const float s = __fmul_rn(__fmul_rn(x[h], qc[h]), scale);
+      if (s > __fadd_rn(top[h], kAbove)) {
+        const float next = __fsub_rn(s, kBelow);
+        sum[h] = __fmul_rn(sum[h], top[h] == -INFINITY ? 0.0f : exp2f(__fsub_rn(top[h], next)));
+        top[h] = next;
+      }
+      sum[h] = __fadd_rn(sum[h], exp2f(top[h] == -INFINITY ? s : __fsub_rn(s, top[h])));
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int h = 0; h < HEADS; ++h) {
+    float t = top[h];
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
+    float v = top[h] == -INFINITY ? sum[h] : __fmul_rn(sum[h], exp2f(__fsub_rn(top[h], t)));
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));
+    const uint32_t u = __float_as_uint(v);
+    const float e = __fadd_rn(t, __fsub_rn(__uint_as_float((u >> 23) | 0x4B000000u), 8388734.0f));  // 2^23 + 126
+    // O 2^(its reference - e), as a root twice: the power may lie outside fp32's range
+    const float ref = refs[h];
+    const float root = ref == -INFINITY || t == -INFINITY ? 0.0f : exp2f(__fmul_rn(0.5f, __fsub_rn(ref, e)));
+#pragma unroll
+    for (int d = 0; d < D; d += 32) o[h * D + d + lane] = __fmul_rn(__fmul_rn(o[h * D + d + lane], root), root);
+    __syncwarp();
+    if (lane == 0) {
+      refs[h] = e;
+      sums[h] = __fmul_rn(v, __uint_as_float(0x7E800000u - (u & 0x7F800000u)));
+    }
+  }
+}
+
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(THREADS, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const __grid_constant__ CUtensorMap tm_q, const Args a) {
+                  const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ Args a) {
   using C = Cfg<D, E4M3>;
   constexpr int TOK = C::TOK, NB = TOK / 16, KS = D / 16, STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -544,6 +631,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int o = 4; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       // a warp without tiles has -inf here, and zeros; one whose scores are all -inf (or NaN) a sum of zero (or NaN)
+      // (2^-3: the O of eight warps then add up to less than the largest, see loud_sums)
+      if constexpr (E4M3) top = __fadd_rn(top, 3.0f);
       const bool none = ref == -INFINITY;
       const float f = none ? 0.0f : exp2f(__fsub_rn(ref, top));
       float total = none ? sum : __fmul_rn(sum, f);
@@ -647,6 +736,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
     float ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f};  // of heads 2 t4 and 2 t4 + 1
+    float quiet = 1.0f;  // e4m3: the smallest of one over this lane's keys' V scales
     int slot = -1;  // the slot of the item's last tile, held back: O passes through it
 
     for (int tile = m.t0 + warp * TOK; tile < m.t1; tile += C::ROUND) {
@@ -719,8 +809,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           if (nv < TOK && key >= nv) {
             x[b][2 * i] = x[b][2 * i + 1] = -INFINITY;
-            if constexpr (E4M3) inv[b][i] = fac[b][i] = 0.0f;  // whatever the scale's place holds
+            if constexpr (E4M3) {
+              inv[b][i] = 1.0f;  // whatever the scale's place holds
+              fac[b][i] = 0.0f;
+            }
           }
+          if constexpr (E4M3) quiet = fminf(quiet, inv[b][i]);
 #pragma unroll
           for (int h = 0; h < 2; ++h) tmax[h] = fmaxf(tmax[h], x[b][2 * i + h]);
         }
@@ -833,6 +927,14 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
     }
+    if constexpr (E4M3) {
+      if (__builtin_expect(__any_sync(0xffffffffu, quiet <= kLoud), 0)) {
+        const int at = (par * WARPS + warp) * HEADS;
+        __syncwarp();
+        loud_sums<D>(a, m.row, m.g, m.t0 + warp * TOK, m.t1, smem + C::Q + is * HEADS * D * 2, s_qc + is * HEADS,
+                     s_ref + at, s_sum + at, reinterpret_cast<float*>(ring + slot * 2 * C::KT));
+      }
+    }
     if (lane == 0) s_slot[par * WARPS + warp] = slot;
     fence_proxy_async_smem();  // the slot goes back to the copies through the joiners
     __syncwarp();
@@ -844,8 +946,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // Joins the ranges of a (row, head): out = (sum of f_s O_s) / (sum of f_s l_s), f_s the factor of range s
-// under the largest reference. The order is fixed: the f l of 32 ranges at a time by a butterfly, these
-// sums in order; the f O of the ranges s, s + 8, ... in order from zero, then the eight sums in order.
+// under the largest reference, times 2^-9: less than 2^8 ranges' O then add up to less than the largest, which
+// may be at the end of fp32's range (loud V scales). The order is fixed: the f l of 32 ranges at a time by a
+// butterfly, these sums in order; the f O of the ranges s, s + 8, ... in order from zero, then the eight sums in
+// order.
 // Two forms with the same bits: a warp for each 64 dims of a (row, head), the eight sums in its registers, or
 // (kWide) a CTA a (row, head) and a warp each sum, which reads all ranges at once but starts more threads.
 // Rows of one range were written by decode_kernel.
@@ -922,6 +1026,8 @@ __global__ void __launch_bounds__(kWide ? MOST_WIDE : 32 * NARROW_WARPS) join_ke
 #pragma unroll
     for (int k = 0; k < 8; ++k) top = fmaxf(top, s_top[k]);
   }
+  static_assert(MOST_WIDE <= 256, "the factors' sum");
+  top = __fadd_rn(top, 9.0f);
   // the factor of this thread's range and 32 ranges' sum; a range without a weight has -inf here, and a sum of
   // zero (or NaN: kept)
   float f, total;
@@ -1111,6 +1217,7 @@ extern "C" int mot_paged_decode_attention(const mot_bf16* qkv, int64_t R, int Hq
   a.table = table;
   a.lens = lens;
   a.scales = scales;
+  a.k = static_cast<const uint8_t*>(k_cache);
   a.n_pages = n_pages;
   a.R = int(R);
   a.max_pages = max_pages;

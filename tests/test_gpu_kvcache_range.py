@@ -1,0 +1,101 @@
+"""The paged key-value cache at the ends of its number ranges, through the C ABI.
+
+Decoded outputs are compared with the fp64 golden under the bound of test_gpu_kvcache, whose terms count each
+rounding, plus 2^-16 of sum p|v|: a weight's exponent here is up to 2^8 in magnitude (score and scale), so its
+fp32 sums round by up to 2^-17 each, twice.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_transformers_token_gb300 as mot
+
+from _util import f64, need_gpu
+from test_gpu_kvcache import DEV, E4M3, Batch, _bound, _ws
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def _rewrite(b):
+    """Writes the rows b.x into the batch's cache again."""
+    tab = b.table.cpu().numpy()
+    for r, x in enumerate(b.x):
+        if len(x):
+            j = np.arange(len(x))
+            slots = (tab[r, j // b.page].astype(np.int64) * b.page + j % b.page).astype(np.int32)
+            mot.mot_kv_cache_write(x.to(DEV), torch.from_numpy(slots).to(DEV), b.k, b.v, b.Hq, _ws(), scales=b.scales)
+
+
+def _check(b, what):
+    out = b.run()
+    g = b.golden()
+    got = f64(out).reshape(g["out_pre"].shape)
+    d = np.abs(got - g["out_pre"])
+    bound = _bound(g, b.lens, b.D, b.kv) + 2.0 ** -16 * g["p_abs_v"]
+    assert np.isfinite(got).all(), f"{what}: {np.argwhere(~np.isfinite(got))[:5]}"
+    assert np.all(d <= bound), f"{what}: {np.argwhere(d > bound)[:5]} worst {np.max(d / bound):.3g} of the bound"
+    return out
+
+
+# keys of a row, the loud key's place: one tile, another warp of the item, another range of the row
+PLACES = [(2, 0), (2, 1), (64, 40), (300, 0), (1500, 5), (1500, 1499), (20000, 9000)]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,at", PLACES)
+@pytest.mark.parametrize("top", [60, 90, 104, 119])
+def test_one_loud_value_among_quiet_ones_keeps_the_others_in_the_sum(kv, n, at, top):
+    # equal scores: the output is the mean of the values, whatever their scales; the quiet values are zeros (the
+    # smallest scale there is) or of unit size
+    D = 128 if top % 2 else 64
+    Hq, Hkv = (20, 2) if n == 300 else (2, 1)
+    for zeros in (True, False):
+        b = Batch([n, 3], Hq, Hkv, D, kv, 16, seed=n + top, q_gain=0.0)
+        x = b.x[0].float()
+        v = x[:, (Hq + Hkv) * D:]
+        if zeros:
+            v[:] = 0.0
+        v[at] = 1.5 * 2.0 ** top * torch.where(torch.arange(Hkv * D) % 3 == 0, -1.0, 1.0)
+        b.x[0] = x.to(torch.bfloat16)
+        _rewrite(b)
+        _check(b, f"2^{top} at {at} of {n}, zeros {zeros}")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,at", PLACES)
+@pytest.mark.parametrize("lead", [10.0, 60.0, 95.0])
+def test_a_loud_value_whose_key_has_next_to_no_weight(kv, n, at, lead):
+    # the other keys lead by `lead` powers of two, and the loud value's share still outweighs theirs
+    Hq, Hkv, D = 2, 1, 128
+    b = Batch([n], Hq, Hkv, D, kv, 16, seed=n + int(lead))
+    x = b.x[0].float()
+    q = torch.zeros(D)
+    q[:64] = 1.0
+    b.q[:, : Hq * D] = torch.cat([q, q]).to(torch.bfloat16).to(DEV)
+    # scores: 64 k / sqrt(128) nats
+    x[:, Hq * D: (Hq + Hkv) * D] = 0.0
+    x[at, Hq * D: Hq * D + 64] = -lead * np.log(2.0) * np.sqrt(128.0) / 64
+    x[:, (Hq + Hkv) * D:] *= 2.0 ** -20
+    x[:, (Hq + Hkv) * D:][at] = 1.25 * 2.0 ** 118
+    b.x[0] = x.to(torch.bfloat16)
+    _rewrite(b)
+    _check(b, f"lead {lead} at {at} of {n}")
+
+
+@pytest.mark.parametrize("n,at", PLACES)
+def test_scales_at_both_ends_of_their_range(n, at):
+    # scales of 2^-64 beside one of 2^126, code 1, equal scores
+    Hq, Hkv, D, page = 3, 1, 64, 16
+    b = Batch([n], Hq, Hkv, D, "e4m3", page, seed=5, q_gain=0.0)
+    b.v.copy_(torch.ones(b.v.shape, device=DEV).to(E4M3))
+    b.scales[..., 1] = 2.0 ** -64
+    b.scales[int(b.table[0, at // page]), 0, at % page, 1] = 2.0 ** 126
+    want = 2.0 ** 126 / n   # + (n - 1) 2^-64 / n
+    got = f64(b.run())
+    assert np.all(np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16) * want), got[0, 0] / want
