@@ -375,8 +375,10 @@ size_t mot_paged_decode_workspace_bytes(int64_t R, int Hq, int Hkv, int D, int m
  * length and the head geometry alone set, and the ranges are joined in a fixed order, so a row's bits
  * depend neither on the other rows nor on where its pages lie. scales may be any
  * numbers from 2^-64 to 2^126 (MOT_KV_E4M3; NaN makes what its head sees NaN), however far apart: every key
- * keeps its part of the weights' sum. A product of a weight and v's scale below 2^-30 of the head's largest may
- * count as zero. V scales of 2^17 and more make their row take up to five times as long.
+ * keeps its part of the weights' sum. Outputs are finite wherever scores and values are. What that range costs
+ * at its other end: a product of a weight and v's scale below 2^-30 of the head's largest may count as zero
+ * (MOT_KV_E4M3); weights below 2^-86 of the largest, and values below 2^-85, lose bits (MOT_KV_BF16). V scales
+ * of 2^17 and more make their row take up to five times as long.
  * Rows of one sequence (several new tokens) are several rows with equal page tables and their own
  * lengths. The call's tensors do not overlap; calls that may run at the same time (other streams, graphs)
  * have workspaces of their own. Geometry: 1 <= R <= MOT_MAX_TOKENS, R * (Hq + 2 Hkv) < 2^31, max_pages >= 1,

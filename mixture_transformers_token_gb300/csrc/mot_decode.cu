@@ -16,13 +16,15 @@
 //
 // Arithmetic of an item (a key range of one KV head, up to 8 of its query heads): warp w of 8 takes
 // the range's tiles w, w + 8, ... of TOK keys. Per tile S^T = K Q^T with mma.sync (m16n8k16: 16 keys x
-// 8 heads), x = S c in powers of two, then w = 2^(x - ref) where a head's reference starts as the
-// tile's maximum less 6 and moves only when a tile's maximum exceeds it by more than 14 (so w <= 2^14,
-// and the largest w is at least 2^6); sums of w in fp32 per lane; O^T += V^T W^T (m16n8k16: 16 dims x 8
+// 8 heads), x = S c in powers of two, then w = 2^(x - ref) where a head's reference starts from the
+// tile's maximum and moves only when a tile's maximum is 2^8 above the one that set it (e4m3: the largest w is
+// at least 2^6, and w <= 2^14); sums of w in fp32 per lane; O^T += V^T W^T (m16n8k16: 16 dims x 8
 // heads), the weights turned by movmatrix. The 8 warps' (ref, sum, O) are joined in a fixed order, the
 // ranges' in a fixed order by join_kernel. Every fp32 operation is rounded on its own.
 // bf16 cache: w goes into the product as two bf16 (w and what its rounding leaves), so the weights
-// keep 16 bits: one bf16 each would put an error the size of the output's own rounding beside it.
+// keep 16 bits: one bf16 each would put an error the size of the output's own rounding beside it. Two bf16
+// have fp32's exponents, so w needs no headroom above the smallest: with n keys in the item w <= 2^-m, m the
+// smallest that has n <= 2^m. An item's weights then add up to at most 1, and O is finite wherever the values are.
 // e4m3 cache: codes become halves (exact), the query too, scaled by a power of two that takes its largest
 // element into [2^14, 2^15) (exact but for elements below 2^-24 of it), and a weight is a half. A token's
 // V scale belongs into its weight, so the reference follows x + log2(scale): the halves' range is then
@@ -76,7 +78,9 @@ constexpr int ITEMS = 4;                  // item descriptors in flight
 constexpr int WINDOW = 256;               // rows whose item counts the producer holds at a time
 constexpr int HEADS = 8;      // query heads of an item
 constexpr int SPLIT_ITEMS = 152;  // items that one row is cut into, at most: one for each SM
-constexpr float kAbove = 14.0f, kBelow = 6.0f;  // the reference's slack, powers of two
+// e4m3: the largest weight, and the largest weight of the tile that sets a reference, as powers of two. bf16: the
+// same distance, shifted (see `above` and `below`)
+constexpr float kAbove = 14.0f, kBelow = 6.0f;
 constexpr float kLoud = 0x1p-17f;  // one over the V scales from which on loud_sums has the sums
 
 template <int D, bool E4M3>
@@ -735,6 +739,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+    // a reference moves when a maximum is more than `above` over it, to `below` under that
+    const float above = E4M3 ? kAbove : -float(32 - __clz(m.t1 - m.t0 - 1));
+    const float below = above - (kAbove - kBelow);
     float ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f};  // of heads 2 t4 and 2 t4 + 1
     float quiet = 1.0f;  // e4m3: the smallest of one over this lane's keys' V scales
     int slot = -1;  // the slot of the item's last tile, held back: O passes through it
@@ -820,7 +827,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       // a head's tile maximum is above its reference's slack (also from -inf) if a lane's is: only then do the
       // lanes exchange them
-      if (__any_sync(0xffffffffu, tmax[0] > __fadd_rn(ref[0], kAbove) || tmax[1] > __fadd_rn(ref[1], kAbove))) {
+      if (__any_sync(0xffffffffu, tmax[0] > __fadd_rn(ref[0], above) || tmax[1] > __fadd_rn(ref[1], above))) {
 #pragma unroll
         for (int off = 4; off <= 16; off <<= 1)
 #pragma unroll
@@ -828,13 +835,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (tile == m.t0 + warp * TOK) {
           // the item's first tile: nothing to scale yet
 #pragma unroll
-          for (int h = 0; h < 2; ++h) ref[h] = __fsub_rn(tmax[h], kBelow);
+          for (int h = 0; h < 2; ++h) ref[h] = __fsub_rn(tmax[h], below);
         } else {
           float alpha[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const bool moves = tmax[h] > __fadd_rn(ref[h], kAbove);
-            const float next = moves ? __fsub_rn(tmax[h], kBelow) : ref[h];
+            const bool moves = tmax[h] > __fadd_rn(ref[h], above);
+            const float next = moves ? __fsub_rn(tmax[h], below) : ref[h];
             alpha[h] = moves ? (ref[h] == -INFINITY ? 0.0f : exp2f(__fsub_rn(ref[h], next))) : 1.0f;
             ref[h] = next;
             sum[h] = __fmul_rn(sum[h], alpha[h]);
@@ -947,7 +954,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // Joins the ranges of a (row, head): out = (sum of f_s O_s) / (sum of f_s l_s), f_s the factor of range s
 // under the largest reference, times 2^-9: less than 2^8 ranges' O then add up to less than the largest, which
-// may be at the end of fp32's range (loud V scales). The order is fixed: the f l of 32 ranges at a time by a
+// may be at the end of fp32's range. The order is fixed: the f l of 32 ranges at a time by a
 // butterfly, these sums in order; the f O of the ranges s, s + 8, ... in order from zero, then the eight sums in
 // order.
 // Two forms with the same bits: a warp for each 64 dims of a (row, head), the eight sums in its registers, or

@@ -16,6 +16,8 @@ from test_gpu_kvcache import DEV, E4M3, Batch, _bound, _ws
 
 pytestmark = pytest.mark.gpu
 
+BF16_MAX = float(torch.finfo(torch.bfloat16).max)
+
 
 @pytest.fixture(scope="module", autouse=True)
 def _gpu():
@@ -99,3 +101,24 @@ def test_scales_at_both_ends_of_their_range(n, at):
     want = 2.0 ** 126 / n   # + (n - 1) 2^-64 / n
     got = f64(b.run())
     assert np.all(np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16) * want), got[0, 0] / want
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 5, 64, 700, 3000, 20000])
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_of_the_types_largest_size_do_not_overflow(n, D, kv):
+    # an output is a mean of values: finite wherever they are. e4m3 holds 1.75 2^127 exactly, bf16 its largest value
+    Hq, Hkv = 3, 1
+    top = BF16_MAX if kv == "bf16" else 1.75 * 2.0 ** 127
+    for gain, rising in ((0.0, False), (1.0, False), (1.0, True)):
+        b = Batch([n, 2], Hq, Hkv, D, kv, 16, seed=n + D, q_gain=gain)
+        for r, x in enumerate(b.x):
+            x = x.float()
+            if rising:  # scores that rise with the keys, so that a reference lags behind and moves
+                q = b.q[r, :D].float().cpu()
+                x[:, Hq * D: (Hq + Hkv) * D] = q[None, :] * (torch.arange(len(x))[:, None] / len(x) * 4.0)
+            v = x[:, (Hq + Hkv) * D:]
+            v[:] = torch.where(torch.arange(D) % 3 == 0, -top, top)
+            b.x[r] = x.to(torch.bfloat16)
+        _rewrite(b)
+        _check(b, f"gain {gain}, rising {rising}")
