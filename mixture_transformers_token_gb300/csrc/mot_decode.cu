@@ -374,7 +374,7 @@ __device__ __noinline__ void loud_sums(const Args& a, int row, int g, int t0, in
     }
 #pragma unroll
     for (int h = 0; h < HEADS; ++h) {
-      const float s = __fmul_rn(__fmul_rn(x[h], qc[h]), scale);
+      const float s = __fmul_rn(x[h], __fmul_rn(qc[h], scale));
       if (s > __fadd_rn(top[h], kAbove)) {
         const float next = __fsub_rn(s, kBelow);
         sum[h] = __fmul_rn(sum[h], top[h] == -INFINITY ? 0.0f : exp2f(__fsub_rn(top[h], next)));
@@ -807,9 +807,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float ev = __fsub_rn(__uint_as_float((u >> 23) | 0x4B000000u), 8388735.0f);  // 2^23 + 127
             inv[b][i] = __uint_as_float(0x7F000000u - (u & 0x7F800000u));
             fac[b][i] = __fmul_rn(sc.y, inv[b][i]);  // NaN for a scale of NaN
+            // the two factors first: either may be near an end of fp32's range where the score is not
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              x[b][2 * i + h] = __fadd_rn(__fmul_rn(__fmul_rn(x[b][2 * i + h], c[h]), sc.x), ev);
+              x[b][2 * i + h] = __fadd_rn(__fmul_rn(x[b][2 * i + h], __fmul_rn(c[h], sc.x)), ev);
           } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) x[b][2 * i + h] = __fmul_rn(x[b][2 * i + h], c[h]);
@@ -821,10 +822,13 @@ __global__ void __launch_bounds__(THREADS, 1)
               fac[b][i] = 0.0f;
             }
           }
-          if constexpr (E4M3) quiet = fminf(quiet, inv[b][i]);
 #pragma unroll
           for (int h = 0; h < 2; ++h) tmax[h] = fmaxf(tmax[h], x[b][2 * i + h]);
         }
+      if constexpr (E4M3) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) quiet = fminf(quiet, fminf(inv[b][0], inv[b][1]));
+      }
       // a head's tile maximum is above its reference's slack (also from -inf) if a lane's is: only then do the
       // lanes exchange them
       if (__any_sync(0xffffffffu, tmax[0] > __fadd_rn(ref[0], above) || tmax[1] > __fadd_rn(ref[1], above))) {

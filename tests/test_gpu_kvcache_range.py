@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import mixture_transformers_token_gb300 as mot
+from oracle import mot_oracle as O
 
 from _util import f64, need_gpu
 from test_gpu_kvcache import DEV, E4M3, Batch, _bound, _ws
@@ -122,3 +123,43 @@ def test_values_of_the_types_largest_size_do_not_overflow(n, D, kv):
             b.x[r] = x.to(torch.bfloat16)
         _rewrite(b)
         _check(b, f"gain {gain}, rising {rising}")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("up,down", [(119, -58), (127, -60), (-126, 100)])
+def test_queries_and_keys_of_opposite_sizes(up, down, kv):
+    # every score is exact in fp32 and far below its end, although a factor of it may be near an end of the range.
+    # Large ones: the even keys share the row, the odd ones have nothing; tiny ones: every key has the same weight
+    Hq, Hkv, D = 4, 2, 128
+    b = Batch([70, 1200], Hq, Hkv, D, kv, 16, seed=200 + up)
+    sign = torch.where(torch.arange(D) % 5 == 0, -1.0, 1.0)
+    b.q[:, : Hq * D] = (sign.repeat(Hq) * 2.0 ** up).to(torch.bfloat16).to(DEV)
+    for r, x in enumerate(b.x):
+        x = x.float()
+        each = torch.where(torch.arange(len(x))[:, None] % 2 == 0, 1.0, 0.75) * 2.0 ** down
+        x[:, Hq * D: (Hq + Hkv) * D] = sign.repeat(Hkv)[None, :] * each
+        b.x[r] = x.to(torch.bfloat16)
+    _rewrite(b)
+    got = f64(b.run()).reshape(2, Hq, D)
+    for r, x in enumerate(b.x):
+        v = f64(x)[:, (Hq + Hkv) * D:].reshape(-1, Hkv, D)
+        if kv == "e4m3":
+            y, s = O.kv_quantise(v)
+            v = y * s[..., None]
+        if up > 0:
+            v = v[::2]
+        want, mean_abs = v.mean(0), np.abs(v).mean(0)
+        # the output's rounding; a weight's, and a handful of fp32 factors; the sums
+        bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -16 + 4 * len(v) * 2.0 ** -24) * mean_abs
+        # e4m3: the exponent of a weight is the score, here about 2^65 (or 2^71) with a spacing of 2^42, plus log2 of
+        # its V scale, at most 2^8: that sum rounds to the score, so that the keys' weights p differ by up to the ratio
+        # of their scales, which the bound's 2^-22 |s| = 2^43 covers. Both sums take the same p >= 0, so the output is
+        # some mean of the even keys' values: within their hull, a half's and a bf16's rounding aside
+        any_mean = kv == "e4m3" and up > 0
+        slack = (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16 + 4 * len(v) * 2.0 ** -24) * np.abs(v).max(0)
+        for h in range(Hq):
+            g, o = h // 2, got[r, h]
+            if any_mean:
+                assert np.all(o >= v.min(0)[g] - slack[g]) and np.all(o <= v.max(0)[g] + slack[g]), (r, h)
+            else:
+                assert np.all(np.abs(o - want[g]) <= bound[g]), (r, h)
