@@ -340,7 +340,9 @@ int mot_kv_cache_write(const mot_bf16* qkv, int64_t T, int Hq, int Hkv, int D, c
  *                                     the row is left as it is; other values outside the cache set
  *                                     MOT_DEV_BAD_PAGE and leave the row as it is.
  *   qkv    [T][(Hq + 2 Hkv) D] bf16   out: the K and V columns of the rows; the q columns are kept.
- * MOT_KV_BF16 copies; MOT_KV_E4M3 gives bf16(code * scale), exact within bf16's range.
+ * MOT_KV_BF16 copies; MOT_KV_E4M3 gives the product code * scale rounded once to bf16, which is exact for a
+ * scale that is a power of two (mot_kv_cache_write's are), but for the vectors whose largest magnitude is
+ * 1.9375 2^127 or more: their largest codes stand for 2^128 and read as infinities.
  */
 int mot_kv_cache_read(const void* k_cache, const void* v_cache, const float* scales, int kv_type, int64_t n_pages,
                       int page, const int32_t* slots, int64_t T, int Hq, int Hkv, int D, mot_bf16* qkv, void* ws,

@@ -10,10 +10,11 @@ import pytest
 import torch
 
 import mixture_transformers_token_gb300 as mot
+from mixture_transformers_token_gb300 import workloads as W
 from oracle import mot_oracle as O
 
 from _util import f64, need_gpu
-from test_gpu_kvcache import DEV, E4M3, Batch, _bound, _ws
+from test_gpu_kvcache import DEV, E4M3, Batch, _bound, _empty_cache, _ws
 
 pytestmark = pytest.mark.gpu
 
@@ -163,3 +164,35 @@ def test_queries_and_keys_of_opposite_sizes(up, down, kv):
                 assert np.all(o >= v.min(0)[g] - slack[g]) and np.all(o <= v.max(0)[g] + slack[g]), (r, h)
             else:
                 assert np.all(np.abs(o - want[g]) <= bound[g]), (r, h)
+
+
+def test_read_back_rounds_once_whatever_the_scale():
+    # code * scale has up to 28 bits: scales for which rounding it to fp32 and then to bf16 would differ from rounding
+    # it to bf16 at once, every code with each
+    Hkv, D, page = 1, 128, 16
+    r = W.rng_for(9, 609)
+    s = (r.integers(1 << 23, 1 << 24, 1 << 20).astype(np.float64) * 2.0 ** -23)
+    odd = []
+    for m in (9.0, 11.0, 13.0, 15.0):
+        twice = O.bf16((s * m).astype(np.float32).astype(np.float64))
+        odd.append(s[twice != O.bf16(s * m)])
+    odd = np.concatenate(odd)[:32]
+    assert len(odd) >= 8
+    scales = np.concatenate([odd * np.exp2(r.integers(-60, 100, len(odd))), np.exp2(r.uniform(-60, 100, 64 - len(odd)))])
+    scales = scales.astype(np.float32)
+    codes = np.arange(128, dtype=np.uint8)
+    codes[127] = 0x7E
+    codes = np.concatenate([codes, codes | 0x80])
+    k, v, sc = _empty_cache(64 // page, Hkv, page, D, "e4m3")
+    k.view(torch.uint8).copy_(torch.from_numpy(codes[:128]).to(DEV).expand(k.shape))
+    v.view(torch.uint8).copy_(torch.from_numpy(codes[128:]).to(DEV).expand(v.shape))
+    sc[..., 0] = torch.from_numpy(scales).to(DEV).reshape(sc.shape[:-1])
+    sc[..., 1] = torch.from_numpy(scales[::-1].copy()).to(DEV).reshape(sc.shape[:-1])
+    ws = _ws()
+    y = torch.zeros((64, 3 * D), dtype=torch.bfloat16, device=DEV)
+    mot.mot_kv_cache_read(k, v, torch.arange(64, dtype=torch.int32, device=DEV), y, 1, ws, scales=sc)
+    assert mot.mot_device_status(ws) == 0
+    vals = k.to(torch.float32).cpu().numpy()[0, 0, 0].astype(np.float64)
+    got = f64(y)
+    np.testing.assert_array_equal(got[:, D: 2 * D], O.bf16(vals[None, :] * scales.astype(np.float64)[:, None]))
+    np.testing.assert_array_equal(got[:, 2 * D:], O.bf16(-vals[None, :] * scales.astype(np.float64)[::-1, None]))
