@@ -404,7 +404,7 @@ def mot_joint_attention(qkv, seqs, Hq: int, Hkv: int, D: int, ws, scale: float |
 
 def _kv_cache(k_cache, v_cache, scales):
     """Checks a cache's tensors: (kv_type, n_pages, Hkv, page, D, the three pointers; no scales: None)."""
-    e4m3 = k_cache.dtype is torch.float8_e4m3fn
+    e4m3 = getattr(k_cache, "dtype", None) is torch.float8_e4m3fn  # _dev refuses what is no tensor
     dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
     kp = _dev(k_cache, "k_cache", dtype, 4)
     vp = _dev(v_cache, "v_cache", dtype, 4)
@@ -423,9 +423,9 @@ def _kv_cache(k_cache, v_cache, scales):
 
 
 def _kv_rows(qkv, slots, Hq: int, Hkv: int, D: int):
-    T, N = qkv.shape
     qp = _dev(qkv, "qkv", torch.bfloat16, 2)
     lp = _dev(slots, "slots", torch.int32, 1)
+    T, N = qkv.shape
     if N != (Hq + 2 * Hkv) * D or slots.shape[0] != T:
         raise ValueError(f"qkv must be [T, {(Hq + 2 * Hkv) * D}] and slots [T]")
     return T, qp, lp
@@ -464,11 +464,11 @@ def mot_paged_decode_attention(qkv, table, lens, k_cache, v_cache, Hq: int, ws, 
     mot_kv_cache_write. `ws` (>= mot_paged_decode_workspace_bytes) is scratch after its 64-byte header.
     Returns out [R][Hq D] bf16."""
     kt, n_pages, Hkv, page, D, kp, vp, sp = _kv_cache(k_cache, v_cache, scales)
-    R, N = qkv.shape
     qp = _dev(qkv, "qkv", torch.bfloat16, 2)
     tp = _dev(table, "table", torch.int32, 2)
     lp = _dev(lens, "lens", torch.int32, 1)
     wp = _dev(ws, "ws", torch.uint8, 1)
+    R, N = qkv.shape
     if N != (Hq + 2 * Hkv) * D:
         raise ValueError(f"qkv must be [R, {(Hq + 2 * Hkv) * D}]")
     max_pages = table.shape[1]
