@@ -22,8 +22,8 @@
  *     plan array of mot_routed_gemm_noalloc.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream of the current
  *     device). Every pointer must belong to the stream's device (the device guard of
- *     [PR-503]'s RMSNorm launcher commit); the launch runs on that device. While a stream is
- *     being captured into a graph, its device must be the current one.
+ *     [PR-503]'s RMSNorm launcher commit); the launch runs on that device,
+ *     also while the stream is being captured into a graph.
  *   - Calls are asynchronous on `stream`. A nonzero return is a host-detected error: no
  *     kernel was launched and no output was written (fail closed: [RFC-435] §3 Numerical
  *     contract). Errors found on the device (a modality other than 0/1, a position

@@ -17,14 +17,45 @@ constexpr int kMaxDevices = 64;
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Device that owns `stream` (the current device for the legacy default stream). Asking a stream that
-// is being captured for its device would invalidate the capture, so the current device is taken
-// there too; the pointers' check then refuses a stream of another device.
+// A driver function, resolved once through the runtime so that the library does not link against the driver
+// library; null if the driver lacks it.
+template <typename Fn>
+inline Fn driver_fn(const char* name, unsigned version, std::atomic<void*>& cached) {
+  void* f = cached.load();
+  if (f == nullptr) {
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion(name, &f, version, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    cached.store(f);
+  }
+  return reinterpret_cast<Fn>(f);
+}
+
+// Device of the context that a stream being captured belongs to. cudaStreamGetDevice would invalidate the
+// capture; asking for the context is allowed.
+inline int capturing_stream_device(cudaStream_t s, int* dev) {
+  static std::atomic<void*> get_ctx{nullptr}, push{nullptr}, pop{nullptr}, get_device{nullptr};
+  auto stream_ctx = driver_fn<CUresult (*)(CUstream, CUcontext*)>("cuStreamGetCtx", 9020, get_ctx);
+  auto ctx_push = driver_fn<CUresult (*)(CUcontext)>("cuCtxPushCurrent", 4000, push);
+  auto ctx_pop = driver_fn<CUresult (*)(CUcontext*)>("cuCtxPopCurrent", 4000, pop);
+  auto ctx_device = driver_fn<CUresult (*)(CUdevice*)>("cuCtxGetDevice", 2000, get_device);
+  if (stream_ctx == nullptr || ctx_push == nullptr || ctx_pop == nullptr || ctx_device == nullptr) return MOT_ERR_CUDA;
+  CUcontext ctx, popped;
+  if (stream_ctx(s, &ctx) != CUDA_SUCCESS || ctx_push(ctx) != CUDA_SUCCESS) return MOT_ERR_CUDA;
+  CUdevice d = -1;
+  const bool ok = ctx_device(&d) == CUDA_SUCCESS;
+  if (ctx_pop(&popped) != CUDA_SUCCESS || !ok) return MOT_ERR_CUDA;
+  *dev = int(d);
+  return MOT_OK;
+}
+
+// Device that owns `stream` (the current device for the legacy default stream).
 inline int stream_device(cudaStream_t s, int* dev) {
+  if (s == nullptr) return cudaGetDevice(dev) == cudaSuccess ? MOT_OK : MOT_ERR_CUDA;
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-  if (s != nullptr && cudaStreamIsCapturing(s, &capture) != cudaSuccess) return MOT_ERR_CUDA;
-  if (s == nullptr || capture != cudaStreamCaptureStatusNone)
-    return cudaGetDevice(dev) == cudaSuccess ? MOT_OK : MOT_ERR_CUDA;
+  if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) return MOT_ERR_CUDA;
+  if (capture != cudaStreamCaptureStatusNone) return capturing_stream_device(s, dev);
   return cudaStreamGetDevice(s, dev) == cudaSuccess ? MOT_OK : MOT_ERR_CUDA;
 }
 
@@ -118,23 +149,13 @@ inline int check_device(cudaStream_t s, const void* const* ptrs, int n, int* dev
   return MOT_OK;
 }
 
-// cuTensorMapEncodeTiled, resolved once through the runtime's driver entry point so that
-// the library does not link against the driver library directly.
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 inline EncodeTiledFn encode_tiled_fn() {
   static std::atomic<void*> fn{nullptr};
-  void* f = fn.load();
-  if (f == nullptr) {
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    fn.store(f);
-  }
-  return reinterpret_cast<EncodeTiledFn>(f);
+  return driver_fn<EncodeTiledFn>("cuTensorMapEncodeTiled", 12000, fn);
 }
 
 // 2D bf16 tensor map over a row-major [rows][cols] array with the 128-byte swizzle.

@@ -196,3 +196,26 @@ def test_read_back_rounds_once_whatever_the_scale():
     got = f64(y)
     np.testing.assert_array_equal(got[:, D: 2 * D], O.bf16(vals[None, :] * scales.astype(np.float64)[:, None]))
     np.testing.assert_array_equal(got[:, 2 * D:], O.bf16(-vals[None, :] * scales.astype(np.float64)[::-1, None]))
+
+
+def test_a_refused_call_leaves_a_capture_usable():
+    # the stream's device is asked for while it is being captured, and a pointer of no device is refused there
+    Hq, Hkv, D, page, T = 2, 1, 64, 16, 20
+    x = W.bf16_normal(W.rng_for(3, 611), (T, (Hq + 2 * Hkv) * D)).to(DEV)
+    slots = torch.arange(T, dtype=torch.int32, device=DEV)
+    k, v, _ = _empty_cache(2, Hkv, page, D, "bf16")
+    ws, host = _ws(), np.zeros(64, np.uint8)
+    at = (host.ctypes.data + 15) // 16 * 16
+    side, graph, lib = torch.cuda.Stream(), torch.cuda.CUDAGraph(), mot.load_library()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        mot.mot_kv_cache_write(x, slots, k, v, Hq, ws)
+        # qkv in host memory
+        assert lib.mot_kv_cache_write(at, 1, Hq, Hkv, D, slots.data_ptr(), mot.KV_BF16, 2, page, k.data_ptr(),
+                                      v.data_ptr(), None, ws.data_ptr(), 64, side.cuda_stream) == 4
+    x.neg_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert mot.mot_device_status(ws) == 0
+    got = k.transpose(1, 2).reshape(-1, D)[:T]
+    assert torch.equal(got, x[:, Hq * D: (Hq + 1) * D])
