@@ -366,7 +366,7 @@ size_t mot_paged_decode_workspace_bytes(int64_t R, int Hq, int Hkv, int D, int m
  *                                     MOT_DEV_BAD_PAGE and the row is not written. A page index outside
  *                                     [0, n_pages) among the entries read sets MOT_DEV_BAD_PAGE and
  *                                     leaves the row's output undefined.
- *   scale  softmax scale (1 / sqrt(D) for the standard attention), > 0.
+ *   scale  softmax scale (1 / sqrt(D) for the standard attention), > 0, with scale log2 e finite.
  *   ws     at least mot_paged_decode_workspace_bytes(R, Hq, Hkv, D, max_pages, page) bytes; everything
  *          after its first 64 bytes is scratch that the call overwrites (so not a routing plan in use).
  *   out    [R][Hq D] bf16             out.

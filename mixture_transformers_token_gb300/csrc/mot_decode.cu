@@ -59,6 +59,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
+
 #include "mot_kvcache.cuh"
 
 namespace mot {
@@ -1212,7 +1214,8 @@ extern "C" int mot_paged_decode_attention(const mot_bf16* qkv, int64_t R, int Hq
   if (st != MOT_OK) return st;
   const size_t need = mot_paged_decode_workspace_bytes(R, Hq, Hkv, D, max_pages, page);
   if (need == 0) return MOT_ERR_GEOMETRY;
-  if (!(scale > 0.0f) || !(scale < 3.0e38f)) return MOT_ERR_ARG;
+  const float c = scale * 1.4426950408889634f;
+  if (!(scale > 0.0f) || !(c <= FLT_MAX)) return MOT_ERR_ARG;
   if (!aligned16(qkv) || !kv::aligned4(table) || !kv::aligned4(lens) || !aligned16(k_cache) || !aligned16(v_cache) ||
       !aligned16(ws) || !aligned16(out) || (e4m3 && !aligned16(scales)))
     return MOT_ERR_ALIGN;
@@ -1237,7 +1240,7 @@ extern "C" int mot_paged_decode_attention(const mot_bf16* qkv, int64_t R, int Hq
   a.Hkv = Hkv;
   a.G = Hq / Hkv;
   a.HC = (a.G + decode::HEADS - 1) / decode::HEADS;
-  a.c = scale * 1.4426950408889634f;
+  a.c = c;
   a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + sizeof(PlanHeader));
   a.out = out;
   a.err = &static_cast<PlanHeader*>(ws)->error;
