@@ -135,6 +135,19 @@ __device__ __forceinline__ float product_to_odd(float a, float b) {
   return __uint_as_float(__float_as_uint(p) | (__fmaf_rn(a, b, -p) != 0.0f ? 1u : 0u));
 }
 
+// Eight codes times a scale that is no power of two, rounded once.
+__device__ __forceinline__ void store_to_odd(uint4* dst, uint2 c, float scale) {
+  const uint32_t codes[4] = {c.x & 0xFFFFu, c.x >> 16, c.y & 0xFFFFu, c.y >> 16};
+  uint32_t o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 v = h2_to_f2(e4m3x2_to_h2(codes[k]));
+    o[k] = pack_bf2(product_to_odd(v.x, scale), product_to_odd(v.y, scale));
+  }
+  *dst = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Eight blocks an SM, as many as its threads allow: with 40 registers instead of 32 the 36864 rows took 23.7 us.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(THREADS, 8) kv_read_kernel(const MoveArgs a) {
   constexpr int LANES = kLanes<D>;
@@ -157,23 +170,24 @@ __global__ void __launch_bounds__(THREADS, 8) kv_read_kernel(const MoveArgs a) {
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) c[i] = __ldg(reinterpret_cast<const uint2*>(src + from * D) + lane + i * LANES);
       const float scale = __ldg(a.scales + from * 2 + (p.j & 1));
-      uint32_t o[PIECES][4];
-      auto products = [&](auto mul) {
+      // a power of two is exact. The others apart, a whole vector: as a choice an element 36864 rows took 21.5 us, as
+      // two equal branches 777 rows 1.9 instead of 1.7
+      if (__builtin_expect((__float_as_uint(scale) & 0x007FFFFFu) != 0u, 0)) {
 #pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-          const uint32_t codes[4] = {c[i].x & 0xFFFFu, c[i].x >> 16, c[i].y & 0xFFFFu, c[i].y >> 16};
+        for (int i = 0; i < PIECES; ++i) store_to_odd(dst + i * LANES, c[i], scale);
+        continue;
+      }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 v = h2_to_f2(e4m3x2_to_h2(codes[k]));
-            o[i][k] = pack_bf2(mul(v.x), mul(v.y));
-          }
+      for (int i = 0; i < PIECES; ++i) {
+        const uint32_t codes[4] = {c[i].x & 0xFFFFu, c[i].x >> 16, c[i].y & 0xFFFFu, c[i].y >> 16};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = h2_to_f2(e4m3x2_to_h2(codes[k]));
+          o[k] = pack_bf2(__fmul_rn(v.x, scale), __fmul_rn(v.y, scale));
         }
-      };
-      // a power of two: exact. The rest once a vector, and not a choice an element (36864 rows 20.7 against 21.5 us)
-      if ((__float_as_uint(scale) & 0x007FFFFFu) == 0u) products([&](float x) { return __fmul_rn(x, scale); });
-      else products([&](float x) { return product_to_odd(x, scale); });
-#pragma unroll
-      for (int i = 0; i < PIECES; ++i) dst[i * LANES] = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
+        dst[i * LANES] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
     }
   }
 }
