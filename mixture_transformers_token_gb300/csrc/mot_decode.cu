@@ -332,13 +332,14 @@ __device__ __forceinline__ uint32_t chunk(int r, int c) {
 // 2^score. A lane takes a tile's key; K comes from memory again, the queries (halves, [half][8 heads][128 bytes],
 // swizzled) and their factors from shared memory. refs, sums and o (the warp's references, sums and O, [HEADS][D])
 // become e, the sum over 2^e, in [1/2, 1), and O under 2^e: then O is the warp's own output times that number, so in
-// range wherever the values are. It is code beside the loop, for values that no model has, because there a second
-// exponential a weight, or a vote a tile, cost every row time (256 rows of up to 4096 keys 113.3 or 111.4 instead of
-// 109.9 us, 256 of up to 300 23.4 or 22.2 instead of 20.6); beside it these take 110.2 and 21.2. Loud rows take up to
-// five times theirs (568 us a call instead of 121; 6.1 us a round of 256 keys, so 0.4 s a range of 2^24 keys).
+// range wherever the values are. It stands beside the loop, for values that no model has, because there a second
+// exponential a weight, or a vote a tile, cost every row time: 256 rows of up to 4096 keys took 113.3 or 111.4 us, 256
+// of up to 300 23.4 or 22.2; with the sums' one reference alone they take 110.0 and 20.6, with this 110.3 and 21.3.
+// Loud rows take up to five times theirs (537 us a call instead of 122; 5.9 us a round of 256 keys, which is 0.4 s in
+// a range of 2^24 keys, while a wait is given up after one).
 template <int D>
-__device__ __noinline__ void loud_sums(const Args& a, int row, int g, int t0, int t1, const uint8_t* q,
-                                       const float* qc, float* refs, float* sums, float* o) {
+__device__ __forceinline__ void loud_sums(const Args& a, int row, int g, int t0, int t1, const uint8_t* q,
+                                          const float* qc, float* refs, float* sums, float* o) {
   using C = Cfg<D, true>;
   static_assert(C::TOK == 32, "a lane for each key of a tile");
   const int lane = threadIdx.x & 31;
@@ -412,7 +413,7 @@ __device__ __noinline__ void loud_sums(const Args& a, int row, int g, int t0, in
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(THREADS, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ Args a) {
+                  const __grid_constant__ CUtensorMap tm_q, const Args a) {
   using C = Cfg<D, E4M3>;
   constexpr int TOK = C::TOK, NB = TOK / 16, KS = D / 16, STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
