@@ -10,9 +10,9 @@
 // multiple of a CTA's round (8 warps x TOK keys), 512 keys at least, that cuts one row into no more
 // (range, KV head) items than there are SMs: a single long row then fills the machine in one wave, and
 // each long row of a batch gives every SM about one item. Of the shortest spans 256, 512, 768 and 1024,
-// 512 was taken over 20 batches: 1024 is 12 % faster on 12 rows of 2000 keys and 2 % on 64 of up to
-// 8192, but 24 % slower on one row of 4000; 256 is 9 % faster there and 28 % slower on 256 e4m3
-// rows of up to 4096. A persistent CTA per SM takes every 152nd item.
+// 512 was taken over 20 batches: 1024 is 12 % faster on 12 rows of 2000 keys, 7 % on 128 of 750 and 2 % on 64
+// of up to 8192, but 24 % slower on one row of 4000 and 13 % on 33 of 750; 256 is 9 % faster on one row of 4000
+// and 28 % slower on 256 e4m3 rows of up to 4096. A persistent CTA per SM takes every 152nd item.
 //
 // Arithmetic of an item (a key range of one KV head, up to 8 of its query heads): warp w of 8 takes
 // the range's tiles w, w + 8, ... of TOK keys. Per tile S^T = K Q^T with mma.sync (m16n8k16: 16 keys x
@@ -47,14 +47,17 @@
 // itself 157 and 294 us; producers 111 and 219; joiners, one warp a head in narrow joins, spans of
 // 512 110 and 130; queries by the joiners, two heads a joiner 107 and 118; the L2 policy 103 and 116;
 // K Q^T 103 and 115; maxima exchanged only when a reference moves 103 and 114; a walk that loads its lengths
-// at once and a join whose loads do not wait for one another 102 and 109 (6.2 and 5.6 TB/s). One e4m3
-// row of 131072 keys takes 27 us (floor 20), one bf16 row of 500 7. A KV head's query heads beyond 8 are
+// at once and a join whose loads do not wait for one another 102 and 109 (6.2 and 5.6 TB/s); sums that no scale
+// takes out of range 102 and 110. One e4m3 row of 131072 keys takes 27 us (floor 20), one bf16 row of 500 7. (Times
+// of calls in a replayed graph; from Python that row takes 10.) A KV head's query heads beyond 8 are
 // items of their own, which read the tiles again through L2: 64 rows of up to 4096 keys of 2 KV heads take
-// 35 and 23 us with 8 heads each, 50 and 37 with 16; items of 16 heads took 41 and 34 there, but 9.6 us
+// 34 and 23 us with 8 heads each, 48 and 35 with 16; items of 16 heads took 41 and 34 there, but 9.6 us
 // instead of 6.9 on one row of 500 and up to 13 % more on 12 to 40 rows. What is above the floors now: the
 // start (lengths, page table, first tiles one after the other: 3 us), the join (2 us, 5 on 256 rows) and the last
 // CTAs' rest. With the products and weights left out, the 256 e4m3 rows take 3 us less and the 64 bf16 rows
-// the same; only rows of one or two tiles a warp wait for arithmetic (256 e4m3 rows of up to 300: 21 us, floor 9).
+// the same. What waits for arithmetic are rows of one or two tiles a warp (256 e4m3 rows of up to 300: 21 us, floor
+// 9) and e4m3 heads of 64, whose tiles have half the bytes for the same keys (64 rows of up to 8192 over 8 KV heads:
+// 88 us, floor 50; in bf16 102, floor 93).
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -1193,8 +1196,9 @@ using namespace mot;
 
 extern "C" size_t mot_paged_decode_workspace_bytes(int64_t R, int Hq, int Hkv, int D, int max_pages, int page) {
   if (kv::check_shape(Hq, Hkv, D, MOT_KV_BF16, 1, page) != MOT_OK) return 0;
-  // with more than 76 (KV head, group of 8 heads) pairs a row is one range, which the joiners wait for: 2^24
-  // keys take about 0.2 s (1.6 us a round of 128 at HBM's rate), against the 1 s after which a wait is given up
+  // with more than 76 (KV head, group of 8 heads) pairs a row is one range, which the joiners wait for: by the times of
+  // one row of 2^18 keys, 2^24 take 0.2 s (bf16, 1.5 us a round of 128 at HBM's rate) or 0.4 s (loud e4m3 scales, 5.9 us
+  // a round of 256), against the 1 s after which a wait is given up
   if (R < 1 || R > MOT_MAX_TOKENS || max_pages < 1 || int64_t(max_pages) * page > (int64_t(1) << 24)) return 0;
   if (R * (Hq + 2 * Hkv) > (int64_t(1) << 31) - 1) return 0;  // head vectors have 32-bit TMA coordinates
   const int G = Hq / Hkv, heads = Hkv * ((G + decode::HEADS - 1) / decode::HEADS);
