@@ -9,7 +9,7 @@ from oracle import mot_oracle as O
 
 from _util import assert_bitwise, f64, need_gpu
 from test_gpu_kvcache import DEV, Batch, _empty_cache, _kv, _qkv, _slots, _ws
-from test_gpu_kvcache_range import _check, _rewrite
+from test_gpu_kvcache_range import PLACES, _check, _rewrite
 
 pytestmark = pytest.mark.gpu
 
@@ -134,3 +134,25 @@ def test_joint_attention_over_a_prefix_read_from_a_quantised_cache():
     want = mot.mot_joint_attention(z, seqs, Hq, Hkv, D, ws)
     assert mot.mot_device_status(ws) == 0
     assert_bitwise(got[pre:], want[pre:], "second chunk")
+
+
+@pytest.mark.parametrize("n,at", PLACES)
+@pytest.mark.parametrize("top", [24, 25])
+def test_either_side_of_the_scale_from_which_sums_stand_apart(n, at, top):
+    # one value with a V scale of 2^16 or 2^17 among zero vectors (2^-64) or values of 2^-50; its key is behind the
+    # others' by up to 2^35, or leads
+    Hq, Hkv, D = 2, 1, 64
+    for lead in (0.0, 12.0, 35.0, -20.0):
+        for quiet in (0.0, 2.0 ** -50):
+            b = Batch([n, 2], Hq, Hkv, D, "e4m3", 16, seed=n + top)
+            b.q[:, : Hq * D] = 1.0
+            x = b.x[0].float()
+            x[:, Hq * D:] = 0.0
+            x[at, Hq * D: (Hq + Hkv) * D] = -lead * np.log(2.0) * np.sqrt(float(D)) / D
+            x[:, (Hq + Hkv) * D:] = quiet
+            x[at, (Hq + Hkv) * D:] = 1.5 * 2.0 ** top
+            b.x[0] = x.to(torch.bfloat16)
+            _rewrite(b)
+            page = int(b.table[0, at // 16])
+            assert float(b.scales[page, 0, at % 16, 1]) == 2.0 ** (top - 8)
+            _check(b, f"2^{top} at {at} of {n}, lead {lead}, quiet {quiet}")
