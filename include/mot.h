@@ -45,7 +45,7 @@
 extern "C" {
 #endif
 
-#define MOT_ABI_VERSION 5
+#define MOT_ABI_VERSION 6
 
 /* host-detected status codes (return values) */
 #define MOT_OK            0
@@ -67,6 +67,7 @@ extern "C" {
 #define MOT_DEV_BAD_SEQUENCE  0x10u /* an attention sequence descriptor out of range */
 #define MOT_DEV_BAD_TIME      0x20u /* SDE step times outside 0 <= t_next < t_i <= 1 */
 #define MOT_DEV_BAD_PAGE      0x40u /* a cache slot, a page index or a sequence length out of range */
+#define MOT_DEV_BAD_HYPER     0x80u /* an optimizer step's numbers out of range (the step was skipped) */
 
 /* epilogues of mot_routed_gemm */
 #define MOT_EPI_CAST   0  /* out = bf16(acc) */
@@ -86,6 +87,12 @@ extern "C" {
 /* element types of a paged key-value cache */
 #define MOT_KV_BF16 0
 #define MOT_KV_E4M3 1  /* 8-bit floats (4 exponent, 3 fraction bits, largest value 448) with scales */
+
+/* flags of an optimizer's tensor */
+#define MOT_ADAMW_GRAD_BF16  1  /* the gradient is bf16, else fp32 */
+#define MOT_ADAMW_STATE_E4M3 2  /* the states are 8-bit floats with scales, else fp32 */
+#define MOT_ADAMW_BLOCK    256  /* consecutive elements of an 8-bit state that share a scale */
+#define MOT_ADAMW_HYPER_WORDS 16 /* 32-bit words of a step's numbers */
 
 /* largest packed batch the library accepts */
 #define MOT_MAX_TOKENS (1 << 24)
@@ -304,6 +311,55 @@ int mot_joint_attention(const mot_bf16* qkv, int64_t T, int Hq, int Hkv, int D, 
                         int n_seq, float scale, void* ws, size_t ws_bytes, mot_bf16* out, void* stream);
 
 /*
+ * mot_joint_attention_lse -- mot_joint_attention that also writes what its backward pass needs.
+ *   lse   [Hq][T] fp32   out: ln of each query row's softmax sum, ln sum_j exp(scale S_j) over the keys
+ *                        it sees (m scale + ln l of the forward's m and l, in fp32); columns of rows
+ *                        that are no query untouched. 16-byte aligned.
+ * Everything else, out's bits included, as for mot_joint_attention.
+ */
+int mot_joint_attention_lse(const mot_bf16* qkv, int64_t T, int Hq, int Hkv, int D, const int32_t* seqs,
+                            int n_seq, float scale, void* ws, size_t ws_bytes, mot_bf16* out, float* lse,
+                            void* stream);
+
+/*
+ * mot_joint_attention_backward_workspace_bytes -- workspace bytes of mot_joint_attention_backward: the
+ * 64-byte header (its error word), the row sums and the partial gradients. 0 for a geometry that the
+ * call rejects.
+ */
+size_t mot_joint_attention_backward_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int n_seq);
+
+/*
+ * mot_joint_attention_backward -- gradient of mot_joint_attention with respect to its fused input
+ * ([RFC-435] §3 BAGEL-specific rules: phase A trains the gen set, and the frozen und operators still
+ * need dX, which reaches them through the keys that latents share with the prompt; §3 Numerical
+ * contract: fixed accumulation order, no atomics). The probabilities are recomputed, none is stored.
+ *   dout   [T][Hq D] bf16             gradient of out (rows that are no query are not used).
+ *   qkv    [T][(Hq + 2 Hkv) D] bf16   the forward's input.
+ *   out    [T][Hq D] bf16             the forward's output.
+ *   lse    [Hq][T] fp32               mot_joint_attention_lse's.
+ *   seqs, n_seq, scale                the forward's.
+ *   ws     at least mot_joint_attention_backward_workspace_bytes(T, Hq, Hkv, D, n_seq) bytes; everything
+ *          after its first 64 bytes is scratch that the call overwrites (so not a routing plan in use).
+ *          Its error word receives MOT_DEV_BAD_SEQUENCE as in the forward.
+ *   dqkv   [T][(Hq + 2 Hkv) D] bf16   out: the q columns of rows that are some sequence's query, and the
+ *          K and V columns of rows that are some sequence's key, each row written once, whole; all other
+ *          columns are left as they were. A row that several sequences see as a key gets the sum over
+ *          them. A bad descriptor contributes nothing.
+ * Per query i and key j that it sees, S = q . k: P = exp(scale S - lse), dP = dout_i . v_j,
+ * delta_i = sum of dout_i out_i over the head's columns, dS = P (dP - delta_i); then dq_i = scale sum_j
+ * dS k_j, dk_j = scale sum dS q_i and dv_j = sum P dout_i over the sequences, query heads of the group
+ * and queries that see j. S, dP and the three sums in fp32 on the tensor cores; P and dS are formed in
+ * fp32 and enter their products as bf16; one cast. The order of every sum is fixed by the row's own
+ * sequences, the head geometry and the order of seqs: a row's bits do not depend on the other sequences
+ * of the pack or on where its rows lie. Rows of other sequences, whatever they hold, add nothing; a NaN
+ * or infinity in a row of a sequence leaves that sequence's gradients undefined. Tensors do not
+ * overlap. Geometry as mot_joint_attention; scale log2 e from 2^-100 to 2^100, else MOT_ERR_ARG.
+ */
+int mot_joint_attention_backward(const mot_bf16* dout, const mot_bf16* qkv, const mot_bf16* out, const float* lse,
+                                 int64_t T, int Hq, int Hkv, int D, const int32_t* seqs, int n_seq, float scale,
+                                 void* ws, size_t ws_bytes, mot_bf16* dqkv, void* stream);
+
+/*
  * Paged key-value cache ([RFC-435] §1 Motivation item 2: latent tokens query the prompt KV at every
  * step; §2 Reference hazards: cached prefill. The pages fix no cache layout). The caller owns the
  * pages; the three calls below write, read back and attend over
@@ -482,6 +538,105 @@ int mot_add_rmsnorm_backward(const mot_bf16* dy, const mot_bf16* d_res_out, cons
  */
 int mot_rmsnorm_dweight(const float* dw_partials, int64_t T, int H, int sets, void* ws, size_t ws_bytes,
                         float* dw, void* stream);
+
+/*
+ * mot_qk_norm_rope_backward_workspace_bytes -- scratch bytes of mot_qk_norm_rope_backward's weight
+ * gradients for T rows and heads of D. 0 for a geometry that the call rejects.
+ */
+size_t mot_qk_norm_rope_backward_workspace_bytes(int64_t T, int D);
+
+/*
+ * mot_qk_norm_rope_backward -- gradient through the epilogue of mot_routed_qkv_norm_rope, from its
+ * output to the projection's rows ([RFC-435] §3 BAGEL-specific rules: the frozen und operators still
+ * need dX; [PR-503] gated-norm commit: deterministic pieces). Its result feeds mot_routed_gemm_dx and
+ * mot_routed_gemm_dw with w_qkv.
+ *   d_out     [T][N] bf16, N = (Hq + 2 Hkv) D   gradient of qkv_out (mot_joint_attention_backward's dqkv).
+ *   x         [T][N] bf16             the projection's rows q = bf16(acc + b) before the norm:
+ *                                     mot_routed_gemm(MOT_EPI_CAST) on the same weights gives them bit for
+ *                                     bit where there is no bias. V columns are not read.
+ *   q_norm_w, k_norm_w, pos, rope_cs, P, eps   the forward's (any position outside [0, P) sets
+ *                                     MOT_DEV_BAD_POSITION and is taken as 0, as in the forward).
+ *   ws        the routing plan of the forward's mod for this T: each row's weight set, and the error word.
+ *   dx        [T][N] bf16             out: the gradient of x, rows in token order; may be d_out (in place).
+ *   dw        [2][2][D] fp32 or NULL  out: gradients of q_norm_w (dw[0]) and k_norm_w (dw[1]), [2][D] each.
+ *   sets      MOT_SET_UND, MOT_SET_GEN or MOT_SET_BOTH (ignored without dw): the weight sets whose rows of dw
+ *             are written; the others are left as they are. Every row's dx is formed either way.
+ *   scratch   at least mot_qk_norm_rope_backward_workspace_bytes(T, D) bytes, overwritten (ignored
+ *             without dw).
+ * Per Q/K head, in fp32, the forward's casts differentiated as the identity: rstd = 1 / sqrt(sum x^2 / D + eps);
+ * du_i = d_i c + d_{i+D/2} s, du_{i+D/2} = d_{i+D/2} c - d_i s; xh = x rstd; g = du w[e];
+ * dx = bf16(rstd (g - xh (sum g xh) / D)); dw[e] = sum over e's rows and the kind's heads of du xh, in an
+ * order that T, the plan and the head geometry fix. V columns of dx are d_out's. Geometry: D in {64, 128};
+ * Hq, Hkv in 1 .. 1024; 1 <= T <= MOT_MAX_TOKENS; P >= 1. All pointers 16-byte aligned device memory of the
+ * stream's device. A plan that failed (bad modality) leaves the outputs undefined. Calls that may run at
+ * the same time have scratch of their own.
+ */
+int mot_qk_norm_rope_backward(const mot_bf16* d_out, const mot_bf16* x, const mot_bf16* q_norm_w,
+                              const mot_bf16* k_norm_w, const int32_t* pos, const mot_bf16* rope_cs, int P, int64_t T,
+                              int Hq, int Hkv, int D, float eps, void* ws, size_t ws_bytes, mot_bf16* dx, float* dw,
+                              int sets, void* scratch, size_t scratch_bytes, void* stream);
+
+/* mot_qk_norm_rope_backward_fp32 -- the same through mot_routed_qkv_norm_rope_fp32 and its fp32 table. */
+int mot_qk_norm_rope_backward_fp32(const mot_bf16* d_out, const mot_bf16* x, const mot_bf16* q_norm_w,
+                                   const mot_bf16* k_norm_w, const int32_t* pos, const float* rope_cs_f32, int P,
+                                   int64_t T, int Hq, int Hkv, int D, float eps, void* ws, size_t ws_bytes, mot_bf16* dx,
+                                   float* dw, int sets, void* scratch, size_t scratch_bytes, void* stream);
+
+/*
+ * AdamW over many tensors ([RFC-435] §3 BAGEL-specific rules: phase A updates the gen weight set; the pages
+ * name no optimizer: the update is the decoupled-weight-decay Adam of Loshchilov and Hutter, ICLR 2019).
+ * One entry of the host array that mot_adamw_step takes: n consecutive elements of a parameter (a whole
+ * tensor, or one weight set of it) with their gradient and states.
+ */
+typedef struct mot_adamw_tensor {
+  float* p;            /* fp32 weights (master copy), updated */
+  mot_bf16* p16;       /* receives bf16(p), the weights that the routed calls read; or NULL */
+  const void* g;       /* gradient: fp32, or bf16 with MOT_ADAMW_GRAD_BF16 */
+  void* m;             /* first moment: fp32, or e4m3 codes with MOT_ADAMW_STATE_E4M3; updated */
+  void* v;             /* second moment: fp32 v, or e4m3 codes of sqrt(v); updated */
+  float* scales;       /* e4m3 only (else ignored): [ceil(n / 256)][2] scales of m and sqrt(v); updated */
+  int64_t n;           /* elements, 1 .. 2^40 */
+  float weight_decay;  /* >= 0 */
+  int32_t flags;       /* MOT_ADAMW_* or 0 */
+} mot_adamw_tensor;
+
+/*
+ * mot_adamw_hyper_host -- the numbers of step t >= 1, each rounded once from double: host_row receives
+ * (lr, beta1, 1 - beta1, beta2, 1 - beta2, lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t), eps, grad_scale) and t
+ * as an integer word, then zeros: MOT_ADAMW_HYPER_WORDS words. A training program fills a table of them,
+ * or copies one a step; a captured step then needs no new capture.
+ * Errors: MOT_ERR_ARG unless lr >= 0, 0 <= beta1, beta2 < 1, eps > 0, all finite, 1 <= step < 2^31.
+ */
+int mot_adamw_hyper_host(double lr, double beta1, double beta2, double eps, double grad_scale, int64_t step,
+                         float* host_row);
+
+/*
+ * mot_adamw_step -- one AdamW step of n_tensors tensors.
+ *   tensors   host array (read before the call returns). All its pointers are device memory of the
+ *             stream's device, 16-byte aligned (scales: 8-byte); tensors do not overlap.
+ *   hyper     device row of mot_adamw_hyper_host, 16-byte aligned. Its grad_scale may be replaced on the
+ *             device before the call (a clipping factor). Numbers out of mot_adamw_hyper_host's range, or a
+ *             grad_scale that is not finite, set MOT_DEV_BAD_HYPER in ws: nothing is updated.
+ *   seed      of the 8-bit states' rounding: a training run keeps one.
+ *   ws        at least 64 bytes: the error word.
+ * Per element, every operation rounded on its own in fp32: g' = g grad_scale; m' = m beta1 + g' (1 - beta1);
+ * v' = v beta2 + (g' g') (1 - beta2); p' = p - ((m' lr1) / (sqrt(v') r2 + eps) + p (lr weight_decay)) with the
+ * row's lr1 = lr / (1 - beta1^t) and r2 = 1 / sqrt(1 - beta2^t); p16 = bf16(p').
+ * MOT_ADAMW_STATE_E4M3: m = code * scale, sqrt(v) = code * scale. After the update, per block of 256 elements
+ * (the last one of a tensor may be shorter) and state, with a = the block's largest magnitude (of m', of
+ * sqrt(v')): scale = a (1 / 448), y = min(|x| ((1 / a) 448), 448) (each operation and both
+ * reciprocals rounded on their own); y is rounded to one of the two neighbouring e4m3
+ * values at random, up with probability equal to its distance from the lower one (to 2^-16 of a step), so
+ * that the states' expectations are exact and small changes are not lost; a positive v' whose code would
+ * be zero gets the smallest one. a < 2^-100 makes scale and codes zero; a block with an infinity or a NaN
+ * gets the scale NaN and codes of zero. The 16 random bits of element e of tensor i (its index in `tensors`) are the low (m)
+ * and high (v) half of word e % 4 of the Philox4x32-7 block (Salmon et al., SC 2011) with counter
+ * (e / 4 low, e / 4 high, i, t) and key (seed low, seed high).
+ * Geometry: 1 <= n_tensors <= 65536, n in 1 .. 2^40, else MOT_ERR_GEOMETRY; unknown flags or a negative or
+ * non-finite weight_decay are MOT_ERR_ARG.
+ */
+int mot_adamw_step(const mot_adamw_tensor* tensors, int n_tensors, const float* hyper, uint64_t seed, void* ws,
+                   size_t ws_bytes, void* stream);
 
 /*
  * mot_flow_schedule_host -- the sampler's n step times from 1 down to 0 ([RFC-435] §3

@@ -32,9 +32,12 @@ __all__ = [
     "mot_flow_sde_step", "mot_flow_cfg_sde_step", "mot_flow_noise",
     "DEV_BAD_PAGE", "KV_BF16", "KV_E4M3", "mot_kv_cache_write", "mot_kv_cache_read",
     "mot_paged_decode_workspace_bytes", "mot_paged_decode_attention",
+    "mot_joint_attention_lse", "mot_joint_attention_backward_workspace_bytes", "mot_joint_attention_backward",
+    "mot_qk_norm_rope_backward_workspace_bytes", "mot_qk_norm_rope_backward", "mot_qk_norm_rope_backward_fp32",
+    "DEV_BAD_HYPER", "ADAMW_BLOCK", "AdamWTensors", "mot_adamw_hyper_host", "mot_adamw_step",
 ]
 
-ABI_VERSION = 5
+ABI_VERSION = 6
 EPI_CAST = 0
 EPI_SWIGLU = 1
 A_PLAN_ORDER = 0x100
@@ -47,8 +50,11 @@ DEV_BAD_POSITION = 0x8
 DEV_BAD_SEQUENCE = 0x10
 DEV_BAD_TIME = 0x20
 DEV_BAD_PAGE = 0x40
+DEV_BAD_HYPER = 0x80
 KV_BF16, KV_E4M3 = 0, 1  # element types of a paged key-value cache
 NOALLOC_MAX_TOKENS = 65536
+ADAMW_BLOCK = 256  # elements of an 8-bit optimizer state that share a scale
+_ADAMW_GRAD_BF16, _ADAMW_STATE_E4M3, _ADAMW_HYPER_WORDS = 1, 2, 16
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -96,6 +102,18 @@ _SIGNATURES = {
     "mot_paged_decode_workspace_bytes": (_c_sz, [_c_i64, _c_i, _c_i, _c_i, _c_i, _c_i]),
     "mot_paged_decode_attention": (_c_i, [_c_p, _c_i64, _c_i, _c_i, _c_i, _c_p, _c_p, _c_i, _c_i, _c_i64, _c_i, _c_p,
                                           _c_p, _c_p, _c_f, _c_p, _c_sz, _c_p, _c_p]),
+    "mot_joint_attention_lse": (_c_i, [_c_p, _c_i64, _c_i, _c_i, _c_i, _c_p, _c_i, _c_f, _c_p, _c_sz, _c_p, _c_p, _c_p]),
+    "mot_joint_attention_backward_workspace_bytes": (_c_sz, [_c_i64, _c_i, _c_i, _c_i, _c_i]),
+    "mot_joint_attention_backward": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_i64, _c_i, _c_i, _c_i, _c_p, _c_i, _c_f, _c_p, _c_sz,
+                                            _c_p, _c_p]),
+    "mot_qk_norm_rope_backward_workspace_bytes": (_c_sz, [_c_i64, _c_i]),
+    "mot_qk_norm_rope_backward": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i64, _c_i, _c_i, _c_i, _c_f, _c_p,
+                                         _c_sz, _c_p, _c_p, _c_i, _c_p, _c_sz, _c_p]),
+    "mot_qk_norm_rope_backward_fp32": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i64, _c_i, _c_i, _c_i, _c_f,
+                                              _c_p, _c_sz, _c_p, _c_p, _c_i, _c_p, _c_sz, _c_p]),
+    "mot_adamw_hyper_host": (_c_i, [ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                    _c_i64, _c_p]),
+    "mot_adamw_step": (_c_i, [_c_p, _c_i, _c_p, ctypes.c_uint64, _c_p, _c_sz, _c_p]),
     "mot_device_status": (_c_i, [_c_p, ctypes.POINTER(ctypes.c_uint32), _c_p]),
 }
 
@@ -400,6 +418,205 @@ def mot_joint_attention(qkv, seqs, Hq: int, Hkv: int, D: int, ws, scale: float |
         qkv.data_ptr(), T, Hq, Hkv, D, seqs.data_ptr(), seqs.shape[0], sc, ws.data_ptr(), ws.numel(),
         out.data_ptr(), _stream(qkv, stream)))
     return out
+
+
+def mot_joint_attention_lse(qkv, seqs, Hq: int, Hkv: int, D: int, ws, scale: float | None = None, out=None, lse=None,
+                            stream=None):
+    """mot_joint_attention that also returns lse [Hq][T] fp32, the natural log of each query row's softmax sum, for
+    mot_joint_attention_backward: (out, lse)."""
+    qp = _dev(qkv, "qkv", torch.bfloat16, 2)
+    sp = _dev(seqs, "seqs", torch.int32, 2)
+    wp = _dev(ws, "ws", torch.uint8, 1)
+    T, N = qkv.shape
+    if N != (Hq + 2 * Hkv) * D:
+        raise ValueError(f"qkv must be [T, {(Hq + 2 * Hkv) * D}]")
+    if seqs.shape[1] != 5:
+        raise ValueError("seqs must be [n_seq, 5]")
+    if out is None:
+        out = torch.zeros((T, Hq * D), dtype=torch.bfloat16, device=qkv.device)
+    if lse is None:
+        lse = torch.zeros((Hq, T), dtype=torch.float32, device=qkv.device)
+    op = _dev(out, "out", torch.bfloat16, 2)
+    lp = _dev(lse, "lse", torch.float32, 2)
+    if out.shape != (T, Hq * D) or lse.shape != (Hq, T):
+        raise ValueError(f"out must be [{T}, {Hq * D}] and lse [{Hq}, {T}]")
+    sc = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    _check("mot_joint_attention_lse", _lib().mot_joint_attention_lse(
+        qp, T, Hq, Hkv, D, sp, seqs.shape[0], sc, wp, ws.numel(), op, lp, _stream(qkv, stream)))
+    return out, lse
+
+
+def mot_joint_attention_backward_workspace_bytes(T: int, Hq: int, Hkv: int, D: int, n_seq: int) -> int:
+    return int(_lib().mot_joint_attention_backward_workspace_bytes(T, Hq, Hkv, D, n_seq))
+
+
+def mot_joint_attention_backward(dout, qkv, out, lse, seqs, Hq: int, Hkv: int, D: int, ws, scale: float | None = None,
+                                 dqkv=None, stream=None):
+    """Gradient of mot_joint_attention with respect to qkv, from dout and out [T][Hq D], qkv and the lse of
+    mot_joint_attention_lse, over the same seqs. `ws` (>= mot_joint_attention_backward_workspace_bytes) is scratch after
+    its 64-byte header. Returns dqkv [T][(Hq + 2 Hkv) D] bf16 (what is no sequence's query or key: left as it is, zeros
+    if dqkv is None)."""
+    dp = _dev(dout, "dout", torch.bfloat16, 2)
+    qp = _dev(qkv, "qkv", torch.bfloat16, 2)
+    op = _dev(out, "out", torch.bfloat16, 2)
+    lp = _dev(lse, "lse", torch.float32, 2)
+    sp = _dev(seqs, "seqs", torch.int32, 2)
+    wp = _dev(ws, "ws", torch.uint8, 1)
+    T, N = qkv.shape
+    if N != (Hq + 2 * Hkv) * D:
+        raise ValueError(f"qkv must be [T, {(Hq + 2 * Hkv) * D}]")
+    if dout.shape != (T, Hq * D) or out.shape != (T, Hq * D) or lse.shape != (Hq, T):
+        raise ValueError(f"dout and out must be [{T}, {Hq * D}] and lse [{Hq}, {T}]")
+    if seqs.shape[1] != 5:
+        raise ValueError("seqs must be [n_seq, 5]")
+    if dqkv is None:
+        dqkv = torch.zeros_like(qkv)
+    gp = _dev(dqkv, "dqkv", torch.bfloat16, 2)
+    if dqkv.shape != (T, N):
+        raise ValueError(f"dqkv must be [{T}, {N}]")
+    sc = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    _check("mot_joint_attention_backward", _lib().mot_joint_attention_backward(
+        dp, qp, op, lp, T, Hq, Hkv, D, sp, seqs.shape[0], sc, wp, ws.numel(), gp, _stream(qkv, stream)))
+    return dqkv
+
+
+def mot_qk_norm_rope_backward_workspace_bytes(T: int, D: int) -> int:
+    return int(_lib().mot_qk_norm_rope_backward_workspace_bytes(T, D))
+
+
+def mot_qk_norm_rope_backward(d_out, x, q_norm_w, k_norm_w, pos, rope_cs, Hq: int, Hkv: int, D: int, eps: float, ws,
+                              dx=None, dw=None, sets: int = SET_BOTH, scratch=None, stream=None):
+    """Gradient through the epilogue of mot_routed_qkv_norm_rope: from d_out [T][(Hq + 2 Hkv) D] (gradient of its
+    output) and x, the projection's rows before the norm, the gradient dx of x (may be d_out: in place) and the norm
+    weights' gradients dw [2 (q, k)][2 (und, gen)][D] fp32 of the weight sets in `sets` (0: none, dw is None).
+    `ws` holds the plan, `scratch` (>= mot_qk_norm_rope_backward_workspace_bytes, allocated if None) is overwritten.
+    A bf16 `rope_cs` is the BF16 RoPE profile's, an fp32 one the FP32 profile's. Returns (dx, dw)."""
+    dp = _dev(d_out, "d_out", torch.bfloat16, 2)
+    xp = _dev(x, "x", torch.bfloat16, 2)
+    qp = _dev(q_norm_w, "q_norm_w", torch.bfloat16, 2)
+    kp = _dev(k_norm_w, "k_norm_w", torch.bfloat16, 2)
+    pp = _dev(pos, "pos", torch.int32, 1)
+    fp32 = getattr(rope_cs, "dtype", None) is torch.float32  # _dev refuses what is no tensor
+    cp = _dev(rope_cs, "rope_cs", torch.float32 if fp32 else torch.bfloat16, 3)
+    wp = _dev(ws, "ws", torch.uint8, 1)
+    T, N = d_out.shape
+    if N != (Hq + 2 * Hkv) * D or x.shape != (T, N):
+        raise ValueError(f"d_out and x must be [T, {(Hq + 2 * Hkv) * D}]")
+    if q_norm_w.shape != (2, D) or k_norm_w.shape != (2, D) or pos.shape[0] != T:
+        raise ValueError("q_norm_w/k_norm_w must be [2, D] and pos [T]")
+    if rope_cs.shape[1:] != (D // 2, 2):
+        raise ValueError("rope_cs must be [P, D/2, 2]")
+    if dx is None:
+        dx = torch.empty_like(d_out)
+    gp = _dev(dx, "dx", torch.bfloat16, 2)
+    if dx.shape != (T, N):
+        raise ValueError(f"dx must be [{T}, {N}]")
+    wgp = sp = None
+    sb = 0
+    if sets != 0:
+        if dw is None:
+            dw = torch.zeros((2, 2, D), dtype=torch.float32, device=d_out.device)
+        wgp = _dev(dw, "dw", torch.float32, 3)
+        if dw.shape != (2, 2, D):
+            raise ValueError(f"dw must be [2, 2, {D}]")
+        if scratch is None:
+            scratch = torch.empty(max(mot_qk_norm_rope_backward_workspace_bytes(T, D), 16), dtype=torch.uint8,
+                                  device=d_out.device)
+        sp = _dev(scratch, "scratch", torch.uint8, 1)
+        sb = scratch.numel()
+    elif dw is not None:
+        raise ValueError("dw is given but sets is 0")
+    name = "mot_qk_norm_rope_backward_fp32" if fp32 else "mot_qk_norm_rope_backward"
+    _check(name, getattr(_lib(), name)(
+        dp, xp, qp, kp, pp, cp, rope_cs.shape[0], T, Hq, Hkv, D, eps, wp, ws.numel(), gp, wgp, sets, sp, sb,
+        _stream(d_out, stream)))
+    return dx, dw
+
+
+def mot_qk_norm_rope_backward_fp32(d_out, x, q_norm_w, k_norm_w, pos, rope_cs_f32, Hq: int, Hkv: int, D: int, eps: float,
+                                   ws, dx=None, dw=None, sets: int = SET_BOTH, scratch=None, stream=None):
+    """The FP32 RoPE profile of mot_qk_norm_rope_backward; `rope_cs_f32` is the fp32 table."""
+    if getattr(rope_cs_f32, "dtype", None) is not torch.float32:
+        raise TypeError("rope_cs_f32 must be float32 (mot_rope_table_fill_host_fp32)")
+    return mot_qk_norm_rope_backward(d_out, x, q_norm_w, k_norm_w, pos, rope_cs_f32, Hq, Hkv, D, eps, ws, dx=dx, dw=dw,
+                                     sets=sets, scratch=scratch, stream=stream)
+
+
+class _AdamWTensor(ctypes.Structure):
+    _fields_ = [("p", _c_p), ("p16", _c_p), ("g", _c_p), ("m", _c_p), ("v", _c_p), ("scales", _c_p), ("n", _c_i64),
+                ("weight_decay", _c_f), ("flags", ctypes.c_int32)]
+
+
+class AdamWTensors:
+    """The tensors of mot_adamw_step, checked once; keeps them alive. Lists of equal length, one entry a tensor (any
+    shape; only the number of elements counts):
+      params  fp32 weights, updated.            grads   fp32 or bf16.
+      m, v    states, updated: fp32, or float8_e4m3fn codes of m and sqrt(v) with `scales`.
+      p16     bf16 copies of the weights that the step writes, or None (also as an entry).
+      scales  fp32 [ceil(n / ADAMW_BLOCK)][2] for 8-bit states (zeros to begin with, as m and v).
+      weight_decay  a number, or one a tensor.
+    The entries are slices like w[1] of a [2][N][K] weight as well as whole tensors."""
+
+    def __init__(self, params, grads, m, v, p16=None, scales=None, weight_decay=0.0):
+        n = len(params)
+        p16 = [None] * n if p16 is None else p16
+        scales = [None] * n if scales is None else scales
+        decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [float(x) for x in weight_decay]
+        if not n or any(len(x) != n for x in (grads, m, v, p16, scales, decay)):
+            raise ValueError("the lists must have one entry for each parameter, at least one")
+        self.table = (_AdamWTensor * n)()
+        for i in range(n):
+            e = self.table[i]
+            e.p = _dev_any(params[i], f"params[{i}]", torch.float32)
+            e.n = params[i].numel()
+            bf16 = getattr(grads[i], "dtype", None) is torch.bfloat16
+            e.g = _dev_any(grads[i], f"grads[{i}]", torch.bfloat16 if bf16 else torch.float32)
+            e4m3 = getattr(m[i], "dtype", None) is torch.float8_e4m3fn
+            state = torch.float8_e4m3fn if e4m3 else torch.float32
+            e.m = _dev_any(m[i], f"m[{i}]", state)
+            e.v = _dev_any(v[i], f"v[{i}]", state)
+            sizes = [grads[i].numel(), m[i].numel(), v[i].numel()]
+            if p16[i] is not None:
+                e.p16 = _dev_any(p16[i], f"p16[{i}]", torch.bfloat16)
+                sizes.append(p16[i].numel())
+            if any(x != e.n for x in sizes):
+                raise ValueError(f"grads, m, v and p16 of tensor {i} must have its {e.n} elements")
+            if e4m3:
+                e.scales = _dev_any(scales[i], f"scales[{i}]", torch.float32)
+                if scales[i].numel() != 2 * -(-e.n // ADAMW_BLOCK):
+                    raise ValueError(f"scales[{i}] must be [{-(-e.n // ADAMW_BLOCK)}, 2]")
+            e.weight_decay = decay[i]
+            e.flags = (_ADAMW_GRAD_BF16 if bf16 else 0) | (_ADAMW_STATE_E4M3 if e4m3 else 0)
+        self.tensors = (list(params), list(grads), list(m), list(v), list(p16), list(scales))
+        self.address = ctypes.addressof(self.table)
+
+    def __len__(self):
+        return len(self.table)
+
+
+def _dev_any(t, name: str, dtype: torch.dtype) -> int:
+    """_dev for a tensor of any rank."""
+    return _dev(t, name, dtype, t.dim() if isinstance(t, torch.Tensor) else None)
+
+
+def mot_adamw_hyper_host(lr: float, beta1: float, beta2: float, eps: float, step: int, grad_scale: float = 1.0) -> torch.Tensor:
+    """The numbers of AdamW step `step` (from 1) as a CPU fp32 tensor [16]: copy it to the device, or a table of them."""
+    t = torch.empty((_ADAMW_HYPER_WORDS,), dtype=torch.float32)
+    _check("mot_adamw_hyper_host", _lib().mot_adamw_hyper_host(lr, beta1, beta2, eps, grad_scale, step, t.data_ptr()))
+    return t
+
+
+def mot_adamw_step(tensors: AdamWTensors, hyper, ws, seed: int = 0, stream=None) -> None:
+    """One AdamW step of all `tensors`, in place. `hyper` is a device fp32 row [16] of mot_adamw_hyper_host, `ws` (>= 64
+    bytes) receives DEV_BAD_HYPER (then nothing is updated), `seed` is that of the 8-bit states' rounding."""
+    if not isinstance(tensors, AdamWTensors):
+        raise TypeError("tensors must be AdamWTensors")
+    hp = _dev(hyper, "hyper", torch.float32, 1)
+    if hyper.shape[0] != _ADAMW_HYPER_WORDS:
+        raise ValueError(f"hyper must be [{_ADAMW_HYPER_WORDS}]")
+    wp = _dev(ws, "ws", torch.uint8, 1)
+    _check("mot_adamw_step", _lib().mot_adamw_step(tensors.address, len(tensors.table), hp, int(seed) & (2 ** 64 - 1), wp,
+                                                   ws.numel(), _stream(hyper, stream)))
 
 
 def _kv_cache(k_cache, v_cache, scales):

@@ -1,0 +1,361 @@
+// AdamW over many tensors in one launch, states in 32 or in 8 bits.
+//
+// Source: [RFC][BAGEL-7B-MoT][CUDA/ROCm] WS1/WS2 kernel roadmap and integration plan #435 (§3 BAGEL-specific rules: phase A
+// updates the gen weight set). The update is the decoupled-weight-decay Adam of Loshchilov and Hutter (ICLR 2019); 8-bit
+// states in blocks with a scale of their own are those of Dettmers et al. (ICLR 2022), here in e4m3 and rounded at random
+// (Philox4x32 of Salmon, Moraes, Dror and Shaw, SC 2011): rounded to nearest, a second moment that changes by 1 - beta2
+// a step would stay where it is, for its neighbours are 6 to 12 % away.
+//
+// Every element is read and written once: 30 bytes with fp32 states, fp32 gradients and the bf16 copy, 16.06 with 8-bit states
+// and bf16 gradients. The bound is memory.
+
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "mot.h"
+#include "mot_device.cuh"
+#include "mot_host.hpp"
+#include "mot_kvcache.cuh"
+
+namespace mot {
+namespace adamw {
+
+constexpr int THREADS = 256;
+constexpr int BLOCK = MOT_ADAMW_BLOCK;
+constexpr int CHUNK = 2048;       // elements of a CTA's share of a tensor: eight blocks
+constexpr int kMaxTensors = 128;  // of one launch: its table is part of the launch's parameters
+
+struct Table {
+  mot_adamw_tensor t[kMaxTensors];
+  uint32_t first[kMaxTensors + 1];  // first chunk of each tensor
+  int n;
+  int base;                         // index of t[0] in the caller's array
+  const float* hyper;
+  uint32_t seed_lo, seed_hi;
+  uint32_t* err;
+};
+
+// words of the step's row
+enum { LR, B1, C1, B2, C2, LR1, R2, EPS, GS, STEP };
+
+struct Hyper {
+  float lr, b1, c1, b2, c2, lr1, r2, eps, gs;
+  uint32_t step;
+};
+
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
+
+__device__ __forceinline__ bool load_hyper(const float* row, Hyper& h) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(row)), b = __ldg(reinterpret_cast<const float4*>(row) + 1),
+               c = __ldg(reinterpret_cast<const float4*>(row) + 2);
+  h = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, __float_as_uint(c.y)};
+  return h.lr >= 0.0f && finite(h.lr) && h.b1 >= 0.0f && h.b1 < 1.0f && h.c1 > 0.0f && h.c1 <= 1.0f && h.b2 >= 0.0f &&
+         h.b2 < 1.0f && h.c2 > 0.0f && h.c2 <= 1.0f && h.lr1 >= 0.0f && finite(h.lr1) && h.r2 >= 1.0f && finite(h.r2) &&
+         h.eps > 0.0f && finite(h.eps) && finite(h.gs) && h.step >= 1u && h.step < 0x80000000u;
+}
+
+// One element: m and v become the new moments, r the square root of v; returns the new weight.
+__device__ __forceinline__ float update(const Hyper& h, float wl, float g, float& m, float& v, float& r, float p) {
+  g = __fmul_rn(g, h.gs);
+  m = __fadd_rn(__fmul_rn(m, h.b1), __fmul_rn(g, h.c1));
+  v = __fadd_rn(__fmul_rn(v, h.b2), __fmul_rn(__fmul_rn(g, g), h.c2));
+  r = __fsqrt_rn(v);
+  const float u = __fdiv_rn(__fmul_rn(m, h.lr1), __fadd_rn(__fmul_rn(r, h.r2), h.eps));
+  return __fsub_rn(p, __fadd_rn(u, __fmul_rn(p, wl)));
+}
+
+__device__ __forceinline__ void philox_round(uint32_t (&x)[4], uint32_t k0, uint32_t k1) {
+  const uint64_t a = uint64_t(x[0]) * 0xD2511F53u, b = uint64_t(x[2]) * 0xCD9E8D57u;
+  x[0] = uint32_t(b >> 32) ^ x[1] ^ k0;
+  x[1] = uint32_t(b);
+  x[2] = uint32_t(a >> 32) ^ x[3] ^ k1;
+  x[3] = uint32_t(a);
+}
+
+// Philox4x32-7: the words of elements 4 b .. 4 b + 3.
+__device__ __forceinline__ void random_words(uint32_t (&x)[4], uint64_t b, uint32_t tensor, uint32_t step, uint32_t k0,
+                                             uint32_t k1) {
+  x[0] = uint32_t(b);
+  x[1] = uint32_t(b >> 32);
+  x[2] = tensor;
+  x[3] = step;
+#pragma unroll
+  for (int i = 0; i < 7; ++i) {
+    philox_round(x, k0, k1);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+}
+
+// A block's quantiser from its largest magnitude's bits (whose order is the floats', infinities and NaNs last).
+struct Scale {
+  float scale, inv;
+};
+__device__ __forceinline__ Scale block_scale(uint32_t top) {
+  const float a = __uint_as_float(top);
+  if (top >= 0x7F800000u) return {__uint_as_float(0x7FC00000u), 0.0f};
+  if (!(a >= 0x1p-100f)) return {0.0f, 0.0f};
+  return {__fmul_rn(a, 1.0f / 448.0f), __fmul_rn(__frcp_rn(a), 448.0f)};
+}
+
+// |x| inv, at most 448, rounded to one of its e4m3 neighbours by 16 random bits below the last kept one. Values under 2^-6
+// (e4m3's subnormals) move up by 2^-6, where fp32 values have the subnormals' step in the same bit. inv is zero in a block
+// without a scale: its codes are zero.
+__device__ __forceinline__ float round_at_random(float x, float inv, uint32_t bits16) {
+  const float y = inv > 0.0f ? fminf(__fmul_rn(fabsf(x), inv), 448.0f) : 0.0f;
+  const float lift = y < 0x1p-6f ? 0x1p-6f : 0.0f;
+  const uint32_t z = (__float_as_uint(__fadd_rn(y, lift)) + (bits16 << 4)) & 0xFFF00000u;
+  return __fsub_rn(__uint_as_float(z), lift);
+}
+
+// Elements [0, 8) of a lane, of which the first `have` are there.
+template <bool BF16>
+__device__ __forceinline__ void load_grad(const void* g, int64_t e, int have, float (&x)[8]) {
+  if (have == 8) {
+    if constexpr (BF16) {
+      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g) + e));
+      x[0] = bf_lo(w.x), x[1] = bf_hi(w.x), x[2] = bf_lo(w.y), x[3] = bf_hi(w.y);
+      x[4] = bf_lo(w.z), x[5] = bf_hi(w.z), x[6] = bf_lo(w.w), x[7] = bf_hi(w.w);
+    } else {
+      const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(g) + e);
+      const float4 a = __ldcs(s), b = __ldcs(s + 1);
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = i >= have ? 0.0f : BF16 ? bf_to_f(static_cast<const uint16_t*>(g)[e + i]) : static_cast<const float*>(g)[e + i];
+  }
+}
+
+__device__ __forceinline__ void load8(const float* s, int have, float (&x)[8]) {
+  if (have == 8) {
+    const float4 a = *reinterpret_cast<const float4*>(s), b = *(reinterpret_cast<const float4*>(s) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < have ? s[i] : 0.0f;
+  }
+}
+
+__device__ __forceinline__ void store8(float* d, int have, const float (&x)[8]) {
+  if (have == 8) {
+    *reinterpret_cast<float4*>(d) = make_float4(x[0], x[1], x[2], x[3]);
+    *(reinterpret_cast<float4*>(d) + 1) = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < have) d[i] = x[i];
+  }
+}
+
+__device__ __forceinline__ void store_bf16(uint16_t* d, int have, const float (&x)[8]) {
+  if (have == 8) {
+    *reinterpret_cast<uint4*>(d) =
+        make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < have) d[i] = f_to_bf(x[i]);
+  }
+}
+
+__device__ __forceinline__ void load_codes(const uint8_t* s, int have, float scale, float (&x)[8]) {
+  uint32_t w[2] = {0u, 0u};
+  if (have == 8) {
+    const uint2 c = *reinterpret_cast<const uint2*>(s);
+    w[0] = c.x, w[1] = c.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < have) w[i >> 2] |= uint32_t(s[i]) << (8 * (i & 3));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = kv::h2_to_f2(kv::e4m3x2_to_h2((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu));
+    x[2 * i] = __fmul_rn(v.x, scale);
+    x[2 * i + 1] = __fmul_rn(v.y, scale);
+  }
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* d, int have, uint32_t lo, uint32_t hi) {
+  if (have == 8) {
+    *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < have) d[i] = uint8_t((i < 4 ? lo : hi) >> (8 * (i & 3)));
+  }
+}
+
+__device__ __forceinline__ uint32_t warp_max(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+
+// A warp takes a block of 256 elements, eight consecutive ones a lane: the block's scales need no shared memory.
+template <bool BF16, bool E4M3>
+__device__ __forceinline__ void warp_block(const Table& a, const Hyper& h, const mot_adamw_tensor& t, int id, int64_t block,
+                                           int lane) {
+  const int64_t e = block * BLOCK + lane * 8;
+  const int64_t left = t.n - e;
+  const int have = left >= 8 ? 8 : left > 0 ? int(left) : 0;
+  const float wl = __fmul_rn(h.lr, t.weight_decay);
+  float g[8], m[8], v[8], r[8], p[8];
+  load_grad<BF16>(t.g, e, have, g);
+  load8(t.p + e, have, p);
+  if constexpr (E4M3) {
+    const float2 s = *reinterpret_cast<const float2*>(t.scales + 2 * block);
+    load_codes(static_cast<const uint8_t*>(t.m) + e, have, s.x, m);
+    load_codes(static_cast<const uint8_t*>(t.v) + e, have, s.y, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], v[i]);
+  } else {
+    load8(static_cast<const float*>(t.m) + e, have, m);
+    load8(static_cast<const float*>(t.v) + e, have, v);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) p[i] = update(h, wl, g[i], m[i], v[i], r[i], p[i]);
+  store8(t.p + e, have, p);
+  if (t.p16) store_bf16(t.p16 + e, have, p);
+  if constexpr (E4M3) {
+    uint32_t tm = 0, tr = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // elements past the end are zero but for a NaN weight_decay, which the host refuses
+      tm = max(tm, __float_as_uint(m[i]) & 0x7FFFFFFFu);
+      tr = max(tr, __float_as_uint(r[i]) & 0x7FFFFFFFu);
+    }
+    const Scale sm = block_scale(warp_max(tm)), sr = block_scale(warp_max(tr));
+    uint32_t cm[2], cr[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      uint32_t w[4];
+      random_words(w, uint64_t(e) / 4 + q, uint32_t(id), h.step, a.seed_lo, a.seed_hi);
+      float ym[4], yr[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ym[i] = copysignf(round_at_random(m[4 * q + i], sm.inv, w[i] & 0xFFFFu), m[4 * q + i]);
+        yr[i] = round_at_random(r[4 * q + i], sr.inv, w[i] >> 16);
+        if (v[4 * q + i] > 0.0f && sr.scale > 0.0f) yr[i] = fmaxf(yr[i], 0x1p-9f);
+      }
+      cm[q] = kv::e4m3x2(ym[0], ym[1]) | (kv::e4m3x2(ym[2], ym[3]) << 16);
+      cr[q] = kv::e4m3x2(yr[0], yr[1]) | (kv::e4m3x2(yr[2], yr[3]) << 16);
+    }
+    store_codes(static_cast<uint8_t*>(t.m) + e, have, cm[0], cm[1]);
+    store_codes(static_cast<uint8_t*>(t.v) + e, have, cr[0], cr[1]);
+    if (lane == 0) *reinterpret_cast<float2*>(t.scales + 2 * block) = make_float2(sm.scale, sr.scale);
+  } else {
+    store8(static_cast<float*>(t.m) + e, have, m);
+    store8(static_cast<float*>(t.v) + e, have, v);
+  }
+}
+
+__global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ Table a) {
+  Hyper h;
+  if (!load_hyper(a.hyper, h)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, MOT_DEV_BAD_HYPER);
+    return;
+  }
+  int lo = 0, hi = a.n;  // the tensor of this chunk
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.first[mid] <= blockIdx.x) lo = mid;
+    else hi = mid;
+  }
+  const mot_adamw_tensor& t = a.t[lo];
+  const int64_t block = int64_t(blockIdx.x - a.first[lo]) * (CHUNK / BLOCK) + (threadIdx.x >> 5);
+  if (block * BLOCK >= t.n) return;
+  const int lane = threadIdx.x & 31, id = a.base + lo;
+  switch (t.flags) {
+    case 0: warp_block<false, false>(a, h, t, id, block, lane); break;
+    case MOT_ADAMW_GRAD_BF16: warp_block<true, false>(a, h, t, id, block, lane); break;
+    case MOT_ADAMW_STATE_E4M3: warp_block<false, true>(a, h, t, id, block, lane); break;
+    default: warp_block<true, true>(a, h, t, id, block, lane); break;
+  }
+}
+
+inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+}  // namespace adamw
+}  // namespace mot
+
+using namespace mot;
+
+extern "C" int mot_adamw_hyper_host(double lr, double beta1, double beta2, double eps, double grad_scale, int64_t step,
+                                    float* host_row) {
+  if (!host_row) return MOT_ERR_NULL;
+  if (!std::isfinite(lr) || !(lr >= 0) || !(beta1 >= 0) || !(beta1 < 1) || !(beta2 >= 0) || !(beta2 < 1) ||
+      !std::isfinite(eps) || !std::isfinite(grad_scale) || step < 1 || step >= (int64_t(1) << 31))
+    return MOT_ERR_ARG;
+  const double t = double(step);
+  float row[MOT_ADAMW_HYPER_WORDS] = {};
+  row[adamw::LR] = float(lr);
+  row[adamw::B1] = float(beta1);
+  row[adamw::C1] = float(1 - beta1);
+  row[adamw::B2] = float(beta2);
+  row[adamw::C2] = float(1 - beta2);
+  row[adamw::LR1] = float(lr / (1 - std::pow(beta1, t)));
+  row[adamw::R2] = float(1 / std::sqrt(1 - std::pow(beta2, t)));
+  row[adamw::EPS] = float(eps);
+  row[adamw::GS] = float(grad_scale);
+  // what rounds out of range in fp32 is refused like what is out of range itself
+  if (!(row[adamw::EPS] > 0) || row[adamw::B1] >= 1 || row[adamw::B2] >= 1 || !std::isfinite(row[adamw::LR]) ||
+      !std::isfinite(row[adamw::LR1]) || !std::isfinite(row[adamw::EPS]) || !std::isfinite(row[adamw::GS]))
+    return MOT_ERR_ARG;
+  const uint32_t word = uint32_t(step);
+  static_assert(sizeof(row) == 4 * MOT_ADAMW_HYPER_WORDS, "a row of 32-bit words");
+  __builtin_memcpy(&row[adamw::STEP], &word, 4);
+  __builtin_memcpy(host_row, row, sizeof(row));
+  return MOT_OK;
+}
+
+extern "C" int mot_adamw_step(const mot_adamw_tensor* tensors, int n_tensors, const float* hyper, uint64_t seed, void* ws,
+                              size_t ws_bytes, void* stream) {
+  if (!tensors || !hyper || !ws) return MOT_ERR_NULL;
+  if (n_tensors < 1 || n_tensors > 65536) return MOT_ERR_GEOMETRY;
+  for (int i = 0; i < n_tensors; ++i) {
+    const mot_adamw_tensor& t = tensors[i];
+    const bool e4m3 = (t.flags & MOT_ADAMW_STATE_E4M3) != 0;
+    if (!t.p || !t.g || !t.m || !t.v || (e4m3 && !t.scales)) return MOT_ERR_NULL;
+    if (t.n < 1 || t.n > (int64_t(1) << 40)) return MOT_ERR_GEOMETRY;
+    if ((t.flags & ~(MOT_ADAMW_GRAD_BF16 | MOT_ADAMW_STATE_E4M3)) != 0 || !(t.weight_decay >= 0.0f) ||
+        !(t.weight_decay <= 3.4e38f))
+      return MOT_ERR_ARG;
+    if (!aligned16(t.p) || !aligned16(t.p16) || !aligned16(t.g) || !aligned16(t.m) || !aligned16(t.v) ||
+        (e4m3 && !adamw::aligned8(t.scales)))
+      return MOT_ERR_ALIGN;
+  }
+  if (!aligned16(hyper) || !aligned16(ws)) return MOT_ERR_ALIGN;
+  if (ws_bytes < sizeof(PlanHeader)) return MOT_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const void* ptrs[] = {hyper, ws};
+  int dev = -1;
+  int st = check_device(s, ptrs, 2, &dev);
+  if (st != MOT_OK) return st;
+  for (int i = 0; i < n_tensors; ++i) {
+    const mot_adamw_tensor& t = tensors[i];
+    const void* mine[] = {t.p, t.p16, t.g, t.m, t.v, (t.flags & MOT_ADAMW_STATE_E4M3) ? t.scales : nullptr};
+    for (const void* p : mine)
+      if (p != nullptr && (st = check_ptr(p, dev)) != MOT_OK) return st;
+  }
+  DeviceGuard guard(dev);
+  adamw::Table a;
+  a.hyper = hyper;
+  a.seed_lo = uint32_t(seed);
+  a.seed_hi = uint32_t(seed >> 32);
+  a.err = &static_cast<PlanHeader*>(ws)->error;
+  for (int i = 0; i < n_tensors;) {
+    a.n = 0;
+    a.base = i;
+    int64_t chunks = 0;
+    for (; i < n_tensors && a.n < adamw::kMaxTensors; ++i) {
+      const int64_t mine = (tensors[i].n + adamw::CHUNK - 1) / adamw::CHUNK;
+      if (chunks + mine > (int64_t(1) << 31) - 1) break;  // one tensor has at most 2^29
+      a.t[a.n] = tensors[i];
+      a.first[a.n++] = uint32_t(chunks);
+      chunks += mine;
+    }
+    a.first[a.n] = uint32_t(chunks);
+    adamw::adamw_kernel<<<unsigned(chunks), adamw::THREADS, 0, s>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return MOT_ERR_CUDA;
+  }
+  return MOT_OK;
+}

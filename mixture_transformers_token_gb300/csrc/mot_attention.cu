@@ -77,6 +77,8 @@ struct Args {
   float c;              // scale * log2(e)
   uint16_t* out;        // [T][Hq D]
   uint32_t* err;
+  float* lse;           // [Hq][T] ln of each row's softmax sum, or null
+  float scale;
 };
 
 // 2^x: CUDA's exp2f (the library's accurate function, with subnormal results; this code is
@@ -480,6 +482,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (ok)
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&o_full[t]), uint32_t(nblk - 1) & 1u, abort_flag, a.err));
       const float rl = __frcp_rn(l);  // one rounded reciprocal per row, then products
+      if (a.lse != nullptr && ok && valid)
+        a.lse[int64_t(h) * a.T + q0 + i] = __fadd_rn(__fmul_rn(m, a.scale), logf(l));
       if (i0 + t * BQ + BQ <= nq) {
         // every row of the tile is a query: the bf16 tile goes to the tile's Q buffer (no MMA
         // reads it any more) in the 128-byte swizzled box layout, then out by tensor stores.
@@ -562,20 +566,21 @@ static int launch(const mot_bf16* qkv, const Args& a, int n_tiles_max, cudaStrea
 
 using namespace mot;
 
-extern "C" int mot_joint_attention(const mot_bf16* qkv, int64_t T, int Hq, int Hkv, int D, const int32_t* seqs,
-                                   int n_seq, float scale, void* ws, size_t ws_bytes, mot_bf16* out, void* stream) {
+// `lse` may be null.
+static int joint_attention(const mot_bf16* qkv, int64_t T, int Hq, int Hkv, int D, const int32_t* seqs, int n_seq,
+                           float scale, void* ws, size_t ws_bytes, mot_bf16* out, float* lse, void* stream) {
   if (!qkv || !seqs || !ws || !out) return MOT_ERR_NULL;
   if (T < 1 || T > MOT_MAX_TOKENS) return MOT_ERR_GEOMETRY;
   if (D != 64 && D != 128) return MOT_ERR_GEOMETRY;
   if (Hq < 1 || Hkv < 1 || Hq > 1024 || Hkv > 1024 || Hq % Hkv != 0) return MOT_ERR_GEOMETRY;
   if (n_seq < 1 || n_seq > MOT_MAX_TOKENS) return MOT_ERR_GEOMETRY;
   if (!(scale > 0.0f) || !(scale < 3.0e38f)) return MOT_ERR_ARG;
-  if (!aligned16(qkv) || !aligned16(seqs) || !aligned16(ws) || !aligned16(out)) return MOT_ERR_ALIGN;
+  if (!aligned16(qkv) || !aligned16(seqs) || !aligned16(ws) || !aligned16(out) || !aligned16(lse)) return MOT_ERR_ALIGN;
   if (ws_bytes < sizeof(PlanHeader)) return MOT_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const void* ptrs[] = {qkv, seqs, ws, out};
+  const void* ptrs[] = {qkv, seqs, ws, out, lse};
   int dev = -1;
-  int st = check_device(s, ptrs, 4, &dev);
+  int st = check_device(s, ptrs, 5, &dev);
   if (st != MOT_OK) return st;
   DeviceGuard guard(dev);
   attn::Args a{};
@@ -587,10 +592,24 @@ extern "C" int mot_joint_attention(const mot_bf16* qkv, int64_t T, int Hq, int H
   a.c = scale * 1.4426950408889634f;
   a.out = out;
   a.err = &static_cast<PlanHeader*>(ws)->error;
+  a.lse = lse;
+  a.scale = scale;
   // every sequence has at most nq / 256 + 1 work items (pairs of 128-row tiles) and the query
   // ranges do not overlap (checked on the device), so T / 256 + n_seq bounds their count
   const int64_t tiles = (T + attn::TILES * attn::BQ - 1) / (attn::TILES * attn::BQ) + n_seq;
   if (tiles * Hq > (int64_t(1) << 31) - 1) return MOT_ERR_GEOMETRY;
   if (D == 64) return attn::launch<64>(qkv, a, int(tiles), s);
   return attn::launch<128>(qkv, a, int(tiles), s);
+}
+
+extern "C" int mot_joint_attention(const mot_bf16* qkv, int64_t T, int Hq, int Hkv, int D, const int32_t* seqs,
+                                   int n_seq, float scale, void* ws, size_t ws_bytes, mot_bf16* out, void* stream) {
+  return joint_attention(qkv, T, Hq, Hkv, D, seqs, n_seq, scale, ws, ws_bytes, out, nullptr, stream);
+}
+
+extern "C" int mot_joint_attention_lse(const mot_bf16* qkv, int64_t T, int Hq, int Hkv, int D, const int32_t* seqs,
+                                       int n_seq, float scale, void* ws, size_t ws_bytes, mot_bf16* out, float* lse,
+                                       void* stream) {
+  if (!lse) return MOT_ERR_NULL;
+  return joint_attention(qkv, T, Hq, Hkv, D, seqs, n_seq, scale, ws, ws_bytes, out, lse, stream);
 }

@@ -946,3 +946,202 @@ def g_flow_noise(seeds, step, N):
         out[r, 1::2] = rad * np.sin(ang)
     return out
 
+
+
+# ---------------------------------------------------------------------------
+# The training step's other gradients: joint attention, the QK norm and RoPE; and the AdamW update
+# ---------------------------------------------------------------------------
+#
+# [RFC-435] §3 BAGEL-specific rules: phase A trains the gen weight set, and the frozen und operators still
+# need dX. The pages hold no formulas for these gradients: they are the derivatives of the forward
+# definitions above, the bf16 casts differentiated as the identity.
+
+U32 = 2.0 ** -24  # half a step of fp32, relative
+U16 = 2.0 ** -8   # half a step of bf16, relative
+
+
+def attention_sees(nq, nk, nc) -> np.ndarray:
+    """[nq][nk]: whether query i sees key j (bottom-right aligned, rows below nc causal)."""
+    i, j = np.arange(nq)[:, None], np.arange(nk)[None, :]
+    return np.where(i < nc, j <= nk - nq + i, True)
+
+
+def g_attention_lse(qkv, seqs, Hq: int, Hkv: int, D: int, scale: float | None = None):
+    """ln of every query row's softmax sum [Hq][T] in float64 (0 for rows that are no query), and the rounding of
+    a score sum |q||k| scale, the largest of each row."""
+    qkv = np.asarray(qkv, np.float64)
+    sc = 1.0 / np.sqrt(D) if scale is None else float(scale)
+    lse, s_abs = np.zeros((Hq, qkv.shape[0])), np.zeros((Hq, qkv.shape[0]))
+    for q0, k0, nq, nk, nc in seqs:
+        see = attention_sees(nq, nk, nc)
+        for h in range(Hq if nq else 0):
+            g = h // (Hq // Hkv)
+            q, k = qkv[q0:q0 + nq, h * D:(h + 1) * D], qkv[k0:k0 + nk, (Hq + g) * D:(Hq + g + 1) * D]
+            s = np.where(see, q @ k.T * sc, -np.inf)
+            m = s.max(1)
+            lse[h, q0:q0 + nq] = m + np.log(np.exp(s - m[:, None]).sum(1))
+            s_abs[h, q0:q0 + nq] = (np.where(see, np.abs(q) @ np.abs(k).T, 0.0) * sc).max(1)
+    return lse, s_abs
+
+
+def g_joint_attention_backward(dout, qkv, out, lse, seqs, Hq: int, Hkv: int, D: int, scale: float | None = None):
+    """Gradient of g_joint_attention with respect to qkv in float64, from the forward's out and lse [Hq][T]: P =
+    exp(scale S - lse), dS = P (dP - sum dout out). Returns dqkv, which columns are written, and err, a bound on the
+    difference of a calculation in fp32 whose P and dS are rounded once to bf16 and whose result once more."""
+    dout, qkv, out, lse = (np.asarray(x, np.float64) for x in (dout, qkv, out, lse))
+    sc = 1.0 / np.sqrt(D) if scale is None else float(scale)
+    G = Hq // Hkv
+    d, err, terms = np.zeros_like(qkv), np.zeros_like(qkv), np.zeros_like(qkv)
+    written = np.zeros(qkv.shape, bool)
+    count = np.zeros(qkv.shape)
+    for q0, k0, nq, nk, nc in seqs:
+        see = attention_sees(nq, nk, nc)
+        R, C = slice(q0, q0 + nq), slice(k0, k0 + nk)
+        written[R, :Hq * D] = True
+        written[C, Hq * D:] = True
+        for h in range(Hq if nq else 0):
+            g = h // G
+            at_q = (R, slice(h * D, (h + 1) * D))
+            at_k, at_v = (C, slice((Hq + g) * D, (Hq + g + 1) * D)), (C, slice((Hq + Hkv + g) * D, (Hq + Hkv + g + 1) * D))
+            q, k, v, do, o = qkv[at_q], qkv[at_k], qkv[at_v], dout[at_q], out[at_q]
+            L = lse[h, R][:, None]
+            s = q @ k.T * sc
+            p = np.where(see, np.exp(np.where(see, s - L, 0.0)), 0.0)
+            dp = do @ v.T
+            delta = (do * o).sum(1)[:, None]
+            ds = p * (dp - delta)
+            d[at_q] += sc * ds @ k
+            d[at_k] += sc * ds.T @ q
+            d[at_v] += p.T @ do
+            # relative error of p before its cast: the score's sum (each of D additions, counted twice for a
+            # rounding that is not to nearest), the roundings of lse / scale and of the two operations on it,
+            # the log2 e in c, and two units of 2^x
+            e_p = (np.abs(q) @ np.abs(k).T * sc) * 2 * D * U32 + (np.abs(s) + np.abs(L)) * 6 * U32 + 6 * U32
+            # of dP and delta, then of their difference and product, times P; and P's own error
+            e_ds = p * ((np.abs(do) @ np.abs(v).T + np.abs(do * o).sum(1)[:, None]) * 2 * D * U32) + np.abs(ds) * (e_p + 4 * U32)
+            e_ds = e_ds * (1 + U16) + np.abs(ds) * U16
+            err[at_q] += sc * e_ds @ np.abs(k)
+            err[at_k] += sc * e_ds.T @ np.abs(q)
+            err[at_v] += (p * (e_p * (1 + U16) + U16)).T @ np.abs(do)
+            terms[at_q] += sc * np.abs(ds) @ np.abs(k)
+            terms[at_k] += sc * np.abs(ds).T @ np.abs(q)
+            terms[at_v] += p.T @ np.abs(do)
+            count[at_q] += nk + 2
+            count[at_k] += nq + 2
+            count[at_v] += nq + 2
+    err += 2 * count * U32 * (terms + err)          # the long sums, and scale
+    err += (np.abs(d) + err) * U16 * (1 + U16)      # the last cast
+    return {"dqkv": d, "written": written, "err": err}
+
+
+def g_qk_norm_rope_backward(d_out, x, q_norm, k_norm, cos, sin, mod, Hq: int, Hkv: int, D: int, eps: float):
+    """Gradient through the QK norm and RoPE in float64. d_out, x [T][(Hq + 2 Hkv) D]; cos, sin [T][D/2]. Returns dx
+    (V columns: d_out's), dw [2 kinds][2 sets][D], and bounds err_dx, err_dw on a calculation in fp32 (dx rounded once to
+    bf16)."""
+    d_out, x = np.asarray(d_out, np.float64), np.asarray(x, np.float64)
+    T, nqk, h2 = x.shape[0], Hq + Hkv, D // 2
+    e = _check_mod(mod)
+    xx = x[:, :nqk * D].reshape(T, nqk, D)
+    d = d_out[:, :nqk * D].reshape(T, nqk, D)
+    c, s = np.asarray(cos, np.float64)[:, None, :], np.asarray(sin, np.float64)[:, None, :]
+    du = np.concatenate([d[..., :h2] * c + d[..., h2:] * s, d[..., h2:] * c - d[..., :h2] * s], -1)
+    a_du = np.concatenate([np.abs(d[..., :h2] * c) + np.abs(d[..., h2:] * s),
+                           np.abs(d[..., h2:] * c) + np.abs(d[..., :h2] * s)], -1)
+    w = np.concatenate([np.repeat(np.asarray(q_norm, np.float64)[e][:, None], Hq, 1),
+                        np.repeat(np.asarray(k_norm, np.float64)[e][:, None], Hkv, 1)], 1)
+    rstd = 1.0 / np.sqrt((xx * xx).mean(-1, keepdims=True) + _eps32(eps))
+    xh, g = xx * rstd, du * w
+    dx = rstd * (g - xh * (g * xh).mean(-1, keepdims=True))
+    size = rstd * (a_du * np.abs(w) + np.abs(xh) * (a_du * np.abs(w) * np.abs(xh)).mean(-1, keepdims=True))
+    # rstd: half the error of a sum of D squares, and four operations; it enters three times beside the sum of D
+    # products and at most ten operations of one rounding each
+    err = size * ((3 * (D / 2 + 4) + D + 10) * U32) * 1.01
+    err = err + (np.abs(dx) + err) * U16 * (1 + U16)
+    full, full_err = d_out.copy(), np.zeros_like(d_out)
+    full[:, :nqk * D], full_err[:, :nqk * D] = dx.reshape(T, -1), err.reshape(T, -1)
+    dw, err_dw = np.zeros((2, 2, D)), np.zeros((2, 2, D))
+    for k, heads in enumerate((slice(0, Hq), slice(Hq, nqk))):
+        for i in (0, 1):
+            t, a = (du * xh)[e == i][:, heads], (a_du * np.abs(xh))[e == i][:, heads]
+            dw[k, i] = t.sum((0, 1))
+            err_dw[k, i] = a.sum((0, 1)) * (t.shape[0] * t.shape[1] + D / 2 + 10) * U32 * 1.01
+    return {"dx": full, "err_dx": full_err, "dw": dw, "err_dw": err_dw}
+
+
+def philox4x32_7(ctr, key):
+    """Philox4x32 with seven rounds on arrays of 32-bit words (Salmon et al., SC 2011): as philox4x64_10, with 32-bit
+    words, the multipliers 0xD2511F53 and 0xCD9E8D57 and the key increments 0x9E3779B9 and 0xBB67AE85."""
+    low = np.uint64(0xFFFFFFFF)
+    x0, x1, x2, x3 = (np.asarray(c, np.uint64) & low for c in ctr)
+    k0, k1 = (int(k) & 0xFFFFFFFF for k in key)
+    for _ in range(7):
+        p0, p1 = np.uint64(0xD2511F53) * x0, np.uint64(0xCD9E8D57) * x2
+        x0, x1, x2, x3 = (p1 >> np.uint64(32)) ^ x1 ^ np.uint64(k0), p1 & low, (p0 >> np.uint64(32)) ^ x3 ^ np.uint64(k1), p0 & low
+        k0, k1 = (k0 + 0x9E3779B9) & 0xFFFFFFFF, (k1 + 0xBB67AE85) & 0xFFFFFFFF
+    return x0, x1, x2, x3
+
+
+def adamw_words(n: int, tensor: int, step: int, seed: int) -> np.ndarray:
+    """The random 32-bit word of each of a tensor's n elements."""
+    b = np.arange(-(-n // 4), dtype=np.uint64)
+    key = (seed & 0xFFFFFFFF, seed >> 32 & 0xFFFFFFFF)
+    words = philox4x32_7((b & np.uint64(0xFFFFFFFF), b >> np.uint64(32), np.full_like(b, tensor), np.full_like(b, step)), key)
+    return np.stack(words, 1).reshape(-1)[:n].astype(np.uint32)
+
+
+def adamw_quantise(x, bits16, keep_positive: bool = False):
+    """fp32 values [n] to (e4m3 values, scales [ceil(n / 256)]), in fp32 as defined: scale = a (1 / 448), y = min(|x|
+    ((1 / a) 448), 448), which lies k steps and a rest above zero or above its binade's start; the rest, plus bits16 / 2^16 of a
+    step, decides between the two neighbours. keep_positive: a positive value has at least the smallest code."""
+    x = np.asarray(x, F32)
+    n = x.size
+    pad = (-n) % 256
+    xb = np.concatenate([x, np.zeros(pad, F32)]).reshape(-1, 256)
+    up = np.concatenate([np.asarray(bits16, np.float64), np.zeros(pad)]).reshape(-1, 256) / 65536.0
+    a = np.abs(xb).max(1)
+    fine = np.isfinite(a)
+    some = fine & (a >= F32(2.0 ** -100))
+    with np.errstate(all="ignore"):
+        scale = np.where(fine, np.where(some, a * (F32(1) / F32(448)), F32(0)), F32(np.nan)).astype(F32)
+        inv = np.where(some, (F32(1) / a) * F32(448), F32(0)).astype(F32)
+        y = np.where(fine[:, None], np.minimum(np.abs(xb) * inv[:, None], F32(448)), F32(0)).astype(F32)
+    y64 = np.where(y < 2.0 ** -6, (y + F32(2.0 ** -6)).astype(F32), y).astype(np.float64)  # subnormals: moved to that step
+    _, ex = np.frexp(y64)
+    unit = np.ldexp(1.0, ex - 4)  # a step of the binade [2^(ex - 1), 2^ex)
+    z = np.floor(y64 / unit + up) * unit
+    z = np.where(y < 2.0 ** -6, z - 2.0 ** -6, z)
+    if keep_positive:
+        z = np.where((xb > 0) & some[:, None], np.maximum(z, 2.0 ** -9), z)
+    z = np.copysign(z, xb)
+    return z.reshape(-1)[:n], scale
+
+
+def adamw_hyper(lr, beta1, beta2, eps, step, grad_scale=1.0) -> np.ndarray:
+    """The nine fp32 numbers of a step, each rounded once from double."""
+    return np.array([lr, beta1, 1 - beta1, beta2, 1 - beta2, lr / (1 - beta1 ** step), 1 / np.sqrt(1 - beta2 ** step), eps,
+                     grad_scale], np.float64).astype(F32)
+
+
+def e_adamw(p, g, m, v, hyper, weight_decay, tensor: int = 0, step: int = 1, seed: int = 0, scales=None):
+    """One tensor's update with every fp32 operation rounded on its own. fp32 states (scales None): m, v; else e4m3
+    values with scales [blocks][2], v holding sqrt(v). Returns p, m, v (and scales)."""
+    lr, b1, c1, b2, c2, lr1, r2, eps, gs = (F32(x) for x in hyper)
+    p, g = np.asarray(p, F32), np.asarray(g, F32)
+    with np.errstate(all="ignore"):
+        if scales is None:
+            m, v = np.asarray(m, F32), np.asarray(v, F32)
+        else:
+            each = np.repeat(np.asarray(scales, F32), 256, 0)[:p.size]
+            m, v = np.asarray(m, F32) * each[:, 0], np.asarray(v, F32) * each[:, 1]
+            v = v * v
+        g = g * gs
+        m = m * b1 + g * c1
+        v = v * b2 + (g * g) * c2
+        r = np.sqrt(v)
+        p = p - ((m * lr1) / (r * r2 + eps) + p * (lr * F32(weight_decay)))
+    if scales is None:
+        return p, m, v
+    words = adamw_words(p.size, tensor, step, seed)
+    qm, sm = adamw_quantise(m, words & 0xFFFF)
+    qr, sr = adamw_quantise(r, words >> 16, keep_positive=True)
+    return p, qm, qr, np.stack([sm, sr], 1)
