@@ -1,146 +1,1032 @@
-// Gradient of joint attention with respect to its fused QKV rows.
+// Gradient of joint attention with respect to its fused QKV rows, on the 5th-generation tensor cores.
 //
 // Sources: [RFC][BAGEL-7B-MoT][CUDA/ROCm] WS1/WS2 kernel roadmap and integration plan #435 (§1 Motivation item 2, §2 Reference
 // hazards: the masks, as in the forward; §3 BAGEL-specific rules: dX passes through the frozen und operators; §3 Numerical
 // contract: fixed accumulation order, no atomics).
 //
 // Per query i and visible key j: P = 2^((S - lse / scale) c) with c = scale log2 e, dP = dout_i . v_j, delta_i = dout_i . out_i,
-// dS = P (dP - delta_i); dq_i = scale sum_j dS k_j, dk_j = scale sum_i dS q_i, dv_j = sum_i P dout_i.
+// dS = P (dP - delta_i); dq_i = scale sum_j dS k_j, dk_j = scale sum_i dS q_i, dv_j = sum_i P dout_i. P is recomputed from S: no
+// probability is stored.
 //
-// One warp per query row and head (dq) and per key row and KV head (dk, dv), in fp32: the plain kernels.
+// dq sums over keys, dk and dv over queries, and neither sum may be cut between CTAs in an order that the schedule sets. So
+// there are two kernels, each with its sums in tensor memory from the first block to the last, at the price of forming S and dP
+// twice: seven products of 128 x 128 x D a block instead of five.
+//
+//   stats_kernel  -delta and -lse / scale of every row and head, [Hq][T] (reads dout and out once); its first CTA makes the
+//                 lists of work.
+//   dkv_kernel    one CTA per (tile of keys, KV head, share of its query heads). The borders of the sequences' key ranges cut
+//                 the pack's rows into runs that the same sequences see, and a tile is 128 rows of a run or what is left of it.
+//                 So nothing that a sequence holds reaches the sums of rows that are not its keys, as it would through 0 NaN
+//                 in a tile of two sequences. Over the sequences that see these rows, the share's heads and the blocks of 128 queries, S' = K Q' and dP' = V dO' (keys in the rows),
+//                 P' and dS' as bf16 into tensor memory in the places of S' and dP', dV += P' dO, dK += dS' Q with A from
+//                 tensor memory. The CTAs of a cluster hold the shares of one KV head; each sends its sums to shared memory
+//                 and adds and writes its part of the rows, in the order of the shares, through the cluster's shared memory.
+//   dq_kernel     one CTA per (128 queries of a sequence, head): over the blocks of 128 keys, S = Q K', dP = dO V', dS as bf16
+//                 into tensor memory in the place of S, dQ += dS K. Its grid starts while the last CTAs of dkv_kernel run.
+//
+// A block's tiles are copied by TMA (128-byte swizzle) two or three blocks ahead; one warp copies, one issues the products, and
+// eight compute (each thread half of the 128 columns of one row). Rows past a sequence's end inside its last block are other
+// sequences' rows: they are zeroed in shared memory where they would be summed over, and masked where they are columns.
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "mot.h"
+#include "mot_attention.cuh"
 #include "mot_device.cuh"
 #include "mot_host.hpp"
 
 namespace mot {
 namespace attnb {
 
-constexpr int WARPS = 8, THREADS = 32 * WARPS;
+using namespace attn;
+
+constexpr int BQ = 128, BK = 128;
+constexpr int COMPUTE_WARPS = 8;
+constexpr int THREADS = 32 * (2 + COMPUTE_WARPS);
+constexpr uint32_t SUB = 128 * 64 * 2;  // a [128 rows x 64 columns] bf16 swizzled tile
+
+// Lists in the workspace, made by stats_kernel's first CTA.
+struct Work {
+  int4* tiles;    // (first row, rows, first and last sequence that may see them), ascending
+  int2* items;    // (sequence, first query row) of dq_kernel, for more than kSortedSeqs sequences
+  int32_t* counts;  // tiles, items
+  // scratch: changes of the number of sequences that see a row, at each row; borders, a bit a row; the borders in order
+  int32_t* change;
+  uint32_t* border;
+  int32_t* runs;
+  int max_tiles, max_items;
+};
 
 struct Args {
-  const uint16_t* dout;
-  const uint16_t* qkv;
-  const uint16_t* out;
-  const float* lse;
-  const int32_t* seqs;
+  const int32_t* seqs;  // [n_seq][5]
   int n_seq, T, Hq, Hkv;
-  float c, scale, rscale;
-  float* delta;  // [Hq][T]
+  int shares;           // CTAs of a cluster of dkv_kernel
+  Work work;
+  float c, scale;
+  const float* nlse;    // [Hq][T] -lse / scale
+  const float* ndelta;  // [Hq][T] -delta
   uint16_t* dqkv;
   uint32_t* err;
 };
 
-__device__ __forceinline__ bool bad_seq(const int32_t* d, int T) {
-  const int q0 = d[0], k0 = d[1], nq = d[2], nk = d[3], c = d[4];
-  return q0 < 0 || k0 < 0 || nq < 0 || nk < 1 || c < 0 || c > nq || (c > 0 && nk < nq) ||
-         int64_t(q0) + nq > T || int64_t(k0) + nk > T;
-}
+// ---------------------------------------------------------------------------
+// -delta and -lse / scale
+// ---------------------------------------------------------------------------
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, off));
-  return x;
-}
+struct StatsArgs {
+  const uint16_t* dout;
+  const uint16_t* out;
+  const float* lse;
+  int T, Hq;
+  float rscale;
+  float* nlse;
+  float* ndelta;
+  const int32_t* seqs;
+  int n_seq;
+  Work work;
+  uint32_t* err;
+};
 
-// A lane's D / 32 values of a head, or their dot product with another row's.
-template <int D>
-__device__ __forceinline__ void load(const uint16_t* p, int lane, float (&x)[D / 32]) {
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) x[i] = bf_to_f(p[lane + 32 * i]);
-}
-template <int D>
-__device__ __forceinline__ float dot(const float (&a)[D / 32], const float (&b)[D / 32]) {
-  float s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) s = __fadd_rn(s, __fmul_rn(a[i], b[i]));
-  return warp_sum(s);
-}
-template <int D>
-__device__ __forceinline__ void add(float (&s)[D / 32], float f, const float (&x)[D / 32]) {
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) s[i] = __fadd_rn(s[i], __fmul_rn(f, x[i]));
-}
-template <int D>
-__device__ __forceinline__ void store(uint16_t* p, int lane, float f, const float (&x)[D / 32]) {
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) p[lane + 32 * i] = f_to_bf(__fmul_rn(f, x[i]));
-}
+constexpr int STATS_THREADS = 256;
 
-template <int D>
-__global__ void __launch_bounds__(THREADS) dq_kernel(const Args a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = int64_t(blockIdx.x) * WARPS + (threadIdx.x >> 5);
-  if (item >= int64_t(a.T) * a.Hq) return;
-  const int row = int(item / a.Hq), h = int(item % a.Hq), g = h / (a.Hq / a.Hkv);
-  const int64_t N = int64_t(a.Hq + 2 * a.Hkv) * D;
-  for (int s = 0; s < a.n_seq; ++s) {
-    const int32_t* d = a.seqs + 5 * s;
-    if (bad_seq(d, a.T)) {
-      if (item == 0 && lane == 0) atomicOr(a.err, MOT_DEV_BAD_SEQUENCE);
-      continue;
-    }
-    const int i = row - d[0];
-    if (i < 0 || i >= d[2]) continue;
-    float q[D / 32], dy[D / 32], o[D / 32], sum[D / 32] = {};
-    load<D>(a.qkv + row * N + h * D, lane, q);
-    load<D>(a.dout + (int64_t(row) * a.Hq + h) * D, lane, dy);
-    load<D>(a.out + (int64_t(row) * a.Hq + h) * D, lane, o);
-    const float delta = dot<D>(dy, o);
-    if (lane == 0) a.delta[int64_t(h) * a.T + row] = delta;
-    const float l = __fmul_rn(a.lse[int64_t(h) * a.T + row], a.rscale);
-    const int lim = i < d[4] ? d[3] - d[2] + i + 1 : d[3];
-    for (int j = 0; j < lim; ++j) {
-      float k[D / 32], v[D / 32];
-      load<D>(a.qkv + int64_t(d[1] + j) * N + (a.Hq + g) * D, lane, k);
-      load<D>(a.qkv + int64_t(d[1] + j) * N + (a.Hq + a.Hkv + g) * D, lane, v);
-      const float p = exp2f(__fmul_rn(__fsub_rn(dot<D>(q, k), l), a.c));
-      add<D>(sum, __fmul_rn(p, __fsub_rn(dot<D>(dy, v), delta)), k);
-    }
-    store<D>(a.dqkv + row * N + h * D, lane, a.scale, sum);
+// Sum over the CTA's threads before this one; `total` is the whole sum.
+__device__ __forceinline__ int scan_before(int x, int* room, int& total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int incl = x;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += o;
   }
+  __syncthreads();  // the last use of `room`
+  if (lane == 31) room[warp] = incl;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < STATS_THREADS / 32; ++w) {
+    if (w < warp) before += room[w];
+    total += room[w];
+  }
+  return before + incl - x;
 }
 
-template <int D>
-__global__ void __launch_bounds__(THREADS) dkv_kernel(const Args a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = int64_t(blockIdx.x) * WARPS + (threadIdx.x >> 5);
-  if (item >= int64_t(a.T) * a.Hkv) return;
-  const int row = int(item / a.Hkv), g = int(item % a.Hkv), G = a.Hq / a.Hkv;
-  const int64_t N = int64_t(a.Hq + 2 * a.Hkv) * D;
-  float k[D / 32], v[D / 32], dk[D / 32] = {}, dv[D / 32] = {};
-  load<D>(a.qkv + row * N + (a.Hq + g) * D, lane, k);
-  load<D>(a.qkv + row * N + (a.Hq + a.Hkv + g) * D, lane, v);
-  bool key = false;
-  for (int s = 0; s < a.n_seq; ++s) {
-    const int32_t* d = a.seqs + 5 * s;
-    if (bad_seq(d, a.T)) continue;
-    const int j = row - d[1];
-    if (j < 0 || j >= d[3]) continue;
-    key = true;
-    for (int h = g * G; h < (g + 1) * G; ++h)
-      for (int i = 0; i < d[2]; ++i) {
-        if (i < d[4] && j > d[3] - d[2] + i) continue;
-        const int64_t r = d[0] + i;
-        float q[D / 32], dy[D / 32];
-        load<D>(a.qkv + r * N + h * D, lane, q);
-        load<D>(a.dout + (r * a.Hq + h) * D, lane, dy);
-        const float l = __fmul_rn(a.lse[int64_t(h) * a.T + r], a.rscale);
-        const float p = exp2f(__fmul_rn(__fsub_rn(dot<D>(q, k), l), a.c));
-        add<D>(dv, p, dy);
-        add<D>(dk, __fmul_rn(p, __fsub_rn(dot<D>(dy, v), a.delta[int64_t(h) * a.T + r])), q);
+// The lists of work, by one CTA: T / 8 + 4 T bytes to clear and to read, and the descriptors.
+__device__ void make_work(const StatsArgs& a, int* room) {
+  const Work& w = a.work;
+  const int tid = threadIdx.x, words = (a.T >> 5) + 1;
+  for (int i = tid; i <= a.T; i += STATS_THREADS) w.change[i] = 0;
+  for (int i = tid; i < words; i += STATS_THREADS) w.border[i] = 0u;
+  __syncthreads();
+  // every good descriptor's borders and changes; its items; and that the query ranges do not overlap
+  int items = 0;
+  int64_t rows = 0;
+  bool bad_any = false;
+  for (int s0 = 0; s0 < a.n_seq; s0 += STATS_THREADS) {
+    const int s = s0 + tid;
+    int mine = 0;
+    if (s < a.n_seq) {
+      const int32_t* d = a.seqs + 5 * int64_t(s);
+      if (bad_seq(d, a.T)) {
+        bad_any = true;
+      } else {
+        const int k0 = d[1], k1 = d[1] + d[3];
+        atomicAdd(w.change + k0, 1);
+        atomicAdd(w.change + k1, -1);
+        atomicOr(w.border + (k0 >> 5), 1u << (k0 & 31));
+        atomicOr(w.border + (k1 >> 5), 1u << (k1 & 31));
+        mine = (d[2] + BQ - 1) / BQ;
+        rows += d[2];
       }
+    }
+    if (a.n_seq > kSortedSeqs) {
+      int total;
+      const int at = items + scan_before(mine, room, total);
+      for (int r = 0; r < mine; ++r)  // the last queries of a sequence, which see the most keys, first
+        if (at + r < w.max_items) w.items[at + r] = make_int2(s, (mine - 1 - r) * BQ);
+      items = items + total < w.max_items ? items + total : w.max_items;  // more only where queries overlap
+    } else {
+      items += mine;  // this thread's own
+    }
   }
-  if (!key) return;
-  store<D>(a.dqkv + row * N + (a.Hq + g) * D, lane, a.scale, dk);
-  store<D>(a.dqkv + row * N + (a.Hq + a.Hkv + g) * D, lane, 1.0f, dv);
+  {
+    int64_t sum = 0;  // rows of all threads, 21 bits at a time: 256 of them fit 32 bits
+    for (int part = 0; part < 3; ++part) {
+      int total;
+      scan_before(int((rows >> (21 * part)) & 0x1FFFFF), room, total);
+      sum += int64_t(total) << (21 * part);
+    }
+    const bool any = __syncthreads_or(bad_any ? 1 : 0) != 0;
+    if (tid == 0 && (any || sum > a.T)) atomicOr(a.err, MOT_DEV_BAD_SEQUENCE);
+  }
+  // the borders in ascending order
+  int n = 0;
+  for (int w0 = 0; w0 < words; w0 += STATS_THREADS) {
+    uint32_t bits = w0 + tid < words ? __ldcg(w.border + w0 + tid) : 0u;
+    int total;
+    int at = n + scan_before(__popc(bits), room, total);
+    for (; bits != 0u; bits &= bits - 1) w.runs[at++] = (w0 + tid) * 32 + __ffs(bits) - 1;
+    n += total;
+  }
+  __syncthreads();
+  // the runs that some sequence sees, in tiles
+  int seen = 0, tiles = 0;
+  for (int i0 = 0; i0 < n; i0 += STATS_THREADS) {
+    const int i = i0 + tid;
+    const int from = i < n ? w.runs[i] : 0, to = i + 1 < n ? w.runs[i + 1] : from;
+    int total;
+    const int change = i < n ? __ldcg(w.change + from) : 0;
+    const int seers = seen + scan_before(change, room, total) + change;
+    seen += total;
+    const int mine = i < n && seers > 0 ? (to - from + BK - 1) / BK : 0;
+    const int at = tiles + scan_before(mine, room, total);
+    for (int r = 0; r < mine; ++r) {
+      const int row = from + r * BK;
+      w.tiles[at + r] = make_int4(row, to - row < BK ? to - row : BK, a.n_seq, -1);
+    }
+    tiles += total;
+  }
+  __syncthreads();
+  // the first and the last sequence of each tile: a warp a sequence, a lane a tile
+  for (int s = tid >> 5; s < a.n_seq; s += STATS_THREADS / 32) {
+    const int32_t* d = a.seqs + 5 * int64_t(s);
+    if (bad_seq(d, a.T)) continue;
+    int lo = 0, hi = tiles;  // the tile that begins with the sequence's first key
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (w.tiles[mid].x <= d[1]) lo = mid;
+      else hi = mid;
+    }
+    for (int i = lo + (tid & 31); i < tiles && w.tiles[i].x < d[1] + d[3]; i += 32) {
+      atomicMin(&w.tiles[i].z, s);
+      atomicMax(&w.tiles[i].w, s);
+    }
+  }
+  if (tid == 0) {
+    w.counts[0] = tiles;
+    w.counts[1] = items < w.max_items ? items : w.max_items;
+  }
+}
+
+// A CTA takes 32 rows and 32 heads; D / 8 lanes a row and head, the sums through shared memory into rows of [Hq][T].
+template <int D>
+__global__ void __launch_bounds__(STATS_THREADS) stats_kernel(const StatsArgs a) {
+  constexpr int LANES = D / 8, GROUPS = STATS_THREADS / LANES;
+  __shared__ float sums[32][33];
+  pdl_trigger();
+  if (blockIdx.x == 0) {
+    if (blockIdx.y == 0) make_work(a, reinterpret_cast<int*>(&sums[0][0]));
+    return;
+  }
+  const int sub = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+  const int row0 = int(blockIdx.x - 1) * 32, h0 = int(blockIdx.y) * 32;
+  const int nh = a.Hq - h0 < 32 ? a.Hq - h0 : 32;
+#pragma unroll 4
+  for (int i = grp; i < 32 * 32; i += GROUPS) {
+    const int r = i >> 5, h = i & 31;
+    float s = 0.0f;
+    if (row0 + r < a.T && h < nh) {
+      const int64_t off = (int64_t(row0 + r) * a.Hq + h0 + h) * D + 8 * sub;
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.dout + off)), y = __ldg(reinterpret_cast<const uint4*>(a.out + off));
+      s = __fadd_rn(__fmul_rn(bf_lo(x.x), bf_lo(y.x)), __fmul_rn(bf_hi(x.x), bf_hi(y.x)));
+      s = __fadd_rn(s, __fadd_rn(__fmul_rn(bf_lo(x.y), bf_lo(y.y)), __fmul_rn(bf_hi(x.y), bf_hi(y.y))));
+      s = __fadd_rn(s, __fadd_rn(__fmul_rn(bf_lo(x.z), bf_lo(y.z)), __fmul_rn(bf_hi(x.z), bf_hi(y.z))));
+      s = __fadd_rn(s, __fadd_rn(__fmul_rn(bf_lo(x.w), bf_lo(y.w)), __fmul_rn(bf_hi(x.w), bf_hi(y.w))));
+    }
+#pragma unroll
+    for (int off = LANES / 2; off >= 1; off >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
+    if (sub == 0) sums[h][r] = s;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * 32; i += STATS_THREADS) {
+    const int h = i >> 5, r = i & 31;
+    if (row0 + r < a.T && h < nh) {
+      const int64_t at = int64_t(h0 + h) * a.T + row0 + r;
+      a.ndelta[at] = -sums[h][r];
+      a.nlse[at] = -__fmul_rn(a.lse[at], a.rscale);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// pieces of both kernels
+// ---------------------------------------------------------------------------
+
+// The sequences that see a tile's rows, in order; used by a whole warp, the descriptors read one a lane.
+struct SeqIter {
+  const int32_t* seqs;
+  int T, row, last, lane, base;
+  uint32_t mask = 0;
+  int d[5];
+  __device__ SeqIter(const Args& a, const int4& tile, int lane_)
+      : seqs(a.seqs), T(a.T), row(tile.x), last(tile.w), lane(lane_), base(tile.z - 32) {}
+  __device__ bool next(int (&s)[5]) {
+    while (mask == 0) {
+      base += 32;
+      if (base > last) return false;
+      bool in = base + lane <= last;
+      if (in) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) d[i] = seqs[5 * int64_t(base + lane) + i];
+        in = !bad_seq(d, T) && d[1] <= row && d[1] + d[3] > row;  // all of a tile's rows or none
+      }
+      mask = __ballot_sync(0xffffffffu, in);
+    }
+    const int l = __ffs(mask) - 1;
+    mask &= mask - 1;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) s[i] = __shfl_sync(0xffffffffu, d[i], l);
+    return true;
+  }
+};
+
+// Query blocks [first, end) of a sequence that see a key of the tile from row `row` on: causal query i sees keys up to nk - nq + i.
+__device__ __forceinline__ void query_blocks(const int (&s)[5], int row, int& first, int& end) {
+  const int off = s[3] - s[2], j = row - s[1];
+  const int i = s[4] < j - off ? s[4] : j - off;
+  first = i > 0 ? i / BQ : 0;
+  end = (s[2] + BQ - 1) / BQ;
+}
+
+// Zeroes rows [from, 128) of `tiles` swizzled [128 x 64] tiles that follow one another (a row is 128 consecutive bytes).
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int tiles, int from, int lane) {
+  for (int b = 0; b < tiles; ++b)
+    for (int i = from * 8 + lane; i < 128 * 8; i += 32) *reinterpret_cast<uint4*>(tile + b * SUB + i * 16) = make_uint4(0, 0, 0, 0);
+}
+
+template <int D>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
+#pragma unroll
+  for (int b = 0; b < D / 64; ++b) tma_load_2d(dst + b * SUB, m, x + 64 * b, y, bar);
+}
+
+// D[128 x 128] = A B' of two row-major [128][DK] tiles.
+template <int DK>
+__device__ __forceinline__ void product_nt(uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
+#pragma unroll
+  for (int kk = 0; kk < DK / 16; ++kk)
+    mma_bf16(d, smem_desc_sw128(a + (kk / 4) * SUB + (kk % 4) * 32), smem_desc_sw128(b + (kk / 4) * SUB + (kk % 4) * 32), idesc,
+             kk > 0);
+}
+
+// D[128 x DN] += A B of a bf16 [128 x 128] A in tensor memory (its halves of 64 columns of K 64 TMEM columns apart) and a
+// row-major [128][DN] tile.
+template <int DN>
+__device__ __forceinline__ void product_ta(uint32_t d, uint32_t a_tmem, uint32_t b, bool accumulate) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, DN) | kIdescBMnMajor;
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_bf16_ta(d, a_tmem + (kk / 4) * 64 + (kk % 4) * 8, smem_desc_mn_sw128(b + kk * 2048, SUB), idesc, accumulate || kk > 0);
+}
+
+__device__ __forceinline__ void ld_shared_f4(uint32_t addr_cluster, float (&v)[4]) {
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(addr_cluster)
+               : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// dK and dV
+// ---------------------------------------------------------------------------
+
+template <int D>
+struct KvLayout {
+  static constexpr int STAGES = D == 128 ? 2 : 4;
+  static constexpr uint32_t TILE = 128 * D * 2;
+  static constexpr uint32_t K = 0, V = TILE;
+  static constexpr uint32_t QD = 2 * TILE;                        // STAGES of (Q, dO); at the end dV and dK in fp32
+  static constexpr uint32_t STATS = QD + STAGES * 2 * TILE;       // STAGES of (-lse / scale, -delta) of 128 queries
+  static constexpr uint32_t BAR = STATS + STAGES * 1024;
+  static constexpr size_t BYTES = 1024 + size_t(BAR) + 512;
+  static constexpr uint32_t S = 0, DP = 128, DV = 256, DK = 384;  // tensor memory
+  static_assert(2 * 128 * D * 4 <= STAGES * 2 * TILE, "the sums fit where the blocks were");
+};
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    dkv_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __grid_constant__ CUtensorMap tm_do, const Args a) {
+  using L = KvLayout<D>;
+  constexpr int STAGES = L::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
+  uint64_t* kv_full = bars;
+  uint64_t* raw = bars + 1;         // a block that is zeroed in part before it is full
+  uint64_t* full = bars + 2;        // [STAGES]
+  uint64_t* empty = bars + 6;       // [STAGES]: every product of the block is done
+  uint64_t* stat_full = bars + 10;  // [STAGES]
+  uint64_t* s_full = bars + 14;
+  uint64_t* dp_full = bars + 15;
+  uint64_t* p_full = bars + 16;
+  uint64_t* ds_full = bars + 17;
+  uint64_t* dv_done = bars + 18;
+  uint64_t* dk_done = bars + 19;
+  uint64_t* drain = bars + 20;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  int* blocks = reinterpret_cast<int*>(tmem_slot + 2);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int share = int(blockIdx.x) % a.shares, rest = int(blockIdx.x) / a.shares;
+  const int g = rest % a.Hkv, G = a.Hq / a.Hkv, heads = (G - share + a.shares - 1) / a.shares;  // g G + share, + shares, ...
+  if (threadIdx.x == 32) {
+    mbar_init(smem_u32(kv_full), 1);
+    mbar_init(smem_u32(raw), 1);
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), 1);
+      mbar_init(smem_u32(&stat_full[i]), 1);
+    }
+    mbar_init(smem_u32(s_full), 1);
+    mbar_init(smem_u32(dp_full), 1);
+    mbar_init(smem_u32(p_full), COMPUTE_WARPS);
+    mbar_init(smem_u32(ds_full), COMPUTE_WARPS);
+    mbar_init(smem_u32(dv_done), 1);
+    mbar_init(smem_u32(dk_done), 1);
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_qkv);
+    tma_prefetch_desc(&tm_do);
+  }
+  pdl_wait();     // stats_kernel, also on behalf of dq_kernel, whose grid starts after every CTA's trigger
+  pdl_trigger();
+  if (rest / a.Hkv >= __ldcg(a.work.counts)) return;  // no such tile, for every CTA of the cluster
+  const int4 tile = __ldcg(a.work.tiles + rest / a.Hkv);
+  const int row0 = tile.x;
+  if (warp == 0) {  // what there is to do
+    SeqIter it(a, tile, lane);
+    int s[5], n = 0;
+    while (it.next(s)) {
+      int first, end;
+      query_blocks(s, row0, first, end);
+      n += (end > first ? end - first : 0) * heads;
+    }
+    if (lane == 0) *blocks = n;
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int n_it = *blocks;
+
+  if (warp == 0) {
+    // ---------------- copies ----------------
+    bool ok = true;
+    int t = 0, raws = 0;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(smem_u32(kv_full), 2 * L::TILE);
+      load_tile<D>(smem_u32(smem + L::K), &tm_qkv, (a.Hq + g) * D, row0, smem_u32(kv_full));
+      load_tile<D>(smem_u32(smem + L::V), &tm_qkv, (a.Hq + a.Hkv + g) * D, row0, smem_u32(kv_full));
+    }
+    SeqIter it(a, tile, lane);
+    int s[5];
+    while (ok && it.next(s)) {
+      int first, end;
+      query_blocks(s, row0, first, end);
+      for (int hh = 0; hh < heads && ok; ++hh) {
+        const int h = g * G + share + hh * a.shares;
+        for (int b = first; b < end; ++b, ++t) {
+          const int st = t % STAGES;
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[st]), (uint32_t(t / STAGES) & 1u) ^ 1u, abort_flag, a.err));
+          if (!ok) break;
+          const int y = s[0] + b * BQ, have = s[2] - b * BQ < BQ ? s[2] - b * BQ : BQ;
+          uint8_t* q = smem + L::QD + st * 2 * L::TILE;
+          const uint32_t bar = smem_u32(have == BQ ? &full[st] : raw);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar, 2 * L::TILE);
+            load_tile<D>(smem_u32(q), &tm_qkv, h * D, y, bar);
+            load_tile<D>(smem_u32(q + L::TILE), &tm_do, h * D, y, bar);
+          }
+          float* stats = reinterpret_cast<float*>(smem + L::STATS + st * 1024);
+          const int64_t at = int64_t(h) * a.T + y;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = lane + 32 * i;
+            stats[c] = c < have ? __ldcg(a.nlse + at + c) : 0.0f;
+            stats[128 + c] = c < have ? __ldcg(a.ndelta + at + c) : 0.0f;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&stat_full[st]));
+          if (have < BQ) {
+            ok = __all_sync(0xffffffffu, mbar_wait(bar, uint32_t(raws) & 1u, abort_flag, a.err));
+            if (!ok) break;
+            ++raws;
+            zero_rows(q, 2 * D / 64, have, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&full[st]));
+          }
+        }
+      }
+    }
+    // every copy has landed before the CTA can exit (after a timeout: as far as one more limit shows)
+    if (lane == 0) {
+      mbar_drain(smem_u32(kv_full), 0);
+      for (int j = t - STAGES > 0 ? t - STAGES : 0; j < t; ++j) mbar_drain(smem_u32(&full[j % STAGES]), uint32_t(j / STAGES) & 1u);
+      if (!ok) mbar_drain(smem_u32(raw), uint32_t(raws) & 1u);
+    }
+  } else if (warp == 1) {
+    // ---------------- products ----------------
+    const uint32_t ks = smem_u32(smem + L::K), vs = smem_u32(smem + L::V);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag, a.err));
+    };
+    bool ok = wait(kv_full, 0);
+    for (int t = 0; t < n_it && ok; ++t) {
+      const int st = t % STAGES;
+      const uint32_t q = smem_u32(smem + L::QD + st * 2 * L::TILE), dy = q + L::TILE;
+      const uint32_t now = uint32_t(t) & 1u, before = now ^ 1u;
+      if (!(ok = wait(&full[st], uint32_t(t / STAGES) & 1u))) break;
+      if (t > 0 && !(ok = wait(dv_done, before))) break;  // P' of the block before has been read
+      tc_fence_after();
+      if (lane == 0) {
+        product_nt<D>(tmem + L::S, ks, q);
+        mma_commit(smem_u32(s_full));
+      }
+      __syncwarp();
+      if (t > 0 && !(ok = wait(dk_done, before))) break;  // dS' of the block before has been read
+      tc_fence_after();
+      if (lane == 0) {
+        product_nt<D>(tmem + L::DP, vs, dy);
+        mma_commit(smem_u32(dp_full));
+      }
+      __syncwarp();
+      if (!(ok = wait(p_full, now))) break;
+      tc_fence_after();
+      if (lane == 0) {
+        product_ta<D>(tmem + L::DV, tmem + L::S, dy, t > 0);
+        mma_commit(smem_u32(dv_done));
+      }
+      __syncwarp();
+      if (!(ok = wait(ds_full, now))) break;
+      tc_fence_after();
+      if (lane == 0) {
+        product_ta<D>(tmem + L::DK, tmem + L::DP, q, t > 0);
+        mma_commit(smem_u32(dk_done));
+        mma_commit(smem_u32(&empty[st]));
+      }
+      __syncwarp();
+    }
+    // every product issued is done before tensor memory is released
+    if (lane == 0) mma_commit(smem_u32(drain));
+    __syncwarp();
+    mbar_drain(smem_u32(drain), 0);
+  } else {
+    // ---------------- P' and dS': key row 32 (warp % 4) + lane, queries [64 half, 64 half + 64) of the block ----------------
+    const int half = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane, cb = 64 * half;
+    const uint32_t at = tmem + (uint32_t(quarter * 32) << 16);
+    const unsigned long long c2 = f2_pack(a.c, a.c);
+    bool ok = true;
+    int t = 0;
+    SeqIter it(a, tile, lane);
+    int s[5];
+    while (it.next(s)) {
+      int first, end;
+      query_blocks(s, row0, first, end);
+      const int j = row0 + row - s[1] - (s[3] - s[2]);  // the causal query whose last key is this row
+      const int from = row >= tile.y ? s[2] : s[4] < j ? s[4] : j;  // queries [from, nq) see the key
+      for (int hh = 0; hh < heads && ok; ++hh)
+        for (int b = first; b < end; ++b, ++t) {
+          const int st = t % STAGES;
+          const uint32_t now = uint32_t(t) & 1u;
+          // columns [lo, hi) of this thread's 64 are visible
+          const int lo = from - b * BQ - cb, hi = s[2] - b * BQ - cb;
+          const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < 64);
+          const float4* nl = reinterpret_cast<const float4*>(smem + L::STATS + st * 1024) + cb / 4;
+          const float4* nd = nl + 32;
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&stat_full[st]), uint32_t(t / STAGES) & 1u, abort_flag, a.err));
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(s_full), now, abort_flag, a.err));
+          if (!ok) break;
+          tc_fence_after();
+          float x[64];
+          tmem_ld64(at + L::S + cb, x);
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) x[c] = c >= lo && c < hi ? x[c] : -INFINITY;
+          }
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            const float4 l = nl[c / 4];
+            float u[4];
+            f2_unpack(f2_mul(f2_add(f2_pack(x[c], x[c + 1]), f2_pack(l.x, l.y)), c2), u[0], u[1]);
+            f2_unpack(f2_mul(f2_add(f2_pack(x[c + 2], x[c + 3]), f2_pack(l.z, l.w)), c2), u[2], u[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[c + i] = ex2(u[i]);
+            pk[c / 2] = pack_bf2(x[c], x[c + 1]);
+            pk[c / 2 + 1] = pack_bf2(x[c + 2], x[c + 3]);
+          }
+          tmem_st32_words(at + L::S + cb, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(p_full));
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(dp_full), now, abort_flag, a.err));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float y[32];
+            tmem_ld32(at + L::DP + cb + 32 * hf, y);
+            if (masked) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) y[c] = 32 * hf + c >= lo && 32 * hf + c < hi ? y[c] : 0.0f;
+            }
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              const int k = 32 * hf + c;
+              const float4 d = nd[k / 4];
+              float u[4];
+              f2_unpack(f2_mul(f2_add(f2_pack(y[c], y[c + 1]), f2_pack(d.x, d.y)), f2_pack(x[k], x[k + 1])), u[0], u[1]);
+              f2_unpack(f2_mul(f2_add(f2_pack(y[c + 2], y[c + 3]), f2_pack(d.z, d.w)), f2_pack(x[k + 2], x[k + 3])), u[2], u[3]);
+              pk[k / 2] = pack_bf2(u[0], u[1]);
+              pk[k / 2 + 1] = pack_bf2(u[2], u[3]);
+            }
+          }
+          tmem_st32_words(at + L::DP + cb, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(ds_full));
+        }
+    }
+    // the sums to shared memory, in fp32: 16-byte piece k of a row at k ^ row, so that a warp's rows meet no bank twice
+    if (ok && n_it > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(dk_done), uint32_t(n_it - 1) & 1u, abort_flag, a.err));
+    tc_fence_after();
+#pragma unroll 1
+    for (int m = 0; m < 2 && ok; ++m) {
+      uint8_t* to = smem + L::QD + m * 128 * D * 4 + row * D * 4;
+#pragma unroll 1
+      for (int c0 = half * D / 2; c0 < (half + 1) * D / 2; c0 += 32) {
+        float v[32];
+        if (n_it > 0) {
+          tmem_ld32(at + (m ? L::DK : L::DV) + c0, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float4*>(to + (((c0 / 4 + i) ^ (row & (D / 4 - 1))) << 4)) =
+              make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  __syncwarp();
+  cluster_sync();  // every share's sums are there
+  if (*abort_flag == 0u) {
+    const int rows = BK / a.shares, r0 = share * rows;
+    const int64_t N = int64_t(a.Hq + 2 * a.Hkv) * D;
+    for (int i = threadIdx.x; i < 2 * rows * (D / 8); i += THREADS) {
+      const int m = i / (rows * (D / 8)), r = r0 + i / (D / 8) % rows, k = i % (D / 8) * 2;
+      if (r >= tile.y) continue;
+      const uint32_t from = smem_u32(smem + L::QD + m * 128 * D * 4 + r * D * 4), x = uint32_t(r & (D / 4 - 1));
+      float v[8] = {};
+      for (int p = 0; p < a.shares; ++p) {
+        float u[4], w[4];
+        ld_shared_f4(map_to_rank(from + ((k ^ x) << 4), p), u);
+        ld_shared_f4(map_to_rank(from + (((k + 1) ^ x) << 4), p), w);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v[q] = p == 0 ? u[q] : __fadd_rn(v[q], u[q]);
+          v[4 + q] = p == 0 ? w[q] : __fadd_rn(v[4 + q], w[q]);
+        }
+      }
+      const float f = m ? a.scale : 1.0f;
+      uint32_t o[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) o[q] = pack_bf2(__fmul_rn(v[2 * q], f), __fmul_rn(v[2 * q + 1], f));
+      *reinterpret_cast<uint4*>(a.dqkv + (row0 + r) * N + (a.Hq + (m ? 0 : a.Hkv) + g) * D + 4 * k) =
+          make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  cluster_sync();  // no CTA leaves while another reads its shared memory
+}
+
+// ---------------------------------------------------------------------------
+// dQ
+// ---------------------------------------------------------------------------
+
+template <int D>
+struct QLayout {
+  static constexpr int K_STAGES = D == 128 ? 3 : 4, V_STAGES = D == 128 ? 2 : 3;
+  static constexpr uint32_t TILE = 128 * D * 2;
+  static constexpr uint32_t Q = 0, DO = TILE, K = 2 * TILE, V = K + K_STAGES * TILE, BAR = V + V_STAGES * TILE;
+  static constexpr size_t BYTES = 1024 + size_t(BAR) + 512;
+  static constexpr uint32_t S = 0, DP = 256, DQ = 384;  // tensor memory: S of block t at 128 (t % 2)
+};
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    dq_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __grid_constant__ CUtensorMap tm_do,
+              const __grid_constant__ CUtensorMap tm_out, const Args a) {
+  using L = QLayout<D>;
+  constexpr int K_STAGES = L::K_STAGES, V_STAGES = L::V_STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
+  uint64_t* q_full = bars;
+  uint64_t* raw = bars + 1;       // a K block that is zeroed in part before it is full
+  uint64_t* k_full = bars + 2;    // [K_STAGES]
+  uint64_t* k_empty = bars + 6;   // [K_STAGES]
+  uint64_t* v_full = bars + 10;   // [V_STAGES]
+  uint64_t* v_empty = bars + 14;  // [V_STAGES]
+  uint64_t* s_full = bars + 18;   // [2]
+  uint64_t* dp_full = bars + 20;
+  uint64_t* ds_full = bars + 21;
+  uint64_t* dq_done = bars + 22;
+  uint64_t* drain = bars + 23;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  int* item = reinterpret_cast<int*>(tmem_slot + 2);  // found, q0, k0, nq, nk, n_causal, i0
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    int4 sq = make_int4(0, 0, 0, 0);
+    int c = 0, i = 0;
+    bool ok;
+    if (a.n_seq > kSortedSeqs) {
+      ok = int(blockIdx.x) / a.Hq < __ldcg(a.work.counts + 1);
+      if (ok) {
+        const int2 w = __ldcg(a.work.items + int(blockIdx.x) / a.Hq);
+        const int32_t* d = a.seqs + 5 * int64_t(w.x);
+        sq = make_int4(d[0], d[1], d[2], d[3]);
+        c = d[4];
+        i = w.y;
+      }
+    } else {
+      ok = find_item<BQ>(a.seqs, a.n_seq, a.T, int(blockIdx.x) / a.Hq, lane, sq, c, i);
+    }
+    if (lane == 0) {
+      item[0] = ok ? 1 : 0;
+      item[1] = sq.x;
+      item[2] = sq.y;
+      item[3] = sq.z;
+      item[4] = sq.w;
+      item[5] = c;
+      item[6] = i;
+    }
+  }
+  if (threadIdx.x == 32) {
+    mbar_init(smem_u32(q_full), 1);
+    mbar_init(smem_u32(raw), 1);
+    for (int i = 0; i < K_STAGES; ++i) {
+      mbar_init(smem_u32(&k_full[i]), 1);
+      mbar_init(smem_u32(&k_empty[i]), 1);
+    }
+    for (int i = 0; i < V_STAGES; ++i) {
+      mbar_init(smem_u32(&v_full[i]), 1);
+      mbar_init(smem_u32(&v_empty[i]), 1);
+    }
+    mbar_init(smem_u32(&s_full[0]), 1);
+    mbar_init(smem_u32(&s_full[1]), 1);
+    mbar_init(smem_u32(dp_full), 1);
+    mbar_init(smem_u32(ds_full), COMPUTE_WARPS);
+    mbar_init(smem_u32(dq_done), 1);
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_qkv);
+    tma_prefetch_desc(&tm_do);
+    tma_prefetch_desc(&tm_out);
+  }
+  __syncthreads();
+  if (!item[0]) {
+    if (blockIdx.x == 0) pdl_wait();
+    return;
+  }
+  const int q0 = item[1], k0 = item[2], nq = item[3], nk = item[4], nc = item[5], i0 = item[6];
+  const int h = int(blockIdx.x) % a.Hq, g = h / (a.Hq / a.Hkv);
+  const int i1 = i0 + BQ < nq ? i0 + BQ : nq;
+  const int kmax = i1 > nc ? nk : nk - nq + i1;
+  const int nblk = (kmax + BK - 1) / BK;
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ---------------- copies ----------------
+    bool ok = true;
+    int kdone = 0, vdone = 0;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(smem_u32(q_full), 2 * L::TILE);
+      load_tile<D>(smem_u32(smem + L::Q), &tm_qkv, h * D, q0 + i0, smem_u32(q_full));
+      load_tile<D>(smem_u32(smem + L::DO), &tm_do, h * D, q0 + i0, smem_u32(q_full));
+    }
+    for (int t = 0; t < nblk && ok; ++t) {
+      const int ks = t % K_STAGES, vs = t % V_STAGES, y = k0 + t * BK, have = nk - t * BK < BK ? nk - t * BK : BK;
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&k_empty[ks]), (uint32_t(t / K_STAGES) & 1u) ^ 1u, abort_flag, a.err));
+      if (!ok) break;
+      uint8_t* k = smem + L::K + ks * L::TILE;
+      const uint32_t bar = smem_u32(have == BK ? &k_full[ks] : raw);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, L::TILE);
+        load_tile<D>(smem_u32(k), &tm_qkv, (a.Hq + g) * D, y, bar);
+      }
+      kdone = t + 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&v_empty[vs]), (uint32_t(t / V_STAGES) & 1u) ^ 1u, abort_flag, a.err));
+      if (ok && lane == 0) {
+        mbar_arrive_expect_tx(smem_u32(&v_full[vs]), L::TILE);
+        load_tile<D>(smem_u32(smem + L::V + vs * L::TILE), &tm_qkv, (a.Hq + a.Hkv + g) * D, y, smem_u32(&v_full[vs]));
+      }
+      if (ok) vdone = t + 1;
+      if (have < BK) {  // the last block: its rows past the sequence's keys are summed over in dS K
+        ok = __all_sync(0xffffffffu, mbar_wait(bar, 0, abort_flag, a.err)) && ok;
+        zero_rows(k, D / 64, have, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&k_full[ks]));
+      }
+    }
+    if (lane == 0) {
+      mbar_drain(smem_u32(q_full), 0);
+      for (int j = kdone - K_STAGES > 0 ? kdone - K_STAGES : 0; j < kdone; ++j)
+        mbar_drain(smem_u32(&k_full[j % K_STAGES]), uint32_t(j / K_STAGES) & 1u);
+      for (int j = vdone - V_STAGES > 0 ? vdone - V_STAGES : 0; j < vdone; ++j)
+        mbar_drain(smem_u32(&v_full[j % V_STAGES]), uint32_t(j / V_STAGES) & 1u);
+    }
+  } else if (warp == 1) {
+    // ---------------- products: per block dQ += dS K, dP of the next block, S of the one after it ----------------
+    const uint32_t q = smem_u32(smem + L::Q), dy = smem_u32(smem + L::DO);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag, a.err));
+    };
+    auto form_s = [&](int t) {
+      const int ks = t % K_STAGES;
+      if (!wait(&k_full[ks], uint32_t(t / K_STAGES) & 1u)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+        product_nt<D>(tmem + L::S + 128 * (t & 1), q, smem_u32(smem + L::K + ks * L::TILE));
+        mma_commit(smem_u32(&s_full[t & 1]));
+      }
+      __syncwarp();
+      return true;
+    };
+    auto form_dp = [&](int t) {
+      const int vs = t % V_STAGES;
+      if (!wait(&v_full[vs], uint32_t(t / V_STAGES) & 1u)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+        product_nt<D>(tmem + L::DP, dy, smem_u32(smem + L::V + vs * L::TILE));
+        mma_commit(smem_u32(dp_full));
+        mma_commit(smem_u32(&v_empty[vs]));
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = wait(q_full, 0) && form_s(0) && form_dp(0) && (nblk < 2 || form_s(1));
+    for (int t = 0; t < nblk && ok; ++t) {
+      const int ks = t % K_STAGES;
+      if (!(ok = wait(ds_full, uint32_t(t) & 1u))) break;  // S and dP of the block have been read, dS is written
+      tc_fence_after();
+      if (lane == 0) {
+        product_ta<D>(tmem + L::DQ, tmem + L::S + 128 * (t & 1), smem_u32(smem + L::K + ks * L::TILE), t > 0);
+        mma_commit(smem_u32(dq_done));
+        mma_commit(smem_u32(&k_empty[ks]));
+      }
+      __syncwarp();
+      if (t + 1 < nblk && !(ok = form_dp(t + 1))) break;
+      if (t + 2 < nblk) ok = wait(dq_done, uint32_t(t) & 1u) && form_s(t + 2);  // into dS's place
+    }
+    if (lane == 0) mma_commit(smem_u32(drain));
+    __syncwarp();
+    mbar_drain(smem_u32(drain), 0);
+  } else {
+    // ---------------- dS: query row 32 (warp % 4) + lane, keys [64 half, 64 half + 64) of the block ----------------
+    const int half = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane, cb = 64 * half;
+    const uint32_t at = tmem + (uint32_t(quarter * 32) << 16);
+    const int i = i0 + row;
+    const bool valid = i < nq;
+    const int lim = !valid ? 0 : i < nc ? nk - nq + i + 1 : nk;  // keys [0, lim) are visible
+    const int64_t st = int64_t(h) * a.T + q0 + i;
+    const float nl = valid ? __ldcg(a.nlse + st) : 0.0f, nd = valid ? __ldcg(a.ndelta + st) : 0.0f;
+    const unsigned long long c2 = f2_pack(a.c, a.c), nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+    bool ok = true;
+    for (int t = 0; t < nblk; ++t) {
+      const int hi = lim - t * BK - cb;  // columns [0, hi) of this thread's 64 are visible
+      const bool masked = __any_sync(0xffffffffu, hi < 64);
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[t & 1]), uint32_t(t >> 1) & 1u, abort_flag, a.err));
+      if (!ok) break;
+      tc_fence_after();
+      float x[64];
+      tmem_ld64(at + L::S + 128 * (t & 1) + cb, x);
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) x[c] = c < hi ? x[c] : -INFINITY;
+      }
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        float u0, u1;
+        f2_unpack(f2_mul(f2_add(f2_pack(x[c], x[c + 1]), nl2), c2), u0, u1);
+        x[c] = ex2(u0);
+        x[c + 1] = ex2(u1);
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(dp_full), uint32_t(t) & 1u, abort_flag, a.err));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t pk[32];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float y[32];
+        tmem_ld32(at + L::DP + cb + 32 * hf, y);
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) y[c] = 32 * hf + c < hi ? y[c] : 0.0f;
+        }
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const int k = 32 * hf + c;
+          float u0, u1;
+          f2_unpack(f2_mul(f2_add(f2_pack(y[c], y[c + 1]), nd2), f2_pack(x[k], x[k + 1])), u0, u1);
+          pk[k / 2] = pack_bf2(u0, u1);
+        }
+      }
+      tmem_st32_words(at + L::S + 128 * (t & 1) + cb, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(ds_full));
+    }
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(dq_done), uint32_t(nblk - 1) & 1u, abort_flag, a.err));
+    tc_fence_after();
+    const bool whole = i0 + BQ <= nq;
+    const int64_t N = int64_t(a.Hq + 2 * a.Hkv) * D;
+    if (ok) {
+#pragma unroll 1
+      for (int c0 = half * D / 2; c0 < (half + 1) * D / 2; c0 += 32) {
+        float v[32];
+        tmem_ld32(at + L::DQ + c0, v);
+        uint32_t o[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) o[u] = pack_bf2(__fmul_rn(v[2 * u], a.scale), __fmul_rn(v[2 * u + 1], a.scale));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint4 w = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          const int k = c0 / 8 + u;  // 16-byte piece of the row
+          if (whole)  // into Q's place (no product reads it any more), in the boxes' swizzled layout
+            *reinterpret_cast<uint4*>(smem + L::Q + (k >> 3) * SUB + row * 128 + (((k & 7) ^ (row & 7)) << 4)) = w;
+          else if (valid)  // rows past the sequence's queries belong to others
+            *reinterpret_cast<uint4*>(a.dqkv + (q0 + i) * N + h * D + 8 * k) = w;
+        }
+      }
+    }
+    if (whole) {
+      fence_proxy_async_smem();
+      named_bar_sync(1, 32 * COMPUTE_WARPS);
+      if (warp == 2 && lane == 0 && *abort_flag == 0u) {
+        for (int b = 0; b < D / 64; ++b) tma_store_2d(&tm_out, smem_u32(smem + L::Q + b * SUB), h * D + 64 * b, q0 + i0);
+        bulk_store_commit_and_wait_read();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  // This grid starts before dkv_kernel's has ended: one CTA ends after it, so that what follows this grid follows both.
+  if (blockIdx.x == 0) pdl_wait();
 }
 
 inline bool shape_ok(int64_t T, int Hq, int Hkv, int D, int n_seq) {
   return T >= 1 && T <= MOT_MAX_TOKENS && (D == 64 || D == 128) && Hq >= 1 && Hkv >= 1 && Hq <= 1024 && Hkv <= 1024 &&
          Hq % Hkv == 0 && n_seq >= 1 && n_seq <= MOT_MAX_TOKENS;
+}
+
+// CTAs that share a KV head's query heads: a rule on the group alone, as it sets the order of the sums.
+inline int shares_of(int G) { return G >= 8 ? 8 : G >= 4 ? 4 : G >= 2 ? 2 : 1; }
+
+// The workspace after its header, in bytes.
+struct Room {
+  int64_t nlse, ndelta, tiles, items, counts, change, border, runs, end;
+  int max_tiles, max_items;
+  Room(int64_t T, int Hq, int64_t n_seq) {
+    auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
+    const int64_t borders = 2 * n_seq < T + 1 ? 2 * n_seq : T + 1, blocks = (T + 127) / 128;
+    max_tiles = int(blocks + borders < T ? blocks + borders : T);  // a run adds at most one short tile
+    max_items = int(blocks + n_seq < T ? blocks + n_seq : T);
+    nlse = 0;
+    ndelta = nlse + up(T * Hq * 4);
+    tiles = ndelta + up(T * Hq * 4);
+    items = tiles + int64_t(max_tiles) * 16;
+    counts = items + up(int64_t(max_items) * 8);
+    change = counts + 16;
+    border = change + up((T + 1) * 4);
+    runs = border + up((T / 32 + 1) * 4);
+    end = runs + up(borders * 4);
+  }
+};
+
+template <int D>
+static int launch(const uint16_t* dout, const uint16_t* qkv, const uint16_t* out, const float* lse, const Args& a,
+                  cudaStream_t s) {
+  CUtensorMap tm_qkv, tm_do, tm_out;
+  const uint64_t N = uint64_t(a.Hq + 2 * a.Hkv) * D;
+  if (!make_tmap_bf16(&tm_qkv, qkv, N, uint64_t(a.T), 64, 128) ||
+      !make_tmap_bf16(&tm_do, dout, uint64_t(a.Hq) * D, uint64_t(a.T), 64, 128) ||
+      !make_tmap_bf16(&tm_out, a.dqkv, N, uint64_t(a.T), 64, 128))
+    return MOT_ERR_CUDA;
+  constexpr int kv_bytes = int(KvLayout<D>::BYTES), q_bytes = int(QLayout<D>::BYTES);
+  static_assert(kv_bytes > 114 * 1024 && q_bytes > 114 * 1024, "one CTA an SM: two would compete for tensor memory");
+  static_assert(kv_bytes <= 227 * 1024 && q_bytes <= 227 * 1024, "shared memory of a CTA");
+  if (cudaFuncSetAttribute(dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kv_bytes) != cudaSuccess ||
+      cudaFuncSetAttribute(dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, q_bytes) != cudaSuccess)
+    return MOT_ERR_CUDA;
+  const int64_t kv_ctas = int64_t(a.work.max_tiles) * a.Hkv * a.shares, q_ctas = int64_t(a.work.max_items) * a.Hq;
+  if (kv_ctas > (int64_t(1) << 31) - 1 || q_ctas > (int64_t(1) << 31) - 1) return MOT_ERR_GEOMETRY;
+  StatsArgs st{};
+  st.dout = dout;
+  st.out = out;
+  st.lse = lse;
+  st.T = a.T;
+  st.Hq = a.Hq;
+  st.rscale = 1.0f / a.scale;
+  st.nlse = const_cast<float*>(a.nlse);
+  st.ndelta = const_cast<float*>(a.ndelta);
+  st.seqs = a.seqs;
+  st.n_seq = a.n_seq;
+  st.work = a.work;
+  st.err = a.err;
+  stats_kernel<D><<<dim3(unsigned((a.T + 31) / 32 + 1), unsigned((a.Hq + 31) / 32)), STATS_THREADS, 0, s>>>(st);
+  if (cudaGetLastError() != cudaSuccess) return MOT_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(kv_ctas));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = kv_bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(a.shares);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, dkv_kernel<D>, tm_qkv, tm_do, a) != cudaSuccess) return MOT_ERR_CUDA;
+  if (launch_dependent(dq_kernel<D>, dim3(unsigned(q_ctas)), dim3(THREADS), size_t(q_bytes), s, tm_qkv, tm_do, tm_out, a) !=
+      cudaSuccess)
+    return MOT_ERR_CUDA;
+  return MOT_OK;
 }
 
 }  // namespace attnb
@@ -150,7 +1036,7 @@ using namespace mot;
 
 extern "C" size_t mot_joint_attention_backward_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int n_seq) {
   if (!attnb::shape_ok(T, Hq, Hkv, D, n_seq)) return 0;
-  return sizeof(PlanHeader) + (size_t(T) * Hq * sizeof(float) + 15) / 16 * 16;
+  return sizeof(PlanHeader) + size_t(attnb::Room(T, Hq, n_seq).end);
 }
 
 extern "C" int mot_joint_attention_backward(const mot_bf16* dout, const mot_bf16* qkv, const mot_bf16* out,
@@ -171,30 +1057,29 @@ extern "C" int mot_joint_attention_backward(const mot_bf16* dout, const mot_bf16
   const int st = check_device(s, ptrs, 7, &dev);
   if (st != MOT_OK) return st;
   DeviceGuard guard(dev);
+  uint8_t* base = static_cast<uint8_t*>(ws) + sizeof(PlanHeader);
   attnb::Args a{};
-  a.dout = dout;
-  a.qkv = qkv;
-  a.out = out;
-  a.lse = lse;
   a.seqs = seqs;
   a.n_seq = n_seq;
   a.T = int(T);
   a.Hq = Hq;
   a.Hkv = Hkv;
+  a.shares = attnb::shares_of(Hq / Hkv);
   a.c = c;
   a.scale = scale;
-  a.rscale = 1.0f / scale;
-  a.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sizeof(PlanHeader));
+  const attnb::Room room(T, Hq, n_seq);
+  a.nlse = reinterpret_cast<float*>(base + room.nlse);
+  a.ndelta = reinterpret_cast<float*>(base + room.ndelta);
+  a.work.tiles = reinterpret_cast<int4*>(base + room.tiles);
+  a.work.items = reinterpret_cast<int2*>(base + room.items);
+  a.work.counts = reinterpret_cast<int32_t*>(base + room.counts);
+  a.work.change = reinterpret_cast<int32_t*>(base + room.change);
+  a.work.border = reinterpret_cast<uint32_t*>(base + room.border);
+  a.work.runs = reinterpret_cast<int32_t*>(base + room.runs);
+  a.work.max_tiles = room.max_tiles;
+  a.work.max_items = room.max_items;
   a.dqkv = dqkv;
   a.err = &static_cast<PlanHeader*>(ws)->error;
-  const int64_t nq = (T * Hq + attnb::WARPS - 1) / attnb::WARPS, nkv = (T * Hkv + attnb::WARPS - 1) / attnb::WARPS;
-  if (nq > (int64_t(1) << 31) - 1) return MOT_ERR_GEOMETRY;
-  if (D == 64) {
-    attnb::dq_kernel<64><<<unsigned(nq), attnb::THREADS, 0, s>>>(a);
-    attnb::dkv_kernel<64><<<unsigned(nkv), attnb::THREADS, 0, s>>>(a);
-  } else {
-    attnb::dq_kernel<128><<<unsigned(nq), attnb::THREADS, 0, s>>>(a);
-    attnb::dkv_kernel<128><<<unsigned(nkv), attnb::THREADS, 0, s>>>(a);
-  }
-  return cudaGetLastError() == cudaSuccess ? MOT_OK : MOT_ERR_CUDA;
+  if (D == 64) return attnb::launch<64>(dout, qkv, out, lse, a, s);
+  return attnb::launch<128>(dout, qkv, out, lse, a, s);
 }
