@@ -153,7 +153,7 @@ __device__ __forceinline__ void store8(float* d, int have, const float (&x)[8]) 
 __device__ __forceinline__ void store_bf16(uint16_t* d, int have, const float (&x)[8]) {
   if (have == 8) {
     *reinterpret_cast<uint4*>(d) =
-        make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7]));
+        make_uint4(cvt_bf2(x[0], x[1]), cvt_bf2(x[2], x[3]), cvt_bf2(x[4], x[5]), cvt_bf2(x[6], x[7]));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)

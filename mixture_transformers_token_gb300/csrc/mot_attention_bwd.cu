@@ -25,7 +25,7 @@
 //                 into tensor memory in the place of S, dQ += dS K. Its grid starts while the last CTAs of dkv_kernel run.
 //
 // A block's tiles are copied by TMA (128-byte swizzle) two or three blocks ahead; one warp copies, one issues the products, and
-// eight compute (each thread half of the 128 columns of one row). Rows past a sequence's end inside its last block are other
+// sixteen compute (each thread a quarter of the 128 columns of one row). Rows past a sequence's end inside its last block are other
 // sequences' rows: they are zeroed in shared memory where they would be summed over, and masked where they are columns.
 
 #include <cuda.h>
@@ -42,7 +42,7 @@ namespace attnb {
 using namespace attn;
 
 constexpr int BQ = 128, BK = 128;
-constexpr int COMPUTE_WARPS = 8;
+constexpr int COMPUTE_WARPS = 16;  // four to a quarter of the rows (tensor memory gives a warp 32 lanes): 32 columns a thread
 constexpr int THREADS = 32 * (2 + COMPUTE_WARPS);
 constexpr uint32_t SUB = 128 * 64 * 2;  // a [128 rows x 64 columns] bf16 swizzled tile
 
@@ -301,25 +301,41 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* m, in
   for (int b = 0; b < D / 64; ++b) tma_load_2d(dst + b * SUB, m, x + 64 * b, y, bar);
 }
 
-// D[128 x 128] = A B' of two row-major [128][DK] tiles.
-template <int DK>
-__device__ __forceinline__ void product_nt(uint32_t d, uint32_t a, uint32_t b) {
-  constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
-#pragma unroll
-  for (int kk = 0; kk < DK / 16; ++kk)
-    mma_bf16(d, smem_desc_sw128(a + (kk / 4) * SUB + (kk % 4) * 32), smem_desc_sw128(b + (kk / 4) * SUB + (kk % 4) * 32), idesc,
-             kk > 0);
+// Shared-memory descriptors (smem_desc_sw128, smem_desc_mn_sw128 with halves SUB apart) by their low words: the steps inside a
+// tile are added to these, so that one thread forms an operand in one addition. Formed anew for every product, descriptors took
+// the issuing thread 77 cycles a product, longer than the 64 that the product takes.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_low_mn(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | ((SUB >> 4) << 16); }
+__device__ __forceinline__ uint64_t desc_of(uint32_t low) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(low), "r"(kDescHigh));
+  return d;
 }
 
-// D[128 x DN] += A B of a bf16 [128 x 128] A in tensor memory (its halves of 64 columns of K 64 TMEM columns apart) and a
-// row-major [128][DN] tile.
+// D[128 x 128] = A B' of two row-major [128][DK] tiles (desc_low of each).
+template <int DK>
+__device__ __forceinline__ void product_nt(uint32_t on, uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
+#pragma unroll
+  for (int kk = 0; kk < DK / 16; ++kk) {
+    const uint32_t at = ((kk / 4) * SUB + (kk % 4) * 32) >> 4;
+    mma_bf16_on(on, d, desc_of(a + at), desc_of(b + at), idesc, kk > 0);
+  }
+}
+
+// D[128 x DN] += A B of a bf16 [128 x 128] A in tensor memory (every 32 of its columns, 16 words, where the 32 fp32 values were
+// that they come from) and a row-major [128][DN] tile (its desc_low_mn).
 template <int DN>
-__device__ __forceinline__ void product_ta(uint32_t d, uint32_t a_tmem, uint32_t b, bool accumulate) {
+__device__ __forceinline__ void product_ta(uint32_t on, uint32_t d, uint32_t a_tmem, uint32_t b, bool accumulate) {
   constexpr uint32_t idesc = idesc_bf16_f32(128, DN) | kIdescBMnMajor;
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk)
-    mma_bf16_ta(d, a_tmem + (kk / 4) * 64 + (kk % 4) * 8, smem_desc_mn_sw128(b + kk * 2048, SUB), idesc, accumulate || kk > 0);
+    mma_bf16_ta_on(on, d, a_tmem + (kk / 2) * 32 + (kk % 2) * 8, desc_of(b + ((kk * 2048) >> 4)), idesc, accumulate || kk > 0);
 }
+
+__device__ __forceinline__ void ld_columns(uint32_t taddr, float (&v)[32]) { tmem_ld32(taddr, v); }
+__device__ __forceinline__ void ld_columns(uint32_t taddr, float (&v)[16]) { tmem_ld16(taddr, v); }
 
 __device__ __forceinline__ void ld_shared_f4(uint32_t addr_cluster, float (&v)[4]) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -339,7 +355,8 @@ struct KvLayout {
   static constexpr uint32_t K = 0, V = TILE;
   static constexpr uint32_t QD = 2 * TILE;                        // STAGES of (Q, dO); at the end dV and dK in fp32
   static constexpr uint32_t STATS = QD + STAGES * 2 * TILE;       // STAGES of (-lse / scale, -delta) of 128 queries
-  static constexpr uint32_t BAR = STATS + STAGES * 1024;
+  static constexpr uint32_t EDGES = STATS + STAGES * 1024;        // STAGES of the block's edges, see the copies
+  static constexpr uint32_t BAR = EDGES + STAGES * 16;
   static constexpr size_t BYTES = 1024 + size_t(BAR) + 512;
   static constexpr uint32_t S = 0, DP = 128, DV = 256, DK = 384;  // tensor memory
   static_assert(2 * 128 * D * 4 <= STAGES * 2 * TILE, "the sums fit where the blocks were");
@@ -453,6 +470,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             stats[c] = c < have ? __ldcg(a.nlse + at + c) : 0.0f;
             stats[128 + c] = c < have ? __ldcg(a.ndelta + at + c) : 0.0f;
           }
+          // column c of the block sees key row r if min(x, y + r) <= c < z
+          if (lane == 0)
+            *reinterpret_cast<int4*>(smem + L::EDGES + st * 16) =
+                make_int4(s[4] - b * BQ, row0 - s[1] - (s[3] - s[2]) - b * BQ, have, 0);
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&stat_full[st]));
           if (have < BQ) {
@@ -475,128 +496,114 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp == 1) {
     // ---------------- products ----------------
-    const uint32_t ks = smem_u32(smem + L::K), vs = smem_u32(smem + L::V);
+    const uint32_t on = elect_one();
+    const uint32_t ks = desc_low(smem_u32(smem + L::K)), vs = desc_low(smem_u32(smem + L::V));
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag, a.err));
     };
-    bool ok = wait(kv_full, 0);
+    auto tiles = [&](int t) { return smem_u32(smem + L::QD + t % STAGES * 2 * L::TILE); };
+    auto form_s = [&](int t) {
+      if (!wait(&full[t % STAGES], uint32_t(t / STAGES) & 1u)) return false;
+      if (t > 0 && !wait(dv_done, uint32_t(t - 1) & 1u)) return false;  // P' of the block before has been read
+      tc_fence_after();
+      product_nt<D>(on, tmem + L::S, ks, desc_low(tiles(t)));
+      mma_commit_on(on, smem_u32(s_full));
+      return true;
+    };
+    auto form_dp = [&](int t) {
+      if (t > 0 && !wait(dk_done, uint32_t(t - 1) & 1u)) return false;  // dS' of the block before has been read
+      tc_fence_after();
+      product_nt<D>(on, tmem + L::DP, vs, desc_low(tiles(t) + L::TILE));
+      mma_commit_on(on, smem_u32(dp_full));
+      return true;
+    };
+    // S' of the next block as soon as P' of this one has been read, so that the warps that compute go from dS' to the next P'
+    bool ok = wait(kv_full, 0) && (n_it == 0 || (form_s(0) && form_dp(0)));
     for (int t = 0; t < n_it && ok; ++t) {
-      const int st = t % STAGES;
-      const uint32_t q = smem_u32(smem + L::QD + st * 2 * L::TILE), dy = q + L::TILE;
-      const uint32_t now = uint32_t(t) & 1u, before = now ^ 1u;
-      if (!(ok = wait(&full[st], uint32_t(t / STAGES) & 1u))) break;
-      if (t > 0 && !(ok = wait(dv_done, before))) break;  // P' of the block before has been read
-      tc_fence_after();
-      if (lane == 0) {
-        product_nt<D>(tmem + L::S, ks, q);
-        mma_commit(smem_u32(s_full));
-      }
-      __syncwarp();
-      if (t > 0 && !(ok = wait(dk_done, before))) break;  // dS' of the block before has been read
-      tc_fence_after();
-      if (lane == 0) {
-        product_nt<D>(tmem + L::DP, vs, dy);
-        mma_commit(smem_u32(dp_full));
-      }
-      __syncwarp();
+      const uint32_t now = uint32_t(t) & 1u;
       if (!(ok = wait(p_full, now))) break;
       tc_fence_after();
-      if (lane == 0) {
-        product_ta<D>(tmem + L::DV, tmem + L::S, dy, t > 0);
-        mma_commit(smem_u32(dv_done));
-      }
-      __syncwarp();
+      product_ta<D>(on, tmem + L::DV, tmem + L::S, desc_low_mn(tiles(t) + L::TILE), t > 0);
+      mma_commit_on(on, smem_u32(dv_done));
+      if (t + 1 < n_it && !(ok = form_s(t + 1))) break;
       if (!(ok = wait(ds_full, now))) break;
       tc_fence_after();
-      if (lane == 0) {
-        product_ta<D>(tmem + L::DK, tmem + L::DP, q, t > 0);
-        mma_commit(smem_u32(dk_done));
-        mma_commit(smem_u32(&empty[st]));
-      }
-      __syncwarp();
+      product_ta<D>(on, tmem + L::DK, tmem + L::DP, desc_low_mn(tiles(t)), t > 0);
+      mma_commit_on(on, smem_u32(dk_done));
+      mma_commit_on(on, smem_u32(&empty[t % STAGES]));
+      if (t + 1 < n_it) ok = form_dp(t + 1);
     }
     // every product issued is done before tensor memory is released
-    if (lane == 0) mma_commit(smem_u32(drain));
-    __syncwarp();
+    mma_commit_on(on, smem_u32(drain));
     mbar_drain(smem_u32(drain), 0);
   } else {
-    // ---------------- P' and dS': key row 32 (warp % 4) + lane, queries [64 half, 64 half + 64) of the block ----------------
-    const int half = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane, cb = 64 * half;
+    // ---------------- P' and dS': key row 32 (warp % 4) + lane, queries [32 part, 32 part + 32) of the block ----------------
+    const int part = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane, cb = 32 * part;
     const uint32_t at = tmem + (uint32_t(quarter * 32) << 16);
     const unsigned long long c2 = f2_pack(a.c, a.c);
     bool ok = true;
-    int t = 0;
-    SeqIter it(a, tile, lane);
-    int s[5];
-    while (it.next(s)) {
-      int first, end;
-      query_blocks(s, row0, first, end);
-      const int j = row0 + row - s[1] - (s[3] - s[2]);  // the causal query whose last key is this row
-      const int from = row >= tile.y ? s[2] : s[4] < j ? s[4] : j;  // queries [from, nq) see the key
-      for (int hh = 0; hh < heads && ok; ++hh)
-        for (int b = first; b < end; ++b, ++t) {
-          const int st = t % STAGES;
-          const uint32_t now = uint32_t(t) & 1u;
-          // columns [lo, hi) of this thread's 64 are visible
-          const int lo = from - b * BQ - cb, hi = s[2] - b * BQ - cb;
-          const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < 64);
-          const float4* nl = reinterpret_cast<const float4*>(smem + L::STATS + st * 1024) + cb / 4;
-          const float4* nd = nl + 32;
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&stat_full[st]), uint32_t(t / STAGES) & 1u, abort_flag, a.err));
-          ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(s_full), now, abort_flag, a.err));
-          if (!ok) break;
-          tc_fence_after();
-          float x[64];
-          tmem_ld64(at + L::S + cb, x);
-          if (masked) {
+    for (int t = 0; t < n_it; ++t) {
+      const int st = t % STAGES;
+      const uint32_t now = uint32_t(t) & 1u;
+      const float4* nl = reinterpret_cast<const float4*>(smem + L::STATS + st * 1024) + cb / 4;
+      const float4* nd = nl + 32;
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&stat_full[st]), uint32_t(t / STAGES) & 1u, abort_flag, a.err));
+      if (!ok) break;
+      const int4 edge = *reinterpret_cast<const int4*>(smem + L::EDGES + st * 16);
+      // columns [lo, hi) of this thread's 32 are visible; rows past the tile see none
+      const int hi = row < tile.y ? edge.z - cb : 0, lo = (edge.x < edge.y + row ? edge.x : edge.y + row) - cb;
+      const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < 32);
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(s_full), now, abort_flag, a.err));
+      if (!ok) break;
+      tc_fence_after();
+      float x[32];
+      tmem_ld32(at + L::S + cb, x);
+      if (masked) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c) x[c] = c >= lo && c < hi ? x[c] : -INFINITY;
-          }
-          uint32_t pk[32];
+        for (int c = 0; c < 32; ++c) x[c] = c >= lo && c < hi ? x[c] : -INFINITY;
+      }
+      uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < 64; c += 4) {
-            const float4 l = nl[c / 4];
-            float u[4];
-            f2_unpack(f2_mul(f2_add(f2_pack(x[c], x[c + 1]), f2_pack(l.x, l.y)), c2), u[0], u[1]);
-            f2_unpack(f2_mul(f2_add(f2_pack(x[c + 2], x[c + 3]), f2_pack(l.z, l.w)), c2), u[2], u[3]);
+      for (int c = 0; c < 32; c += 4) {
+        const float4 l = nl[c / 4];
+        float u[4];
+        f2_unpack(f2_mul(f2_add(f2_pack(x[c], x[c + 1]), f2_pack(l.x, l.y)), c2), u[0], u[1]);
+        f2_unpack(f2_mul(f2_add(f2_pack(x[c + 2], x[c + 3]), f2_pack(l.z, l.w)), c2), u[2], u[3]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[c + i] = ex2(u[i]);
-            pk[c / 2] = pack_bf2(x[c], x[c + 1]);
-            pk[c / 2 + 1] = pack_bf2(x[c + 2], x[c + 3]);
-          }
-          tmem_st32_words(at + L::S + cb, pk);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(p_full));
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(dp_full), now, abort_flag, a.err));
-          if (!ok) break;
-          tc_fence_after();
+        for (int i = 0; i < 4; ++i) x[c + i] = ex2(u[i]);
+        pk[c / 2] = cvt_bf2(x[c], x[c + 1]);
+        pk[c / 2 + 1] = cvt_bf2(x[c + 2], x[c + 3]);
+      }
+      tmem_st16_words(at + L::S + cb, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(p_full));
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(dp_full), now, abort_flag, a.err));
+      if (!ok) break;
+      tc_fence_after();
+      {
+        float y[32];
+        tmem_ld32(at + L::DP + cb, y);
+        if (masked) {
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            float y[32];
-            tmem_ld32(at + L::DP + cb + 32 * hf, y);
-            if (masked) {
-#pragma unroll
-              for (int c = 0; c < 32; ++c) y[c] = 32 * hf + c >= lo && 32 * hf + c < hi ? y[c] : 0.0f;
-            }
-#pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              const int k = 32 * hf + c;
-              const float4 d = nd[k / 4];
-              float u[4];
-              f2_unpack(f2_mul(f2_add(f2_pack(y[c], y[c + 1]), f2_pack(d.x, d.y)), f2_pack(x[k], x[k + 1])), u[0], u[1]);
-              f2_unpack(f2_mul(f2_add(f2_pack(y[c + 2], y[c + 3]), f2_pack(d.z, d.w)), f2_pack(x[k + 2], x[k + 3])), u[2], u[3]);
-              pk[k / 2] = pack_bf2(u[0], u[1]);
-              pk[k / 2 + 1] = pack_bf2(u[2], u[3]);
-            }
-          }
-          tmem_st32_words(at + L::DP + cb, pk);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(ds_full));
+          for (int c = 0; c < 32; ++c) y[c] = c >= lo && c < hi ? y[c] : 0.0f;
         }
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 d = nd[c / 4];
+          float u[4];
+          f2_unpack(f2_mul(f2_add(f2_pack(y[c], y[c + 1]), f2_pack(d.x, d.y)), f2_pack(x[c], x[c + 1])), u[0], u[1]);
+          f2_unpack(f2_mul(f2_add(f2_pack(y[c + 2], y[c + 3]), f2_pack(d.z, d.w)), f2_pack(x[c + 2], x[c + 3])), u[2], u[3]);
+          pk[c / 2] = cvt_bf2(u[0], u[1]);
+          pk[c / 2 + 1] = cvt_bf2(u[2], u[3]);
+        }
+      }
+      tmem_st16_words(at + L::DP + cb, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(ds_full));
     }
     // the sums to shared memory, in fp32: 16-byte piece k of a row at k ^ row, so that a warp's rows meet no bank twice
     if (ok && n_it > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(dk_done), uint32_t(n_it - 1) & 1u, abort_flag, a.err));
@@ -604,20 +611,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll 1
     for (int m = 0; m < 2 && ok; ++m) {
       uint8_t* to = smem + L::QD + m * 128 * D * 4 + row * D * 4;
-#pragma unroll 1
-      for (int c0 = half * D / 2; c0 < (half + 1) * D / 2; c0 += 32) {
-        float v[32];
-        if (n_it > 0) {
-          tmem_ld32(at + (m ? L::DK : L::DV) + c0, v);
-        } else {
+      float v[D / 4] = {};
+      if (n_it > 0) ld_columns(at + (m ? L::DK : L::DV) + part * (D / 4), v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float4*>(to + (((c0 / 4 + i) ^ (row & (D / 4 - 1))) << 4)) =
-              make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-      }
+      for (int i = 0; i < D / 16; ++i)
+        *reinterpret_cast<float4*>(to + (((part * (D / 16) + i) ^ (row & (D / 4 - 1))) << 4)) =
+            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     }
   }
   tc_fence_before();
@@ -649,7 +648,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const float f = m ? a.scale : 1.0f;
       uint32_t o[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) o[q] = pack_bf2(__fmul_rn(v[2 * q], f), __fmul_rn(v[2 * q + 1], f));
+      for (int q = 0; q < 4; ++q) o[q] = cvt_bf2(__fmul_rn(v[2 * q], f), __fmul_rn(v[2 * q + 1], f));
       *reinterpret_cast<uint4*>(a.dqkv + (row0 + r) * N + (a.Hq + (m ? 0 : a.Hkv) + g) * D + 4 * k) =
           make_uint4(o[0], o[1], o[2], o[3]);
     }
@@ -806,7 +805,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp == 1) {
     // ---------------- products: per block dQ += dS K, dP of the next block, S of the one after it ----------------
-    const uint32_t q = smem_u32(smem + L::Q), dy = smem_u32(smem + L::DO);
+    const uint32_t on = elect_one();
+    const uint32_t q = desc_low(smem_u32(smem + L::Q)), dy = desc_low(smem_u32(smem + L::DO));
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag, a.err));
     };
@@ -814,23 +814,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int ks = t % K_STAGES;
       if (!wait(&k_full[ks], uint32_t(t / K_STAGES) & 1u)) return false;
       tc_fence_after();
-      if (lane == 0) {
-        product_nt<D>(tmem + L::S + 128 * (t & 1), q, smem_u32(smem + L::K + ks * L::TILE));
-        mma_commit(smem_u32(&s_full[t & 1]));
-      }
-      __syncwarp();
+      product_nt<D>(on, tmem + L::S + 128 * (t & 1), q, desc_low(smem_u32(smem + L::K + ks * L::TILE)));
+      mma_commit_on(on, smem_u32(&s_full[t & 1]));
       return true;
     };
     auto form_dp = [&](int t) {
       const int vs = t % V_STAGES;
       if (!wait(&v_full[vs], uint32_t(t / V_STAGES) & 1u)) return false;
       tc_fence_after();
-      if (lane == 0) {
-        product_nt<D>(tmem + L::DP, dy, smem_u32(smem + L::V + vs * L::TILE));
-        mma_commit(smem_u32(dp_full));
-        mma_commit(smem_u32(&v_empty[vs]));
-      }
-      __syncwarp();
+      product_nt<D>(on, tmem + L::DP, dy, desc_low(smem_u32(smem + L::V + vs * L::TILE)));
+      mma_commit_on(on, smem_u32(dp_full));
+      mma_commit_on(on, smem_u32(&v_empty[vs]));
       return true;
     };
     bool ok = wait(q_full, 0) && form_s(0) && form_dp(0) && (nblk < 2 || form_s(1));
@@ -838,21 +832,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int ks = t % K_STAGES;
       if (!(ok = wait(ds_full, uint32_t(t) & 1u))) break;  // S and dP of the block have been read, dS is written
       tc_fence_after();
-      if (lane == 0) {
-        product_ta<D>(tmem + L::DQ, tmem + L::S + 128 * (t & 1), smem_u32(smem + L::K + ks * L::TILE), t > 0);
-        mma_commit(smem_u32(dq_done));
-        mma_commit(smem_u32(&k_empty[ks]));
-      }
-      __syncwarp();
+      product_ta<D>(on, tmem + L::DQ, tmem + L::S + 128 * (t & 1), desc_low_mn(smem_u32(smem + L::K + ks * L::TILE)), t > 0);
+      mma_commit_on(on, smem_u32(dq_done));
+      mma_commit_on(on, smem_u32(&k_empty[ks]));
       if (t + 1 < nblk && !(ok = form_dp(t + 1))) break;
       if (t + 2 < nblk) ok = wait(dq_done, uint32_t(t) & 1u) && form_s(t + 2);  // into dS's place
     }
-    if (lane == 0) mma_commit(smem_u32(drain));
-    __syncwarp();
+    mma_commit_on(on, smem_u32(drain));
     mbar_drain(smem_u32(drain), 0);
   } else {
-    // ---------------- dS: query row 32 (warp % 4) + lane, keys [64 half, 64 half + 64) of the block ----------------
-    const int half = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane, cb = 64 * half;
+    // ---------------- dS: query row 32 (warp % 4) + lane, keys [32 part, 32 part + 32) of the block ----------------
+    const int part = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane, cb = 32 * part;
     const uint32_t at = tmem + (uint32_t(quarter * 32) << 16);
     const int i = i0 + row;
     const bool valid = i < nq;
@@ -862,45 +852,44 @@ __global__ void __launch_bounds__(THREADS, 1)
     const unsigned long long c2 = f2_pack(a.c, a.c), nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
     bool ok = true;
     for (int t = 0; t < nblk; ++t) {
-      const int hi = lim - t * BK - cb;  // columns [0, hi) of this thread's 64 are visible
-      const bool masked = __any_sync(0xffffffffu, hi < 64);
+      const int hi = lim - t * BK - cb;  // columns [0, hi) of this thread's 32 are visible
+      const bool masked = __any_sync(0xffffffffu, hi < 32);
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[t & 1]), uint32_t(t >> 1) & 1u, abort_flag, a.err));
       if (!ok) break;
       tc_fence_after();
-      float x[64];
-      tmem_ld64(at + L::S + 128 * (t & 1) + cb, x);
+      float x[32];
+      tmem_ld32(at + L::S + 128 * (t & 1) + cb, x);
       if (masked) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c) x[c] = c < hi ? x[c] : -INFINITY;
+        for (int c = 0; c < 32; ++c) x[c] = c < hi ? x[c] : -INFINITY;
       }
 #pragma unroll
-      for (int c = 0; c < 64; c += 2) {
+      for (int c = 0; c < 32; c += 2) {
         float u0, u1;
         f2_unpack(f2_mul(f2_add(f2_pack(x[c], x[c + 1]), nl2), c2), u0, u1);
         x[c] = ex2(u0);
         x[c + 1] = ex2(u1);
+        asm volatile("" : "+f"(x[c]), "+f"(x[c + 1]));  // now, not after the wait for dP
       }
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(dp_full), uint32_t(t) & 1u, abort_flag, a.err));
       if (!ok) break;
       tc_fence_after();
-      uint32_t pk[32];
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+      uint32_t pk[16];
+      {
         float y[32];
-        tmem_ld32(at + L::DP + cb + 32 * hf, y);
+        tmem_ld32(at + L::DP + cb, y);
         if (masked) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) y[c] = 32 * hf + c < hi ? y[c] : 0.0f;
+          for (int c = 0; c < 32; ++c) y[c] = c < hi ? y[c] : 0.0f;
         }
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
-          const int k = 32 * hf + c;
           float u0, u1;
-          f2_unpack(f2_mul(f2_add(f2_pack(y[c], y[c + 1]), nd2), f2_pack(x[k], x[k + 1])), u0, u1);
-          pk[k / 2] = pack_bf2(u0, u1);
+          f2_unpack(f2_mul(f2_add(f2_pack(y[c], y[c + 1]), nd2), f2_pack(x[c], x[c + 1])), u0, u1);
+          pk[c / 2] = cvt_bf2(u0, u1);
         }
       }
-      tmem_st32_words(at + L::S + 128 * (t & 1) + cb, pk);
+      tmem_st16_words(at + L::S + 128 * (t & 1) + cb, pk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -911,22 +900,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool whole = i0 + BQ <= nq;
     const int64_t N = int64_t(a.Hq + 2 * a.Hkv) * D;
     if (ok) {
-#pragma unroll 1
-      for (int c0 = half * D / 2; c0 < (half + 1) * D / 2; c0 += 32) {
-        float v[32];
-        tmem_ld32(at + L::DQ + c0, v);
-        uint32_t o[16];
+      float v[D / 4];
+      ld_columns(at + L::DQ + part * (D / 4), v);
 #pragma unroll
-        for (int u = 0; u < 16; ++u) o[u] = pack_bf2(__fmul_rn(v[2 * u], a.scale), __fmul_rn(v[2 * u + 1], a.scale));
+      for (int u = 0; u < D / 32; ++u) {
+        uint32_t o[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint4 w = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-          const int k = c0 / 8 + u;  // 16-byte piece of the row
-          if (whole)  // into Q's place (no product reads it any more), in the boxes' swizzled layout
-            *reinterpret_cast<uint4*>(smem + L::Q + (k >> 3) * SUB + row * 128 + (((k & 7) ^ (row & 7)) << 4)) = w;
-          else if (valid)  // rows past the sequence's queries belong to others
-            *reinterpret_cast<uint4*>(a.dqkv + (q0 + i) * N + h * D + 8 * k) = w;
-        }
+        for (int q = 0; q < 4; ++q) o[q] = cvt_bf2(__fmul_rn(v[8 * u + 2 * q], a.scale), __fmul_rn(v[8 * u + 2 * q + 1], a.scale));
+        const uint4 w = make_uint4(o[0], o[1], o[2], o[3]);
+        const int k = part * (D / 32) + u;  // 16-byte piece of the row
+        if (whole)  // into Q's place (no product reads it any more), in the boxes' swizzled layout
+          *reinterpret_cast<uint4*>(smem + L::Q + (k >> 3) * SUB + row * 128 + (((k & 7) ^ (row & 7)) << 4)) = w;
+        else if (valid)  // rows past the sequence's queries belong to others
+          *reinterpret_cast<uint4*>(a.dqkv + (q0 + i) * N + h * D + 8 * k) = w;
       }
     }
     if (whole) {

@@ -54,7 +54,7 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
   x[4] = bf_lo(v.z), x[5] = bf_hi(v.z), x[6] = bf_lo(v.w), x[7] = bf_hi(v.w);
 }
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7]));
+  return make_uint4(cvt_bf2(x[0], x[1]), cvt_bf2(x[2], x[3]), cvt_bf2(x[4], x[5]), cvt_bf2(x[6], x[7]));
 }
 
 // cos and sin of the lane's 8 pairs
