@@ -24,6 +24,10 @@
 //   dq_kernel     one CTA per (128 queries of a sequence, head): over the blocks of 128 keys, S = Q K', dP = dO V', dS as bf16
 //                 into tensor memory in the place of S, dQ += dS K. Its grid starts while the last CTAs of dkv_kernel run.
 //
+// In dkv_kernel, lse and delta belong to the columns. They are subtracted by the products themselves: one more step of K, whose A
+// is ones and whose B holds the value as three bf16 (24 bits), so that no thread reads them from shared memory, which the products
+// keep busy.
+//
 // A block's tiles are copied by TMA (128-byte swizzle) two or three blocks ahead; one warp copies, one issues the products, and
 // sixteen compute (each thread a quarter of the 128 columns of one row). Rows past a sequence's end inside its last block are other
 // sequences' rows: they are zeroed in shared memory where they would be summed over, and masked where they are columns.
@@ -324,6 +328,22 @@ __device__ __forceinline__ void product_nt(uint32_t on, uint32_t d, uint32_t a, 
   }
 }
 
+// A [128][16] operand of one step of K without a swizzle: 8 rows of 16 bytes (8 of the 16 values) are 128 consecutive bytes, the
+// other 8 values of the rows follow them, then the next 8 rows.
+__device__ __forceinline__ uint32_t step_offset(int row) { return uint32_t(row >> 3) * 256 + uint32_t(row & 7) * 16; }
+__device__ __forceinline__ uint64_t desc_step(uint32_t addr) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};"
+      : "=l"(d)
+      : "r"(((addr & 0x3FFFFu) >> 4) | ((128u >> 4) << 16)), "r"((256u >> 4) | (1u << 14)));
+  return d;
+}
+// x as the sum of three bf16 (24 bits), in an operand's first values
+__device__ __forceinline__ uint4 in_three(float x) {
+  const float hi = bf_round(x), mid = bf_round(__fsub_rn(x, hi)), lo = __fsub_rn(__fsub_rn(x, hi), mid);
+  return make_uint4(cvt_bf2(hi, mid), cvt_bf2(lo, 0.0f), 0u, 0u);
+}
+
 // D[128 x DN] += A B of a bf16 [128 x 128] A in tensor memory (every 32 of its columns, 16 words, where the 32 fp32 values were
 // that they come from) and a row-major [128][DN] tile (its desc_low_mn).
 template <int DN>
@@ -352,10 +372,12 @@ template <int D>
 struct KvLayout {
   static constexpr int STAGES = D == 128 ? 2 : 4;
   static constexpr uint32_t TILE = 128 * D * 2;
+  static constexpr uint32_t STEP = 128 * 16 * 2;                  // an operand of one step of K
   static constexpr uint32_t K = 0, V = TILE;
   static constexpr uint32_t QD = 2 * TILE;                        // STAGES of (Q, dO); at the end dV and dK in fp32
-  static constexpr uint32_t STATS = QD + STAGES * 2 * TILE;       // STAGES of (-lse / scale, -delta) of 128 queries
-  static constexpr uint32_t EDGES = STATS + STAGES * 1024;        // STAGES of the block's edges, see the copies
+  static constexpr uint32_t ONES = QD + STAGES * 2 * TILE;        // [128][16]: ones in columns 0 to 2
+  static constexpr uint32_t STATS = ONES + STEP;                  // STAGES of [128][16] -lse / scale and of -delta, in three
+  static constexpr uint32_t EDGES = STATS + STAGES * 2 * STEP;    // STAGES of the block's edges, see the copies
   static constexpr uint32_t BAR = EDGES + STAGES * 16;
   static constexpr size_t BYTES = 1024 + size_t(BAR) + 512;
   static constexpr uint32_t S = 0, DP = 128, DV = 256, DK = 384;  // tensor memory
@@ -393,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(smem_u32(kv_full), 1);
     mbar_init(smem_u32(raw), 1);
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&full[i]), 2);  // the tiles, and the stats
       mbar_init(smem_u32(&empty[i]), 1);
       mbar_init(smem_u32(&stat_full[i]), 1);
     }
@@ -409,6 +431,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     tma_prefetch_desc(&tm_qkv);
     tma_prefetch_desc(&tm_do);
   }
+  for (int i = threadIdx.x; i < int((2 * STAGES + 1) * L::STEP / 16); i += THREADS)  // only the stats' first values change
+    *reinterpret_cast<uint4*>(smem + L::ONES + i * 16) =
+        i < int(L::STEP / 16) && (i & 8) == 0 ? make_uint4(0x3F803F80u, 0x3F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
   pdl_wait();     // stats_kernel, also on behalf of dq_kernel, whose grid starts after every CTA's trigger
   pdl_trigger();
   if (rest / a.Hkv >= __ldcg(a.work.counts)) return;  // no such tile, for every CTA of the cluster
@@ -462,20 +488,30 @@ __global__ void __launch_bounds__(THREADS, 1)
             load_tile<D>(smem_u32(q), &tm_qkv, h * D, y, bar);
             load_tile<D>(smem_u32(q + L::TILE), &tm_do, h * D, y, bar);
           }
-          float* stats = reinterpret_cast<float*>(smem + L::STATS + st * 1024);
+          uint8_t* stats = smem + L::STATS + st * 2 * L::STEP;
           const int64_t at = int64_t(h) * a.T + y;
+          float l[4], d[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int c = lane + 32 * i;
-            stats[c] = c < have ? __ldcg(a.nlse + at + c) : 0.0f;
-            stats[128 + c] = c < have ? __ldcg(a.ndelta + at + c) : 0.0f;
+            l[i] = c < have ? __ldcg(a.nlse + at + c) : 0.0f;
+            d[i] = c < have ? __ldcg(a.ndelta + at + c) : 0.0f;
           }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            *reinterpret_cast<uint4*>(stats + step_offset(lane + 32 * i)) = in_three(l[i]);
+            *reinterpret_cast<uint4*>(stats + L::STEP + step_offset(lane + 32 * i)) = in_three(d[i]);
+          }
+          fence_proxy_async_smem();
           // column c of the block sees key row r if min(x, y + r) <= c < z
           if (lane == 0)
             *reinterpret_cast<int4*>(smem + L::EDGES + st * 16) =
                 make_int4(s[4] - b * BQ, row0 - s[1] - (s[3] - s[2]) - b * BQ, have, 0);
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&stat_full[st]));
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&stat_full[st]));
+            mbar_arrive(smem_u32(&full[st]));
+          }
           if (have < BQ) {
             ok = __all_sync(0xffffffffu, mbar_wait(bar, uint32_t(raws) & 1u, abort_flag, a.err));
             if (!ok) break;
@@ -498,6 +534,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---------------- products ----------------
     const uint32_t on = elect_one();
     const uint32_t ks = desc_low(smem_u32(smem + L::K)), vs = desc_low(smem_u32(smem + L::V));
+    const uint64_t ones = desc_step(smem_u32(smem + L::ONES));
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag, a.err));
     };
@@ -507,6 +544,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (t > 0 && !wait(dv_done, uint32_t(t - 1) & 1u)) return false;  // P' of the block before has been read
       tc_fence_after();
       product_nt<D>(on, tmem + L::S, ks, desc_low(tiles(t)));
+      mma_bf16_on(on, tmem + L::S, ones, desc_step(smem_u32(smem + L::STATS + t % STAGES * 2 * L::STEP)), idesc_bf16_f32(128, 128), 1);
       mma_commit_on(on, smem_u32(s_full));
       return true;
     };
@@ -514,6 +552,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (t > 0 && !wait(dk_done, uint32_t(t - 1) & 1u)) return false;  // dS' of the block before has been read
       tc_fence_after();
       product_nt<D>(on, tmem + L::DP, vs, desc_low(tiles(t) + L::TILE));
+      mma_bf16_on(on, tmem + L::DP, ones, desc_step(smem_u32(smem + L::STATS + (t % STAGES * 2 + 1) * L::STEP)),
+                  idesc_bf16_f32(128, 128), 1);
       mma_commit_on(on, smem_u32(dp_full));
       return true;
     };
@@ -545,8 +585,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int t = 0; t < n_it; ++t) {
       const int st = t % STAGES;
       const uint32_t now = uint32_t(t) & 1u;
-      const float4* nl = reinterpret_cast<const float4*>(smem + L::STATS + st * 1024) + cb / 4;
-      const float4* nd = nl + 32;
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&stat_full[st]), uint32_t(t / STAGES) & 1u, abort_flag, a.err));
       if (!ok) break;
       const int4 edge = *reinterpret_cast<const int4*>(smem + L::EDGES + st * 16);
@@ -564,15 +602,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       uint32_t pk[16];
 #pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        const float4 l = nl[c / 4];
-        float u[4];
-        f2_unpack(f2_mul(f2_add(f2_pack(x[c], x[c + 1]), f2_pack(l.x, l.y)), c2), u[0], u[1]);
-        f2_unpack(f2_mul(f2_add(f2_pack(x[c + 2], x[c + 3]), f2_pack(l.z, l.w)), c2), u[2], u[3]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[c + i] = ex2(u[i]);
+      for (int c = 0; c < 32; c += 2) {  // S' - lse / scale came from the products
+        float u0, u1;
+        f2_unpack(f2_mul(f2_pack(x[c], x[c + 1]), c2), u0, u1);
+        x[c] = ex2(u0);
+        x[c + 1] = ex2(u1);
         pk[c / 2] = cvt_bf2(x[c], x[c + 1]);
-        pk[c / 2 + 1] = cvt_bf2(x[c + 2], x[c + 3]);
       }
       tmem_st16_words(at + L::S + cb, pk);
       tmem_st_wait();
@@ -590,13 +625,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int c = 0; c < 32; ++c) y[c] = c >= lo && c < hi ? y[c] : 0.0f;
         }
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 d = nd[c / 4];
-          float u[4];
-          f2_unpack(f2_mul(f2_add(f2_pack(y[c], y[c + 1]), f2_pack(d.x, d.y)), f2_pack(x[c], x[c + 1])), u[0], u[1]);
-          f2_unpack(f2_mul(f2_add(f2_pack(y[c + 2], y[c + 3]), f2_pack(d.z, d.w)), f2_pack(x[c + 2], x[c + 3])), u[2], u[3]);
-          pk[c / 2] = cvt_bf2(u[0], u[1]);
-          pk[c / 2 + 1] = cvt_bf2(u[2], u[3]);
+        for (int c = 0; c < 32; c += 2) {  // and dP' - delta
+          float u0, u1;
+          f2_unpack(f2_mul(f2_pack(y[c], y[c + 1]), f2_pack(x[c], x[c + 1])), u0, u1);
+          pk[c / 2] = cvt_bf2(u0, u1);
         }
       }
       tmem_st16_words(at + L::DP + cb, pk);
