@@ -14,13 +14,14 @@
 //
 //   stats_kernel  -delta and -lse / scale of every row and head, [Hq][T] (reads dout and out once); its first CTA makes the
 //                 lists of work.
-//   dkv_kernel    one CTA per (tile of keys, KV head, share of its query heads). The borders of the sequences' key ranges cut
+//   dkv_kernel    one CTA per (tile of keys, KV head, share of its blocks). The borders of the sequences' key ranges cut
 //                 the pack's rows into runs that the same sequences see, and a tile is 128 rows of a run or what is left of it.
 //                 So nothing that a sequence holds reaches the sums of rows that are not its keys, as it would through 0 NaN
-//                 in a tile of two sequences. Over the sequences that see these rows, the share's heads and the blocks of 128 queries, S' = K Q' and dP' = V dO' (keys in the rows),
-//                 P' and dS' as bf16 into tensor memory in the places of S' and dP', dV += P' dO, dK += dS' Q with A from
-//                 tensor memory. The CTAs of a cluster hold the shares of one KV head; each sends its sums to shared memory
-//                 and adds and writes its part of the rows, in the order of the shares, through the cluster's shared memory.
+//                 in a tile of two sequences. Over the sequences that see these rows, the group's heads and the share's
+//                 blocks of 128 queries: S' = K Q' and dP' = V dO' (keys in the rows), P' and dS' as bf16 into tensor memory in
+//                 the places of S' and dP', dV += P' dO, dK += dS' Q with A from tensor memory. The CTAs of a cluster hold
+//                 the shares of one KV head; each sends its sums to shared memory and adds and writes its part of the rows,
+//                 in the order of the shares, through the cluster's shared memory.
 //   dq_kernel     one CTA per (128 queries of a sequence, head): over the blocks of 128 keys, S = Q K', dP = dO V', dS as bf16
 //                 into tensor memory in the place of S, dQ += dS K. Its grid starts while the last CTAs of dkv_kernel run.
 //
@@ -50,10 +51,15 @@ constexpr int COMPUTE_WARPS = 16;  // four to a quarter of the rows (tensor memo
 constexpr int THREADS = 32 * (2 + COMPUTE_WARPS);
 constexpr uint32_t SUB = 128 * 64 * 2;  // a [128 rows x 64 columns] bf16 swizzled tile
 
+// 128 queries of a sequence: its descriptor and the first of them.
+struct alignas(16) Item {
+  int q0, k0, nq, nk, nc, i0, pad[2];
+};
+
 // Lists in the workspace, made by stats_kernel's first CTA.
 struct Work {
   int4* tiles;    // (first row, rows, first and last sequence that may see them), ascending
-  int2* items;    // (sequence, first query row) of dq_kernel, for more than kSortedSeqs sequences
+  Item* items;    // of dq_kernel
   int32_t* counts;  // tiles, items
   // scratch: changes of the number of sequences that see a row, at each row; borders, a bit a row; the borders in order
   int32_t* change;
@@ -116,7 +122,91 @@ __device__ __forceinline__ int scan_before(int x, int* room, int& total) {
   return before + incl - x;
 }
 
-// The lists of work, by one CTA: T / 8 + 4 T bytes to clear and to read, and the descriptors.
+// The lists of work of up to kSortedSeqs sequences, in shared memory. The items come heaviest first: the last run of queries of
+// every sequence, then the last but one of every sequence, ...
+struct FewRoom {
+  int d[kSortedSeqs][5], items[kSortedSeqs], edge[2 * kSortedSeqs], first[2 * kSortedSeqs], sorted[2 * kSortedSeqs];
+  int scan[STATS_THREADS / 32];
+};
+__device__ void make_work_few(const StatsArgs& a, FewRoom& s) {
+  const Work& w = a.work;
+  const int tid = threadIdx.x;
+  bool bad = false;
+  int rows = 0;
+  if (tid < kSortedSeqs) {
+    int d[5] = {0, 0, 0, 0, 0};
+    if (tid < a.n_seq) {
+#pragma unroll
+      for (int i = 0; i < 5; ++i) d[i] = a.seqs[5 * tid + i];
+      bad = bad_seq(d, a.T);
+      if (bad) d[2] = d[3] = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 5; ++i) s.d[tid][i] = d[i];
+    s.items[tid] = (d[2] + BQ - 1) / BQ;
+    rows = d[2];  // at most 2^24 each
+  }
+  int all_rows;
+  scan_before(rows, s.scan, all_rows);
+  if (__syncthreads_or(bad ? 1 : 0) != 0 || all_rows > a.T) {
+    if (tid == 0) atomicOr(a.err, MOT_DEV_BAD_SEQUENCE);
+  }
+  // the borders of the key ranges, each once, in ascending order
+  constexpr int NONE = 0x7FFFFFFF;
+  const int c = tid & (kSortedSeqs - 1);
+  const bool edge = tid < 2 * kSortedSeqs && s.d[c][3] > 0;
+  const int at = !edge ? NONE : tid < kSortedSeqs ? s.d[c][1] : s.d[c][1] + s.d[c][3];
+  if (tid < 2 * kSortedSeqs) s.edge[tid] = at;
+  __syncthreads();
+  bool first = edge;
+  if (edge)
+    for (int i = 0; i < tid; ++i) first &= s.edge[i] != at;
+  if (tid < 2 * kSortedSeqs) s.first[tid] = first ? at : NONE;
+  const int n = __syncthreads_count(first ? 1 : 0);
+  if (first) {
+    int rank = 0;
+    for (int i = 0; i < 2 * kSortedSeqs; ++i) rank += s.first[i] < at ? 1 : 0;
+    s.sorted[rank] = at;
+  }
+  __syncthreads();
+  // the runs between them that some sequence sees, in tiles
+  int lo = a.n_seq, hi = -1, from = 0, to = 0;
+  if (tid + 1 < n) {
+    from = s.sorted[tid];
+    to = s.sorted[tid + 1];
+    for (int i = 0; i < a.n_seq; ++i)
+      if (s.d[i][1] <= from && s.d[i][1] + s.d[i][3] > from) {
+        lo = lo < i ? lo : i;
+        hi = i;
+      }
+  }
+  const int mine = hi >= 0 ? (to - from + BK - 1) / BK : 0;
+  int tiles;
+  const int t0 = scan_before(mine, s.scan, tiles);
+  for (int r = 0; r < mine; ++r) {
+    const int row = from + r * BK;
+    w.tiles[t0 + r] = make_int4(row, to - row < BK ? to - row : BK, lo, hi);
+  }
+  int items = 0;
+  for (int r = tid / kSortedSeqs; r < s.items[c]; r += STATS_THREADS / kSortedSeqs) {
+    int before = 0;
+    for (int i = 0; i < a.n_seq; ++i) {
+      const int k = s.items[i];
+      before += k < r ? k : r;
+      before += i < c && k > r ? 1 : 0;
+    }
+    if (before < w.max_items)
+      w.items[before] = {s.d[c][0], s.d[c][1], s.d[c][2], s.d[c][3], s.d[c][4], (s.items[c] - 1 - r) * BQ, {0, 0}};
+  }
+  if (tid == 0) {
+    for (int i = 0; i < a.n_seq; ++i) items += s.items[i];  // at most 2^6 2^17
+    w.counts[0] = tiles;
+    w.counts[1] = items < w.max_items ? items : w.max_items;
+  }
+}
+
+// The lists of work of any number of sequences, by one CTA: T / 8 + 4 T bytes to clear and to read, and the descriptors. The items
+// come sequence by sequence.
 __device__ void make_work(const StatsArgs& a, int* room) {
   const Work& w = a.work;
   const int tid = threadIdx.x, words = (a.T >> 5) + 1;
@@ -144,15 +234,13 @@ __device__ void make_work(const StatsArgs& a, int* room) {
         rows += d[2];
       }
     }
-    if (a.n_seq > kSortedSeqs) {
-      int total;
-      const int at = items + scan_before(mine, room, total);
-      for (int r = 0; r < mine; ++r)  // the last queries of a sequence, which see the most keys, first
-        if (at + r < w.max_items) w.items[at + r] = make_int2(s, (mine - 1 - r) * BQ);
-      items = items + total < w.max_items ? items + total : w.max_items;  // more only where queries overlap
-    } else {
-      items += mine;  // this thread's own
+    int total;
+    const int at = items + scan_before(mine, room, total);
+    for (int r = 0; r < mine && at + r < w.max_items; ++r) {  // the last queries of a sequence, which see the most keys, first
+      const int32_t* d = a.seqs + 5 * int64_t(s);
+      w.items[at + r] = {d[0], d[1], d[2], d[3], d[4], (mine - 1 - r) * BQ, {0, 0}};
     }
+    items = items + total < w.max_items ? items + total : w.max_items;  // more only where queries overlap
   }
   {
     int64_t sum = 0;  // rows of all threads, 21 bits at a time: 256 of them fit 32 bits
@@ -209,25 +297,34 @@ __device__ void make_work(const StatsArgs& a, int* room) {
   }
   if (tid == 0) {
     w.counts[0] = tiles;
-    w.counts[1] = items < w.max_items ? items : w.max_items;
+    w.counts[1] = items;
   }
 }
 
-// A CTA takes 32 rows and 32 heads; D / 8 lanes a row and head, the sums through shared memory into rows of [Hq][T].
+// A CTA takes STATS_ROWS rows and 32 heads; D / 8 lanes a row and head, the sums through shared memory into rows of [Hq][T]. (32
+// rows a CTA left a 4096-row pack with 129 CTAs and took 51 us.)
+constexpr int STATS_ROWS = 8;
+
 template <int D>
 __global__ void __launch_bounds__(STATS_THREADS) stats_kernel(const StatsArgs a) {
   constexpr int LANES = D / 8, GROUPS = STATS_THREADS / LANES;
-  __shared__ float sums[32][33];
+  __shared__ union {
+    float sums[32][STATS_ROWS + 1];
+    FewRoom few;
+    int scan[STATS_THREADS / 32];
+  } room;
   pdl_trigger();
   if (blockIdx.x == 0) {
-    if (blockIdx.y == 0) make_work(a, reinterpret_cast<int*>(&sums[0][0]));
+    if (blockIdx.y != 0) return;
+    if (a.n_seq <= kSortedSeqs) make_work_few(a, room.few);
+    else make_work(a, room.scan);
     return;
   }
   const int sub = threadIdx.x % LANES, grp = threadIdx.x / LANES;
-  const int row0 = int(blockIdx.x - 1) * 32, h0 = int(blockIdx.y) * 32;
+  const int row0 = int(blockIdx.x - 1) * STATS_ROWS, h0 = int(blockIdx.y) * 32;
   const int nh = a.Hq - h0 < 32 ? a.Hq - h0 : 32;
-#pragma unroll 4
-  for (int i = grp; i < 32 * 32; i += GROUPS) {
+#pragma unroll 8
+  for (int i = grp; i < STATS_ROWS * 32; i += GROUPS) {
     const int r = i >> 5, h = i & 31;
     float s = 0.0f;
     if (row0 + r < a.T && h < nh) {
@@ -240,16 +337,15 @@ __global__ void __launch_bounds__(STATS_THREADS) stats_kernel(const StatsArgs a)
     }
 #pragma unroll
     for (int off = LANES / 2; off >= 1; off >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
-    if (sub == 0) sums[h][r] = s;
+    if (sub == 0) room.sums[h][r] = s;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 32 * 32; i += STATS_THREADS) {
-    const int h = i >> 5, r = i & 31;
-    if (row0 + r < a.T && h < nh) {
-      const int64_t at = int64_t(h0 + h) * a.T + row0 + r;
-      a.ndelta[at] = -sums[h][r];
-      a.nlse[at] = -__fmul_rn(a.lse[at], a.rscale);
-    }
+  const int h = threadIdx.x / STATS_ROWS, r = threadIdx.x % STATS_ROWS;
+  static_assert(32 * STATS_ROWS == STATS_THREADS, "a thread a row and head");
+  if (row0 + r < a.T && h < nh) {
+    const int64_t at = int64_t(h0 + h) * a.T + row0 + r;
+    a.ndelta[at] = -room.sums[h][r];
+    a.nlse[at] = -__fmul_rn(a.lse[at], a.rscale);
   }
 }
 
@@ -285,6 +381,18 @@ struct SeqIter {
   }
 };
 
+// A tile's blocks are shared out by (query block + head of the group) mod shares, a power of two: the shares differ by few blocks
+// where the group's heads do not divide evenly, and which share adds a block depends on the sequence and the head alone.
+// How many of the blocks [first, end) of all G heads a share has.
+__device__ __forceinline__ int blocks_of_share(int share, int first, int end, int G, int shares) {
+  int n = 0;
+  for (int hh = 0; hh < G; ++hh) {
+    const int b0 = first + ((share - first - hh) & (shares - 1));  // the head's first one
+    n += b0 < end ? (end - 1 - b0) / shares + 1 : 0;
+  }
+  return n;
+}
+
 // Query blocks [first, end) of a sequence that see a key of the tile from row `row` on: causal query i sees keys up to nk - nq + i.
 __device__ __forceinline__ void query_blocks(const int (&s)[5], int row, int& first, int& end) {
   const int off = s[3] - s[2], j = row - s[1];
@@ -297,6 +405,11 @@ __device__ __forceinline__ void query_blocks(const int (&s)[5], int row, int& fi
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int tiles, int from, int lane) {
   for (int b = 0; b < tiles; ++b)
     for (int i = from * 8 + lane; i < 128 * 8; i += 32) *reinterpret_cast<uint4*>(tile + b * SUB + i * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// mbar_drain that costs no reading of the clock (400 ns) where the phase is over.
+__device__ __forceinline__ void drained(uint32_t bar, uint32_t parity) {
+  if (!mbar_try_wait(bar, parity)) mbar_drain(bar, parity);
 }
 
 template <int D>
@@ -406,12 +519,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* drain = bars + 20;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
   volatile uint32_t* abort_flag = tmem_slot + 1;
-  int* blocks = reinterpret_cast<int*>(tmem_slot + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int share = int(blockIdx.x) % a.shares, rest = int(blockIdx.x) / a.shares;
-  const int g = rest % a.Hkv, G = a.Hq / a.Hkv, heads = (G - share + a.shares - 1) / a.shares;  // g G + share, + shares, ...
-  if (threadIdx.x == 32) {
+  const int g = rest % a.Hkv, G = a.Hq / a.Hkv;
+  if (threadIdx.x == 0) {
     mbar_init(smem_u32(kv_full), 1);
     mbar_init(smem_u32(raw), 1);
     for (int i = 0; i < STAGES; ++i) {
@@ -428,8 +540,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0u;
     fence_mbar_init();
-    tma_prefetch_desc(&tm_qkv);
-    tma_prefetch_desc(&tm_do);
+    fence_proxy_async_smem();
   }
   for (int i = threadIdx.x; i < int((2 * STAGES + 1) * L::STEP / 16); i += THREADS)  // only the stats' first values change
     *reinterpret_cast<uint4*>(smem + L::ONES + i * 16) =
@@ -437,18 +548,15 @@ __global__ void __launch_bounds__(THREADS, 1)
   fence_proxy_async_smem();
   pdl_wait();     // stats_kernel, also on behalf of dq_kernel, whose grid starts after every CTA's trigger
   pdl_trigger();
-  if (rest / a.Hkv >= __ldcg(a.work.counts)) return;  // no such tile, for every CTA of the cluster
+  // the count and the tile at once; what lies past the last tile is not used
+  const int n_tiles = __ldcg(a.work.counts);
   const int4 tile = __ldcg(a.work.tiles + rest / a.Hkv);
+  if (rest / a.Hkv >= n_tiles) return;  // for every CTA of the cluster
   const int row0 = tile.x;
-  if (warp == 0) {  // what there is to do
-    SeqIter it(a, tile, lane);
-    int s[5], n = 0;
-    while (it.next(s)) {
-      int first, end;
-      query_blocks(s, row0, first, end);
-      n += (end > first ? end - first : 0) * heads;
-    }
-    if (lane == 0) *blocks = n;
+  if (threadIdx.x == 0) {
+    mbar_arrive_expect_tx(smem_u32(kv_full), 2 * L::TILE);
+    load_tile<D>(smem_u32(smem + L::K), &tm_qkv, (a.Hq + g) * D, row0, smem_u32(kv_full));
+    load_tile<D>(smem_u32(smem + L::V), &tm_qkv, (a.Hq + a.Hkv + g) * D, row0, smem_u32(kv_full));
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -458,25 +566,29 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int n_it = *blocks;
+  int n_it = 0;  // blocks of this share
+  if (warp != 0) {
+    SeqIter it(a, tile, lane);
+    int s[5];
+    while (it.next(s)) {
+      int first, end;
+      query_blocks(s, row0, first, end);
+      n_it += blocks_of_share(share, first, end, G, a.shares);
+    }
+  }
 
   if (warp == 0) {
     // ---------------- copies ----------------
     bool ok = true;
     int t = 0, raws = 0;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(smem_u32(kv_full), 2 * L::TILE);
-      load_tile<D>(smem_u32(smem + L::K), &tm_qkv, (a.Hq + g) * D, row0, smem_u32(kv_full));
-      load_tile<D>(smem_u32(smem + L::V), &tm_qkv, (a.Hq + a.Hkv + g) * D, row0, smem_u32(kv_full));
-    }
     SeqIter it(a, tile, lane);
     int s[5];
     while (ok && it.next(s)) {
       int first, end;
       query_blocks(s, row0, first, end);
-      for (int hh = 0; hh < heads && ok; ++hh) {
-        const int h = g * G + share + hh * a.shares;
-        for (int b = first; b < end; ++b, ++t) {
+      for (int hh = 0; hh < G && ok; ++hh) {
+        const int h = g * G + hh;
+        for (int b = first + ((share - first - hh) & (a.shares - 1)); b < end; b += a.shares, ++t) {
           const int st = t % STAGES;
           ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[st]), (uint32_t(t / STAGES) & 1u) ^ 1u, abort_flag, a.err));
           if (!ok) break;
@@ -526,9 +638,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     // every copy has landed before the CTA can exit (after a timeout: as far as one more limit shows)
     if (lane == 0) {
-      mbar_drain(smem_u32(kv_full), 0);
-      for (int j = t - STAGES > 0 ? t - STAGES : 0; j < t; ++j) mbar_drain(smem_u32(&full[j % STAGES]), uint32_t(j / STAGES) & 1u);
-      if (!ok) mbar_drain(smem_u32(raw), uint32_t(raws) & 1u);
+      drained(smem_u32(kv_full), 0);
+      for (int j = t - STAGES > 0 ? t - STAGES : 0; j < t; ++j) drained(smem_u32(&full[j % STAGES]), uint32_t(j / STAGES) & 1u);
+      if (!ok) drained(smem_u32(raw), uint32_t(raws) & 1u);
     }
   } else if (warp == 1) {
     // ---------------- products ----------------
@@ -575,7 +687,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     // every product issued is done before tensor memory is released
     mma_commit_on(on, smem_u32(drain));
-    mbar_drain(smem_u32(drain), 0);
+    drained(smem_u32(drain), 0);
   } else {
     // ---------------- P' and dS': key row 32 (warp % 4) + lane, queries [32 part, 32 part + 32) of the block ----------------
     const int part = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane, cb = 32 * part;
@@ -723,36 +835,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* drain = bars + 23;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
   volatile uint32_t* abort_flag = tmem_slot + 1;
-  int* item = reinterpret_cast<int*>(tmem_slot + 2);  // found, q0, k0, nq, nk, n_causal, i0
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) {
-    int4 sq = make_int4(0, 0, 0, 0);
-    int c = 0, i = 0;
-    bool ok;
-    if (a.n_seq > kSortedSeqs) {
-      ok = int(blockIdx.x) / a.Hq < __ldcg(a.work.counts + 1);
-      if (ok) {
-        const int2 w = __ldcg(a.work.items + int(blockIdx.x) / a.Hq);
-        const int32_t* d = a.seqs + 5 * int64_t(w.x);
-        sq = make_int4(d[0], d[1], d[2], d[3]);
-        c = d[4];
-        i = w.y;
-      }
-    } else {
-      ok = find_item<BQ>(a.seqs, a.n_seq, a.T, int(blockIdx.x) / a.Hq, lane, sq, c, i);
-    }
-    if (lane == 0) {
-      item[0] = ok ? 1 : 0;
-      item[1] = sq.x;
-      item[2] = sq.y;
-      item[3] = sq.z;
-      item[4] = sq.w;
-      item[5] = c;
-      item[6] = i;
-    }
-  }
-  if (threadIdx.x == 32) {
+  // the counts and the item at once; what lies past the last item is not used
+  const int n_items = __ldcg(a.work.counts + 1);
+  const int4* from = reinterpret_cast<const int4*>(a.work.items + int(blockIdx.x) / a.Hq);
+  const int4 it0 = __ldcg(from), it1 = __ldcg(from + 1);
+  if (threadIdx.x == 0) {
     mbar_init(smem_u32(q_full), 1);
     mbar_init(smem_u32(raw), 1);
     for (int i = 0; i < K_STAGES; ++i) {
@@ -771,20 +860,22 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0u;
     fence_mbar_init();
-    tma_prefetch_desc(&tm_qkv);
-    tma_prefetch_desc(&tm_do);
-    tma_prefetch_desc(&tm_out);
+    fence_proxy_async_smem();
   }
-  __syncthreads();
-  if (!item[0]) {
+  if (int(blockIdx.x) / a.Hq >= n_items) {
     if (blockIdx.x == 0) pdl_wait();
     return;
   }
-  const int q0 = item[1], k0 = item[2], nq = item[3], nk = item[4], nc = item[5], i0 = item[6];
+  const int q0 = it0.x, k0 = it0.y, nq = it0.z, nk = it0.w, nc = it1.x, i0 = it1.y;
   const int h = int(blockIdx.x) % a.Hq, g = h / (a.Hq / a.Hkv);
   const int i1 = i0 + BQ < nq ? i0 + BQ : nq;
   const int kmax = i1 > nc ? nk : nk - nq + i1;
   const int nblk = (kmax + BK - 1) / BK;
+  if (threadIdx.x == 0) {
+    mbar_arrive_expect_tx(smem_u32(q_full), 2 * L::TILE);
+    load_tile<D>(smem_u32(smem + L::Q), &tm_qkv, h * D, q0 + i0, smem_u32(q_full));
+    load_tile<D>(smem_u32(smem + L::DO), &tm_do, h * D, q0 + i0, smem_u32(q_full));
+  }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -798,11 +889,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---------------- copies ----------------
     bool ok = true;
     int kdone = 0, vdone = 0;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(smem_u32(q_full), 2 * L::TILE);
-      load_tile<D>(smem_u32(smem + L::Q), &tm_qkv, h * D, q0 + i0, smem_u32(q_full));
-      load_tile<D>(smem_u32(smem + L::DO), &tm_do, h * D, q0 + i0, smem_u32(q_full));
-    }
     for (int t = 0; t < nblk && ok; ++t) {
       const int ks = t % K_STAGES, vs = t % V_STAGES, y = k0 + t * BK, have = nk - t * BK < BK ? nk - t * BK : BK;
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&k_empty[ks]), (uint32_t(t / K_STAGES) & 1u) ^ 1u, abort_flag, a.err));
@@ -829,11 +915,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     if (lane == 0) {
-      mbar_drain(smem_u32(q_full), 0);
+      drained(smem_u32(q_full), 0);
       for (int j = kdone - K_STAGES > 0 ? kdone - K_STAGES : 0; j < kdone; ++j)
-        mbar_drain(smem_u32(&k_full[j % K_STAGES]), uint32_t(j / K_STAGES) & 1u);
+        drained(smem_u32(&k_full[j % K_STAGES]), uint32_t(j / K_STAGES) & 1u);
       for (int j = vdone - V_STAGES > 0 ? vdone - V_STAGES : 0; j < vdone; ++j)
-        mbar_drain(smem_u32(&v_full[j % V_STAGES]), uint32_t(j / V_STAGES) & 1u);
+        drained(smem_u32(&v_full[j % V_STAGES]), uint32_t(j / V_STAGES) & 1u);
     }
   } else if (warp == 1) {
     // ---------------- products: per block dQ += dS K, dP of the next block, S of the one after it ----------------
@@ -871,7 +957,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (t + 2 < nblk) ok = wait(dq_done, uint32_t(t) & 1u) && form_s(t + 2);  // into dS's place
     }
     mma_commit_on(on, smem_u32(drain));
-    mbar_drain(smem_u32(drain), 0);
+    drained(smem_u32(drain), 0);
   } else {
     // ---------------- dS: query row 32 (warp % 4) + lane, keys [32 part, 32 part + 32) of the block ----------------
     const int part = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane, cb = 32 * part;
@@ -971,7 +1057,7 @@ inline bool shape_ok(int64_t T, int Hq, int Hkv, int D, int n_seq) {
          Hq % Hkv == 0 && n_seq >= 1 && n_seq <= MOT_MAX_TOKENS;
 }
 
-// CTAs that share a KV head's query heads: a rule on the group alone, as it sets the order of the sums.
+// CTAs that share a tile and KV head, a power of two: a rule on the group alone, as it sets the order of the sums.
 inline int shares_of(int G) { return G >= 8 ? 8 : G >= 4 ? 4 : G >= 2 ? 2 : 1; }
 
 // The workspace after its header, in bytes.
@@ -987,7 +1073,7 @@ struct Room {
     ndelta = nlse + up(T * Hq * 4);
     tiles = ndelta + up(T * Hq * 4);
     items = tiles + int64_t(max_tiles) * 16;
-    counts = items + up(int64_t(max_items) * 8);
+    counts = items + int64_t(max_items) * 32;
     change = counts + 16;
     border = change + up((T + 1) * 4);
     runs = border + up((T / 32 + 1) * 4);
@@ -1025,7 +1111,7 @@ static int launch(const uint16_t* dout, const uint16_t* qkv, const uint16_t* out
   st.n_seq = a.n_seq;
   st.work = a.work;
   st.err = a.err;
-  stats_kernel<D><<<dim3(unsigned((a.T + 31) / 32 + 1), unsigned((a.Hq + 31) / 32)), STATS_THREADS, 0, s>>>(st);
+  stats_kernel<D><<<dim3(unsigned((a.T + STATS_ROWS - 1) / STATS_ROWS + 1), unsigned((a.Hq + 31) / 32)), STATS_THREADS, 0, s>>>(st);
   if (cudaGetLastError() != cudaSuccess) return MOT_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(kv_ctas));
@@ -1089,7 +1175,7 @@ extern "C" int mot_joint_attention_backward(const mot_bf16* dout, const mot_bf16
   a.nlse = reinterpret_cast<float*>(base + room.nlse);
   a.ndelta = reinterpret_cast<float*>(base + room.ndelta);
   a.work.tiles = reinterpret_cast<int4*>(base + room.tiles);
-  a.work.items = reinterpret_cast<int2*>(base + room.items);
+  a.work.items = reinterpret_cast<attnb::Item*>(base + room.items);
   a.work.counts = reinterpret_cast<int32_t*>(base + room.counts);
   a.work.change = reinterpret_cast<int32_t*>(base + room.change);
   a.work.border = reinterpret_cast<uint32_t*>(base + room.border);
