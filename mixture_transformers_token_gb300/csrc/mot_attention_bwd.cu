@@ -9,23 +9,24 @@
 // probability is stored.
 //
 // dq sums over keys, dk and dv over queries, and neither sum may be cut between CTAs in an order that the schedule sets. So
-// there are two kernels, each with its sums in tensor memory from the first block to the last, at the price of forming S and dP
-// twice: seven products of 128 x 128 x D a block instead of five.
+// there are two kinds of CTAs, each with its sums in tensor memory from the first block to the last, at the price of forming S
+// and dP twice: seven products of 128 x 128 x D a block instead of five.
 //
 //   stats_kernel  -delta and -lse / scale of every row and head, [Hq][T] (reads dout and out once); its first CTA makes the
 //                 lists of work.
-//   dkv_kernel    one CTA per (tile of keys, KV head, share of its blocks). The borders of the sequences' key ranges cut
-//                 the pack's rows into runs that the same sequences see, and a tile is 128 rows of a run or what is left of it.
-//                 So nothing that a sequence holds reaches the sums of rows that are not its keys, as it would through 0 NaN
-//                 in a tile of two sequences. Over the sequences that see these rows, the group's heads and the share's
-//                 blocks of 128 queries: S' = K Q' and dP' = V dO' (keys in the rows), P' and dS' as bf16 into tensor memory in
-//                 the places of S' and dP', dV += P' dO, dK += dS' Q with A from tensor memory. The CTAs of a cluster hold
-//                 the shares of one KV head; each sends its sums to shared memory and adds and writes its part of the rows,
-//                 in the order of the shares, through the cluster's shared memory.
-//   dq_kernel     one CTA per (128 queries of a sequence, head): over the blocks of 128 keys, S = Q K', dP = dO V', dS as bf16
-//                 into tensor memory in the place of S, dQ += dS K. Its grid starts while the last CTAs of dkv_kernel run.
+//   grad_kernel   first the CTAs of dK and dV, one per (tile of keys, KV head, share of its blocks). The borders of the
+//                 sequences' key ranges cut the pack's rows into runs that the same sequences see, and a tile is 128 rows of a
+//                 run or what is left of it. So nothing that a sequence holds reaches the sums of rows that are not its keys, as
+//                 it would through 0 NaN in a tile of two sequences. Over the sequences that see these rows, the group's heads
+//                 and the share's blocks of 128 queries: S' = K Q' and dP' = V dO' (keys in the rows), P' and dS' as bf16 into
+//                 tensor memory in the places of S' and dP', dV += P' dO, dK += dS' Q with A from tensor memory. Each share's
+//                 sums go to the workspace, and the share that comes last adds them up, in the order of the shares.
+//                 (With the shares in a cluster, added up through its shared memory, a CTA spent 20000 of 120000 cycles in that
+//                 and a twentieth of the SMs had no cluster.)
+//                 Then the CTAs of dQ, one per (128 queries of a sequence, head), which fill the SMs as the others end: over
+//                 the blocks of 128 keys, S = Q K', dP = dO V', dS as bf16 into tensor memory in the place of S, dQ += dS K.
 //
-// In dkv_kernel, lse and delta belong to the columns. They are subtracted by the products themselves: one more step of K, whose A
+// For dK and dV, lse and delta belong to the columns. They are subtracted by the products themselves: one more step of K, whose A
 // is ones and whose B holds the value as three bf16 (24 bits), so that no thread reads them from shared memory, which the products
 // keep busy.
 //
@@ -48,7 +49,7 @@ using namespace attn;
 
 constexpr int BQ = 128, BK = 128;
 constexpr int COMPUTE_WARPS = 16;  // four to a quarter of the rows (tensor memory gives a warp 32 lanes): 32 columns a thread
-constexpr int THREADS = 32 * (2 + COMPUTE_WARPS);
+constexpr int THREADS = 32 * (2 + COMPUTE_WARPS);  // copies, products, P and dS
 constexpr uint32_t SUB = 128 * 64 * 2;  // a [128 rows x 64 columns] bf16 swizzled tile
 
 // 128 queries of a sequence: its descriptor and the first of them.
@@ -59,7 +60,8 @@ struct alignas(16) Item {
 // Lists in the workspace, made by stats_kernel's first CTA.
 struct Work {
   int4* tiles;    // (first row, rows, first and last sequence that may see them), ascending
-  Item* items;    // of dq_kernel
+  Item* items;    // of dQ's CTAs
+  int32_t* ended; // [tile][Hkv] shares whose sums are there
   int32_t* counts;  // tiles, items
   // scratch: changes of the number of sequences that see a row, at each row; borders, a bit a row; the borders in order
   int32_t* change;
@@ -71,8 +73,10 @@ struct Work {
 struct Args {
   const int32_t* seqs;  // [n_seq][5]
   int n_seq, T, Hq, Hkv;
-  int shares;           // CTAs of a cluster of dkv_kernel
+  int shares;           // CTAs of a tile and KV head, a power of two
+  unsigned kv_ctas;     // of grad_kernel's CTAs, the first ones
   Work work;
+  float* sums;          // [tile][Hkv][shares][dV, dK][D / 4][128 rows][4]
   float c, scale;
   const float* nlse;    // [Hq][T] -lse / scale
   const float* ndelta;  // [Hq][T] -delta
@@ -88,7 +92,7 @@ struct StatsArgs {
   const uint16_t* dout;
   const uint16_t* out;
   const float* lse;
-  int T, Hq;
+  int T, Hq, Hkv;
   float rscale;
   float* nlse;
   float* ndelta;
@@ -314,6 +318,10 @@ __global__ void __launch_bounds__(STATS_THREADS) stats_kernel(const StatsArgs a)
     int scan[STATS_THREADS / 32];
   } room;
   pdl_trigger();
+  if (blockIdx.y == 0)
+    for (int64_t i = int64_t(blockIdx.x) * STATS_THREADS + threadIdx.x; i < int64_t(a.work.max_tiles) * a.Hkv;
+         i += int64_t(gridDim.x) * STATS_THREADS)
+      a.work.ended[i] = 0;
   if (blockIdx.x == 0) {
     if (blockIdx.y != 0) return;
     if (a.n_seq <= kSortedSeqs) make_work_few(a, room.few);
@@ -470,13 +478,6 @@ __device__ __forceinline__ void product_ta(uint32_t on, uint32_t d, uint32_t a_t
 __device__ __forceinline__ void ld_columns(uint32_t taddr, float (&v)[32]) { tmem_ld32(taddr, v); }
 __device__ __forceinline__ void ld_columns(uint32_t taddr, float (&v)[16]) { tmem_ld16(taddr, v); }
 
-__device__ __forceinline__ void ld_shared_f4(uint32_t addr_cluster, float (&v)[4]) {
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
-               : "r"(addr_cluster)
-               : "memory");
-}
-
 // ---------------------------------------------------------------------------
 // dK and dV
 // ---------------------------------------------------------------------------
@@ -487,23 +488,55 @@ struct KvLayout {
   static constexpr uint32_t TILE = 128 * D * 2;
   static constexpr uint32_t STEP = 128 * 16 * 2;                  // an operand of one step of K
   static constexpr uint32_t K = 0, V = TILE;
-  static constexpr uint32_t QD = 2 * TILE;                        // STAGES of (Q, dO); at the end dV and dK in fp32
+  static constexpr uint32_t QD = 2 * TILE;                        // STAGES of (Q, dO)
   static constexpr uint32_t ONES = QD + STAGES * 2 * TILE;        // [128][16]: ones in columns 0 to 2
   static constexpr uint32_t STATS = ONES + STEP;                  // STAGES of [128][16] -lse / scale and of -delta, in three
   static constexpr uint32_t EDGES = STATS + STAGES * 2 * STEP;    // STAGES of the block's edges, see the copies
   static constexpr uint32_t BAR = EDGES + STAGES * 16;
   static constexpr size_t BYTES = 1024 + size_t(BAR) + 512;
   static constexpr uint32_t S = 0, DP = 128, DV = 256, DK = 384;  // tensor memory
-  static_assert(2 * 128 * D * 4 <= STAGES * 2 * TILE, "the sums fit where the blocks were");
 };
 
+// Four fp32 of a row: 32 rows of a warp are 512 consecutive bytes.
 template <int D>
-__global__ void __launch_bounds__(THREADS, 1)
-    dkv_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __grid_constant__ CUtensorMap tm_do, const Args a) {
+__device__ __forceinline__ float4* sums_at(float* sums, int m, int piece, int row) {
+  return reinterpret_cast<float4*>(sums) + (m * (D / 4) + piece) * 128 + row;
+}
+
+// The tile's dV and dK as bf16, 16 values of a row a thread: the sums of the shares, in order. All reads of a row's 16 values are
+// under way at once.
+template <int D, int SHARES>
+__device__ __forceinline__ void add_shares(float* sums, const int4& tile, int g, const Args& a) {
+  const int64_t N = int64_t(a.Hq + 2 * a.Hkv) * D;
+  for (int i = threadIdx.x; i < 2 * (D / 16) * 128; i += THREADS) {
+    const int r = i & 127, k = i / 128 % (D / 16), m = i / (128 * (D / 16));
+    if (r >= tile.y) continue;
+    float4 u[SHARES][4];
+#pragma unroll
+    for (int p = 0; p < SHARES; ++p)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) u[p][q] = __ldcg(sums_at<D>(sums + p * (2 * 128 * D), m, 4 * k + q, r));
+    const float f = m ? a.scale : 1.0f;
+    uint32_t o[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float4 v = u[0][q];
+#pragma unroll
+      for (int p = 1; p < SHARES; ++p)
+        v = make_float4(__fadd_rn(v.x, u[p][q].x), __fadd_rn(v.y, u[p][q].y), __fadd_rn(v.z, u[p][q].z), __fadd_rn(v.w, u[p][q].w));
+      o[2 * q] = cvt_bf2(__fmul_rn(v.x, f), __fmul_rn(v.y, f));
+      o[2 * q + 1] = cvt_bf2(__fmul_rn(v.z, f), __fmul_rn(v.w, f));
+    }
+    uint4* to = reinterpret_cast<uint4*>(a.dqkv + (tile.x + r) * N + (a.Hq + (m ? 0 : a.Hkv) + g) * D + 16 * k);
+    to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_qkv, const CUtensorMap& tm_do, const Args& a, uint8_t* smem) {
   using L = KvLayout<D>;
   constexpr int STAGES = L::STAGES;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
   uint64_t* kv_full = bars;
   uint64_t* raw = bars + 1;         // a block that is zeroed in part before it is full
@@ -518,6 +551,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* dk_done = bars + 19;
   uint64_t* drain = bars + 20;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
+  volatile int* last = reinterpret_cast<volatile int*>(tmem_slot + 2);
   volatile uint32_t* abort_flag = tmem_slot + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -546,12 +580,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     *reinterpret_cast<uint4*>(smem + L::ONES + i * 16) =
         i < int(L::STEP / 16) && (i & 8) == 0 ? make_uint4(0x3F803F80u, 0x3F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
-  pdl_wait();     // stats_kernel, also on behalf of dq_kernel, whose grid starts after every CTA's trigger
-  pdl_trigger();
+  pdl_wait();  // stats_kernel
   // the count and the tile at once; what lies past the last tile is not used
   const int n_tiles = __ldcg(a.work.counts);
   const int4 tile = __ldcg(a.work.tiles + rest / a.Hkv);
-  if (rest / a.Hkv >= n_tiles) return;  // for every CTA of the cluster
+  if (rest / a.Hkv >= n_tiles) return;
   const int row0 = tile.x;
   if (threadIdx.x == 0) {
     mbar_arrive_expect_tx(smem_u32(kv_full), 2 * L::TILE);
@@ -749,19 +782,18 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(ds_full));
     }
-    // the sums to shared memory, in fp32: 16-byte piece k of a row at k ^ row, so that a warp's rows meet no bank twice
     if (ok && n_it > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(dk_done), uint32_t(n_it - 1) & 1u, abort_flag, a.err));
     tc_fence_after();
+    float* mine = a.sums + (int64_t(rest) * a.shares + share) * (2 * 128 * D);
 #pragma unroll 1
     for (int m = 0; m < 2 && ok; ++m) {
-      uint8_t* to = smem + L::QD + m * 128 * D * 4 + row * D * 4;
       float v[D / 4] = {};
       if (n_it > 0) ld_columns(at + (m ? L::DK : L::DV) + part * (D / 4), v);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
-        *reinterpret_cast<float4*>(to + (((part * (D / 16) + i) ^ (row & (D / 4 - 1))) << 4)) =
-            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        __stcg(sums_at<D>(mine, m, part * (D / 16) + i, row), make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
     }
+    __threadfence();
   }
   tc_fence_before();
   __syncthreads();
@@ -769,35 +801,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  __syncwarp();
-  cluster_sync();  // every share's sums are there
-  if (*abort_flag == 0u) {
-    const int rows = BK / a.shares, r0 = share * rows;
-    const int64_t N = int64_t(a.Hq + 2 * a.Hkv) * D;
-    for (int i = threadIdx.x; i < 2 * rows * (D / 8); i += THREADS) {
-      const int m = i / (rows * (D / 8)), r = r0 + i / (D / 8) % rows, k = i % (D / 8) * 2;
-      if (r >= tile.y) continue;
-      const uint32_t from = smem_u32(smem + L::QD + m * 128 * D * 4 + r * D * 4), x = uint32_t(r & (D / 4 - 1));
-      float v[8] = {};
-      for (int p = 0; p < a.shares; ++p) {
-        float u[4], w[4];
-        ld_shared_f4(map_to_rank(from + ((k ^ x) << 4), p), u);
-        ld_shared_f4(map_to_rank(from + (((k + 1) ^ x) << 4), p), w);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          v[q] = p == 0 ? u[q] : __fadd_rn(v[q], u[q]);
-          v[4 + q] = p == 0 ? w[q] : __fadd_rn(v[4 + q], w[q]);
-        }
-      }
-      const float f = m ? a.scale : 1.0f;
-      uint32_t o[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) o[q] = cvt_bf2(__fmul_rn(v[2 * q], f), __fmul_rn(v[2 * q + 1], f));
-      *reinterpret_cast<uint4*>(a.dqkv + (row0 + r) * N + (a.Hq + (m ? 0 : a.Hkv) + g) * D + 4 * k) =
-          make_uint4(o[0], o[1], o[2], o[3]);
-    }
-  }
-  cluster_sync();  // no CTA leaves while another reads its shared memory
+  // The share that comes last finds the others' sums; after a timeout the tile is not written.
+  if (threadIdx.x == 0) *last = *abort_flag == 0u ? atomicAdd(a.work.ended + rest, 1) + 1 : 0;
+  __syncthreads();
+  if (*last != a.shares) return;
+  __threadfence();
+  float* sums = a.sums + int64_t(rest) * a.shares * (2 * 128 * D);
+  if (a.shares == 8) add_shares<D, 8>(sums, tile, g, a);
+  else if (a.shares == 4) add_shares<D, 4>(sums, tile, g, a);
+  else if (a.shares == 2) add_shares<D, 2>(sums, tile, g, a);
+  else add_shares<D, 1>(sums, tile, g, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -814,13 +827,10 @@ struct QLayout {
 };
 
 template <int D>
-__global__ void __launch_bounds__(THREADS, 1)
-    dq_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __grid_constant__ CUtensorMap tm_do,
-              const __grid_constant__ CUtensorMap tm_out, const Args a) {
+__device__ __forceinline__ void dq_cta(const CUtensorMap& tm_qkv, const CUtensorMap& tm_do, const CUtensorMap& tm_out,
+                                       const Args& a, uint8_t* smem, unsigned cta) {
   using L = QLayout<D>;
   constexpr int K_STAGES = L::K_STAGES, V_STAGES = L::V_STAGES;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
   uint64_t* q_full = bars;
   uint64_t* raw = bars + 1;       // a K block that is zeroed in part before it is full
@@ -838,8 +848,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the counts and the item at once; what lies past the last item is not used
+  pdl_wait();  // stats_kernel
   const int n_items = __ldcg(a.work.counts + 1);
-  const int4* from = reinterpret_cast<const int4*>(a.work.items + int(blockIdx.x) / a.Hq);
+  const int4* from = reinterpret_cast<const int4*>(a.work.items + int(cta) / a.Hq);
   const int4 it0 = __ldcg(from), it1 = __ldcg(from + 1);
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(q_full), 1);
@@ -862,12 +873,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (int(blockIdx.x) / a.Hq >= n_items) {
-    if (blockIdx.x == 0) pdl_wait();
-    return;
-  }
+  if (int(cta) / a.Hq >= n_items) return;
   const int q0 = it0.x, k0 = it0.y, nq = it0.z, nk = it0.w, nc = it1.x, i0 = it1.y;
-  const int h = int(blockIdx.x) % a.Hq, g = h / (a.Hq / a.Hkv);
+  const int h = int(cta) % a.Hq, g = h / (a.Hq / a.Hkv);
   const int i1 = i0 + BQ < nq ? i0 + BQ : nq;
   const int kmax = i1 > nc ? nk : nk - nq + i1;
   const int nblk = (kmax + BK - 1) / BK;
@@ -1048,8 +1056,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  // This grid starts before dkv_kernel's has ended: one CTA ends after it, so that what follows this grid follows both.
-  if (blockIdx.x == 0) pdl_wait();
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    grad_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __grid_constant__ CUtensorMap tm_do,
+                const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  if (blockIdx.x < a.kv_ctas) dkv_cta<D>(tm_qkv, tm_do, a, smem);
+  else dq_cta<D>(tm_qkv, tm_do, tm_out, a, smem, blockIdx.x - a.kv_ctas);
 }
 
 inline bool shape_ok(int64_t T, int Hq, int Hkv, int D, int n_seq) {
@@ -1062,9 +1078,10 @@ inline int shares_of(int G) { return G >= 8 ? 8 : G >= 4 ? 4 : G >= 2 ? 2 : 1; }
 
 // The workspace after its header, in bytes.
 struct Room {
-  int64_t nlse, ndelta, tiles, items, counts, change, border, runs, end;
+  int64_t nlse, ndelta, tiles, items, counts, ended, change, border, runs, sums, end, ctas;
   int max_tiles, max_items;
-  Room(int64_t T, int Hq, int64_t n_seq) {
+  Room(int64_t T, int Hq, int Hkv, int D, int64_t n_seq) {
+    const int shares = shares_of(Hq / Hkv);
     auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
     const int64_t borders = 2 * n_seq < T + 1 ? 2 * n_seq : T + 1, blocks = (T + 127) / 128;
     max_tiles = int(blocks + borders < T ? blocks + borders : T);  // a run adds at most one short tile
@@ -1074,10 +1091,13 @@ struct Room {
     tiles = ndelta + up(T * Hq * 4);
     items = tiles + int64_t(max_tiles) * 16;
     counts = items + int64_t(max_items) * 32;
-    change = counts + 16;
+    ended = counts + 16;
+    change = ended + up(int64_t(max_tiles) * Hkv * 4);
     border = change + up((T + 1) * 4);
     runs = border + up((T / 32 + 1) * 4);
-    end = runs + up(borders * 4);
+    sums = runs + up(borders * 4);
+    end = sums + int64_t(max_tiles) * Hkv * shares * (2 * 128 * D * 4);
+    ctas = int64_t(max_tiles) * Hkv * shares + int64_t(max_items) * Hq;
   }
 };
 
@@ -1090,20 +1110,18 @@ static int launch(const uint16_t* dout, const uint16_t* qkv, const uint16_t* out
       !make_tmap_bf16(&tm_do, dout, uint64_t(a.Hq) * D, uint64_t(a.T), 64, 128) ||
       !make_tmap_bf16(&tm_out, a.dqkv, N, uint64_t(a.T), 64, 128))
     return MOT_ERR_CUDA;
-  constexpr int kv_bytes = int(KvLayout<D>::BYTES), q_bytes = int(QLayout<D>::BYTES);
-  static_assert(kv_bytes > 114 * 1024 && q_bytes > 114 * 1024, "one CTA an SM: two would compete for tensor memory");
-  static_assert(kv_bytes <= 227 * 1024 && q_bytes <= 227 * 1024, "shared memory of a CTA");
-  if (cudaFuncSetAttribute(dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kv_bytes) != cudaSuccess ||
-      cudaFuncSetAttribute(dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, q_bytes) != cudaSuccess)
+  constexpr int bytes = int(KvLayout<D>::BYTES > QLayout<D>::BYTES ? KvLayout<D>::BYTES : QLayout<D>::BYTES);
+  static_assert(bytes > 114 * 1024, "one CTA an SM: two would compete for tensor memory");
+  static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
+  if (cudaFuncSetAttribute(grad_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return MOT_ERR_CUDA;
-  const int64_t kv_ctas = int64_t(a.work.max_tiles) * a.Hkv * a.shares, q_ctas = int64_t(a.work.max_items) * a.Hq;
-  if (kv_ctas > (int64_t(1) << 31) - 1 || q_ctas > (int64_t(1) << 31) - 1) return MOT_ERR_GEOMETRY;
   StatsArgs st{};
   st.dout = dout;
   st.out = out;
   st.lse = lse;
   st.T = a.T;
   st.Hq = a.Hq;
+  st.Hkv = a.Hkv;
   st.rscale = 1.0f / a.scale;
   st.nlse = const_cast<float*>(a.nlse);
   st.ndelta = const_cast<float*>(a.ndelta);
@@ -1113,22 +1131,8 @@ static int launch(const uint16_t* dout, const uint16_t* qkv, const uint16_t* out
   st.err = a.err;
   stats_kernel<D><<<dim3(unsigned((a.T + STATS_ROWS - 1) / STATS_ROWS + 1), unsigned((a.Hq + 31) / 32)), STATS_THREADS, 0, s>>>(st);
   if (cudaGetLastError() != cudaSuccess) return MOT_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(kv_ctas));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = kv_bytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = unsigned(a.shares);
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, dkv_kernel<D>, tm_qkv, tm_do, a) != cudaSuccess) return MOT_ERR_CUDA;
-  if (launch_dependent(dq_kernel<D>, dim3(unsigned(q_ctas)), dim3(THREADS), size_t(q_bytes), s, tm_qkv, tm_do, tm_out, a) !=
-      cudaSuccess)
+  if (launch_dependent(grad_kernel<D>, dim3(a.kv_ctas + unsigned(a.work.max_items * int64_t(a.Hq))), dim3(THREADS), size_t(bytes), s,
+                       tm_qkv, tm_do, tm_out, a) != cudaSuccess)
     return MOT_ERR_CUDA;
   return MOT_OK;
 }
@@ -1140,7 +1144,8 @@ using namespace mot;
 
 extern "C" size_t mot_joint_attention_backward_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int n_seq) {
   if (!attnb::shape_ok(T, Hq, Hkv, D, n_seq)) return 0;
-  return sizeof(PlanHeader) + size_t(attnb::Room(T, Hq, n_seq).end);
+  const attnb::Room room(T, Hq, Hkv, D, n_seq);
+  return room.ctas <= INT32_MAX ? sizeof(PlanHeader) + size_t(room.end) : 0;
 }
 
 extern "C" int mot_joint_attention_backward(const mot_bf16* dout, const mot_bf16* qkv, const mot_bf16* out,
@@ -1154,6 +1159,8 @@ extern "C" int mot_joint_attention_backward(const mot_bf16* dout, const mot_bf16
   if (!aligned16(dout) || !aligned16(qkv) || !aligned16(out) || !aligned16(lse) || !aligned16(seqs) || !aligned16(ws) ||
       !aligned16(dqkv))
     return MOT_ERR_ALIGN;
+  const attnb::Room room(T, Hq, Hkv, D, n_seq);
+  if (room.ctas > INT32_MAX) return MOT_ERR_GEOMETRY;
   if (ws_bytes < mot_joint_attention_backward_workspace_bytes(T, Hq, Hkv, D, n_seq)) return MOT_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const void* ptrs[] = {dout, qkv, out, lse, seqs, ws, dqkv};
@@ -1171,12 +1178,14 @@ extern "C" int mot_joint_attention_backward(const mot_bf16* dout, const mot_bf16
   a.shares = attnb::shares_of(Hq / Hkv);
   a.c = c;
   a.scale = scale;
-  const attnb::Room room(T, Hq, n_seq);
   a.nlse = reinterpret_cast<float*>(base + room.nlse);
   a.ndelta = reinterpret_cast<float*>(base + room.ndelta);
   a.work.tiles = reinterpret_cast<int4*>(base + room.tiles);
   a.work.items = reinterpret_cast<attnb::Item*>(base + room.items);
   a.work.counts = reinterpret_cast<int32_t*>(base + room.counts);
+  a.work.ended = reinterpret_cast<int32_t*>(base + room.ended);
+  a.sums = reinterpret_cast<float*>(base + room.sums);
+  a.kv_ctas = unsigned(int64_t(room.max_tiles) * Hkv * a.shares);
   a.work.change = reinterpret_cast<int32_t*>(base + room.change);
   a.work.border = reinterpret_cast<uint32_t*>(base + room.border);
   a.work.runs = reinterpret_cast<int32_t*>(base + room.runs);
