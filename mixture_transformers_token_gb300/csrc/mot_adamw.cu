@@ -9,6 +9,7 @@
 // Every element is read and written once: 30 bytes with fp32 states, fp32 gradients and the bf16 copy, 16.06 with 8-bit states
 // and bf16 gradients. The bound is memory.
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -23,16 +24,18 @@ namespace adamw {
 
 constexpr int THREADS = 256;
 constexpr int BLOCK = MOT_ADAMW_BLOCK;
-constexpr int CHUNK = 2048;       // elements of a CTA's share of a tensor: eight blocks
+constexpr int WARPS = THREADS / 32;
 constexpr int kMaxTensors = 128;  // of one launch: its table is part of the launch's parameters
+constexpr int ROUNDS = 7;         // of Philox
 
 struct Table {
   mot_adamw_tensor t[kMaxTensors];
-  uint32_t first[kMaxTensors + 1];  // first chunk of each tensor
+  uint32_t first[kMaxTensors + 1];  // first CTA of each tensor
   int n;
   int base;                         // index of t[0] in the caller's array
+  int blocks;                       // of 256 elements a warp
   const float* hyper;
-  uint32_t seed_lo, seed_hi;
+  uint32_t key[2 * ROUNDS];         // of each round
   uint32_t* err;
 };
 
@@ -55,14 +58,30 @@ __device__ __forceinline__ bool load_hyper(const float* row, Hyper& h) {
          h.eps > 0.0f && finite(h.eps) && finite(h.gs) && h.step >= 1u && h.step < 0x80000000u;
 }
 
-// One element: m and v become the new moments, r the square root of v; returns the new weight.
-__device__ __forceinline__ float update(const Hyper& h, float wl, float g, float& m, float& v, float& r, float p) {
-  g = __fmul_rn(g, h.gs);
-  m = __fadd_rn(__fmul_rn(m, h.b1), __fmul_rn(g, h.c1));
-  v = __fadd_rn(__fmul_rn(v, h.b2), __fmul_rn(__fmul_rn(g, g), h.c2));
-  r = __fsqrt_rn(v);
-  const float u = __fdiv_rn(__fmul_rn(m, h.lr1), __fadd_rn(__fmul_rn(r, h.r2), h.eps));
-  return __fsub_rn(p, __fadd_rn(u, __fmul_rn(p, wl)));
+// Eight elements: m and v become the new moments, r the square roots of v, p the new weights. Products two at a time.
+__device__ __forceinline__ void update(const Hyper& h, float wl, float (&g)[8], float (&m)[8], float (&v)[8], float (&r)[8],
+                                       float (&p)[8]) {
+  float a[8], b[8];
+  mul8(g, h.gs, g);
+  mul8(m, h.b1, m);
+  mul8(g, h.c1, a);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m[i] = __fadd_rn(m[i], a[i]);
+  mul8(v, h.b2, v);
+  mul8(g, g, a);
+  mul8(a, h.c2, a);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = __fadd_rn(v[i], a[i]);
+    r[i] = __fsqrt_rn(v[i]);
+  }
+  mul8(r, h.r2, a);
+  mul8(m, h.lr1, b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = __fdiv_rn(b[i], __fadd_rn(a[i], h.eps));
+  mul8(p, wl, a);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) p[i] = __fsub_rn(p[i], __fadd_rn(b[i], a[i]));
 }
 
 __device__ __forceinline__ void philox_round(uint32_t (&x)[4], uint32_t k0, uint32_t k1) {
@@ -74,18 +93,14 @@ __device__ __forceinline__ void philox_round(uint32_t (&x)[4], uint32_t k0, uint
 }
 
 // Philox4x32-7: the words of elements 4 b .. 4 b + 3.
-__device__ __forceinline__ void random_words(uint32_t (&x)[4], uint64_t b, uint32_t tensor, uint32_t step, uint32_t k0,
-                                             uint32_t k1) {
+__device__ __forceinline__ void random_words(uint32_t (&x)[4], uint64_t b, uint32_t tensor, uint32_t step,
+                                             const uint32_t* key) {
   x[0] = uint32_t(b);
   x[1] = uint32_t(b >> 32);
   x[2] = tensor;
   x[3] = step;
 #pragma unroll
-  for (int i = 0; i < 7; ++i) {
-    philox_round(x, k0, k1);
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
-  }
+  for (int i = 0; i < ROUNDS; ++i) philox_round(x, key[2 * i], key[2 * i + 1]);
 }
 
 // A block's quantiser from its largest magnitude's bits (whose order is the floats', infinities and NaNs last).
@@ -99,20 +114,24 @@ __device__ __forceinline__ Scale block_scale(uint32_t top) {
   return {__fmul_rn(a, 1.0f / 448.0f), __fmul_rn(__frcp_rn(a), 448.0f)};
 }
 
-// |x| inv, at most 448, rounded to one of its e4m3 neighbours by 16 random bits below the last kept one. Values under 2^-6
-// (e4m3's subnormals) move up by 2^-6, where fp32 values have the subnormals' step in the same bit. inv is zero in a block
-// without a scale: its codes are zero.
-__device__ __forceinline__ float round_at_random(float x, float inv, uint32_t bits16) {
-  const float y = inv > 0.0f ? fminf(__fmul_rn(fabsf(x), inv), 448.0f) : 0.0f;
-  const float lift = y < 0x1p-6f ? 0x1p-6f : 0.0f;
-  const uint32_t z = (__float_as_uint(__fadd_rn(y, lift)) + (bits16 << 4)) & 0xFFF00000u;
-  return __fsub_rn(__uint_as_float(z), lift);
+// y = x inv (at most 448 and a few units in magnitude) rounded to one of its e4m3 neighbours by 16 random bits below the last kept
+// one; the sign bit stays, and what is a few units above 448 keeps 448's bits. FULL false: no magnitude is under 2^-6. FULL: those
+// (e4m3's subnormals) move up by 2^-6, where fp32 values have the subnormals' step in the same bit.
+template <bool FULL>
+__device__ __forceinline__ float round_at_random(float y, uint32_t bits16) {
+  if constexpr (FULL) {
+    const float lift = fabsf(y) < 0x1p-6f ? 0x1p-6f : 0.0f;
+    const uint32_t z = (__float_as_uint(__fadd_rn(fabsf(y), lift)) + (bits16 << 4)) & 0xFFF00000u;
+    return copysignf(__fsub_rn(__uint_as_float(z), lift), y);
+  } else {
+    return __uint_as_float((__float_as_uint(y) + (bits16 << 4)) & 0xFFF00000u);
+  }
 }
 
-// Elements [0, 8) of a lane, of which the first `have` are there.
-template <bool BF16>
+// Elements [0, 8) of a lane, of which the first `have` are there (ALL: all of them).
+template <bool ALL, bool BF16>
 __device__ __forceinline__ void load_grad(const void* g, int64_t e, int have, float (&x)[8]) {
-  if (have == 8) {
+  if (ALL || have == 8) {
     if constexpr (BF16) {
       const uint4 w = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g) + e));
       x[0] = bf_lo(w.x), x[1] = bf_hi(w.x), x[2] = bf_lo(w.y), x[3] = bf_hi(w.y);
@@ -129,8 +148,9 @@ __device__ __forceinline__ void load_grad(const void* g, int64_t e, int have, fl
   }
 }
 
+template <bool ALL>
 __device__ __forceinline__ void load8(const float* s, int have, float (&x)[8]) {
-  if (have == 8) {
+  if (ALL || have == 8) {
     const float4 a = *reinterpret_cast<const float4*>(s), b = *(reinterpret_cast<const float4*>(s) + 1);
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
   } else {
@@ -139,8 +159,9 @@ __device__ __forceinline__ void load8(const float* s, int have, float (&x)[8]) {
   }
 }
 
+template <bool ALL>
 __device__ __forceinline__ void store8(float* d, int have, const float (&x)[8]) {
-  if (have == 8) {
+  if (ALL || have == 8) {
     *reinterpret_cast<float4*>(d) = make_float4(x[0], x[1], x[2], x[3]);
     *(reinterpret_cast<float4*>(d) + 1) = make_float4(x[4], x[5], x[6], x[7]);
   } else {
@@ -150,8 +171,9 @@ __device__ __forceinline__ void store8(float* d, int have, const float (&x)[8]) 
   }
 }
 
+template <bool ALL>
 __device__ __forceinline__ void store_bf16(uint16_t* d, int have, const float (&x)[8]) {
-  if (have == 8) {
+  if (ALL || have == 8) {
     *reinterpret_cast<uint4*>(d) =
         make_uint4(cvt_bf2(x[0], x[1]), cvt_bf2(x[2], x[3]), cvt_bf2(x[4], x[5]), cvt_bf2(x[6], x[7]));
   } else {
@@ -161,9 +183,10 @@ __device__ __forceinline__ void store_bf16(uint16_t* d, int have, const float (&
   }
 }
 
+template <bool ALL>
 __device__ __forceinline__ void load_codes(const uint8_t* s, int have, float scale, float (&x)[8]) {
   uint32_t w[2] = {0u, 0u};
-  if (have == 8) {
+  if (ALL || have == 8) {
     const uint2 c = *reinterpret_cast<const uint2*>(s);
     w[0] = c.x, w[1] = c.y;
   } else {
@@ -174,13 +197,15 @@ __device__ __forceinline__ void load_codes(const uint8_t* s, int have, float sca
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 v = kv::h2_to_f2(kv::e4m3x2_to_h2((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu));
-    x[2 * i] = __fmul_rn(v.x, scale);
-    x[2 * i + 1] = __fmul_rn(v.y, scale);
+    x[2 * i] = v.x;
+    x[2 * i + 1] = v.y;
   }
+  mul8(x, scale, x);
 }
 
+template <bool ALL>
 __device__ __forceinline__ void store_codes(uint8_t* d, int have, uint32_t lo, uint32_t hi) {
-  if (have == 8) {
+  if (ALL || have == 8) {
     *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
   } else {
 #pragma unroll
@@ -191,88 +216,163 @@ __device__ __forceinline__ void store_codes(uint8_t* d, int have, uint32_t lo, u
 
 __device__ __forceinline__ uint32_t warp_max(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
 
-// A warp takes a block of 256 elements, eight consecutive ones a lane: the block's scales need no shared memory.
-template <bool BF16, bool E4M3>
-__device__ __forceinline__ void warp_block(const Table& a, const Hyper& h, const mot_adamw_tensor& t, int id, int64_t block,
-                                           int lane) {
-  const int64_t e = block * BLOCK + lane * 8;
-  const int64_t left = t.n - e;
-  const int have = left >= 8 ? 8 : left > 0 ? int(left) : 0;
-  const float wl = __fmul_rn(h.lr, t.weight_decay);
-  float g[8], m[8], v[8], r[8], p[8];
-  load_grad<BF16>(t.g, e, have, g);
-  load8(t.p + e, have, p);
-  if constexpr (E4M3) {
-    const float2 s = *reinterpret_cast<const float2*>(t.scales + 2 * block);
-    load_codes(static_cast<const uint8_t*>(t.m) + e, have, s.x, m);
-    load_codes(static_cast<const uint8_t*>(t.v) + e, have, s.y, v);
+// The largest magnitude of eight values; a NaN if there is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t top_of(const float (&x)[8]) {
+  float a = fabsf(x[0]), b = fabsf(x[1]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], v[i]);
-  } else {
-    load8(static_cast<const float*>(t.m) + e, have, m);
-    load8(static_cast<const float*>(t.v) + e, have, v);
-  }
+  for (int i = 2; i < 8; i += 2) a = max_nan(a, fabsf(x[i])), b = max_nan(b, fabsf(x[i + 1]));
+  return __float_as_uint(max_nan(a, b));
+}
+
+// The codes of 8 values scaled to e4m3's range, by the low or the high halves of the elements' words. `keep` (sqrt(v)): values that
+// are positive in v keep a code (a magnitude of at least 2^-6 has one anyway).
+template <bool FULL, bool HIGH>
+__device__ __forceinline__ void codes_of(const float (&y)[8], const uint32_t (&w)[2][4], bool keep, const float (&v)[8],
+                                         uint32_t (&code)[2]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) p[i] = update(h, wl, g[i], m[i], v[i], r[i], p[i]);
-  store8(t.p + e, have, p);
-  if (t.p16) store_bf16(t.p16 + e, have, p);
-  if constexpr (E4M3) {
-    uint32_t tm = 0, tr = 0;
+  for (int q = 0; q < 2; ++q) {
+    float z[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {  // elements past the end are zero but for a NaN weight_decay, which the host refuses
-      tm = max(tm, __float_as_uint(m[i]) & 0x7FFFFFFFu);
-      tr = max(tr, __float_as_uint(r[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 4; ++i) {
+      z[i] = round_at_random<FULL>(y[4 * q + i], HIGH ? w[q][i] >> 16 : w[q][i] & 0xFFFFu);
+      if (FULL && keep && v[4 * q + i] > 0.0f) z[i] = fmaxf(z[i], 0x1p-9f);
     }
-    const Scale sm = block_scale(warp_max(tm)), sr = block_scale(warp_max(tr));
-    uint32_t cm[2], cr[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t w[4];
-      random_words(w, uint64_t(e) / 4 + q, uint32_t(id), h.step, a.seed_lo, a.seed_hi);
-      float ym[4], yr[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        ym[i] = copysignf(round_at_random(m[4 * q + i], sm.inv, w[i] & 0xFFFFu), m[4 * q + i]);
-        yr[i] = round_at_random(r[4 * q + i], sr.inv, w[i] >> 16);
-        if (v[4 * q + i] > 0.0f && sr.scale > 0.0f) yr[i] = fmaxf(yr[i], 0x1p-9f);
-      }
-      cm[q] = kv::e4m3x2(ym[0], ym[1]) | (kv::e4m3x2(ym[2], ym[3]) << 16);
-      cr[q] = kv::e4m3x2(yr[0], yr[1]) | (kv::e4m3x2(yr[2], yr[3]) << 16);
-    }
-    store_codes(static_cast<uint8_t*>(t.m) + e, have, cm[0], cm[1]);
-    store_codes(static_cast<uint8_t*>(t.v) + e, have, cr[0], cr[1]);
-    if (lane == 0) *reinterpret_cast<float2*>(t.scales + 2 * block) = make_float2(sm.scale, sr.scale);
-  } else {
-    store8(static_cast<float*>(t.m) + e, have, m);
-    store8(static_cast<float*>(t.v) + e, have, v);
+    code[q] = kv::e4m3x2(z[0], z[1]) | (kv::e4m3x2(z[2], z[3]) << 16);
   }
 }
 
-__global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ Table a) {
+// A warp takes a block of 256 elements, eight consecutive ones a lane: the block's scales need no shared memory.
+template <bool ALL, bool BF16, bool E4M3>
+__device__ __forceinline__ void warp_block(const Table& a, const Hyper& h, const mot_adamw_tensor& t, float wl, int id,
+                                           int64_t block, int lane) {
+  const int64_t e = block * BLOCK + lane * 8;
+  int have = 8;
+  if constexpr (!ALL) {
+    const int64_t left = t.n - e;
+    have = left >= 8 ? 8 : left > 0 ? int(left) : 0;
+  }
+  float g[8], m[8], v[8], r[8], p[8];
+  load_grad<ALL, BF16>(t.g, e, have, g);
+  load8<ALL>(t.p + e, have, p);
+  if constexpr (E4M3) {
+    const float2 s = *reinterpret_cast<const float2*>(t.scales + 2 * block);
+    load_codes<ALL>(static_cast<const uint8_t*>(t.m) + e, have, s.x, m);
+    load_codes<ALL>(static_cast<const uint8_t*>(t.v) + e, have, s.y, v);
+    mul8(v, v, v);
+  } else {
+    load8<ALL>(static_cast<const float*>(t.m) + e, have, m);
+    load8<ALL>(static_cast<const float*>(t.v) + e, have, v);
+  }
+  update(h, wl, g, m, v, r, p);
+  store8<ALL>(t.p + e, have, p);
+  if (t.p16) store_bf16<ALL>(t.p16 + e, have, p);
+  if constexpr (E4M3) {
+    uint32_t w[2][4], cm[2], cr[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) random_words(w[q], uint64_t(e) / 4 + q, uint32_t(id), h.step, a.key);
+    // elements past the end are zero
+    const Scale sm = block_scale(warp_max(top_of(m))), sr = block_scale(warp_max(top_of(r)));
+    mul8(m, sm.inv, m);
+    mul8(r, sr.inv, r);
+    float least = fminf(fabsf(m[0]), r[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) least = fminf(least, fminf(fabsf(m[i]), r[i]));
+    if (__all_sync(0xffffffffu, least >= 0x1p-6f)) {  // few blocks reach 2^-15 below their largest value
+      codes_of<false, false>(m, w, false, v, cm);
+      codes_of<false, true>(r, w, false, v, cr);
+    } else {
+      codes_of<true, false>(m, w, false, v, cm);
+      codes_of<true, true>(r, w, sr.scale > 0.0f, v, cr);
+      if (!(sm.scale < INFINITY)) cm[0] = cm[1] = 0u;  // NaN: inv is zero, so `least` is zero or a NaN
+      if (!(sr.scale < INFINITY)) cr[0] = cr[1] = 0u;
+    }
+    store_codes<ALL>(static_cast<uint8_t*>(t.m) + e, have, cm[0], cm[1]);
+    store_codes<ALL>(static_cast<uint8_t*>(t.v) + e, have, cr[0], cr[1]);
+    if (lane == 0) *reinterpret_cast<float2*>(t.scales + 2 * block) = make_float2(sm.scale, sr.scale);
+  } else {
+    store8<ALL>(static_cast<float*>(t.m) + e, have, m);
+    store8<ALL>(static_cast<float*>(t.v) + e, have, v);
+  }
+}
+
+template <bool BF16, bool E4M3>
+__device__ __forceinline__ void warp_blocks(const Table& a, const Hyper& h, const mot_adamw_tensor& t, int id, int64_t block,
+                                            int lane) {
+  const float wl = __fmul_rn(h.lr, t.weight_decay);
+#pragma unroll 1
+  for (int i = 0; i < a.blocks; ++i, block += WARPS) {
+    if ((block + 1) * BLOCK <= t.n) {
+      warp_block<true, BF16, E4M3>(a, h, t, wl, id, block, lane);
+    } else {
+      if (block * BLOCK < t.n) warp_block<false, BF16, E4M3>(a, h, t, wl, id, block, lane);
+      break;
+    }
+  }
+}
+
+// E4M3 false: no tensor has 8-bit states, whose registers would leave the others with fewer warps.
+template <bool E4M3>
+__global__ void __launch_bounds__(THREADS, E4M3 ? 3 : 4) adamw_kernel(const __grid_constant__ Table a) {
   Hyper h;
   if (!load_hyper(a.hyper, h)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, MOT_DEV_BAD_HYPER);
     return;
   }
-  int lo = 0, hi = a.n;  // the tensor of this chunk
+  int lo = 0, hi = a.n;  // the tensor of this CTA
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (a.first[mid] <= blockIdx.x) lo = mid;
     else hi = mid;
   }
   const mot_adamw_tensor& t = a.t[lo];
-  const int64_t block = int64_t(blockIdx.x - a.first[lo]) * (CHUNK / BLOCK) + (threadIdx.x >> 5);
-  if (block * BLOCK >= t.n) return;
+  const int64_t block = int64_t(blockIdx.x - a.first[lo]) * (WARPS * a.blocks) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31, id = a.base + lo;
-  switch (t.flags) {
-    case 0: warp_block<false, false>(a, h, t, id, block, lane); break;
-    case MOT_ADAMW_GRAD_BF16: warp_block<true, false>(a, h, t, id, block, lane); break;
-    case MOT_ADAMW_STATE_E4M3: warp_block<false, true>(a, h, t, id, block, lane); break;
-    default: warp_block<true, true>(a, h, t, id, block, lane); break;
+  const bool bf16 = (t.flags & MOT_ADAMW_GRAD_BF16) != 0;
+  if (E4M3 && (t.flags & MOT_ADAMW_STATE_E4M3) != 0) {
+    if (bf16) warp_blocks<true, E4M3>(a, h, t, id, block, lane);
+    else warp_blocks<false, E4M3>(a, h, t, id, block, lane);
+  } else {
+    if (bf16) warp_blocks<true, false>(a, h, t, id, block, lane);
+    else warp_blocks<false, false>(a, h, t, id, block, lane);
   }
 }
 
 inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// check_ptr for many pointers that lie in few allocations: an allocation that a pointer was found in vouches for the next ones.
+// (560 pointers of 112 tensors, one by one, took 45 us of the host's time.)
+class Allocations {
+ public:
+  explicit Allocations(int dev) : dev_(dev) {}
+  int check(const void* p) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    for (int i = 0; i < n_; ++i)
+      if (at - from_[i] < size_[i]) return MOT_OK;
+    const int st = check_ptr(p, dev_);
+    if (st != MOT_OK) return st;
+    static std::atomic<void*> fn{nullptr};
+    auto range = driver_fn<CUresult (*)(CUdeviceptr*, size_t*, CUdeviceptr)>("cuMemGetAddressRange", 3020, fn);
+    CUdeviceptr from = 0;
+    size_t size = 0;
+    if (range != nullptr && range(&from, &size, CUdeviceptr(at)) == CUDA_SUCCESS) {
+      const int i = n_ < kMax ? n_++ : next_++ % kMax;
+      from_[i] = uintptr_t(from);
+      size_[i] = size;
+    }
+    return MOT_OK;
+  }
+
+ private:
+  static constexpr int kMax = 8;
+  int dev_, n_ = 0, next_ = 0;
+  uintptr_t from_[kMax];
+  size_t size_[kMax];
+};
 
 }  // namespace adamw
 }  // namespace mot
@@ -330,31 +430,41 @@ extern "C" int mot_adamw_step(const mot_adamw_tensor* tensors, int n_tensors, co
   int dev = -1;
   int st = check_device(s, ptrs, 2, &dev);
   if (st != MOT_OK) return st;
+  DeviceGuard guard(dev);
+  adamw::Allocations known(dev);
+  int64_t all = 0;  // blocks
+  bool e4m3 = false;
   for (int i = 0; i < n_tensors; ++i) {
     const mot_adamw_tensor& t = tensors[i];
     const void* mine[] = {t.p, t.p16, t.g, t.m, t.v, (t.flags & MOT_ADAMW_STATE_E4M3) ? t.scales : nullptr};
     for (const void* p : mine)
-      if (p != nullptr && (st = check_ptr(p, dev)) != MOT_OK) return st;
+      if (p != nullptr && (st = known.check(p)) != MOT_OK) return st;
+    all += (t.n + adamw::BLOCK - 1) / adamw::BLOCK;
+    e4m3 |= (t.flags & MOT_ADAMW_STATE_E4M3) != 0;
   }
-  DeviceGuard guard(dev);
   adamw::Table a;
   a.hyper = hyper;
-  a.seed_lo = uint32_t(seed);
-  a.seed_hi = uint32_t(seed >> 32);
+  uint32_t k0 = uint32_t(seed), k1 = uint32_t(seed >> 32);
+  for (int i = 0; i < adamw::ROUNDS; ++i, k0 += 0x9E3779B9u, k1 += 0xBB67AE85u) a.key[2 * i] = k0, a.key[2 * i + 1] = k1;
+  // 8-bit states are bound by instructions, and a warp's setting up (the step's numbers, its tensor) costs about an eighth of a
+  // block: several blocks a warp once every SM has eight CTAs without. (fp32 states, bound by memory, lose by it: 1019 us for 987.)
+  a.blocks = e4m3 && all >= int64_t(sm_count(dev)) * 8 * adamw::WARPS * 4 ? 4 : 1;
+  const int64_t per = int64_t(a.blocks) * adamw::WARPS * adamw::BLOCK;
   a.err = &static_cast<PlanHeader*>(ws)->error;
   for (int i = 0; i < n_tensors;) {
     a.n = 0;
     a.base = i;
-    int64_t chunks = 0;
+    int64_t ctas = 0;
     for (; i < n_tensors && a.n < adamw::kMaxTensors; ++i) {
-      const int64_t mine = (tensors[i].n + adamw::CHUNK - 1) / adamw::CHUNK;
-      if (chunks + mine > (int64_t(1) << 31) - 1) break;  // one tensor has at most 2^29
+      const int64_t mine = (tensors[i].n + per - 1) / per;
+      if (ctas + mine > (int64_t(1) << 31) - 1) break;  // one tensor has at most 2^29
       a.t[a.n] = tensors[i];
-      a.first[a.n++] = uint32_t(chunks);
-      chunks += mine;
+      a.first[a.n++] = uint32_t(ctas);
+      ctas += mine;
     }
-    a.first[a.n] = uint32_t(chunks);
-    adamw::adamw_kernel<<<unsigned(chunks), adamw::THREADS, 0, s>>>(a);
+    a.first[a.n] = uint32_t(ctas);
+    if (e4m3) adamw::adamw_kernel<true><<<unsigned(ctas), adamw::THREADS, 0, s>>>(a);
+    else adamw::adamw_kernel<false><<<unsigned(ctas), adamw::THREADS, 0, s>>>(a);
     if (cudaGetLastError() != cudaSuccess) return MOT_ERR_CUDA;
   }
   return MOT_OK;

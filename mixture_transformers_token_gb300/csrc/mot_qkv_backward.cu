@@ -12,15 +12,15 @@
 //
 // A row is read and written once: 2 N + (Hq + Hkv) D values of bf16, its position and its table entries (16.5 us for 4096 rows
 // of 28/4 heads of 128 at the measured copy rate): the bound is memory. D / 16 lanes hold a head, each 8 values and their 8
-// partners, so that the rotation needs no exchange and a warp has four 16-byte loads a lane in flight.
+// partners, so that the rotation needs no exchange. Loads into registers kept too little under way for the memory's latency (two
+// CTAs of 8 warps, the next heads' loads ahead: 36 us on that pack): each of 16 warps has a ring of three slots in shared memory
+// for a row's next heads, their projection and the table entries, filled by bulk copies, 150 KB an SM.
 //
 // The weights' gradients: each CTA takes a run of the plan's positions, so that its rows are of one weight set, but for the run
-// that holds the border; a lane adds its columns over the warp's rows, the warps' sums are added in order, and a second kernel
-// adds the CTAs' sums in order.
+// that holds the border; a lane adds its columns over the warp's rows, the warps' sums are added in order, and a second kernel,
+// already launched, adds the CTAs' sums in order.
 
 #include <cuda_runtime.h>
-
-#include <type_traits>
 
 #include "mot.h"
 #include "mot_device.cuh"
@@ -29,13 +29,20 @@
 namespace mot {
 namespace qkvb {
 
-constexpr int WARPS = 8, THREADS = 32 * WARPS;
-constexpr int kMaxCtas = 608;  // runs of positions: four for each of 152 SMs
+constexpr int WARPS = 16, THREADS = 32 * WARPS;
+constexpr int kMaxCtas = 152;           // runs of positions: one for each SM
+constexpr int PIECE = 1024;             // values of a slot: the heads of an item
+constexpr int SLOTS = 3;
+constexpr uint32_t SLOT = 2 * PIECE * 2 + 512 + 16;  // gradient, projection, table entries of a position, the row
+constexpr uint32_t RING = WARPS * SLOTS * SLOT;
+constexpr uint32_t WEIGHTS = RING, BARS = WEIGHTS + 4 * 128 * 4;
+constexpr size_t SMEM = BARS + 8 * WARPS * SLOTS + 16;
 
 struct Args {
   const uint16_t* d;
   const uint16_t* x;
-  const uint16_t* w[2];  // q's and k's, [2][D]
+  const uint16_t* qw;    // [2][D]
+  const uint16_t* kw;
   const int32_t* pos;
   const void* cs;
   int P, T, Hq, Hkv;
@@ -64,14 +71,14 @@ __device__ __forceinline__ void load_table(const void* cs, int64_t pair, float (
     const float4* t = reinterpret_cast<const float4*>(static_cast<const float*>(cs) + 2 * pair);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 v = __ldg(t + i);
+      const float4 v = t[i];
       c[2 * i] = v.x, s[2 * i] = v.y, c[2 * i + 1] = v.z, s[2 * i + 1] = v.w;
     }
   } else {
     const uint4* t = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(cs) + 2 * pair);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint4 v = __ldg(t + i);
+      const uint4 v = t[i];
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) c[4 * i + k] = bf_lo(w[k]), s[4 * i + k] = bf_hi(w[k]);
@@ -87,84 +94,177 @@ __device__ __forceinline__ float group_sum(float x) {
 }
 
 template <int D, bool F32>
-__global__ void __launch_bounds__(THREADS) qk_norm_rope_bwd_kernel(const Args a) {
+__global__ void __launch_bounds__(THREADS, 1) qk_norm_rope_bwd_kernel(const Args a) {
   constexpr int LANES = D / 16, HEADS = 32 / LANES, H2 = D / 2;  // lanes of a head, heads of a warp
-  __shared__ float sums[WARPS][2][D];
+  constexpr int ITEM = PIECE / D;                                // heads of an item
+  constexpr uint32_t TABLE = D * (F32 ? 4 : 2);                  // bytes of a position's table entries
+  extern __shared__ __align__(128) uint8_t smem[];
+  pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES, grp = lane / LANES;
+  uint8_t* ring = smem + warp * SLOTS * SLOT;
+  float* weights = reinterpret_cast<float*>(smem + WEIGHTS);  // [q, k][2][D]
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + BARS) + warp * SLOTS;
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + BARS + 8 * WARPS * SLOTS);
   const PlanHeader* hdr = reinterpret_cast<const PlanHeader*>(a.ws);
   if (hdr->magic != kPlanMagic || hdr->T != a.T) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, MOT_DEV_PLAN_MISMATCH);
     return;
   }
-  if (hdr->count[0] + hdr->count[1] != a.T) return;  // no plan (bad modality): nothing is defined
+  const int count0 = hdr->count[0];
+  if (count0 + hdr->count[1] != a.T) return;  // no plan (bad modality): nothing is defined
+  if (lane == 0) {
+    for (int i = 0; i < SLOTS; ++i) mbar_init(smem_u32(&full[i]), 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (threadIdx.x == 0) *abort_flag = 0u;
+  if (threadIdx.x < 4 * D) weights[threadIdx.x] = bf_to_f((threadIdx.x < 2 * D ? a.qw : a.kw)[threadIdx.x % (2 * D)]);
+  __syncthreads();
   const int32_t* perm = reinterpret_cast<const int32_t*>(a.ws + perm_offset());
-  const int nqk = a.Hq + a.Hkv, N = (nqk + a.Hkv) * D;
+  const int nqk = a.Hq + a.Hkv, n_heads = nqk + a.Hkv;
+  // items of a row: the normed heads, and, where the result is elsewhere, the value heads to copy
+  const int normed = (nqk + ITEM - 1) / ITEM, items = normed + (a.dx != a.d ? (a.Hkv + ITEM - 1) / ITEM : 0);
   const int begin = int(int64_t(a.T) * blockIdx.x / a.ctas), end = int(int64_t(a.T) * (blockIdx.x + 1) / a.ctas);
-  const bool copy_v = a.dx != a.d;
+  int issued = 0, taken = 0;  // of all this warp's items
+  bool ok = true;
   for (int e = 0; e < 2; ++e) {
-    const int lo = e == 0 ? begin : max(begin, hdr->count[0]), hi = e == 0 ? min(end, hdr->count[0]) : end;
+    const int lo = e == 0 ? begin : max(begin, count0), hi = e == 0 ? min(end, count0) : end;
     float acc[2][2][8] = {};  // [q, k][half][column]
-    for (int at = lo + warp; at < hi; at += WARPS) {
-      const int64_t row = perm[at];
-      int pos = a.pos[row];
-      if (pos < 0 || pos >= a.P) {
-        if (lane == 0) atomicOr(a.err, MOT_DEV_BAD_POSITION);
-        pos = 0;
+    const int all = hi > lo ? (hi - lo) * items : 0;                 // less than 2^26
+    const int n = all > warp ? (all - warp + WARPS - 1) / WARPS : 0;  // this warp's items: warp, warp + WARPS, ...
+    int my_row = 0, my_pos = 0;                                      // of its items that a lane looks up, 32 at once
+    int next_item = warp % items, this_item = next_item;             // of the row: the next one to issue, and to take
+    auto issue = [&](int j) {
+      if ((j & 31) == 0 && j + lane < n) {
+        my_row = perm[lo + (warp + (j + lane) * WARPS) / items];
+        my_pos = a.pos[my_row];
+        if (my_pos < 0 || my_pos >= a.P) {
+          atomicOr(a.err, MOT_DEV_BAD_POSITION);
+          my_pos = 0;
+        }
       }
-      float c[8], s[8];
-      load_table<F32>(a.cs, int64_t(pos) * H2 + 8 * sub, c, s);
-      for (int h0 = 0; h0 < nqk; h0 += HEADS) {
-        const int h = h0 + grp;
-        const bool has = h < nqk;
-        const int kind = h < a.Hq ? 0 : 1;
-        const int64_t off = row * N + int64_t(has ? h : 0) * D + 8 * sub;
+      const int row = __shfl_sync(0xffffffffu, my_row, j & 31), pos = __shfl_sync(0xffffffffu, my_pos, j & 31);
+      if (lane == 0) {
+        const int item = next_item, s = issued % SLOTS;
+        const int h = item < normed ? item * ITEM : nqk + (item - normed) * ITEM, to = item < normed ? nqk : n_heads;
+        const uint32_t bytes = uint32_t(to - h < ITEM ? to - h : ITEM) * D * 2, bar = smem_u32(&full[s]);
+        uint8_t* slot = ring + s * SLOT;
+        const int64_t off = (int64_t(row) * n_heads + h) * D;
+        *reinterpret_cast<int*>(slot + 4 * PIECE + 512) = row;
+        mbar_arrive_expect_tx(bar, item < normed ? 2 * bytes + TABLE : bytes);
+        bulk_load(smem_u32(slot), a.d + off, bytes, bar);
+        if (item < normed) {
+          bulk_load(smem_u32(slot + 2 * PIECE), a.x + off, bytes, bar);
+          bulk_load(smem_u32(slot + 4 * PIECE), static_cast<const uint8_t*>(a.cs) + int64_t(pos) * TABLE, TABLE, bar);
+        }
+      }
+      ++issued;
+      next_item = (next_item + WARPS) % items;
+    };
+    for (int j = 0; j < n && j < SLOTS - 1; ++j) issue(j);
+    for (int j = 0; j < n; ++j, ++taken) {
+      __syncwarp();  // every lane has read the slot that is filled next
+      if (j + SLOTS - 1 < n) issue(j + SLOTS - 1);
+      const int s = taken % SLOTS;
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), uint32_t(taken / SLOTS) & 1u, abort_flag, a.err));
+      if (!ok) break;
+      const uint8_t* slot = ring + s * SLOT;
+      const int item = this_item;
+      this_item = (this_item + WARPS) % items;
+      const int64_t row = *reinterpret_cast<const int*>(slot + 4 * PIECE + 512);
+      if (item >= normed) {
+        const int h = (item - normed) * ITEM, pieces = min(a.Hkv - h, ITEM) * D / 8;
+        uint4* to = reinterpret_cast<uint4*>(a.dx + (row * n_heads + nqk + h) * D);
+        for (int i = lane; i < pieces; i += 32) to[i] = reinterpret_cast<const uint4*>(slot)[i];
+        continue;
+      }
+      float c[8], sn[8];
+      load_table<F32>(slot + 4 * PIECE, 8 * sub, c, sn);
+#pragma unroll 1
+      for (int h0 = item * ITEM; h0 < min((item + 1) * ITEM, nqk); h0 += HEADS) {
+        const int h = h0 + grp, at = (h - item * ITEM) * D + 8 * sub;  // a head past the last reads what was in the slot
+        const bool has = h < nqk, key = h >= a.Hq;
         float d0[8], d1[8], x0[8], x1[8], w0[8], w1[8];
-        unpack8(*reinterpret_cast<const uint4*>(a.d + off), d0);
-        unpack8(*reinterpret_cast<const uint4*>(a.d + off + H2), d1);
-        unpack8(__ldg(reinterpret_cast<const uint4*>(a.x + off)), x0);
-        unpack8(__ldg(reinterpret_cast<const uint4*>(a.x + off + H2)), x1);
-        const uint16_t* w = a.w[kind] + e * D + 8 * sub;
-        unpack8(__ldg(reinterpret_cast<const uint4*>(w)), w0);
-        unpack8(__ldg(reinterpret_cast<const uint4*>(w + H2)), w1);
-        float ss = 0.0f;
+        const uint16_t* ds = reinterpret_cast<const uint16_t*>(slot) + at;
+        unpack8(*reinterpret_cast<const uint4*>(ds), d0);
+        unpack8(*reinterpret_cast<const uint4*>(ds + H2), d1);
+        unpack8(*reinterpret_cast<const uint4*>(ds + PIECE), x0);
+        unpack8(*reinterpret_cast<const uint4*>(ds + PIECE + H2), x1);
+        const float* w = weights + ((key ? 2 : 0) + e) * D + 8 * sub;
+        *reinterpret_cast<float4*>(w0) = *reinterpret_cast<const float4*>(w);
+        *reinterpret_cast<float4*>(w0 + 4) = *reinterpret_cast<const float4*>(w + 4);
+        *reinterpret_cast<float4*>(w1) = *reinterpret_cast<const float4*>(w + H2);
+        *reinterpret_cast<float4*>(w1 + 4) = *reinterpret_cast<const float4*>(w + H2 + 4);
+        float ss = 0.0f, p0[8], p1[8];
+        mul8(x0, x0, p0);
+        mul8(x1, x1, p1);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = __fadd_rn(ss, __fadd_rn(__fmul_rn(x0[i], x0[i]), __fmul_rn(x1[i], x1[i])));
-        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(group_sum<LANES>(ss), float(D)), a.eps)));
-        float dot = 0.0f;
+        for (int k = 0; k < 8; ++k) ss = __fadd_rn(ss, __fadd_rn(p0[k], p1[k]));
+        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fmul_rn(group_sum<LANES>(ss), 1.0f / D), a.eps)));
+        float u0[8], u1[8], dot = 0.0f;
+        mul8(d0, c, u0);
+        mul8(d1, sn, p0);
+        mul8(d1, c, u1);
+        mul8(d0, sn, p1);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float u0 = __fadd_rn(__fmul_rn(d0[i], c[i]), __fmul_rn(d1[i], s[i]));
-          const float u1 = __fsub_rn(__fmul_rn(d1[i], c[i]), __fmul_rn(d0[i], s[i]));
-          x0[i] = __fmul_rn(x0[i], rstd);
-          x1[i] = __fmul_rn(x1[i], rstd);
-          // a head past the last adds zero; both kinds are added to, so that the sums stay in registers
-          const float p0 = has ? __fmul_rn(u0, x0[i]) : 0.0f, p1 = has ? __fmul_rn(u1, x1[i]) : 0.0f;
-          acc[0][0][i] = __fadd_rn(acc[0][0][i], kind == 0 ? p0 : 0.0f);
-          acc[0][1][i] = __fadd_rn(acc[0][1][i], kind == 0 ? p1 : 0.0f);
-          acc[1][0][i] = __fadd_rn(acc[1][0][i], kind == 1 ? p0 : 0.0f);
-          acc[1][1][i] = __fadd_rn(acc[1][1][i], kind == 1 ? p1 : 0.0f);
-          d0[i] = __fmul_rn(u0, w0[i]);
-          d1[i] = __fmul_rn(u1, w1[i]);
-          dot = __fadd_rn(dot, __fadd_rn(__fmul_rn(d0[i], x0[i]), __fmul_rn(d1[i], x1[i])));
+        for (int k = 0; k < 8; ++k) {
+          u0[k] = __fadd_rn(u0[k], p0[k]);
+          u1[k] = __fsub_rn(u1[k], p1[k]);
         }
-        const float mean = __fdiv_rn(group_sum<LANES>(dot), float(D));
+        mul8(x0, rstd, x0);
+        mul8(x1, rstd, x1);
+        mul8(u0, x0, p0);
+        mul8(u1, x1, p1);
+        if (!__all_sync(0xffffffffu, has)) {  // heads past the last add zero
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          d0[i] = __fmul_rn(rstd, __fsub_rn(d0[i], __fmul_rn(x0[i], mean)));
-          d1[i] = __fmul_rn(rstd, __fsub_rn(d1[i], __fmul_rn(x1[i], mean)));
+          for (int k = 0; k < 8; ++k) {
+            p0[k] = has ? p0[k] : 0.0f;
+            p1[k] = has ? p1[k] : 0.0f;
+          }
         }
+        // q's heads, k's, or some of both
+        if (__all_sync(0xffffffffu, !key)) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            acc[0][0][k] = __fadd_rn(acc[0][0][k], p0[k]);
+            acc[0][1][k] = __fadd_rn(acc[0][1][k], p1[k]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            acc[0][0][k] = __fadd_rn(acc[0][0][k], key ? 0.0f : p0[k]);
+            acc[0][1][k] = __fadd_rn(acc[0][1][k], key ? 0.0f : p1[k]);
+            acc[1][0][k] = __fadd_rn(acc[1][0][k], key ? p0[k] : 0.0f);
+            acc[1][1][k] = __fadd_rn(acc[1][1][k], key ? p1[k] : 0.0f);
+          }
+        }
+        mul8(u0, w0, u0);
+        mul8(u1, w1, u1);
+        mul8(u0, x0, p0);
+        mul8(u1, x1, p1);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dot = __fadd_rn(dot, __fadd_rn(p0[k], p1[k]));
+        const float mean = __fmul_rn(group_sum<LANES>(dot), 1.0f / D);  // D is a power of two
+        mul8(x0, mean, x0);
+        mul8(x1, mean, x1);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          d0[k] = __fsub_rn(u0[k], x0[k]);
+          d1[k] = __fsub_rn(u1[k], x1[k]);
+        }
+        mul8(d0, rstd, d0);
+        mul8(d1, rstd, d1);
         if (has) {
-          *reinterpret_cast<uint4*>(a.dx + off) = pack8(d0);
-          *reinterpret_cast<uint4*>(a.dx + off + H2) = pack8(d1);
+          uint16_t* to = a.dx + (row * n_heads + h) * D + 8 * sub;
+          *reinterpret_cast<uint4*>(to) = pack8(d0);
+          *reinterpret_cast<uint4*>(to + H2) = pack8(d1);
         }
       }
-      if (copy_v)
-        for (int i = lane; i < a.Hkv * D / 8; i += 32)
-          *reinterpret_cast<uint4*>(a.dx + row * N + nqk * D + 8 * i) =
-              *reinterpret_cast<const uint4*>(a.d + row * N + nqk * D + 8 * i);
     }
     if (a.part == nullptr || ((a.sets >> e) & 1) == 0) continue;
-    // the warp's heads, then the warps, in order
+    // the warp's heads, then the warps, in order; through the rings, whose copies have all been taken
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(smem);  // [WARPS][2][D]
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind)
 #pragma unroll
@@ -174,35 +274,44 @@ __global__ void __launch_bounds__(THREADS) qk_norm_rope_bwd_kernel(const Args a)
           float v = acc[kind][half][i];
 #pragma unroll
           for (int off = LANES; off < 32; off <<= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));
-          if (grp == 0) sums[warp][kind][half * H2 + 8 * sub + i] = v;
+          if (grp == 0 && ok) sums[(warp * 2 + kind) * D + half * H2 + 8 * sub + i] = v;
         }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * D; i += THREADS) {
-      float v = sums[0][i / D][i % D];
-      for (int k = 1; k < WARPS; ++k) v = __fadd_rn(v, sums[k][i / D][i % D]);
+      float v = sums[i];
+#pragma unroll
+      for (int k = 1; k < WARPS; ++k) v = __fadd_rn(v, sums[k * 2 * D + i]);
       a.part[((int64_t(blockIdx.x) * 2 + i / D) * 2 + e) * D + i % D] = v;
     }
+    fence_proxy_async_smem();  // before the next set's copies land here
     __syncthreads();
   }
+  // after a timeout: no copy may still land when the CTA exits
+  if (!ok && lane == 0)
+    for (int j = taken; j < issued; ++j) mbar_drain(smem_u32(&full[j % SLOTS]), uint32_t(j / SLOTS) & 1u);
 }
 
-// Adds the CTAs' sums: a CTA takes 32 columns of one kind and set, warp k the runs k, k + 8, ...
+// Adds the CTAs' sums: a CTA takes 32 columns of one kind and set, warp k the runs k, k + 8, ..., eight reads at once.
+constexpr int FOLD_WARPS = 8, FOLD_THREADS = 32 * FOLD_WARPS;
+
 template <int D>
-__global__ void __launch_bounds__(THREADS) qk_dweight_fold_kernel(const Args a) {
-  __shared__ float sums[WARPS][32];
+__global__ void __launch_bounds__(FOLD_THREADS) qk_dweight_fold_kernel(const Args a) {
+  __shared__ float sums[FOLD_WARPS][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = int(blockIdx.x) / (D / 32), col = int(blockIdx.x) % (D / 32) * 32 + lane;  // kind * 2 + set
+  pdl_wait();  // also where nothing is written: this grid ends after the one before it
   if (((a.sets >> (group & 1)) & 1) == 0) return;
   const PlanHeader* hdr = reinterpret_cast<const PlanHeader*>(a.ws);
   if (hdr->magic != kPlanMagic || hdr->T != a.T || hdr->count[0] + hdr->count[1] != a.T) return;
   float v = 0.0f;
-  for (int i = warp; i < a.ctas; i += WARPS) v = __fadd_rn(v, a.part[(int64_t(i) * 4 + group) * D + col]);
+#pragma unroll 8
+  for (int i = warp; i < a.ctas; i += FOLD_WARPS) v = __fadd_rn(v, __ldcg(a.part + (int64_t(i) * 4 + group) * D + col));
   sums[warp][lane] = v;
   __syncthreads();
   if (warp == 0) {
     v = sums[0][lane];
 #pragma unroll
-    for (int k = 1; k < WARPS; ++k) v = __fadd_rn(v, sums[k][lane]);
+    for (int k = 1; k < FOLD_WARPS; ++k) v = __fadd_rn(v, sums[k][lane]);
     a.dw[group * D + col] = v;
   }
 }
@@ -231,8 +340,8 @@ static int run(const uint16_t* d, const uint16_t* x, const uint16_t* qw, const u
   Args a{};
   a.d = d;
   a.x = x;
-  a.w[0] = qw;
-  a.w[1] = kw;
+  a.qw = qw;
+  a.kw = kw;
   a.pos = pos;
   a.cs = cs;
   a.P = P;
@@ -247,13 +356,20 @@ static int run(const uint16_t* d, const uint16_t* x, const uint16_t* qw, const u
   a.dw = dw;
   a.sets = sets;
   a.ctas = ctas_of(T);
-  if (D == 64) qk_norm_rope_bwd_kernel<64, F32><<<a.ctas, THREADS, 0, s>>>(a);
-  else qk_norm_rope_bwd_kernel<128, F32><<<a.ctas, THREADS, 0, s>>>(a);
+  static_assert(SMEM <= 227 * 1024 && WARPS * 2 * 128 * 4 <= RING, "shared memory");
+  if (cudaFuncSetAttribute(D == 64 ? qk_norm_rope_bwd_kernel<64, F32> : qk_norm_rope_bwd_kernel<128, F32>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM)) != cudaSuccess)
+    return MOT_ERR_CUDA;
+  if (D == 64) qk_norm_rope_bwd_kernel<64, F32><<<a.ctas, THREADS, SMEM, s>>>(a);
+  else qk_norm_rope_bwd_kernel<128, F32><<<a.ctas, THREADS, SMEM, s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return MOT_ERR_CUDA;
   if (dw) {
-    if (D == 64) qk_dweight_fold_kernel<64><<<4 * 64 / 32, THREADS, 0, s>>>(a);
-    else qk_dweight_fold_kernel<128><<<4 * 128 / 32, THREADS, 0, s>>>(a);
+    const cudaError_t fold =
+        D == 64 ? launch_dependent(qk_dweight_fold_kernel<64>, dim3(4 * 64 / 32), dim3(FOLD_THREADS), 0, s, a)
+                : launch_dependent(qk_dweight_fold_kernel<128>, dim3(4 * 128 / 32), dim3(FOLD_THREADS), 0, s, a);
+    if (fold != cudaSuccess) return MOT_ERR_CUDA;
   }
-  return cudaGetLastError() == cudaSuccess ? MOT_OK : MOT_ERR_CUDA;
+  return MOT_OK;
 }
 
 }  // namespace qkvb
