@@ -62,7 +62,7 @@ struct Work {
   int4* tiles;    // (first row, rows, first and last sequence that may see them), ascending
   Item* items;    // of dQ's CTAs
   int32_t* ended; // [tile][Hkv] shares whose sums are there
-  int32_t* counts;  // tiles, items
+  int32_t* counts;  // tiles, items, the next piece of work to be drawn
   // scratch: changes of the number of sequences that see a row, at each row; borders, a bit a row; the borders in order
   int32_t* change;
   uint32_t* border;
@@ -74,7 +74,6 @@ struct Args {
   const int32_t* seqs;  // [n_seq][5]
   int n_seq, T, Hq, Hkv;
   int shares;           // CTAs of a tile and KV head, a power of two
-  unsigned kv_ctas;     // of grad_kernel's CTAs, the first ones
   Work work;
   float* sums;          // [tile][Hkv][shares][dV, dK][D / 4][128 rows][4]
   float c, scale;
@@ -206,6 +205,7 @@ __device__ void make_work_few(const StatsArgs& a, FewRoom& s) {
     for (int i = 0; i < a.n_seq; ++i) items += s.items[i];  // at most 2^6 2^17
     w.counts[0] = tiles;
     w.counts[1] = items < w.max_items ? items : w.max_items;
+    w.counts[2] = 0;
   }
 }
 
@@ -302,6 +302,7 @@ __device__ void make_work(const StatsArgs& a, int* room) {
   if (tid == 0) {
     w.counts[0] = tiles;
     w.counts[1] = items;
+    w.counts[2] = 0;
   }
 }
 
@@ -478,6 +479,27 @@ __device__ __forceinline__ void product_ta(uint32_t on, uint32_t d, uint32_t a_t
 __device__ __forceinline__ void ld_columns(uint32_t taddr, float (&v)[32]) { tmem_ld32(taddr, v); }
 __device__ __forceinline__ void ld_columns(uint32_t taddr, float (&v)[16]) { tmem_ld16(taddr, v); }
 
+// The CTA's next piece of work: a number that the copying warp draws and hands to the others, one ahead of them.
+struct Drawn {
+  int4 info[2];  // of the two rings' places: what the work is
+  int4 more[2];
+};
+
+// Warps that wait for a piece of work: those that issue products and those that compute.
+constexpr int TAKERS = 1 + COMPUTE_WARPS;
+
+// A wait by a whole warp.
+struct Waits {
+  volatile uint32_t* abort_flag;
+  uint32_t* err;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t phase) const {
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase & 1u, abort_flag, err));
+  }
+};
+
+// Both phases' barriers and what the CTA's warps share lie behind the larger layout.
+constexpr uint32_t kSharedBytes = 768;
+
 // ---------------------------------------------------------------------------
 // dK and dV
 // ---------------------------------------------------------------------------
@@ -492,9 +514,16 @@ struct KvLayout {
   static constexpr uint32_t ONES = QD + STAGES * 2 * TILE;        // [128][16]: ones in columns 0 to 2
   static constexpr uint32_t STATS = ONES + STEP;                  // STAGES of [128][16] -lse / scale and of -delta, in three
   static constexpr uint32_t EDGES = STATS + STAGES * 2 * STEP;    // STAGES of the block's edges, see the copies
-  static constexpr uint32_t BAR = EDGES + STAGES * 16;
-  static constexpr size_t BYTES = 1024 + size_t(BAR) + 512;
+  static constexpr uint32_t BYTES = EDGES + STAGES * 16;
   static constexpr uint32_t S = 0, DP = 128, DV = 256, DK = 384;  // tensor memory
+};
+
+struct KvBars {
+  uint64_t k_full, v_full, k_free, v_free;  // the tile's K and V; every product of the tile that reads them is done
+  uint64_t raw;                             // a block that is zeroed in part before it is full
+  uint64_t full[4], empty[4], edges[4];     // a block's tiles and stats; its products are done; its edges are there
+  uint64_t s_full, dp_full, p_full, ds_full, dv_done, dk_done, drain;
+  uint64_t drawn[2], taken[2];
 };
 
 // Four fp32 of a row: 32 rows of a warp are 512 consecutive bytes.
@@ -503,266 +532,274 @@ __device__ __forceinline__ float4* sums_at(float* sums, int m, int piece, int ro
   return reinterpret_cast<float4*>(sums) + (m * (D / 4) + piece) * 128 + row;
 }
 
-// The tile's dV and dK as bf16, 16 values of a row a thread: the sums of the shares, in order. All reads of a row's 16 values are
-// under way at once.
+// The thread's row of dV and dK as bf16, its quarter of the columns: the sums of the shares in order, this one's from tensor memory.
 template <int D, int SHARES>
-__device__ __forceinline__ void add_shares(float* sums, const int4& tile, int g, const Args& a) {
+__device__ __forceinline__ void add_shares(float* sums, uint32_t at, bool any, int share, int part, int row, const int4& tile,
+                                           int g, const Args& a) {
+  using L = KvLayout<D>;
   const int64_t N = int64_t(a.Hq + 2 * a.Hkv) * D;
-  for (int i = threadIdx.x; i < 2 * (D / 16) * 128; i += THREADS) {
-    const int r = i & 127, k = i / 128 % (D / 16), m = i / (128 * (D / 16));
-    if (r >= tile.y) continue;
-    float4 u[SHARES][4];
+  constexpr int Q = SHARES == 8 ? 2 : 4;  // pieces of four columns whose reads are under way at once
+#pragma unroll 1
+  for (int m = 0; m < 2; ++m)
+#pragma unroll 1
+    for (int c0 = part * (D / 4); c0 < (part + 1) * (D / 4); c0 += 16) {
+      __syncwarp();
+      float own[16] = {};
+      if (any) tmem_ld16(at + (m ? L::DK : L::DV) + c0, own);
+      if (row < tile.y) {
+        const float f = m ? a.scale : 1.0f;
+        uint32_t o[8];
 #pragma unroll
-    for (int p = 0; p < SHARES; ++p)
+        for (int q0 = 0; q0 < 4; q0 += Q) {
+          float4 u[SHARES][Q];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) u[p][q] = __ldcg(sums_at<D>(sums + p * (2 * 128 * D), m, 4 * k + q, r));
-    const float f = m ? a.scale : 1.0f;
-    uint32_t o[8];
+          for (int p = 0; p < SHARES; ++p)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float4 v = u[0][q];
+            for (int q = 0; q < Q; ++q) {
+              const int k = 4 * (q0 + q);
+              u[p][q] = p == share ? make_float4(own[k], own[k + 1], own[k + 2], own[k + 3])
+                                   : __ldcg(sums_at<D>(sums + p * (2 * 128 * D), m, c0 / 4 + q0 + q, row));
+            }
 #pragma unroll
-      for (int p = 1; p < SHARES; ++p)
-        v = make_float4(__fadd_rn(v.x, u[p][q].x), __fadd_rn(v.y, u[p][q].y), __fadd_rn(v.z, u[p][q].z), __fadd_rn(v.w, u[p][q].w));
-      o[2 * q] = cvt_bf2(__fmul_rn(v.x, f), __fmul_rn(v.y, f));
-      o[2 * q + 1] = cvt_bf2(__fmul_rn(v.z, f), __fmul_rn(v.w, f));
+          for (int q = 0; q < Q; ++q) {
+            float4 v = u[0][q];
+#pragma unroll
+            for (int p = 1; p < SHARES; ++p)
+              v = make_float4(__fadd_rn(v.x, u[p][q].x), __fadd_rn(v.y, u[p][q].y), __fadd_rn(v.z, u[p][q].z),
+                              __fadd_rn(v.w, u[p][q].w));
+            o[2 * (q0 + q)] = cvt_bf2(__fmul_rn(v.x, f), __fmul_rn(v.y, f));
+            o[2 * (q0 + q) + 1] = cvt_bf2(__fmul_rn(v.z, f), __fmul_rn(v.w, f));
+          }
+        }
+        uint4* to = reinterpret_cast<uint4*>(a.dqkv + (tile.x + row) * N + (a.Hq + (m ? 0 : a.Hkv) + g) * D + c0);
+        to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
     }
-    uint4* to = reinterpret_cast<uint4*>(a.dqkv + (tile.x + r) * N + (a.Hq + (m ? 0 : a.Hkv) + g) * D + 16 * k);
-    to[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    to[1] = make_uint4(o[4], o[5], o[6], o[7]);
-  }
+  __syncwarp();
 }
 
+// Pieces of work [0, n_work) by this and the other CTAs, until they are drawn. Returns the first drawn number past them, to the
+// copying warp.
 template <int D>
-__device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_qkv, const CUtensorMap& tm_do, const Args& a, uint8_t* smem) {
+__device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtensorMap& tm_do, const Args& a, uint8_t* smem,
+                                         KvBars& B, Drawn& drawn, volatile int* ended, uint32_t tmem, int n_work,
+                                         const Waits& wait) {
   using L = KvLayout<D>;
   constexpr int STAGES = L::STAGES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
-  uint64_t* kv_full = bars;
-  uint64_t* raw = bars + 1;         // a block that is zeroed in part before it is full
-  uint64_t* full = bars + 2;        // [STAGES]
-  uint64_t* empty = bars + 6;       // [STAGES]: every product of the block is done
-  uint64_t* stat_full = bars + 10;  // [STAGES]
-  uint64_t* s_full = bars + 14;
-  uint64_t* dp_full = bars + 15;
-  uint64_t* p_full = bars + 16;
-  uint64_t* ds_full = bars + 17;
-  uint64_t* dv_done = bars + 18;
-  uint64_t* dk_done = bars + 19;
-  uint64_t* drain = bars + 20;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
-  volatile int* last = reinterpret_cast<volatile int*>(tmem_slot + 2);
-  volatile uint32_t* abort_flag = tmem_slot + 1;
-
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int share = int(blockIdx.x) % a.shares, rest = int(blockIdx.x) / a.shares;
-  const int g = rest % a.Hkv, G = a.Hq / a.Hkv;
-  if (threadIdx.x == 0) {
-    mbar_init(smem_u32(kv_full), 1);
-    mbar_init(smem_u32(raw), 1);
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(smem_u32(&full[i]), 2);  // the tiles, and the stats
-      mbar_init(smem_u32(&empty[i]), 1);
-      mbar_init(smem_u32(&stat_full[i]), 1);
-    }
-    mbar_init(smem_u32(s_full), 1);
-    mbar_init(smem_u32(dp_full), 1);
-    mbar_init(smem_u32(p_full), COMPUTE_WARPS);
-    mbar_init(smem_u32(ds_full), COMPUTE_WARPS);
-    mbar_init(smem_u32(dv_done), 1);
-    mbar_init(smem_u32(dk_done), 1);
-    mbar_init(smem_u32(drain), 1);
-    *abort_flag = 0u;
-    fence_mbar_init();
-    fence_proxy_async_smem();
-  }
-  for (int i = threadIdx.x; i < int((2 * STAGES + 1) * L::STEP / 16); i += THREADS)  // only the stats' first values change
-    *reinterpret_cast<uint4*>(smem + L::ONES + i * 16) =
-        i < int(L::STEP / 16) && (i & 8) == 0 ? make_uint4(0x3F803F80u, 0x3F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
-  fence_proxy_async_smem();
-  pdl_wait();  // stats_kernel
-  // the count and the tile at once; what lies past the last tile is not used
-  const int n_tiles = __ldcg(a.work.counts);
-  const int4 tile = __ldcg(a.work.tiles + rest / a.Hkv);
-  if (rest / a.Hkv >= n_tiles) return;
-  const int row0 = tile.x;
-  if (threadIdx.x == 0) {
-    mbar_arrive_expect_tx(smem_u32(kv_full), 2 * L::TILE);
-    load_tile<D>(smem_u32(smem + L::K), &tm_qkv, (a.Hq + g) * D, row0, smem_u32(kv_full));
-    load_tile<D>(smem_u32(smem + L::V), &tm_qkv, (a.Hq + a.Hkv + g) * D, row0, smem_u32(kv_full));
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  int n_it = 0;  // blocks of this share
-  if (warp != 0) {
-    SeqIter it(a, tile, lane);
-    int s[5];
-    while (it.next(s)) {
-      int first, end;
-      query_blocks(s, row0, first, end);
-      n_it += blocks_of_share(share, first, end, G, a.shares);
-    }
-  }
-
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.Hq / a.Hkv;
+  int past = n_work;
   if (warp == 0) {
-    // ---------------- copies ----------------
+    // ---------------- work and copies ----------------
     bool ok = true;
-    int t = 0, raws = 0;
-    SeqIter it(a, tile, lane);
-    int s[5];
-    while (ok && it.next(s)) {
-      int first, end;
-      query_blocks(s, row0, first, end);
-      for (int hh = 0; hh < G && ok; ++hh) {
-        const int h = g * G + hh;
-        for (int b = first + ((share - first - hh) & (a.shares - 1)); b < end; b += a.shares, ++t) {
-          const int st = t % STAGES;
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[st]), (uint32_t(t / STAGES) & 1u) ^ 1u, abort_flag, a.err));
-          if (!ok) break;
-          const int y = s[0] + b * BQ, have = s[2] - b * BQ < BQ ? s[2] - b * BQ : BQ;
-          uint8_t* q = smem + L::QD + st * 2 * L::TILE;
-          const uint32_t bar = smem_u32(have == BQ ? &full[st] : raw);
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar, 2 * L::TILE);
-            load_tile<D>(smem_u32(q), &tm_qkv, h * D, y, bar);
-            load_tile<D>(smem_u32(q + L::TILE), &tm_do, h * D, y, bar);
-          }
-          uint8_t* stats = smem + L::STATS + st * 2 * L::STEP;
-          const int64_t at = int64_t(h) * a.T + y;
-          float l[4], d[4];
+    int t = 0, raws = 0, n = 0;  // blocks, blocks zeroed in part, pieces of work so far
+    for (;; ++n) {
+      int w = 0;
+      if (lane == 0) w = atomicAdd(a.work.counts + 2, 1);
+      w = __shfl_sync(0xffffffffu, w, 0);
+      if (!(ok = wait(&B.taken[n & 1], (n >> 1) + 1))) break;
+      if (w >= n_work) {
+        past = w;
+        if (lane == 0) {
+          drawn.info[n & 1] = make_int4(-1, 0, 0, 0);
+          mbar_arrive(smem_u32(&B.drawn[n & 1]));
+        }
+        break;
+      }
+      const int share = w & (a.shares - 1), rest = w / a.shares, g = rest % a.Hkv;
+      const int4 tile = __ldcg(a.work.tiles + rest / a.Hkv);
+      const int row0 = tile.x;
+      // K and V: the tile before has been read
+      if (!(ok = wait(&B.k_free, n + 1))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(smem_u32(&B.k_full), L::TILE);
+        load_tile<D>(smem_u32(smem + L::K), &tm_qkv, (a.Hq + g) * D, row0, smem_u32(&B.k_full));
+      }
+      SeqIter count(a, tile, lane);
+      int s[5], blocks = 0;
+      while (count.next(s)) {
+        int first, end;
+        query_blocks(s, row0, first, end);
+        blocks += blocks_of_share(share, first, end, G, a.shares);
+      }
+      if (lane == 0) {
+        drawn.info[n & 1] = make_int4(blocks, rest, share, 0);
+        drawn.more[n & 1] = tile;
+        mbar_arrive(smem_u32(&B.drawn[n & 1]));
+      }
+      if (!(ok = wait(&B.v_free, n + 1))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(smem_u32(&B.v_full), L::TILE);
+        load_tile<D>(smem_u32(smem + L::V), &tm_qkv, (a.Hq + a.Hkv + g) * D, row0, smem_u32(&B.v_full));
+      }
+      SeqIter it(a, tile, lane);
+      while (ok && it.next(s)) {
+        int first, end;
+        query_blocks(s, row0, first, end);
+        for (int hh = 0; hh < G && ok; ++hh) {
+          const int h = g * G + hh;
+          for (int b = first + ((share - first - hh) & (a.shares - 1)); b < end; b += a.shares, ++t) {
+            const int st = t % STAGES;
+            if (!(ok = wait(&B.empty[st], t / STAGES + 1))) break;
+            const int y = s[0] + b * BQ, have = s[2] - b * BQ < BQ ? s[2] - b * BQ : BQ;
+            uint8_t* q = smem + L::QD + st * 2 * L::TILE;
+            uint64_t* bar = have == BQ ? &B.full[st] : &B.raw;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(smem_u32(bar), 2 * L::TILE);
+              load_tile<D>(smem_u32(q), &tm_qkv, h * D, y, smem_u32(bar));
+              load_tile<D>(smem_u32(q + L::TILE), &tm_do, h * D, y, smem_u32(bar));
+            }
+            uint8_t* stats = smem + L::STATS + st * 2 * L::STEP;
+            const int64_t at = int64_t(h) * a.T + y;
+            float l[4], d[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = lane + 32 * i;
-            l[i] = c < have ? __ldcg(a.nlse + at + c) : 0.0f;
-            d[i] = c < have ? __ldcg(a.ndelta + at + c) : 0.0f;
-          }
+            for (int i = 0; i < 4; ++i) {
+              const int c = lane + 32 * i;
+              l[i] = c < have ? __ldcg(a.nlse + at + c) : 0.0f;
+              d[i] = c < have ? __ldcg(a.ndelta + at + c) : 0.0f;
+            }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            *reinterpret_cast<uint4*>(stats + step_offset(lane + 32 * i)) = in_three(l[i]);
-            *reinterpret_cast<uint4*>(stats + L::STEP + step_offset(lane + 32 * i)) = in_three(d[i]);
-          }
-          fence_proxy_async_smem();
-          // column c of the block sees key row r if min(x, y + r) <= c < z
-          if (lane == 0)
-            *reinterpret_cast<int4*>(smem + L::EDGES + st * 16) =
-                make_int4(s[4] - b * BQ, row0 - s[1] - (s[3] - s[2]) - b * BQ, have, 0);
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(smem_u32(&stat_full[st]));
-            mbar_arrive(smem_u32(&full[st]));
-          }
-          if (have < BQ) {
-            ok = __all_sync(0xffffffffu, mbar_wait(bar, uint32_t(raws) & 1u, abort_flag, a.err));
-            if (!ok) break;
-            ++raws;
-            zero_rows(q, 2 * D / 64, have, lane);
+            for (int i = 0; i < 4; ++i) {
+              *reinterpret_cast<uint4*>(stats + step_offset(lane + 32 * i)) = in_three(l[i]);
+              *reinterpret_cast<uint4*>(stats + L::STEP + step_offset(lane + 32 * i)) = in_three(d[i]);
+            }
             fence_proxy_async_smem();
+            // column c of the block sees key row r if min(x, y + r) <= c < z
+            if (lane == 0)
+              *reinterpret_cast<int4*>(smem + L::EDGES + st * 16) =
+                  make_int4(s[4] - b * BQ, row0 - s[1] - (s[3] - s[2]) - b * BQ, have, 0);
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&full[st]));
+            if (lane == 0) {
+              mbar_arrive(smem_u32(&B.edges[st]));
+              mbar_arrive(smem_u32(&B.full[st]));
+            }
+            if (have < BQ) {
+              if (!(ok = wait(bar, raws))) break;
+              ++raws;
+              zero_rows(q, 2 * D / 64, have, lane);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&B.full[st]));
+            }
           }
         }
       }
+      if (!ok) break;
     }
-    // every copy has landed before the CTA can exit (after a timeout: as far as one more limit shows)
+    // every copy has landed before shared memory has another use (after a timeout: as far as one more limit shows)
     if (lane == 0) {
-      drained(smem_u32(kv_full), 0);
-      for (int j = t - STAGES > 0 ? t - STAGES : 0; j < t; ++j) drained(smem_u32(&full[j % STAGES]), uint32_t(j / STAGES) & 1u);
-      if (!ok) drained(smem_u32(raw), uint32_t(raws) & 1u);
+      if (n > 0) drained(smem_u32(&B.k_full), uint32_t(n - 1) & 1u), drained(smem_u32(&B.v_full), uint32_t(n - 1) & 1u);
+      for (int j = t - STAGES > 0 ? t - STAGES : 0; j < t; ++j)
+        drained(smem_u32(&B.full[j % STAGES]), uint32_t(j / STAGES) & 1u);
+      if (!ok) {
+        drained(smem_u32(&B.k_full), uint32_t(n) & 1u);
+        drained(smem_u32(&B.raw), uint32_t(raws) & 1u);
+        drained(smem_u32(&B.full[t % STAGES]), uint32_t(t / STAGES) & 1u);
+      }
     }
   } else if (warp == 1) {
     // ---------------- products ----------------
     const uint32_t on = elect_one();
     const uint32_t ks = desc_low(smem_u32(smem + L::K)), vs = desc_low(smem_u32(smem + L::V));
     const uint64_t ones = desc_step(smem_u32(smem + L::ONES));
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag, a.err));
-    };
     auto tiles = [&](int t) { return smem_u32(smem + L::QD + t % STAGES * 2 * L::TILE); };
     auto form_s = [&](int t) {
-      if (!wait(&full[t % STAGES], uint32_t(t / STAGES) & 1u)) return false;
-      if (t > 0 && !wait(dv_done, uint32_t(t - 1) & 1u)) return false;  // P' of the block before has been read
+      if (!wait(&B.full[t % STAGES], t / STAGES)) return false;
+      if (t > 0 && !wait(&B.dv_done, t - 1)) return false;  // P' of the block before has been read
       tc_fence_after();
       product_nt<D>(on, tmem + L::S, ks, desc_low(tiles(t)));
       mma_bf16_on(on, tmem + L::S, ones, desc_step(smem_u32(smem + L::STATS + t % STAGES * 2 * L::STEP)), idesc_bf16_f32(128, 128), 1);
-      mma_commit_on(on, smem_u32(s_full));
+      mma_commit_on(on, smem_u32(&B.s_full));
       return true;
     };
     auto form_dp = [&](int t) {
-      if (t > 0 && !wait(dk_done, uint32_t(t - 1) & 1u)) return false;  // dS' of the block before has been read
+      if (t > 0 && !wait(&B.dk_done, t - 1)) return false;  // dS' of the block before has been read
       tc_fence_after();
       product_nt<D>(on, tmem + L::DP, vs, desc_low(tiles(t) + L::TILE));
       mma_bf16_on(on, tmem + L::DP, ones, desc_step(smem_u32(smem + L::STATS + (t % STAGES * 2 + 1) * L::STEP)),
                   idesc_bf16_f32(128, 128), 1);
-      mma_commit_on(on, smem_u32(dp_full));
+      mma_commit_on(on, smem_u32(&B.dp_full));
       return true;
     };
-    // S' of the next block as soon as P' of this one has been read, so that the warps that compute go from dS' to the next P'
-    bool ok = wait(kv_full, 0) && (n_it == 0 || (form_s(0) && form_dp(0)));
-    for (int t = 0; t < n_it && ok; ++t) {
-      const uint32_t now = uint32_t(t) & 1u;
-      if (!(ok = wait(p_full, now))) break;
-      tc_fence_after();
-      product_ta<D>(on, tmem + L::DV, tmem + L::S, desc_low_mn(tiles(t) + L::TILE), t > 0);
-      mma_commit_on(on, smem_u32(dv_done));
-      if (t + 1 < n_it && !(ok = form_s(t + 1))) break;
-      if (!(ok = wait(ds_full, now))) break;
-      tc_fence_after();
-      product_ta<D>(on, tmem + L::DK, tmem + L::DP, desc_low_mn(tiles(t)), t > 0);
-      mma_commit_on(on, smem_u32(dk_done));
-      mma_commit_on(on, smem_u32(&empty[t % STAGES]));
-      if (t + 1 < n_it) ok = form_dp(t + 1);
+    bool ok = true;
+    int t = 0;  // blocks so far
+    for (int n = 0; ok; ++n) {
+      if (!(ok = wait(&B.drawn[n & 1], n >> 1))) break;
+      const int blocks = drawn.info[n & 1].x;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&B.taken[n & 1]));
+      if (blocks < 0) break;
+      if (!(ok = wait(&B.k_full, n))) break;
+      const int from = t, to = t + blocks;
+      if (blocks > 0 && !(ok = form_s(t))) break;
+      if (blocks <= 1) mma_commit_on(on, smem_u32(&B.k_free));
+      if (!(ok = wait(&B.v_full, n))) break;
+      if (blocks > 0 && !(ok = form_dp(t))) break;
+      if (blocks <= 1) mma_commit_on(on, smem_u32(&B.v_free));
+      // S' of the next block as soon as P' of this one has been read, so that the warps that compute go from dS' to the next P'
+      for (; t < to; ++t) {
+        if (!(ok = wait(&B.p_full, t))) break;
+        tc_fence_after();
+        product_ta<D>(on, tmem + L::DV, tmem + L::S, desc_low_mn(tiles(t) + L::TILE), t > from);
+        mma_commit_on(on, smem_u32(&B.dv_done));
+        if (t + 1 < to && !(ok = form_s(t + 1))) break;
+        if (t + 2 == to) mma_commit_on(on, smem_u32(&B.k_free));
+        if (!(ok = wait(&B.ds_full, t))) break;
+        tc_fence_after();
+        product_ta<D>(on, tmem + L::DK, tmem + L::DP, desc_low_mn(tiles(t)), t > from);
+        mma_commit_on(on, smem_u32(&B.dk_done));
+        mma_commit_on(on, smem_u32(&B.empty[t % STAGES]));
+        if (t + 1 < to && !(ok = form_dp(t + 1))) break;
+        if (t + 2 == to) mma_commit_on(on, smem_u32(&B.v_free));
+      }
     }
-    // every product issued is done before tensor memory is released
-    mma_commit_on(on, smem_u32(drain));
-    drained(smem_u32(drain), 0);
+    // every product issued is done before tensor memory has another use
+    mma_commit_on(on, smem_u32(&B.drain));
+    drained(smem_u32(&B.drain), 0);
   } else {
     // ---------------- P' and dS': key row 32 (warp % 4) + lane, queries [32 part, 32 part + 32) of the block ----------------
     const int part = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane, cb = 32 * part;
     const uint32_t at = tmem + (uint32_t(quarter * 32) << 16);
     const unsigned long long c2 = f2_pack(a.c, a.c);
     bool ok = true;
-    for (int t = 0; t < n_it; ++t) {
-      const int st = t % STAGES;
-      const uint32_t now = uint32_t(t) & 1u;
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&stat_full[st]), uint32_t(t / STAGES) & 1u, abort_flag, a.err));
-      if (!ok) break;
-      const int4 edge = *reinterpret_cast<const int4*>(smem + L::EDGES + st * 16);
-      // columns [lo, hi) of this thread's 32 are visible; rows past the tile see none
-      const int hi = row < tile.y ? edge.z - cb : 0, lo = (edge.x < edge.y + row ? edge.x : edge.y + row) - cb;
-      const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < 32);
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(s_full), now, abort_flag, a.err));
-      if (!ok) break;
-      tc_fence_after();
-      float x[32];
-      tmem_ld32(at + L::S + cb, x);
-      if (masked) {
-#pragma unroll
-        for (int c = 0; c < 32; ++c) x[c] = c >= lo && c < hi ? x[c] : -INFINITY;
-      }
-      uint32_t pk[16];
-#pragma unroll
-      for (int c = 0; c < 32; c += 2) {  // S' - lse / scale came from the products
-        float u0, u1;
-        f2_unpack(f2_mul(f2_pack(x[c], x[c + 1]), c2), u0, u1);
-        x[c] = ex2(u0);
-        x[c + 1] = ex2(u1);
-        pk[c / 2] = cvt_bf2(x[c], x[c + 1]);
-      }
-      tmem_st16_words(at + L::S + cb, pk);
-      tmem_st_wait();
-      tc_fence_before();
+    int t = 0;  // blocks so far
+    for (int n = 0; ok; ++n) {
+      if (!(ok = wait(&B.drawn[n & 1], n >> 1))) break;
+      const int4 info = drawn.info[n & 1], tile = drawn.more[n & 1];
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(p_full));
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(dp_full), now, abort_flag, a.err));
-      if (!ok) break;
-      tc_fence_after();
-      {
+      if (lane == 0) mbar_arrive(smem_u32(&B.taken[n & 1]));
+      if (info.x < 0) break;
+      for (const int to = t + info.x; t < to; ++t) {
+        const int st = t % STAGES;
+        if (!(ok = wait(&B.edges[st], t / STAGES))) break;
+        const int4 edge = *reinterpret_cast<const int4*>(smem + L::EDGES + st * 16);
+        // columns [lo, hi) of this thread's 32 are visible; rows past the tile see none
+        const int hi = row < tile.y ? edge.z - cb : 0, lo = (edge.x < edge.y + row ? edge.x : edge.y + row) - cb;
+        const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < 32);
+        if (!(ok = wait(&B.s_full, t))) break;
+        tc_fence_after();
+        float x[32];
+        tmem_ld32(at + L::S + cb, x);
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) x[c] = c >= lo && c < hi ? x[c] : -INFINITY;
+        }
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {  // S' - lse / scale came from the products
+          float u0, u1;
+          f2_unpack(f2_mul(f2_pack(x[c], x[c + 1]), c2), u0, u1);
+          x[c] = ex2(u0);
+          x[c + 1] = ex2(u1);
+          pk[c / 2] = cvt_bf2(x[c], x[c + 1]);
+        }
+        tmem_st16_words(at + L::S + cb, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&B.p_full));
+        if (!(ok = wait(&B.dp_full, t))) break;
+        tc_fence_after();
         float y[32];
         tmem_ld32(at + L::DP + cb, y);
         if (masked) {
@@ -775,42 +812,60 @@ __device__ __forceinline__ void dkv_cta(const CUtensorMap& tm_qkv, const CUtenso
           f2_unpack(f2_mul(f2_pack(y[c], y[c + 1]), f2_pack(x[c], x[c + 1])), u0, u1);
           pk[c / 2] = cvt_bf2(u0, u1);
         }
+        tmem_st16_words(at + L::DP + cb, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&B.ds_full));
       }
-      tmem_st16_words(at + L::DP + cb, pk);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(ds_full));
-    }
-    if (ok && n_it > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(dk_done), uint32_t(n_it - 1) & 1u, abort_flag, a.err));
-    tc_fence_after();
-    float* mine = a.sums + (int64_t(rest) * a.shares + share) * (2 * 128 * D);
+      if (!ok) break;
+      // The last dK is done, and with it all before it. (The next tile's dV and dK are formed after these warps' next P' and dS'.)
+      const bool any = info.x > 0;
+      if (any && !(ok = wait(&B.dk_done, t - 1))) break;
+      tc_fence_after();
+      const int rest = info.y, share = info.z, g = rest % a.Hkv;
+      float* sums = a.sums + int64_t(rest) * a.shares * (2 * 128 * D);
+      // The share that comes last adds them up and need not send its own; where two come at once, both send, and one adds.
+      bool mine = a.shares == 1;
+      if (!mine) {
+        named_bar_sync(1, 32 * COMPUTE_WARPS);  // *ended of the tile before has been read
+        if (warp == 2 && lane == 0) {
+          *ended = atomicAdd(a.work.ended + rest, 0);
+          __threadfence();
+        }
+        named_bar_sync(1, 32 * COMPUTE_WARPS);
+        mine = *ended == a.shares - 1;
+        if (!mine) {
+          float* to = sums + share * (2 * 128 * D);
 #pragma unroll 1
-    for (int m = 0; m < 2 && ok; ++m) {
-      float v[D / 4] = {};
-      if (n_it > 0) ld_columns(at + (m ? L::DK : L::DV) + part * (D / 4), v);
+          for (int m = 0; m < 2; ++m) {
+            float v[D / 4] = {};
+            if (any) ld_columns(at + (m ? L::DK : L::DV) + part * (D / 4), v);
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-        __stcg(sums_at<D>(mine, m, part * (D / 16) + i, row), make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+            for (int i = 0; i < D / 16; ++i)
+              __stcg(sums_at<D>(to, m, part * (D / 16) + i, row), make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+          }
+          __threadfence();
+          named_bar_sync(1, 32 * COMPUTE_WARPS);
+          if (warp == 2 && lane == 0) {
+            *ended = atomicAdd(a.work.ended + rest, 1);
+            __threadfence();
+          }
+          named_bar_sync(1, 32 * COMPUTE_WARPS);
+          mine = *ended == a.shares - 1;
+        }
+      }
+      if (mine) {
+        __threadfence();
+        if (a.shares == 8) add_shares<D, 8>(sums, at, any, share, part, row, tile, g, a);
+        else if (a.shares == 4) add_shares<D, 4>(sums, at, any, share, part, row, tile, g, a);
+        else if (a.shares == 2) add_shares<D, 2>(sums, at, any, share, part, row, tile, g, a);
+        else add_shares<D, 1>(sums, at, any, share, part, row, tile, g, a);
+      }
+      tc_fence_before();  // dV and dK have been read: the next P' and dS' say so
     }
-    __threadfence();
   }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 512);
-  }
-  // The share that comes last finds the others' sums; after a timeout the tile is not written.
-  if (threadIdx.x == 0) *last = *abort_flag == 0u ? atomicAdd(a.work.ended + rest, 1) + 1 : 0;
-  __syncthreads();
-  if (*last != a.shares) return;
-  __threadfence();
-  float* sums = a.sums + int64_t(rest) * a.shares * (2 * 128 * D);
-  if (a.shares == 8) add_shares<D, 8>(sums, tile, g, a);
-  else if (a.shares == 4) add_shares<D, 4>(sums, tile, g, a);
-  else if (a.shares == 2) add_shares<D, 2>(sums, tile, g, a);
-  else add_shares<D, 1>(sums, tile, g, a);
+  return past;
 }
 
 // ---------------------------------------------------------------------------
@@ -821,187 +876,194 @@ template <int D>
 struct QLayout {
   static constexpr int K_STAGES = D == 128 ? 3 : 4, V_STAGES = D == 128 ? 2 : 3;
   static constexpr uint32_t TILE = 128 * D * 2;
-  static constexpr uint32_t Q = 0, DO = TILE, K = 2 * TILE, V = K + K_STAGES * TILE, BAR = V + V_STAGES * TILE;
-  static constexpr size_t BYTES = 1024 + size_t(BAR) + 512;
+  static constexpr uint32_t Q = 0, DO = TILE, K = 2 * TILE, V = K + K_STAGES * TILE, BYTES = V + V_STAGES * TILE;
   static constexpr uint32_t S = 0, DP = 256, DQ = 384;  // tensor memory: S of block t at 128 (t % 2)
 };
 
+struct QBars {
+  uint64_t q_full, q_free;  // the item's Q and dO; every product of the item that reads them is done
+  uint64_t raw;             // a K block that is zeroed in part before it is full
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full[2], dp_full, ds_full, dq_done, drain;
+  uint64_t drawn[2], taken[2];
+};
+
+// Items [0, n_work), the first of this CTA's drawn already.
 template <int D>
-__device__ __forceinline__ void dq_cta(const CUtensorMap& tm_qkv, const CUtensorMap& tm_do, const CUtensorMap& tm_out,
-                                       const Args& a, uint8_t* smem, unsigned cta) {
+__device__ __forceinline__ void dq_phase(const CUtensorMap& tm_qkv, const CUtensorMap& tm_do, const Args& a, uint8_t* smem,
+                                         QBars& B, Drawn& drawn, uint32_t tmem, int first, int n_before, int n_work,
+                                         const Waits& wait) {
   using L = QLayout<D>;
   constexpr int K_STAGES = L::K_STAGES, V_STAGES = L::V_STAGES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
-  uint64_t* q_full = bars;
-  uint64_t* raw = bars + 1;       // a K block that is zeroed in part before it is full
-  uint64_t* k_full = bars + 2;    // [K_STAGES]
-  uint64_t* k_empty = bars + 6;   // [K_STAGES]
-  uint64_t* v_full = bars + 10;   // [V_STAGES]
-  uint64_t* v_empty = bars + 14;  // [V_STAGES]
-  uint64_t* s_full = bars + 18;   // [2]
-  uint64_t* dp_full = bars + 20;
-  uint64_t* ds_full = bars + 21;
-  uint64_t* dq_done = bars + 22;
-  uint64_t* drain = bars + 23;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
-  volatile uint32_t* abort_flag = tmem_slot + 1;
-
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // the counts and the item at once; what lies past the last item is not used
-  pdl_wait();  // stats_kernel
-  const int n_items = __ldcg(a.work.counts + 1);
-  const int4* from = reinterpret_cast<const int4*>(a.work.items + int(cta) / a.Hq);
-  const int4 it0 = __ldcg(from), it1 = __ldcg(from + 1);
-  if (threadIdx.x == 0) {
-    mbar_init(smem_u32(q_full), 1);
-    mbar_init(smem_u32(raw), 1);
-    for (int i = 0; i < K_STAGES; ++i) {
-      mbar_init(smem_u32(&k_full[i]), 1);
-      mbar_init(smem_u32(&k_empty[i]), 1);
-    }
-    for (int i = 0; i < V_STAGES; ++i) {
-      mbar_init(smem_u32(&v_full[i]), 1);
-      mbar_init(smem_u32(&v_empty[i]), 1);
-    }
-    mbar_init(smem_u32(&s_full[0]), 1);
-    mbar_init(smem_u32(&s_full[1]), 1);
-    mbar_init(smem_u32(dp_full), 1);
-    mbar_init(smem_u32(ds_full), COMPUTE_WARPS);
-    mbar_init(smem_u32(dq_done), 1);
-    mbar_init(smem_u32(drain), 1);
-    *abort_flag = 0u;
-    fence_mbar_init();
-    fence_proxy_async_smem();
-  }
-  if (int(cta) / a.Hq >= n_items) return;
-  const int q0 = it0.x, k0 = it0.y, nq = it0.z, nk = it0.w, nc = it1.x, i0 = it1.y;
-  const int h = int(cta) % a.Hq, g = h / (a.Hq / a.Hkv);
-  const int i1 = i0 + BQ < nq ? i0 + BQ : nq;
-  const int kmax = i1 > nc ? nk : nk - nq + i1;
-  const int nblk = (kmax + BK - 1) / BK;
-  if (threadIdx.x == 0) {
-    mbar_arrive_expect_tx(smem_u32(q_full), 2 * L::TILE);
-    load_tile<D>(smem_u32(smem + L::Q), &tm_qkv, h * D, q0 + i0, smem_u32(q_full));
-    load_tile<D>(smem_u32(smem + L::DO), &tm_do, h * D, q0 + i0, smem_u32(q_full));
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.Hq / a.Hkv;
+  // an item's blocks of keys: all that its last query sees
+  auto blocks_of = [](const int4& sq, int nc, int i0) {
+    const int i1 = i0 + BQ < sq.z ? i0 + BQ : sq.z;
+    return ((i1 > nc ? sq.w : sq.w - sq.z + i1) + BK - 1) / BK;
+  };
 
   if (warp == 0) {
-    // ---------------- copies ----------------
+    // ---------------- work and copies ----------------
     bool ok = true;
-    int kdone = 0, vdone = 0;
-    for (int t = 0; t < nblk && ok; ++t) {
-      const int ks = t % K_STAGES, vs = t % V_STAGES, y = k0 + t * BK, have = nk - t * BK < BK ? nk - t * BK : BK;
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&k_empty[ks]), (uint32_t(t / K_STAGES) & 1u) ^ 1u, abort_flag, a.err));
-      if (!ok) break;
-      uint8_t* k = smem + L::K + ks * L::TILE;
-      const uint32_t bar = smem_u32(have == BK ? &k_full[ks] : raw);
+    int kt = 0, vt = 0, raws = 0, n = 0;  // K and V blocks, blocks zeroed in part, items so far
+    for (;; ++n) {
+      int w = first;
+      if (n > 0) {
+        if (lane == 0) w = atomicAdd(a.work.counts + 2, 1);
+        w = __shfl_sync(0xffffffffu, w, 0);
+      }
+      w -= n_before;
+      if (!(ok = wait(&B.taken[n & 1], (n >> 1) + 1))) break;
+      if (w >= n_work) {
+        if (lane == 0) {
+          drawn.info[n & 1] = make_int4(0, 0, -1, 0);
+          mbar_arrive(smem_u32(&B.drawn[n & 1]));
+        }
+        break;
+      }
+      const int4* from = reinterpret_cast<const int4*>(a.work.items + w / a.Hq);
+      const int4 sq = __ldcg(from), it = __ldcg(from + 1);  // q0, k0, nq, nk; n_causal, first query
+      const int h = w % a.Hq, g = h / G, blocks = blocks_of(sq, it.x, it.y);
       if (lane == 0) {
-        mbar_arrive_expect_tx(bar, L::TILE);
-        load_tile<D>(smem_u32(k), &tm_qkv, (a.Hq + g) * D, y, bar);
+        drawn.info[n & 1] = sq;
+        drawn.more[n & 1] = make_int4(it.x, it.y, h, 0);
+        mbar_arrive(smem_u32(&B.drawn[n & 1]));
       }
-      kdone = t + 1;
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&v_empty[vs]), (uint32_t(t / V_STAGES) & 1u) ^ 1u, abort_flag, a.err));
-      if (ok && lane == 0) {
-        mbar_arrive_expect_tx(smem_u32(&v_full[vs]), L::TILE);
-        load_tile<D>(smem_u32(smem + L::V + vs * L::TILE), &tm_qkv, (a.Hq + a.Hkv + g) * D, y, smem_u32(&v_full[vs]));
+      if (!(ok = wait(&B.q_free, n + 1))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(smem_u32(&B.q_full), 2 * L::TILE);
+        load_tile<D>(smem_u32(smem + L::Q), &tm_qkv, h * D, sq.x + it.y, smem_u32(&B.q_full));
+        load_tile<D>(smem_u32(smem + L::DO), &tm_do, h * D, sq.x + it.y, smem_u32(&B.q_full));
       }
-      if (ok) vdone = t + 1;
-      if (have < BK) {  // the last block: its rows past the sequence's keys are summed over in dS K
-        ok = __all_sync(0xffffffffu, mbar_wait(bar, 0, abort_flag, a.err)) && ok;
-        zero_rows(k, D / 64, have, lane);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&k_full[ks]));
+      for (int t = 0; t < blocks; ++t) {
+        const int ks = kt % K_STAGES, vs = vt % V_STAGES, y = sq.y + t * BK, have = sq.w - t * BK < BK ? sq.w - t * BK : BK;
+        if (!(ok = wait(&B.k_empty[ks], kt / K_STAGES + 1))) break;
+        uint8_t* k = smem + L::K + ks * L::TILE;
+        uint64_t* bar = have == BK ? &B.k_full[ks] : &B.raw;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(smem_u32(bar), L::TILE);
+          load_tile<D>(smem_u32(k), &tm_qkv, (a.Hq + g) * D, y, smem_u32(bar));
+        }
+        ++kt;
+        if (!(ok = wait(&B.v_empty[vs], vt / V_STAGES + 1))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(smem_u32(&B.v_full[vs]), L::TILE);
+          load_tile<D>(smem_u32(smem + L::V + vs * L::TILE), &tm_qkv, (a.Hq + a.Hkv + g) * D, y, smem_u32(&B.v_full[vs]));
+        }
+        ++vt;
+        if (have < BK) {  // the last block: its rows past the sequence's keys are summed over in dS K
+          if (!(ok = wait(bar, raws))) break;
+          ++raws;
+          zero_rows(k, D / 64, have, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&B.k_full[ks]));
+        }
       }
+      if (!ok) break;
     }
+    // every copy has landed before the CTA can exit (after a timeout: as far as one more limit shows)
     if (lane == 0) {
-      drained(smem_u32(q_full), 0);
-      for (int j = kdone - K_STAGES > 0 ? kdone - K_STAGES : 0; j < kdone; ++j)
-        drained(smem_u32(&k_full[j % K_STAGES]), uint32_t(j / K_STAGES) & 1u);
-      for (int j = vdone - V_STAGES > 0 ? vdone - V_STAGES : 0; j < vdone; ++j)
-        drained(smem_u32(&v_full[j % V_STAGES]), uint32_t(j / V_STAGES) & 1u);
+      const int items = n + (ok ? 0 : 1);
+      if (items > 0) drained(smem_u32(&B.q_full), uint32_t(items - 1) & 1u);
+      for (int j = kt - K_STAGES > 0 ? kt - K_STAGES : 0; j < kt; ++j)
+        drained(smem_u32(&B.k_full[j % K_STAGES]), uint32_t(j / K_STAGES) & 1u);
+      for (int j = vt - V_STAGES > 0 ? vt - V_STAGES : 0; j < vt; ++j)
+        drained(smem_u32(&B.v_full[j % V_STAGES]), uint32_t(j / V_STAGES) & 1u);
+      if (!ok) drained(smem_u32(&B.raw), uint32_t(raws) & 1u);
     }
   } else if (warp == 1) {
     // ---------------- products: per block dQ += dS K, dP of the next block, S of the one after it ----------------
     const uint32_t on = elect_one();
     const uint32_t q = desc_low(smem_u32(smem + L::Q)), dy = desc_low(smem_u32(smem + L::DO));
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag, a.err));
-    };
-    auto form_s = [&](int t) {
-      const int ks = t % K_STAGES;
-      if (!wait(&k_full[ks], uint32_t(t / K_STAGES) & 1u)) return false;
+    auto form_s = [&](int u) {
+      const int ks = u % K_STAGES;
+      if (!wait(&B.k_full[ks], u / K_STAGES)) return false;
       tc_fence_after();
-      product_nt<D>(on, tmem + L::S + 128 * (t & 1), q, desc_low(smem_u32(smem + L::K + ks * L::TILE)));
-      mma_commit_on(on, smem_u32(&s_full[t & 1]));
+      product_nt<D>(on, tmem + L::S + 128 * (u & 1), q, desc_low(smem_u32(smem + L::K + ks * L::TILE)));
+      mma_commit_on(on, smem_u32(&B.s_full[u & 1]));
       return true;
     };
-    auto form_dp = [&](int t) {
-      const int vs = t % V_STAGES;
-      if (!wait(&v_full[vs], uint32_t(t / V_STAGES) & 1u)) return false;
+    auto form_dp = [&](int u) {
+      const int vs = u % V_STAGES;
+      if (!wait(&B.v_full[vs], u / V_STAGES)) return false;
       tc_fence_after();
       product_nt<D>(on, tmem + L::DP, dy, desc_low(smem_u32(smem + L::V + vs * L::TILE)));
-      mma_commit_on(on, smem_u32(dp_full));
-      mma_commit_on(on, smem_u32(&v_empty[vs]));
+      mma_commit_on(on, smem_u32(&B.dp_full));
+      mma_commit_on(on, smem_u32(&B.v_empty[vs]));
       return true;
     };
-    bool ok = wait(q_full, 0) && form_s(0) && form_dp(0) && (nblk < 2 || form_s(1));
-    for (int t = 0; t < nblk && ok; ++t) {
-      const int ks = t % K_STAGES;
-      if (!(ok = wait(ds_full, uint32_t(t) & 1u))) break;  // S and dP of the block have been read, dS is written
-      tc_fence_after();
-      product_ta<D>(on, tmem + L::DQ, tmem + L::S + 128 * (t & 1), desc_low_mn(smem_u32(smem + L::K + ks * L::TILE)), t > 0);
-      mma_commit_on(on, smem_u32(dq_done));
-      mma_commit_on(on, smem_u32(&k_empty[ks]));
-      if (t + 1 < nblk && !(ok = form_dp(t + 1))) break;
-      if (t + 2 < nblk) ok = wait(dq_done, uint32_t(t) & 1u) && form_s(t + 2);  // into dS's place
+    bool ok = true;
+    int u = 0;  // blocks so far
+    for (int n = 0; ok; ++n) {
+      if (!(ok = wait(&B.drawn[n & 1], n >> 1))) break;
+      const int4 sq = drawn.info[n & 1], it = drawn.more[n & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&B.taken[n & 1]));
+      if (sq.z < 0) break;
+      const int from = u, to = u + blocks_of(sq, it.x, it.y);
+      if (!(ok = wait(&B.q_full, n) && form_s(u) && form_dp(u) && (u + 1 >= to || form_s(u + 1)))) break;
+      if (u + 1 == to) mma_commit_on(on, smem_u32(&B.q_free));
+      for (; u < to; ++u) {
+        const int ks = u % K_STAGES;
+        if (!(ok = wait(&B.ds_full, u))) break;  // S and dP of the block have been read, dS is written
+        tc_fence_after();
+        product_ta<D>(on, tmem + L::DQ, tmem + L::S + 128 * (u & 1), desc_low_mn(smem_u32(smem + L::K + ks * L::TILE)), u > from);
+        mma_commit_on(on, smem_u32(&B.dq_done));
+        mma_commit_on(on, smem_u32(&B.k_empty[ks]));
+        if (u + 1 < to && !(ok = form_dp(u + 1))) break;
+        if (u + 2 == to) mma_commit_on(on, smem_u32(&B.q_free));
+        // dS has been read: S of the block after the next comes into its place. (Waited for at every block, before the next dQ
+        // is issued: a barrier two phases ahead looks like one that is not there yet.)
+        if (!(ok = wait(&B.dq_done, u))) break;
+        if (u + 2 < to && !(ok = form_s(u + 2))) break;
+      }
     }
-    mma_commit_on(on, smem_u32(drain));
-    drained(smem_u32(drain), 0);
+    mma_commit_on(on, smem_u32(&B.drain));
+    drained(smem_u32(&B.drain), 0);
   } else {
     // ---------------- dS: query row 32 (warp % 4) + lane, keys [32 part, 32 part + 32) of the block ----------------
     const int part = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane, cb = 32 * part;
     const uint32_t at = tmem + (uint32_t(quarter * 32) << 16);
-    const int i = i0 + row;
-    const bool valid = i < nq;
-    const int lim = !valid ? 0 : i < nc ? nk - nq + i + 1 : nk;  // keys [0, lim) are visible
-    const int64_t st = int64_t(h) * a.T + q0 + i;
-    const float nl = valid ? __ldcg(a.nlse + st) : 0.0f, nd = valid ? __ldcg(a.ndelta + st) : 0.0f;
-    const unsigned long long c2 = f2_pack(a.c, a.c), nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+    const unsigned long long c2 = f2_pack(a.c, a.c);
+    const int64_t N = int64_t(a.Hq + 2 * a.Hkv) * D;
     bool ok = true;
-    for (int t = 0; t < nblk; ++t) {
-      const int hi = lim - t * BK - cb;  // columns [0, hi) of this thread's 32 are visible
-      const bool masked = __any_sync(0xffffffffu, hi < 32);
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[t & 1]), uint32_t(t >> 1) & 1u, abort_flag, a.err));
-      if (!ok) break;
-      tc_fence_after();
-      float x[32];
-      tmem_ld32(at + L::S + 128 * (t & 1) + cb, x);
-      if (masked) {
+    int u = 0;  // blocks so far
+    for (int n = 0; ok; ++n) {
+      if (!(ok = wait(&B.drawn[n & 1], n >> 1))) break;
+      const int4 sq = drawn.info[n & 1], it = drawn.more[n & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&B.taken[n & 1]));
+      if (sq.z < 0) break;
+      const int i = it.y + row, h = it.z;
+      const bool valid = i < sq.z;
+      const int lim = !valid ? 0 : i < it.x ? sq.w - sq.z + i + 1 : sq.w;  // keys [0, lim) are visible
+      const int64_t stat = int64_t(h) * a.T + sq.x + i;
+      const float nl = valid ? __ldcg(a.nlse + stat) : 0.0f, nd = valid ? __ldcg(a.ndelta + stat) : 0.0f;
+      const unsigned long long nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+      const int from = u;
+      for (const int to = u + blocks_of(sq, it.x, it.y); u < to; ++u) {
+        const int hi = lim - (u - from) * BK - cb;  // columns [0, hi) of this thread's 32 are visible
+        const bool masked = __any_sync(0xffffffffu, hi < 32);
+        if (!(ok = wait(&B.s_full[u & 1], u >> 1))) break;
+        tc_fence_after();
+        float x[32];
+        tmem_ld32(at + L::S + 128 * (u & 1) + cb, x);
+        if (masked) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) x[c] = c < hi ? x[c] : -INFINITY;
-      }
+          for (int c = 0; c < 32; ++c) x[c] = c < hi ? x[c] : -INFINITY;
+        }
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        float u0, u1;
-        f2_unpack(f2_mul(f2_add(f2_pack(x[c], x[c + 1]), nl2), c2), u0, u1);
-        x[c] = ex2(u0);
-        x[c + 1] = ex2(u1);
-        asm volatile("" : "+f"(x[c]), "+f"(x[c + 1]));  // now, not after the wait for dP
-      }
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(dp_full), uint32_t(t) & 1u, abort_flag, a.err));
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t pk[16];
-      {
+        for (int c = 0; c < 32; c += 2) {
+          float u0, u1;
+          f2_unpack(f2_mul(f2_add(f2_pack(x[c], x[c + 1]), nl2), c2), u0, u1);
+          x[c] = ex2(u0);
+          x[c + 1] = ex2(u1);
+          asm volatile("" : "+f"(x[c]), "+f"(x[c + 1]));  // now, not after the wait for dP
+        }
+        if (!(ok = wait(&B.dp_full, u))) break;
+        tc_fence_after();
+        uint32_t pk[16];
         float y[32];
         tmem_ld32(at + L::DP + cb, y);
         if (masked) {
@@ -1014,58 +1076,105 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tm_qkv, const CUtensor
           f2_unpack(f2_mul(f2_add(f2_pack(y[c], y[c + 1]), nd2), f2_pack(x[c], x[c + 1])), u0, u1);
           pk[c / 2] = cvt_bf2(u0, u1);
         }
+        tmem_st16_words(at + L::S + 128 * (u & 1) + cb, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&B.ds_full));
       }
-      tmem_st16_words(at + L::S + 128 * (t & 1) + cb, pk);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(ds_full));
-    }
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(dq_done), uint32_t(nblk - 1) & 1u, abort_flag, a.err));
-    tc_fence_after();
-    const bool whole = i0 + BQ <= nq;
-    const int64_t N = int64_t(a.Hq + 2 * a.Hkv) * D;
-    if (ok) {
+      if (!ok) break;
+      // the item's last dQ is done: dP of its last block, which these warps have read, came after the dQ before it
+      if (!(ok = wait(&B.dq_done, u - 1))) break;
+      tc_fence_after();
       float v[D / 4];
       ld_columns(at + L::DQ + part * (D / 4), v);
+      tc_fence_before();  // dQ has been read: the next item's first dS says so
+      if (valid) {
+        uint4* to = reinterpret_cast<uint4*>(a.dqkv + (sq.x + i) * N + h * D + part * (D / 4));
 #pragma unroll
-      for (int u = 0; u < D / 32; ++u) {
-        uint32_t o[4];
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t o[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = cvt_bf2(__fmul_rn(v[8 * u + 2 * q], a.scale), __fmul_rn(v[8 * u + 2 * q + 1], a.scale));
-        const uint4 w = make_uint4(o[0], o[1], o[2], o[3]);
-        const int k = part * (D / 32) + u;  // 16-byte piece of the row
-        if (whole)  // into Q's place (no product reads it any more), in the boxes' swizzled layout
-          *reinterpret_cast<uint4*>(smem + L::Q + (k >> 3) * SUB + row * 128 + (((k & 7) ^ (row & 7)) << 4)) = w;
-        else if (valid)  // rows past the sequence's queries belong to others
-          *reinterpret_cast<uint4*>(a.dqkv + (q0 + i) * N + h * D + 8 * k) = w;
-      }
-    }
-    if (whole) {
-      fence_proxy_async_smem();
-      named_bar_sync(1, 32 * COMPUTE_WARPS);
-      if (warp == 2 && lane == 0 && *abort_flag == 0u) {
-        for (int b = 0; b < D / 64; ++b) tma_store_2d(&tm_out, smem_u32(smem + L::Q + b * SUB), h * D + 64 * b, q0 + i0);
-        bulk_store_commit_and_wait_read();
+          for (int e = 0; e < 4; ++e) o[e] = cvt_bf2(__fmul_rn(v[8 * k + 2 * e], a.scale), __fmul_rn(v[8 * k + 2 * e + 1], a.scale));
+          to[k] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
       }
     }
   }
+}
+
+// What a CTA's warps share beside the tiles.
+struct Shared {
+  KvBars kv;
+  QBars q;
+  Drawn drawn[2];  // one for each phase
+  uint32_t tmem, abort_flag;
+  int ended, first;
+};
+static_assert(sizeof(Shared) <= kSharedBytes, "room behind the tiles");
+
+template <int D>
+constexpr uint32_t kTileBytes = (KvLayout<D>::BYTES > QLayout<D>::BYTES ? KvLayout<D>::BYTES : QLayout<D>::BYTES);
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    grad_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __grid_constant__ CUtensorMap tm_do,
+                const __grid_constant__ Args a) {
+  using L = KvLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Shared& sh = *reinterpret_cast<Shared*>(smem + kTileBytes<D>);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    auto init = [](uint64_t& bar, int count) { mbar_init(smem_u32(&bar), uint32_t(count)); };
+    for (uint64_t* b : {&sh.kv.k_full, &sh.kv.v_full, &sh.kv.k_free, &sh.kv.v_free, &sh.kv.raw, &sh.kv.s_full, &sh.kv.dp_full,
+                        &sh.kv.dv_done, &sh.kv.dk_done, &sh.kv.drain, &sh.q.q_full, &sh.q.q_free, &sh.q.raw, &sh.q.s_full[0],
+                        &sh.q.s_full[1], &sh.q.dp_full, &sh.q.dq_done, &sh.q.drain})
+      init(*b, 1);
+    for (uint64_t* b : {&sh.kv.p_full, &sh.kv.ds_full, &sh.q.ds_full}) init(*b, COMPUTE_WARPS);
+    for (int i = 0; i < 4; ++i) {
+      init(sh.kv.full[i], 2);  // the tiles, and the stats
+      for (uint64_t* b : {&sh.kv.empty[i], &sh.kv.edges[i], &sh.q.k_full[i], &sh.q.k_empty[i], &sh.q.v_full[i], &sh.q.v_empty[i]})
+        init(*b, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      init(sh.kv.drawn[i], 1);
+      init(sh.q.drawn[i], 1);
+      init(sh.kv.taken[i], TAKERS);
+      init(sh.q.taken[i], TAKERS);
+    }
+    sh.abort_flag = 0u;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  for (int i = threadIdx.x; i < int((2 * L::STAGES + 1) * L::STEP / 16); i += THREADS)  // only the stats' first values change
+    *reinterpret_cast<uint4*>(smem + L::ONES + i * 16) =
+        i < int(L::STEP / 16) && (i & 8) == 0 ? make_uint4(0x3F803F80u, 0x3F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sh.tmem), 512);
+    tmem_relinquish();
+  }
+  pdl_wait();  // stats_kernel
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const Waits wait{&sh.abort_flag, a.err};
+  const int n_kv = __ldcg(a.work.counts) * a.Hkv * a.shares, n_q = __ldcg(a.work.counts + 1) * a.Hq;
+  const int first = dkv_phase<D>(tm_qkv, tm_do, a, smem, sh.kv, sh.drawn[0], &sh.ended, tmem, n_kv, wait);
+  tc_fence_before();
+  fence_proxy_async_smem();  // what was written to the tiles comes before the second phase's copies
+  __syncthreads();           // every product and copy of the first phase is done
+  tc_fence_after();
+  if (*const_cast<volatile uint32_t*>(&sh.abort_flag) == 0u)
+    dq_phase<D>(tm_qkv, tm_do, a, smem, sh.q, sh.drawn[1], tmem, first, n_kv, n_q, wait);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-}
-
-template <int D>
-__global__ void __launch_bounds__(THREADS, 1)
-    grad_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __grid_constant__ CUtensorMap tm_do,
-                const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ Args a) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  if (blockIdx.x < a.kv_ctas) dkv_cta<D>(tm_qkv, tm_do, a, smem);
-  else dq_cta<D>(tm_qkv, tm_do, tm_out, a, smem, blockIdx.x - a.kv_ctas);
 }
 
 inline bool shape_ok(int64_t T, int Hq, int Hkv, int D, int n_seq) {
@@ -1075,6 +1184,8 @@ inline bool shape_ok(int64_t T, int Hq, int Hkv, int D, int n_seq) {
 
 // CTAs that share a tile and KV head, a power of two: a rule on the group alone, as it sets the order of the sums.
 inline int shares_of(int G) { return G >= 8 ? 8 : G >= 4 ? 4 : G >= 2 ? 2 : 1; }
+
+constexpr int64_t kMostWork = 1 << 30;  // pieces of work: drawn as 32-bit numbers, some past the last
 
 // The workspace after its header, in bytes.
 struct Room {
@@ -1101,16 +1212,16 @@ struct Room {
   }
 };
 
+// `most`: at least as many as there are pieces of work.
 template <int D>
-static int launch(const uint16_t* dout, const uint16_t* qkv, const uint16_t* out, const float* lse, const Args& a,
-                  cudaStream_t s) {
-  CUtensorMap tm_qkv, tm_do, tm_out;
+static int launch(const uint16_t* dout, const uint16_t* qkv, const uint16_t* out, const float* lse, const Args& a, int64_t most,
+                  int sms, cudaStream_t s) {
+  CUtensorMap tm_qkv, tm_do;
   const uint64_t N = uint64_t(a.Hq + 2 * a.Hkv) * D;
   if (!make_tmap_bf16(&tm_qkv, qkv, N, uint64_t(a.T), 64, 128) ||
-      !make_tmap_bf16(&tm_do, dout, uint64_t(a.Hq) * D, uint64_t(a.T), 64, 128) ||
-      !make_tmap_bf16(&tm_out, a.dqkv, N, uint64_t(a.T), 64, 128))
+      !make_tmap_bf16(&tm_do, dout, uint64_t(a.Hq) * D, uint64_t(a.T), 64, 128))
     return MOT_ERR_CUDA;
-  constexpr int bytes = int(KvLayout<D>::BYTES > QLayout<D>::BYTES ? KvLayout<D>::BYTES : QLayout<D>::BYTES);
+  constexpr int bytes = 1024 + int(kTileBytes<D>) + int(kSharedBytes);
   static_assert(bytes > 114 * 1024, "one CTA an SM: two would compete for tensor memory");
   static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
   if (cudaFuncSetAttribute(grad_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
@@ -1131,8 +1242,8 @@ static int launch(const uint16_t* dout, const uint16_t* qkv, const uint16_t* out
   st.err = a.err;
   stats_kernel<D><<<dim3(unsigned((a.T + STATS_ROWS - 1) / STATS_ROWS + 1), unsigned((a.Hq + 31) / 32)), STATS_THREADS, 0, s>>>(st);
   if (cudaGetLastError() != cudaSuccess) return MOT_ERR_CUDA;
-  if (launch_dependent(grad_kernel<D>, dim3(a.kv_ctas + unsigned(a.work.max_items * int64_t(a.Hq))), dim3(THREADS), size_t(bytes), s,
-                       tm_qkv, tm_do, tm_out, a) != cudaSuccess)
+  if (launch_dependent(grad_kernel<D>, dim3(unsigned(most < sms ? most : sms)), dim3(THREADS), size_t(bytes), s, tm_qkv, tm_do, a) !=
+      cudaSuccess)
     return MOT_ERR_CUDA;
   return MOT_OK;
 }
@@ -1145,7 +1256,7 @@ using namespace mot;
 extern "C" size_t mot_joint_attention_backward_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int n_seq) {
   if (!attnb::shape_ok(T, Hq, Hkv, D, n_seq)) return 0;
   const attnb::Room room(T, Hq, Hkv, D, n_seq);
-  return room.ctas <= INT32_MAX ? sizeof(PlanHeader) + size_t(room.end) : 0;
+  return room.ctas <= attnb::kMostWork ? sizeof(PlanHeader) + size_t(room.end) : 0;
 }
 
 extern "C" int mot_joint_attention_backward(const mot_bf16* dout, const mot_bf16* qkv, const mot_bf16* out,
@@ -1160,7 +1271,7 @@ extern "C" int mot_joint_attention_backward(const mot_bf16* dout, const mot_bf16
       !aligned16(dqkv))
     return MOT_ERR_ALIGN;
   const attnb::Room room(T, Hq, Hkv, D, n_seq);
-  if (room.ctas > INT32_MAX) return MOT_ERR_GEOMETRY;
+  if (room.ctas > attnb::kMostWork) return MOT_ERR_GEOMETRY;
   if (ws_bytes < mot_joint_attention_backward_workspace_bytes(T, Hq, Hkv, D, n_seq)) return MOT_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const void* ptrs[] = {dout, qkv, out, lse, seqs, ws, dqkv};
@@ -1185,7 +1296,6 @@ extern "C" int mot_joint_attention_backward(const mot_bf16* dout, const mot_bf16
   a.work.counts = reinterpret_cast<int32_t*>(base + room.counts);
   a.work.ended = reinterpret_cast<int32_t*>(base + room.ended);
   a.sums = reinterpret_cast<float*>(base + room.sums);
-  a.kv_ctas = unsigned(int64_t(room.max_tiles) * Hkv * a.shares);
   a.work.change = reinterpret_cast<int32_t*>(base + room.change);
   a.work.border = reinterpret_cast<uint32_t*>(base + room.border);
   a.work.runs = reinterpret_cast<int32_t*>(base + room.runs);
@@ -1193,6 +1303,6 @@ extern "C" int mot_joint_attention_backward(const mot_bf16* dout, const mot_bf16
   a.work.max_items = room.max_items;
   a.dqkv = dqkv;
   a.err = &static_cast<PlanHeader*>(ws)->error;
-  if (D == 64) return attnb::launch<64>(dout, qkv, out, lse, a, s);
-  return attnb::launch<128>(dout, qkv, out, lse, a, s);
+  if (D == 64) return attnb::launch<64>(dout, qkv, out, lse, a, room.ctas, sm_count(dev), s);
+  return attnb::launch<128>(dout, qkv, out, lse, a, room.ctas, sm_count(dev), s);
 }
