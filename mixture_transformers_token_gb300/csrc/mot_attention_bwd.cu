@@ -476,6 +476,33 @@ __device__ __forceinline__ void product_ta(uint32_t on, uint32_t d, uint32_t a_t
     mma_bf16_ta_on(on, d, a_tmem + (kk / 2) * 32 + (kk % 2) * 8, desc_of(b + ((kk * 2048) >> 4)), idesc, accumulate || kk > 0);
 }
 
+// Writes PIECES 16-byte pieces of each lane's row, rows `stride` values apart from `to` on, of which the first `rows` are written.
+// PIECES lanes exchange theirs first, so that they write pieces that lie side by side: 32 rows at once, 16 bytes each, held the
+// load and store unit for 3500 cycles a tile, and the products' warp with it.
+template <int PIECES>
+__device__ __forceinline__ void write_rows(uint16_t* to, int64_t stride, int rows, int lane, uint4 (&p)[PIECES]) {
+#pragma unroll
+  for (int bit = 1; bit < PIECES; bit <<= 1) {
+    const bool upper = (lane & bit) != 0;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      if (i & bit) continue;
+      uint4 send = upper ? p[i] : p[i + bit];
+      send.x = __shfl_xor_sync(0xffffffffu, send.x, bit);
+      send.y = __shfl_xor_sync(0xffffffffu, send.y, bit);
+      send.z = __shfl_xor_sync(0xffffffffu, send.z, bit);
+      send.w = __shfl_xor_sync(0xffffffffu, send.w, bit);
+      if (upper) p[i] = send;
+      else p[i + bit] = send;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < PIECES; ++k) {  // piece lane % PIECES of row PIECES (lane / PIECES) + k
+    const int row = lane / PIECES * PIECES + k;
+    if (row < rows) *reinterpret_cast<uint4*>(to + row * stride + lane % PIECES * 8) = p[k];
+  }
+}
+
 __device__ __forceinline__ void ld_columns(uint32_t taddr, float (&v)[32]) { tmem_ld32(taddr, v); }
 __device__ __forceinline__ void ld_columns(uint32_t taddr, float (&v)[16]) { tmem_ld16(taddr, v); }
 
@@ -498,7 +525,7 @@ struct Waits {
 };
 
 // Both phases' barriers and what the CTA's warps share lie behind the larger layout.
-constexpr uint32_t kSharedBytes = 768;
+constexpr uint32_t kSharedBytes = 896;
 
 // ---------------------------------------------------------------------------
 // dK and dV
@@ -520,9 +547,10 @@ struct KvLayout {
 
 struct KvBars {
   uint64_t k_full, v_full, k_free, v_free;  // the tile's K and V; every product of the tile that reads them is done
-  uint64_t raw;                             // a block that is zeroed in part before it is full
-  uint64_t full[4], empty[4], edges[4];     // a block's tiles and stats; its products are done; its edges are there
-  uint64_t s_full, dp_full, p_full, ds_full, dv_done, dk_done, drain;
+  uint64_t raw;                             // a tile that is zeroed in part before it is full
+  uint64_t q_full[4], q_empty[4], do_full[4], do_empty[4];  // a block's tiles and their stats; their products are done
+  uint64_t edges[4];                        // a block's edges are there
+  uint64_t s_full, dp_full, p_full, ds_full, dv_done, dk_done, drain, meet;
   uint64_t drawn[2], taken[2];
 };
 
@@ -532,49 +560,51 @@ __device__ __forceinline__ float4* sums_at(float* sums, int m, int piece, int ro
   return reinterpret_cast<float4*>(sums) + (m * (D / 4) + piece) * 128 + row;
 }
 
-// The thread's row of dV and dK as bf16, its quarter of the columns: the sums of the shares in order, this one's from tensor memory.
+// The thread's row of dV and dK as bf16, its quarter of the columns: the sums of the shares in order (of one: from tensor memory).
 template <int D, int SHARES>
-__device__ __forceinline__ void add_shares(float* sums, uint32_t at, bool any, int share, int part, int row, const int4& tile,
-                                           int g, const Args& a) {
+__device__ __forceinline__ void add_shares(float* sums, uint32_t at, bool any, int part, int row, int row0, int rows, int g,
+                                           const Args& a) {
   using L = KvLayout<D>;
-  const int64_t N = int64_t(a.Hq + 2 * a.Hkv) * D;
   constexpr int Q = SHARES == 8 ? 2 : 4;  // pieces of four columns whose reads are under way at once
+  const int64_t N = int64_t(a.Hq + 2 * a.Hkv) * D;
+  const int lane = row & 31, base = row - lane;  // the warp's first row
 #pragma unroll 1
   for (int m = 0; m < 2; ++m)
 #pragma unroll 1
     for (int c0 = part * (D / 4); c0 < (part + 1) * (D / 4); c0 += 16) {
       __syncwarp();
-      float own[16] = {};
-      if (any) tmem_ld16(at + (m ? L::DK : L::DV) + c0, own);
-      if (row < tile.y) {
-        const float f = m ? a.scale : 1.0f;
-        uint32_t o[8];
+      float v[16] = {};
+      if constexpr (SHARES == 1) {
+        if (any) tmem_ld16(at + (m ? L::DK : L::DV) + c0, v);
+      } else {
 #pragma unroll
         for (int q0 = 0; q0 < 4; q0 += Q) {
           float4 u[SHARES][Q];
 #pragma unroll
           for (int p = 0; p < SHARES; ++p)
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
-              const int k = 4 * (q0 + q);
-              u[p][q] = p == share ? make_float4(own[k], own[k + 1], own[k + 2], own[k + 3])
-                                   : __ldcg(sums_at<D>(sums + p * (2 * 128 * D), m, c0 / 4 + q0 + q, row));
-            }
+            for (int q = 0; q < Q; ++q) u[p][q] = __ldcg(sums_at<D>(sums + p * (2 * 128 * D), m, c0 / 4 + q0 + q, row));
 #pragma unroll
           for (int q = 0; q < Q; ++q) {
-            float4 v = u[0][q];
+            float4 s = u[0][q];
 #pragma unroll
             for (int p = 1; p < SHARES; ++p)
-              v = make_float4(__fadd_rn(v.x, u[p][q].x), __fadd_rn(v.y, u[p][q].y), __fadd_rn(v.z, u[p][q].z),
-                              __fadd_rn(v.w, u[p][q].w));
-            o[2 * (q0 + q)] = cvt_bf2(__fmul_rn(v.x, f), __fmul_rn(v.y, f));
-            o[2 * (q0 + q) + 1] = cvt_bf2(__fmul_rn(v.z, f), __fmul_rn(v.w, f));
+              s = make_float4(__fadd_rn(s.x, u[p][q].x), __fadd_rn(s.y, u[p][q].y), __fadd_rn(s.z, u[p][q].z),
+                              __fadd_rn(s.w, u[p][q].w));
+            const int k = 4 * (q0 + q);
+            v[k] = s.x, v[k + 1] = s.y, v[k + 2] = s.z, v[k + 3] = s.w;
           }
         }
-        uint4* to = reinterpret_cast<uint4*>(a.dqkv + (tile.x + row) * N + (a.Hq + (m ? 0 : a.Hkv) + g) * D + c0);
-        to[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        to[1] = make_uint4(o[4], o[5], o[6], o[7]);
       }
+      const float f = m ? a.scale : 1.0f;
+      uint4 o[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        o[k] = make_uint4(cvt_bf2(__fmul_rn(v[8 * k], f), __fmul_rn(v[8 * k + 1], f)),
+                          cvt_bf2(__fmul_rn(v[8 * k + 2], f), __fmul_rn(v[8 * k + 3], f)),
+                          cvt_bf2(__fmul_rn(v[8 * k + 4], f), __fmul_rn(v[8 * k + 5], f)),
+                          cvt_bf2(__fmul_rn(v[8 * k + 6], f), __fmul_rn(v[8 * k + 7], f)));
+      write_rows<2>(a.dqkv + (row0 + base) * N + (a.Hq + (m ? 0 : a.Hkv) + g) * D + c0, N, rows - base, lane, o);
     }
   __syncwarp();
 }
@@ -609,12 +639,6 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
       const int share = w & (a.shares - 1), rest = w / a.shares, g = rest % a.Hkv;
       const int4 tile = __ldcg(a.work.tiles + rest / a.Hkv);
       const int row0 = tile.x;
-      // K and V: the tile before has been read
-      if (!(ok = wait(&B.k_free, n + 1))) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(smem_u32(&B.k_full), L::TILE);
-        load_tile<D>(smem_u32(smem + L::K), &tm_qkv, (a.Hq + g) * D, row0, smem_u32(&B.k_full));
-      }
       SeqIter count(a, tile, lane);
       int s[5], blocks = 0;
       while (count.next(s)) {
@@ -626,6 +650,12 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
         drawn.info[n & 1] = make_int4(blocks, rest, share, 0);
         drawn.more[n & 1] = tile;
         mbar_arrive(smem_u32(&B.drawn[n & 1]));
+      }
+      // K and V: the tile before has been read
+      if (!(ok = wait(&B.k_free, n + 1))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(smem_u32(&B.k_full), L::TILE);
+        load_tile<D>(smem_u32(smem + L::K), &tm_qkv, (a.Hq + g) * D, row0, smem_u32(&B.k_full));
       }
       if (!(ok = wait(&B.v_free, n + 1))) break;
       if (lane == 0) {
@@ -639,48 +669,45 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
         for (int hh = 0; hh < G && ok; ++hh) {
           const int h = g * G + hh;
           for (int b = first + ((share - first - hh) & (a.shares - 1)); b < end; b += a.shares, ++t) {
-            const int st = t % STAGES;
-            if (!(ok = wait(&B.empty[st], t / STAGES + 1))) break;
-            const int y = s[0] + b * BQ, have = s[2] - b * BQ < BQ ? s[2] - b * BQ : BQ;
-            uint8_t* q = smem + L::QD + st * 2 * L::TILE;
-            uint64_t* bar = have == BQ ? &B.full[st] : &B.raw;
-            if (lane == 0) {
-              mbar_arrive_expect_tx(smem_u32(bar), 2 * L::TILE);
-              load_tile<D>(smem_u32(q), &tm_qkv, h * D, y, smem_u32(bar));
-              load_tile<D>(smem_u32(q + L::TILE), &tm_do, h * D, y, smem_u32(bar));
-            }
-            uint8_t* stats = smem + L::STATS + st * 2 * L::STEP;
-            const int64_t at = int64_t(h) * a.T + y;
-            float l[4], d[4];
+            const int st = t % STAGES, y = s[0] + b * BQ, have = s[2] - b * BQ < BQ ? s[2] - b * BQ : BQ;
+            // dO before Q: its place is free when dV is done, Q's when dK is, and S' wants Q first
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int c = lane + 32 * i;
-              l[i] = c < have ? __ldcg(a.nlse + at + c) : 0.0f;
-              d[i] = c < have ? __ldcg(a.ndelta + at + c) : 0.0f;
-            }
+            for (int m = 1; m >= 0 && ok; --m) {
+              const float* from = (m ? a.ndelta : a.nlse) + int64_t(h) * a.T + y;
+              float v[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              *reinterpret_cast<uint4*>(stats + step_offset(lane + 32 * i)) = in_three(l[i]);
-              *reinterpret_cast<uint4*>(stats + L::STEP + step_offset(lane + 32 * i)) = in_three(d[i]);
-            }
-            fence_proxy_async_smem();
-            // column c of the block sees key row r if min(x, y + r) <= c < z
-            if (lane == 0)
-              *reinterpret_cast<int4*>(smem + L::EDGES + st * 16) =
-                  make_int4(s[4] - b * BQ, row0 - s[1] - (s[3] - s[2]) - b * BQ, have, 0);
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(smem_u32(&B.edges[st]));
-              mbar_arrive(smem_u32(&B.full[st]));
-            }
-            if (have < BQ) {
-              if (!(ok = wait(bar, raws))) break;
-              ++raws;
-              zero_rows(q, 2 * D / 64, have, lane);
+              for (int i = 0; i < 4; ++i) v[i] = lane + 32 * i < have ? __ldcg(from + lane + 32 * i) : 0.0f;
+              if (!(ok = wait(m ? &B.do_empty[st] : &B.q_empty[st], t / STAGES + 1))) break;
+              uint8_t* tile_at = smem + L::QD + (st * 2 + m) * L::TILE;
+              uint64_t* full = m ? &B.do_full[st] : &B.q_full[st];
+              uint64_t* bar = have == BQ ? full : &B.raw;
+              if (lane == 0) {
+                mbar_arrive_expect_tx(smem_u32(bar), L::TILE);
+                load_tile<D>(smem_u32(tile_at), m ? &tm_do : &tm_qkv, h * D, y, smem_u32(bar));
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(smem + L::STATS + (st * 2 + m) * L::STEP + step_offset(lane + 32 * i)) = in_three(v[i]);
               fence_proxy_async_smem();
+              // column c of the block sees key row r if min(x, y + r) <= c < z
+              if (m == 0 && lane == 0)
+                *reinterpret_cast<int4*>(smem + L::EDGES + st * 16) =
+                    make_int4(s[4] - b * BQ, row0 - s[1] - (s[3] - s[2]) - b * BQ, have, 0);
               __syncwarp();
-              if (lane == 0) mbar_arrive(smem_u32(&B.full[st]));
+              if (lane == 0) {
+                if (m == 0) mbar_arrive(smem_u32(&B.edges[st]));
+                mbar_arrive(smem_u32(full));
+              }
+              if (have < BQ) {
+                if (!(ok = wait(bar, raws))) break;
+                ++raws;
+                zero_rows(tile_at, D / 64, have, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(full));
+              }
             }
+            if (!ok) break;
           }
         }
       }
@@ -690,11 +717,13 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
     if (lane == 0) {
       if (n > 0) drained(smem_u32(&B.k_full), uint32_t(n - 1) & 1u), drained(smem_u32(&B.v_full), uint32_t(n - 1) & 1u);
       for (int j = t - STAGES > 0 ? t - STAGES : 0; j < t; ++j)
-        drained(smem_u32(&B.full[j % STAGES]), uint32_t(j / STAGES) & 1u);
+        drained(smem_u32(&B.q_full[j % STAGES]), uint32_t(j / STAGES) & 1u),
+            drained(smem_u32(&B.do_full[j % STAGES]), uint32_t(j / STAGES) & 1u);
       if (!ok) {
         drained(smem_u32(&B.k_full), uint32_t(n) & 1u);
         drained(smem_u32(&B.raw), uint32_t(raws) & 1u);
-        drained(smem_u32(&B.full[t % STAGES]), uint32_t(t / STAGES) & 1u);
+        drained(smem_u32(&B.q_full[t % STAGES]), uint32_t(t / STAGES) & 1u);
+        drained(smem_u32(&B.do_full[t % STAGES]), uint32_t(t / STAGES) & 1u);
       }
     }
   } else if (warp == 1) {
@@ -704,7 +733,7 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
     const uint64_t ones = desc_step(smem_u32(smem + L::ONES));
     auto tiles = [&](int t) { return smem_u32(smem + L::QD + t % STAGES * 2 * L::TILE); };
     auto form_s = [&](int t) {
-      if (!wait(&B.full[t % STAGES], t / STAGES)) return false;
+      if (!wait(&B.q_full[t % STAGES], t / STAGES)) return false;
       if (t > 0 && !wait(&B.dv_done, t - 1)) return false;  // P' of the block before has been read
       tc_fence_after();
       product_nt<D>(on, tmem + L::S, ks, desc_low(tiles(t)));
@@ -713,6 +742,7 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
       return true;
     };
     auto form_dp = [&](int t) {
+      if (!wait(&B.do_full[t % STAGES], t / STAGES)) return false;
       if (t > 0 && !wait(&B.dk_done, t - 1)) return false;  // dS' of the block before has been read
       tc_fence_after();
       product_nt<D>(on, tmem + L::DP, vs, desc_low(tiles(t) + L::TILE));
@@ -742,13 +772,14 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
         tc_fence_after();
         product_ta<D>(on, tmem + L::DV, tmem + L::S, desc_low_mn(tiles(t) + L::TILE), t > from);
         mma_commit_on(on, smem_u32(&B.dv_done));
+        mma_commit_on(on, smem_u32(&B.do_empty[t % STAGES]));
         if (t + 1 < to && !(ok = form_s(t + 1))) break;
         if (t + 2 == to) mma_commit_on(on, smem_u32(&B.k_free));
         if (!(ok = wait(&B.ds_full, t))) break;
         tc_fence_after();
         product_ta<D>(on, tmem + L::DK, tmem + L::DP, desc_low_mn(tiles(t)), t > from);
         mma_commit_on(on, smem_u32(&B.dk_done));
-        mma_commit_on(on, smem_u32(&B.empty[t % STAGES]));
+        mma_commit_on(on, smem_u32(&B.q_empty[t % STAGES]));
         if (t + 1 < to && !(ok = form_dp(t + 1))) break;
         if (t + 2 == to) mma_commit_on(on, smem_u32(&B.v_free));
       }
@@ -761,6 +792,34 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
     const int part = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane, cb = 32 * part;
     const uint32_t at = tmem + (uint32_t(quarter * 32) << 16);
     const unsigned long long c2 = f2_pack(a.c, a.c);
+    // A share's sums are sent when its blocks are done, and said to be there after the next piece's first block: by then they have
+    // arrived (a fence at once took 3000 cycles). The share that comes last adds them up.
+    int sent_rest = -1, sent_row0 = 0, sent_rows = 0, met = 0;
+    auto meet = [&]() {  // of the warps that compute; like every wait it gives up
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&B.meet));
+      return wait(&B.meet, met++);
+    };
+    auto publish = [&]() {
+      if (sent_rest < 0) return true;
+      __threadfence();
+      if (!meet()) return false;  // all warps' sums are there, and *ended of the piece before has been read
+      if (warp == 2 && lane == 0) {
+        *ended = atomicAdd(a.work.ended + sent_rest, 1);
+        __threadfence();
+      }
+      if (!meet()) return false;
+      if (*ended == a.shares - 1) {
+        __threadfence();
+        float* sums = a.sums + int64_t(sent_rest) * a.shares * (2 * 128 * D);
+        const int g = sent_rest % a.Hkv;
+        if (a.shares == 8) add_shares<D, 8>(sums, at, true, part, row, sent_row0, sent_rows, g, a);
+        else if (a.shares == 4) add_shares<D, 4>(sums, at, true, part, row, sent_row0, sent_rows, g, a);
+        else add_shares<D, 2>(sums, at, true, part, row, sent_row0, sent_rows, g, a);
+      }
+      sent_rest = -1;
+      return true;
+    };
     bool ok = true;
     int t = 0;  // blocks so far
     for (int n = 0; ok; ++n) {
@@ -817,53 +876,33 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&B.ds_full));
+        if (!(ok = publish())) break;
       }
       if (!ok) break;
       // The last dK is done, and with it all before it. (The next tile's dV and dK are formed after these warps' next P' and dS'.)
       const bool any = info.x > 0;
       if (any && !(ok = wait(&B.dk_done, t - 1))) break;
       tc_fence_after();
-      const int rest = info.y, share = info.z, g = rest % a.Hkv;
-      float* sums = a.sums + int64_t(rest) * a.shares * (2 * 128 * D);
-      // The share that comes last adds them up and need not send its own; where two come at once, both send, and one adds.
-      bool mine = a.shares == 1;
-      if (!mine) {
-        named_bar_sync(1, 32 * COMPUTE_WARPS);  // *ended of the tile before has been read
-        if (warp == 2 && lane == 0) {
-          *ended = atomicAdd(a.work.ended + rest, 0);
-          __threadfence();
-        }
-        named_bar_sync(1, 32 * COMPUTE_WARPS);
-        mine = *ended == a.shares - 1;
-        if (!mine) {
-          float* to = sums + share * (2 * 128 * D);
+      if (a.shares == 1) {
+        add_shares<D, 1>(nullptr, at, any, part, row, tile.x, tile.y, info.y % a.Hkv, a);
+      } else {
+        if (!(ok = publish())) break;  // the piece before's, where this one had no block
+        float* to = a.sums + (int64_t(info.y) * a.shares + info.z) * (2 * 128 * D);
 #pragma unroll 1
-          for (int m = 0; m < 2; ++m) {
-            float v[D / 4] = {};
-            if (any) ld_columns(at + (m ? L::DK : L::DV) + part * (D / 4), v);
+        for (int m = 0; m < 2; ++m) {
+          float v[D / 4] = {};
+          if (any) ld_columns(at + (m ? L::DK : L::DV) + part * (D / 4), v);
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-              __stcg(sums_at<D>(to, m, part * (D / 16) + i, row), make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
-          }
-          __threadfence();
-          named_bar_sync(1, 32 * COMPUTE_WARPS);
-          if (warp == 2 && lane == 0) {
-            *ended = atomicAdd(a.work.ended + rest, 1);
-            __threadfence();
-          }
-          named_bar_sync(1, 32 * COMPUTE_WARPS);
-          mine = *ended == a.shares - 1;
+          for (int i = 0; i < D / 16; ++i)
+            __stcg(sums_at<D>(to, m, part * (D / 16) + i, row), make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
         }
-      }
-      if (mine) {
-        __threadfence();
-        if (a.shares == 8) add_shares<D, 8>(sums, at, any, share, part, row, tile, g, a);
-        else if (a.shares == 4) add_shares<D, 4>(sums, at, any, share, part, row, tile, g, a);
-        else if (a.shares == 2) add_shares<D, 2>(sums, at, any, share, part, row, tile, g, a);
-        else add_shares<D, 1>(sums, at, any, share, part, row, tile, g, a);
+        sent_rest = info.y;
+        sent_row0 = tile.x;
+        sent_rows = tile.y;
       }
       tc_fence_before();  // dV and dK have been read: the next P' and dS' say so
     }
+    if (ok) publish();
   }
   return past;
 }
@@ -1089,16 +1128,15 @@ __device__ __forceinline__ void dq_phase(const CUtensorMap& tm_qkv, const CUtens
       float v[D / 4];
       ld_columns(at + L::DQ + part * (D / 4), v);
       tc_fence_before();  // dQ has been read: the next item's first dS says so
-      if (valid) {
-        uint4* to = reinterpret_cast<uint4*>(a.dqkv + (sq.x + i) * N + h * D + part * (D / 4));
+      uint4 o[D / 32];
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = cvt_bf2(__fmul_rn(v[8 * k + 2 * e], a.scale), __fmul_rn(v[8 * k + 2 * e + 1], a.scale));
-          to[k] = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-      }
+      for (int k = 0; k < D / 32; ++k)
+        o[k] = make_uint4(cvt_bf2(__fmul_rn(v[8 * k], a.scale), __fmul_rn(v[8 * k + 1], a.scale)),
+                          cvt_bf2(__fmul_rn(v[8 * k + 2], a.scale), __fmul_rn(v[8 * k + 3], a.scale)),
+                          cvt_bf2(__fmul_rn(v[8 * k + 4], a.scale), __fmul_rn(v[8 * k + 5], a.scale)),
+                          cvt_bf2(__fmul_rn(v[8 * k + 6], a.scale), __fmul_rn(v[8 * k + 7], a.scale)));
+      const int r0 = it.y + quarter * 32;  // the warp's first query
+      write_rows<D / 32>(a.dqkv + (sq.x + r0) * N + h * D + part * (D / 4), N, sq.z - r0, lane, o);
     }
   }
 }
@@ -1131,10 +1169,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                         &sh.kv.dv_done, &sh.kv.dk_done, &sh.kv.drain, &sh.q.q_full, &sh.q.q_free, &sh.q.raw, &sh.q.s_full[0],
                         &sh.q.s_full[1], &sh.q.dp_full, &sh.q.dq_done, &sh.q.drain})
       init(*b, 1);
-    for (uint64_t* b : {&sh.kv.p_full, &sh.kv.ds_full, &sh.q.ds_full}) init(*b, COMPUTE_WARPS);
+    for (uint64_t* b : {&sh.kv.p_full, &sh.kv.ds_full, &sh.kv.meet, &sh.q.ds_full}) init(*b, COMPUTE_WARPS);
     for (int i = 0; i < 4; ++i) {
-      init(sh.kv.full[i], 2);  // the tiles, and the stats
-      for (uint64_t* b : {&sh.kv.empty[i], &sh.kv.edges[i], &sh.q.k_full[i], &sh.q.k_empty[i], &sh.q.v_full[i], &sh.q.v_empty[i]})
+      for (uint64_t* b : {&sh.kv.q_full[i], &sh.kv.do_full[i]}) init(*b, 2);  // the tile, and its stats
+      for (uint64_t* b : {&sh.kv.q_empty[i], &sh.kv.do_empty[i], &sh.kv.edges[i], &sh.q.k_full[i], &sh.q.k_empty[i], &sh.q.v_full[i], &sh.q.v_empty[i]})
         init(*b, 1);
     }
     for (int i = 0; i < 2; ++i) {
