@@ -14,7 +14,7 @@
 //
 //   stats_kernel  -delta and -lse / scale of every row and head, [Hq][T] (reads dout and out once); its first CTA makes the
 //                 lists of work.
-//   grad_kernel   first the CTAs of dK and dV, one per (tile of keys, KV head, share of its blocks). The borders of the
+//   grad_kernel   first the CTAs of dK and dV, one per (tile of keys, KV head, share of the blocks). The borders of the
 //                 sequences' key ranges cut the pack's rows into runs that the same sequences see, and a tile is 128 rows of a
 //                 run or what is left of it. So nothing that a sequence holds reaches the sums of rows that are not its keys, as
 //                 it would through 0 NaN in a tile of two sequences. Over the sequences that see these rows, the group's heads
@@ -60,9 +60,10 @@ struct alignas(16) Item {
 // Lists in the workspace, made by stats_kernel's first CTA.
 struct Work {
   int4* tiles;    // (first row, rows, first and last sequence that may see them), ascending
+  int4* parts;    // of dK's and dV's CTAs: (tile, share, shares, the tile's first part)
   Item* items;    // of dQ's CTAs
   int32_t* ended; // [tile][Hkv] shares whose sums are there
-  int32_t* counts;  // tiles, items, the next piece of work to be drawn
+  int32_t* counts;  // parts, items, the next piece of work to be drawn
   // scratch: changes of the number of sequences that see a row, at each row; borders, a bit a row; the borders in order
   int32_t* change;
   uint32_t* border;
@@ -73,9 +74,8 @@ struct Work {
 struct Args {
   const int32_t* seqs;  // [n_seq][5]
   int n_seq, T, Hq, Hkv;
-  int shares;           // CTAs of a tile and KV head, a power of two
   Work work;
-  float* sums;          // [tile][Hkv][shares][dV, dK][D / 4][128 rows][4]
+  float* sums;          // [part][Hkv][dV, dK][D / 4][128 rows][4]
   float c, scale;
   const float* nlse;    // [Hq][T] -lse / scale
   const float* ndelta;  // [Hq][T] -delta
@@ -97,11 +97,30 @@ struct StatsArgs {
   float* ndelta;
   const int32_t* seqs;
   int n_seq;
+  int most_shares;
   Work work;
   uint32_t* err;
 };
 
 constexpr int STATS_THREADS = 256;
+
+// Query blocks [first, end) of a sequence that see a key of the tile from row `row` on: causal query i sees keys up to nk - nq + i.
+__device__ __forceinline__ void query_blocks(const int (&s)[5], int row, int& first, int& end) {
+  const int off = s[3] - s[2], j = row - s[1];
+  const int i = s[4] < j - off ? s[4] : j - off;
+  first = i > 0 ? i / BQ : 0;
+  end = (s[2] + BQ - 1) / BQ;
+}
+
+// How many CTAs share a tile's blocks, a power of two: as many as give the longest of the sequences that see it about 192 pieces of
+// work, if a piece keeps eight blocks. Sums that are cut cost about four blocks a piece to send and to add up. A rule on the tile's
+// own sequences and the heads alone, as it sets the order of the sums.
+__device__ __forceinline__ int shares_of(int64_t blocks, int keys, int Hkv, int most) {
+  const int pieces = (keys + BK - 1) / BK * Hkv;
+  int s = 1;
+  while (s < most && pieces * s < 192 && blocks >= 16 * s) s *= 2;
+  return s;
+}
 
 // Sum over the CTA's threads before this one; `total` is the whole sum.
 __device__ __forceinline__ int scan_before(int x, int* room, int& total) {
@@ -123,6 +142,36 @@ __device__ __forceinline__ int scan_before(int x, int* room, int& total) {
     total += room[w];
   }
   return before + incl - x;
+}
+
+// Shares the tiles out; returns the number of parts. `seq` gives a sequence's descriptor, or false for a bad one.
+template <typename Seq>
+__device__ int make_parts(const StatsArgs& a, int* room, int tiles, const Seq& seq) {
+  const Work& w = a.work;
+  __syncthreads();  // the tiles are there
+  int parts = 0;
+  for (int i0 = 0; i0 < tiles; i0 += STATS_THREADS) {
+    const int i = i0 + threadIdx.x;
+    int shares = 0;
+    if (i < tiles) {
+      const int4 tile = __ldcg(w.tiles + i);
+      int64_t blocks = 0;
+      int keys = 0, d[5];
+      for (int s = tile.z; s <= tile.w; ++s) {
+        if (!seq(s, d) || d[1] > tile.x || d[1] + d[3] <= tile.x) continue;
+        int first, end;
+        query_blocks(d, tile.x, first, end);
+        blocks += (end > first ? end - first : 0) * int64_t(a.Hq / a.Hkv);
+        keys = keys > d[3] ? keys : d[3];
+      }
+      shares = shares_of(blocks, keys, a.Hkv, a.most_shares);
+    }
+    int total;
+    const int at = parts + scan_before(shares, room, total);
+    for (int p = 0; p < shares; ++p) w.parts[at + p] = make_int4(i, p, shares, at);
+    parts += total;
+  }
+  return parts;
 }
 
 // The lists of work of up to kSortedSeqs sequences, in shared memory. The items come heaviest first: the last run of queries of
@@ -190,6 +239,12 @@ __device__ void make_work_few(const StatsArgs& a, FewRoom& s) {
     const int row = from + r * BK;
     w.tiles[t0 + r] = make_int4(row, to - row < BK ? to - row : BK, lo, hi);
   }
+  auto seq = [&](int i, int (&d)[5]) {
+#pragma unroll
+    for (int k = 0; k < 5; ++k) d[k] = s.d[i][k];
+    return d[3] > 0;
+  };
+  const int parts = make_parts(a, s.scan, tiles, seq);
   int items = 0;
   for (int r = tid / kSortedSeqs; r < s.items[c]; r += STATS_THREADS / kSortedSeqs) {
     int before = 0;
@@ -203,7 +258,7 @@ __device__ void make_work_few(const StatsArgs& a, FewRoom& s) {
   }
   if (tid == 0) {
     for (int i = 0; i < a.n_seq; ++i) items += s.items[i];  // at most 2^6 2^17
-    w.counts[0] = tiles;
+    w.counts[0] = parts;
     w.counts[1] = items < w.max_items ? items : w.max_items;
     w.counts[2] = 0;
   }
@@ -299,8 +354,13 @@ __device__ void make_work(const StatsArgs& a, int* room) {
       atomicMax(&w.tiles[i].w, s);
     }
   }
+  auto seq = [&](int s, int (&d)[5]) {
+    for (int k = 0; k < 5; ++k) d[k] = a.seqs[5 * int64_t(s) + k];
+    return !bad_seq(d, a.T);
+  };
+  const int parts = make_parts(a, room, tiles, seq);
   if (tid == 0) {
-    w.counts[0] = tiles;
+    w.counts[0] = parts;
     w.counts[1] = items;
     w.counts[2] = 0;
   }
@@ -400,14 +460,6 @@ __device__ __forceinline__ int blocks_of_share(int share, int first, int end, in
     n += b0 < end ? (end - 1 - b0) / shares + 1 : 0;
   }
   return n;
-}
-
-// Query blocks [first, end) of a sequence that see a key of the tile from row `row` on: causal query i sees keys up to nk - nq + i.
-__device__ __forceinline__ void query_blocks(const int (&s)[5], int row, int& first, int& end) {
-  const int off = s[3] - s[2], j = row - s[1];
-  const int i = s[4] < j - off ? s[4] : j - off;
-  first = i > 0 ? i / BQ : 0;
-  end = (s[2] + BQ - 1) / BQ;
 }
 
 // Zeroes rows [from, 128) of `tiles` swizzled [128 x 64] tiles that follow one another (a row is 128 consecutive bytes).
@@ -510,6 +562,7 @@ __device__ __forceinline__ void ld_columns(uint32_t taddr, float (&v)[16]) { tme
 struct Drawn {
   int4 info[2];  // of the two rings' places: what the work is
   int4 more[2];
+  int first[2];
 };
 
 // Warps that wait for a piece of work: those that issue products and those that compute.
@@ -565,7 +618,6 @@ template <int D, int SHARES>
 __device__ __forceinline__ void add_shares(float* sums, uint32_t at, bool any, int part, int row, int row0, int rows, int g,
                                            const Args& a) {
   using L = KvLayout<D>;
-  constexpr int Q = SHARES == 8 ? 2 : 4;  // pieces of four columns whose reads are under way at once
   const int64_t N = int64_t(a.Hq + 2 * a.Hkv) * D;
   const int lane = row & 31, base = row - lane;  // the warp's first row
 #pragma unroll 1
@@ -577,23 +629,19 @@ __device__ __forceinline__ void add_shares(float* sums, uint32_t at, bool any, i
       if constexpr (SHARES == 1) {
         if (any) tmem_ld16(at + (m ? L::DK : L::DV) + c0, v);
       } else {
+        float4 u[SHARES][4];  // all reads under way at once
 #pragma unroll
-        for (int q0 = 0; q0 < 4; q0 += Q) {
-          float4 u[SHARES][Q];
+        for (int p = 0; p < SHARES; ++p)
 #pragma unroll
-          for (int p = 0; p < SHARES; ++p)
+          for (int q = 0; q < 4; ++q) u[p][q] = __ldcg(sums_at<D>(sums + p * int64_t(a.Hkv) * (2 * 128 * D), m, c0 / 4 + q, row));
 #pragma unroll
-            for (int q = 0; q < Q; ++q) u[p][q] = __ldcg(sums_at<D>(sums + p * (2 * 128 * D), m, c0 / 4 + q0 + q, row));
+        for (int q = 0; q < 4; ++q) {
+          float4 s = u[0][q];
 #pragma unroll
-          for (int q = 0; q < Q; ++q) {
-            float4 s = u[0][q];
-#pragma unroll
-            for (int p = 1; p < SHARES; ++p)
-              s = make_float4(__fadd_rn(s.x, u[p][q].x), __fadd_rn(s.y, u[p][q].y), __fadd_rn(s.z, u[p][q].z),
-                              __fadd_rn(s.w, u[p][q].w));
-            const int k = 4 * (q0 + q);
-            v[k] = s.x, v[k + 1] = s.y, v[k + 2] = s.z, v[k + 3] = s.w;
-          }
+          for (int p = 1; p < SHARES; ++p)
+            s = make_float4(__fadd_rn(s.x, u[p][q].x), __fadd_rn(s.y, u[p][q].y), __fadd_rn(s.z, u[p][q].z),
+                            __fadd_rn(s.w, u[p][q].w));
+          v[4 * q] = s.x, v[4 * q + 1] = s.y, v[4 * q + 2] = s.z, v[4 * q + 3] = s.w;
         }
       }
       const float f = m ? a.scale : 1.0f;
@@ -636,18 +684,21 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
         }
         break;
       }
-      const int share = w & (a.shares - 1), rest = w / a.shares, g = rest % a.Hkv;
-      const int4 tile = __ldcg(a.work.tiles + rest / a.Hkv);
+      const int g = w % a.Hkv;
+      const int4 part = __ldcg(a.work.parts + w / a.Hkv);
+      const int share = part.y, shares = part.z;
+      const int4 tile = __ldcg(a.work.tiles + part.x);
       const int row0 = tile.x;
       SeqIter count(a, tile, lane);
       int s[5], blocks = 0;
       while (count.next(s)) {
         int first, end;
         query_blocks(s, row0, first, end);
-        blocks += blocks_of_share(share, first, end, G, a.shares);
+        blocks += blocks_of_share(share, first, end, G, shares);
       }
       if (lane == 0) {
-        drawn.info[n & 1] = make_int4(blocks, rest, share, 0);
+        drawn.info[n & 1] = make_int4(blocks, part.x * a.Hkv + g, shares, w);
+        drawn.first[n & 1] = part.w * a.Hkv + g;
         drawn.more[n & 1] = tile;
         mbar_arrive(smem_u32(&B.drawn[n & 1]));
       }
@@ -668,7 +719,7 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
         query_blocks(s, row0, first, end);
         for (int hh = 0; hh < G && ok; ++hh) {
           const int h = g * G + hh;
-          for (int b = first + ((share - first - hh) & (a.shares - 1)); b < end; b += a.shares, ++t) {
+          for (int b = first + ((share - first - hh) & (shares - 1)); b < end; b += shares, ++t) {
             const int st = t % STAGES, y = s[0] + b * BQ, have = s[2] - b * BQ < BQ ? s[2] - b * BQ : BQ;
             // dO before Q: its place is free when dV is done, Q's when dK is, and S' wants Q first
 #pragma unroll
@@ -794,30 +845,29 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
     const unsigned long long c2 = f2_pack(a.c, a.c);
     // A share's sums are sent when its blocks are done, and said to be there after the next piece's first block: by then they have
     // arrived (a fence at once took 3000 cycles). The share that comes last adds them up.
-    int sent_rest = -1, sent_row0 = 0, sent_rows = 0, met = 0;
+    int sent = -1, sent_shares = 0, sent_first = 0, sent_row0 = 0, sent_rows = 0, met = 0;
     auto meet = [&]() {  // of the warps that compute; like every wait it gives up
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&B.meet));
       return wait(&B.meet, met++);
     };
     auto publish = [&]() {
-      if (sent_rest < 0) return true;
+      if (sent < 0) return true;
       __threadfence();
       if (!meet()) return false;  // all warps' sums are there, and *ended of the piece before has been read
       if (warp == 2 && lane == 0) {
-        *ended = atomicAdd(a.work.ended + sent_rest, 1);
+        *ended = atomicAdd(a.work.ended + sent, 1);
         __threadfence();
       }
       if (!meet()) return false;
-      if (*ended == a.shares - 1) {
+      if (*ended == sent_shares - 1) {
         __threadfence();
-        float* sums = a.sums + int64_t(sent_rest) * a.shares * (2 * 128 * D);
-        const int g = sent_rest % a.Hkv;
-        if (a.shares == 8) add_shares<D, 8>(sums, at, true, part, row, sent_row0, sent_rows, g, a);
-        else if (a.shares == 4) add_shares<D, 4>(sums, at, true, part, row, sent_row0, sent_rows, g, a);
+        float* sums = a.sums + int64_t(sent_first) * (2 * 128 * D);
+        const int g = sent % a.Hkv;
+        if (sent_shares == 4) add_shares<D, 4>(sums, at, true, part, row, sent_row0, sent_rows, g, a);
         else add_shares<D, 2>(sums, at, true, part, row, sent_row0, sent_rows, g, a);
       }
-      sent_rest = -1;
+      sent = -1;
       return true;
     };
     bool ok = true;
@@ -825,6 +875,7 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
     for (int n = 0; ok; ++n) {
       if (!(ok = wait(&B.drawn[n & 1], n >> 1))) break;
       const int4 info = drawn.info[n & 1], tile = drawn.more[n & 1];
+      const int first = drawn.first[n & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&B.taken[n & 1]));
       if (info.x < 0) break;
@@ -883,11 +934,11 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
       const bool any = info.x > 0;
       if (any && !(ok = wait(&B.dk_done, t - 1))) break;
       tc_fence_after();
-      if (a.shares == 1) {
+      if (info.z == 1) {
         add_shares<D, 1>(nullptr, at, any, part, row, tile.x, tile.y, info.y % a.Hkv, a);
       } else {
         if (!(ok = publish())) break;  // the piece before's, where this one had no block
-        float* to = a.sums + (int64_t(info.y) * a.shares + info.z) * (2 * 128 * D);
+        float* to = a.sums + int64_t(info.w) * (2 * 128 * D);
 #pragma unroll 1
         for (int m = 0; m < 2; ++m) {
           float v[D / 4] = {};
@@ -896,7 +947,9 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
           for (int i = 0; i < D / 16; ++i)
             __stcg(sums_at<D>(to, m, part * (D / 16) + i, row), make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
         }
-        sent_rest = info.y;
+        sent = info.y;
+        sent_shares = info.z;
+        sent_first = first;
         sent_row0 = tile.x;
         sent_rows = tile.y;
       }
@@ -1199,7 +1252,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const Waits wait{&sh.abort_flag, a.err};
-  const int n_kv = __ldcg(a.work.counts) * a.Hkv * a.shares, n_q = __ldcg(a.work.counts + 1) * a.Hq;
+  const int n_kv = __ldcg(a.work.counts) * a.Hkv, n_q = __ldcg(a.work.counts + 1) * a.Hq;
   const int first = dkv_phase<D>(tm_qkv, tm_do, a, smem, sh.kv, sh.drawn[0], &sh.ended, tmem, n_kv, wait);
   tc_fence_before();
   fence_proxy_async_smem();  // what was written to the tiles comes before the second phase's copies
@@ -1220,17 +1273,17 @@ inline bool shape_ok(int64_t T, int Hq, int Hkv, int D, int n_seq) {
          Hq % Hkv == 0 && n_seq >= 1 && n_seq <= MOT_MAX_TOKENS;
 }
 
-// CTAs that share a tile and KV head, a power of two: a rule on the group alone, as it sets the order of the sums.
-inline int shares_of(int G) { return G >= 8 ? 8 : G >= 4 ? 4 : G >= 2 ? 2 : 1; }
+// The most CTAs that share a tile: with one query head a KV head (or two) there are as many tiles and KV heads for fewer blocks.
+inline int most_shares(int G) { return G >= 4 ? 4 : G >= 2 ? 2 : 1; }
 
 constexpr int64_t kMostWork = 1 << 30;  // pieces of work: drawn as 32-bit numbers, some past the last
 
 // The workspace after its header, in bytes.
 struct Room {
-  int64_t nlse, ndelta, tiles, items, counts, ended, change, border, runs, sums, end, ctas;
+  int64_t nlse, ndelta, tiles, parts, items, counts, ended, change, border, runs, sums, end, ctas;
   int max_tiles, max_items;
   Room(int64_t T, int Hq, int Hkv, int D, int64_t n_seq) {
-    const int shares = shares_of(Hq / Hkv);
+    const int64_t most = most_shares(Hq / Hkv);
     auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
     const int64_t borders = 2 * n_seq < T + 1 ? 2 * n_seq : T + 1, blocks = (T + 127) / 128;
     max_tiles = int(blocks + borders < T ? blocks + borders : T);  // a run adds at most one short tile
@@ -1238,15 +1291,16 @@ struct Room {
     nlse = 0;
     ndelta = nlse + up(T * Hq * 4);
     tiles = ndelta + up(T * Hq * 4);
-    items = tiles + int64_t(max_tiles) * 16;
+    parts = tiles + int64_t(max_tiles) * 16;
+    items = parts + int64_t(max_tiles) * most * 16;
     counts = items + int64_t(max_items) * 32;
     ended = counts + 16;
     change = ended + up(int64_t(max_tiles) * Hkv * 4);
     border = change + up((T + 1) * 4);
     runs = border + up((T / 32 + 1) * 4);
     sums = runs + up(borders * 4);
-    end = sums + int64_t(max_tiles) * Hkv * shares * (2 * 128 * D * 4);
-    ctas = int64_t(max_tiles) * Hkv * shares + int64_t(max_items) * Hq;
+    end = sums + (most > 1 ? int64_t(max_tiles) * Hkv * most * (2 * 128 * D * 4) : 0);
+    ctas = int64_t(max_tiles) * Hkv * most + int64_t(max_items) * Hq;
   }
 };
 
@@ -1277,6 +1331,7 @@ static int launch(const uint16_t* dout, const uint16_t* qkv, const uint16_t* out
   st.seqs = a.seqs;
   st.n_seq = a.n_seq;
   st.work = a.work;
+  st.most_shares = most_shares(a.Hq / a.Hkv);
   st.err = a.err;
   stats_kernel<D><<<dim3(unsigned((a.T + STATS_ROWS - 1) / STATS_ROWS + 1), unsigned((a.Hq + 31) / 32)), STATS_THREADS, 0, s>>>(st);
   if (cudaGetLastError() != cudaSuccess) return MOT_ERR_CUDA;
@@ -1324,12 +1379,12 @@ extern "C" int mot_joint_attention_backward(const mot_bf16* dout, const mot_bf16
   a.T = int(T);
   a.Hq = Hq;
   a.Hkv = Hkv;
-  a.shares = attnb::shares_of(Hq / Hkv);
   a.c = c;
   a.scale = scale;
   a.nlse = reinterpret_cast<float*>(base + room.nlse);
   a.ndelta = reinterpret_cast<float*>(base + room.ndelta);
   a.work.tiles = reinterpret_cast<int4*>(base + room.tiles);
+  a.work.parts = reinterpret_cast<int4*>(base + room.parts);
   a.work.items = reinterpret_cast<attnb::Item*>(base + room.items);
   a.work.counts = reinterpret_cast<int32_t*>(base + room.counts);
   a.work.ended = reinterpret_cast<int32_t*>(base + room.ended);
