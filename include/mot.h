@@ -32,8 +32,9 @@
  *     Outputs are defined only when both are clean.
  *   - Numerics ([RFC-435] §3): fixed fp32 accumulation and reduction order, no split-K,
  *     stream-K or atomics in any reduction, no TF32 or fast math, round-to-nearest-even
- *     casts only at the points each entry point declares. (mot_paged_decode_attention alone cuts
- *     a long sum, over a row's keys: at borders of the row's own, joined in a fixed order.)
+ *     casts only at the points each entry point declares. (mot_paged_decode_attention cuts a long
+ *     sum, over a row's keys, and mot_joint_attention_backward one over the queries that see a
+ *     tile of keys: at borders that their own sequences set, joined in a fixed order.)
  */
 #ifndef MOT_H
 #define MOT_H
@@ -349,9 +350,11 @@ size_t mot_joint_attention_backward_workspace_bytes(int64_t T, int Hq, int Hkv, 
  * delta_i = sum of dout_i out_i over the head's columns, dS = P (dP - delta_i); then dq_i = scale sum_j
  * dS k_j, dk_j = scale sum dS q_i and dv_j = sum P dout_i over the sequences, query heads of the group
  * and queries that see j. S, dP and the three sums in fp32 on the tensor cores; P and dS are formed in
- * fp32 and enter their products as bf16; one cast. The order of every sum is fixed by the row's own
- * sequences, the head geometry and the order of seqs: a row's bits do not depend on the other sequences
- * of the pack or on where its rows lie. Rows of other sequences, whatever they hold, add nothing; a NaN
+ * fp32 and enter their products as bf16; one cast. For dk and dv, lse / scale and delta are subtracted in the
+ * products' own sums, as three bf16 each (24 bits). dk and dv of up to 128 neighbouring keys are summed in one,
+ * two or four shares of the queries and heads (by how many see them), joined in order. The order of every sum is
+ * fixed by the sequences that share a key with the row's own, the head geometry and the order of seqs: a row's
+ * bits do not depend on the pack's other sequences or on where its rows lie. Rows of other sequences, whatever they hold, add nothing; a NaN
  * or infinity in a row of a sequence leaves that sequence's gradients undefined. Tensors do not
  * overlap. Geometry as mot_joint_attention; scale log2 e from 2^-100 to 2^100, else MOT_ERR_ARG.
  */

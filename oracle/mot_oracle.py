@@ -947,7 +947,6 @@ def g_flow_noise(seeds, step, N):
     return out
 
 
-
 # ---------------------------------------------------------------------------
 # The training step's other gradients: joint attention, the QK norm and RoPE; and the AdamW update
 # ---------------------------------------------------------------------------
@@ -1013,12 +1012,14 @@ def g_joint_attention_backward(dout, qkv, out, lse, seqs, Hq: int, Hkv: int, D: 
             d[at_q] += sc * ds @ k
             d[at_k] += sc * ds.T @ q
             d[at_v] += p.T @ do
-            # relative error of p before its cast: the score's sum (each of D additions, counted twice for a
-            # rounding that is not to nearest), the roundings of lse / scale and of the two operations on it,
-            # the log2 e in c, and two units of 2^x
-            e_p = (np.abs(q) @ np.abs(k).T * sc) * 2 * D * U32 + (np.abs(s) + np.abs(L)) * 6 * U32 + 6 * U32
-            # of dP and delta, then of their difference and product, times P; and P's own error
-            e_ds = p * ((np.abs(do) @ np.abs(v).T + np.abs(do * o).sum(1)[:, None]) * 2 * D * U32) + np.abs(ds) * (e_p + 4 * U32)
+            # relative error of p before its cast: the score's sum (each of D additions, counted twice for a rounding
+            # that is not to nearest), and lse / scale subtracted in it as three more terms (as much each, of partial
+            # sums up to |s| + |L|: 6 units); 4 more for 1 / scale, lse times it, the log2 e in c, and c times the
+            # difference; two units of 2^x and what is of second order
+            e_p = (np.abs(q) @ np.abs(k).T * sc) * 2 * (D + 3) * U32 + (np.abs(s) + np.abs(L)) * 10 * U32 + 6 * U32
+            # of dP and of delta (D additions each, and delta's three terms in dP's sum), then of their product with P; and
+            # P's own error
+            e_ds = p * ((np.abs(do) @ np.abs(v).T + np.abs(do * o).sum(1)[:, None]) * 2 * (D + 3) * U32) + np.abs(ds) * (e_p + 4 * U32)
             e_ds = e_ds * (1 + U16) + np.abs(ds) * U16
             err[at_q] += sc * e_ds @ np.abs(k)
             err[at_k] += sc * e_ds.T @ np.abs(q)

@@ -230,6 +230,34 @@ def test_many_sequences():
     _check(d, dout, qkv, out, lse, seqs, Hq, Hkv, D)
 
 
+def test_long_sequences_among_many():
+    # a prompt with latents that see its keys and a sequence that sees some of them, alone and beside more sequences than a table in
+    # shared memory holds: the lists of work are made in another way, the bits are the same
+    Hq, Hkv, D, T = 7, 1, 128, 1600
+    few = [(0, 0, 1100, 1100, 900), (1100, 0, 300, 1100, 0), (1400, 200, 50, 333, 20)]
+    many = [(1450 + i, 1450 + i, 1, 1, i % 2) for i in range(100)]
+    qkv, dout = _inputs(T, Hq, Hkv, D, seed=19)
+    s, out, lse = _forward(qkv, few, Hq, Hkv, D)
+    want = _backward(dout, qkv, out, lse, s, Hq, Hkv, D)
+    _check(want, dout, qkv, out, lse, few, Hq, Hkv, D)
+    for seqs in (few + many, many[:40] + few + many[40:], many + few):
+        s, out, lse = _forward(qkv, seqs, Hq, Hkv, D)
+        d = _backward(dout, qkv, out, lse, s, Hq, Hkv, D)
+        assert_bitwise(d[:1450], want[:1450], f"{len(seqs)} sequences")
+        _check(d[1450:, :], dout[1450:], qkv[1450:], out[1450:], lse[:, 1450:], [(q - 1450, k - 1450, *x) for q, k, *x in many],
+               Hq, Hkv, D)
+
+
+@pytest.mark.parametrize("n", [63, 64, 65, 128])
+def test_where_the_table_of_sequences_ends(n):
+    Hq, Hkv, D = 4, 2, 64
+    seqs = [(3 * i, 3 * i, 3, 3, i % 4) for i in range(n)] + [(3 * n, 0, 20, 3 * n, 0)]
+    qkv, dout = _inputs(3 * n + 20, Hq, Hkv, D, seed=n)
+    s, out, lse = _forward(qkv, seqs, Hq, Hkv, D)
+    d = _backward(dout, qkv, out, lse, s, Hq, Hkv, D)
+    _check(d, dout, qkv, out, lse, seqs, Hq, Hkv, D)
+
+
 def test_layer_sampled_rows():
     # a whole layer's pack: sampled rows against the golden of their own (heads of one group)
     Hq, Hkv, D, T = 28, 4, 128, 2500
