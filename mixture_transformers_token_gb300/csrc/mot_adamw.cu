@@ -62,24 +62,24 @@ __device__ __forceinline__ bool load_hyper(const float* row, Hyper& h) {
 __device__ __forceinline__ void update(const Hyper& h, float wl, float (&g)[8], float (&m)[8], float (&v)[8], float (&r)[8],
                                        float (&p)[8]) {
   float a[8], b[8];
-  mul8(g, h.gs, g);
-  mul8(m, h.b1, m);
-  mul8(g, h.c1, a);
+  mul_each(g, h.gs, g);
+  mul_each(m, h.b1, m);
+  mul_each(g, h.c1, a);
 #pragma unroll
   for (int i = 0; i < 8; ++i) m[i] = __fadd_rn(m[i], a[i]);
-  mul8(v, h.b2, v);
-  mul8(g, g, a);
-  mul8(a, h.c2, a);
+  mul_each(v, h.b2, v);
+  mul_each(g, g, a);
+  mul_each(a, h.c2, a);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     v[i] = __fadd_rn(v[i], a[i]);
     r[i] = __fsqrt_rn(v[i]);
   }
-  mul8(r, h.r2, a);
-  mul8(m, h.lr1, b);
+  mul_each(r, h.r2, a);
+  mul_each(m, h.lr1, b);
 #pragma unroll
   for (int i = 0; i < 8; ++i) b[i] = __fdiv_rn(b[i], __fadd_rn(a[i], h.eps));
-  mul8(p, wl, a);
+  mul_each(p, wl, a);
 #pragma unroll
   for (int i = 0; i < 8; ++i) p[i] = __fsub_rn(p[i], __fadd_rn(b[i], a[i]));
 }
@@ -200,7 +200,7 @@ __device__ __forceinline__ void load_codes(const uint8_t* s, int have, float sca
     x[2 * i] = v.x;
     x[2 * i + 1] = v.y;
   }
-  mul8(x, scale, x);
+  mul_each(x, scale, x);
 }
 
 template <bool ALL>
@@ -263,7 +263,7 @@ __device__ __forceinline__ void warp_block(const Table& a, const Hyper& h, const
     const float2 s = *reinterpret_cast<const float2*>(t.scales + 2 * block);
     load_codes<ALL>(static_cast<const uint8_t*>(t.m) + e, have, s.x, m);
     load_codes<ALL>(static_cast<const uint8_t*>(t.v) + e, have, s.y, v);
-    mul8(v, v, v);
+    mul_each(v, v, v);
   } else {
     load8<ALL>(static_cast<const float*>(t.m) + e, have, m);
     load8<ALL>(static_cast<const float*>(t.v) + e, have, v);
@@ -277,8 +277,8 @@ __device__ __forceinline__ void warp_block(const Table& a, const Hyper& h, const
     for (int q = 0; q < 2; ++q) random_words(w[q], uint64_t(e) / 4 + q, uint32_t(id), h.step, a.key);
     // elements past the end are zero
     const Scale sm = block_scale(warp_max(top_of(m))), sr = block_scale(warp_max(top_of(r)));
-    mul8(m, sm.inv, m);
-    mul8(r, sr.inv, r);
+    mul_each(m, sm.inv, m);
+    mul_each(r, sr.inv, r);
     float least = fminf(fabsf(m[0]), r[0]);
 #pragma unroll
     for (int i = 1; i < 8; ++i) least = fminf(least, fminf(fabsf(m[i]), r[i]));

@@ -62,7 +62,7 @@ __device__ __forceinline__ uint32_t cvt_bf2(float lo, float hi) {
   return r;
 }
 
-// Products of eight values two at a time (mul.rn.f32x2: each rounded as the scalar one would be). What they feed are scalar
+// Products of values two at a time (mul.rn.f32x2: each rounded as the scalar one would be). What they feed are scalar
 // additions and further products: a packed addition would be fused with them.
 __device__ __forceinline__ void mul2(float a0, float a1, float b0, float b1, float& o0, float& o1) {
   unsigned long long a, b, o;
@@ -71,13 +71,15 @@ __device__ __forceinline__ void mul2(float a0, float a1, float b0, float b1, flo
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(o) : "l"(a), "l"(b));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(o0), "=f"(o1) : "l"(o));
 }
-__device__ __forceinline__ void mul8(const float (&a)[8], const float (&b)[8], float (&o)[8]) {
+template <int N>
+__device__ __forceinline__ void mul_each(const float (&a)[N], const float (&b)[N], float (&o)[N]) {
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) mul2(a[i], a[i + 1], b[i], b[i + 1], o[i], o[i + 1]);
+  for (int i = 0; i < N; i += 2) mul2(a[i], a[i + 1], b[i], b[i + 1], o[i], o[i + 1]);
 }
-__device__ __forceinline__ void mul8(const float (&a)[8], float b, float (&o)[8]) {
+template <int N>
+__device__ __forceinline__ void mul_each(const float (&a)[N], float b, float (&o)[N]) {
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) mul2(a[i], a[i + 1], b, b, o[i], o[i + 1]);
+  for (int i = 0; i < N; i += 2) mul2(a[i], a[i + 1], b, b, o[i], o[i + 1]);
 }
 
 // ---------------------------------------------------------------------------

@@ -11,10 +11,14 @@
 // in fp32, each operation rounded on its own, the forward's casts differentiated as the identity.
 //
 // A row is read and written once: 2 N + (Hq + Hkv) D values of bf16, its position and its table entries (16.5 us for 4096 rows
-// of 28/4 heads of 128 at the measured copy rate): the bound is memory. D / 16 lanes hold a head, each 8 values and their 8
+// of 28/4 heads of 128 at the measured copy rate): the bound is memory. D / 8 lanes hold a head, each 4 values and their 4
 // partners, so that the rotation needs no exchange. Loads into registers kept too little under way for the memory's latency (two
-// CTAs of 8 warps, the next heads' loads ahead: 36 us on that pack): each of 16 warps has a ring of three slots in shared memory
-// for a row's next heads, their projection and the table entries, filled by bulk copies, 150 KB an SM.
+// CTAs of 8 warps, the next heads' loads ahead: 36 us on that pack): each warp has a ring of slots in shared memory for a row's
+// next heads, their projection and the table entries, filled by bulk copies. 24 warps with two slots, 33.1 us there and 177 us
+// (83% of that rate) for 36001 rows of the FP32 profile; 16 warps with three 35.3 and 192 us, 20 with two 34.4 and 194 us, 32 with
+// slots of half the size 37.5 and 207 us. With D / 16 lanes a head a thread's registers allow 16 warps: 35.7 and 198 us. What is
+// left on the small pack is the start (header, row numbers, positions, first rows: each waits for the one before) and the second
+// kernel: a pack of 64 rows takes 13 us.
 //
 // The weights' gradients: each CTA takes a run of the plan's positions, so that its rows are of one weight set, but for the run
 // that holds the border; a lane adds its columns over the warp's rows, the warps' sums are added in order, and a second kernel,
@@ -29,10 +33,10 @@
 namespace mot {
 namespace qkvb {
 
-constexpr int WARPS = 16, THREADS = 32 * WARPS;
+constexpr int WARPS = 24, THREADS = 32 * WARPS;
 constexpr int kMaxCtas = 152;           // runs of positions: one for each SM
 constexpr int PIECE = 1024;             // values of a slot: the heads of an item
-constexpr int SLOTS = 3;
+constexpr int SLOTS = 2;
 constexpr uint32_t SLOT = 2 * PIECE * 2 + 512 + 16;  // gradient, projection, table entries of a position, the row
 constexpr uint32_t RING = WARPS * SLOTS * SLOT;
 constexpr uint32_t WEIGHTS = RING, BARS = WEIGHTS + 4 * 128 * 4;
@@ -56,33 +60,27 @@ struct Args {
   int ctas;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+// Four of a lane's values.
+__device__ __forceinline__ void unpack4(const uint2& v, float (&x)[4]) {
   x[0] = bf_lo(v.x), x[1] = bf_hi(v.x), x[2] = bf_lo(v.y), x[3] = bf_hi(v.y);
-  x[4] = bf_lo(v.z), x[5] = bf_hi(v.z), x[6] = bf_lo(v.w), x[7] = bf_hi(v.w);
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(cvt_bf2(x[0], x[1]), cvt_bf2(x[2], x[3]), cvt_bf2(x[4], x[5]), cvt_bf2(x[6], x[7]));
-}
+__device__ __forceinline__ uint2 pack4(const float (&x)[4]) { return make_uint2(cvt_bf2(x[0], x[1]), cvt_bf2(x[2], x[3])); }
 
-// cos and sin of the lane's 8 pairs
+// cos and sin of the lane's 4 pairs
 template <bool F32>
-__device__ __forceinline__ void load_table(const void* cs, int64_t pair, float (&c)[8], float (&s)[8]) {
+__device__ __forceinline__ void load_table(const void* cs, int pair, float (&c)[4], float (&s)[4]) {
   if constexpr (F32) {
     const float4* t = reinterpret_cast<const float4*>(static_cast<const float*>(cs) + 2 * pair);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const float4 v = t[i];
       c[2 * i] = v.x, s[2 * i] = v.y, c[2 * i + 1] = v.z, s[2 * i + 1] = v.w;
     }
   } else {
-    const uint4* t = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(cs) + 2 * pair);
+    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(cs) + 2 * pair);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 v = t[i];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) c[4 * i + k] = bf_lo(w[k]), s[4 * i + k] = bf_hi(w[k]);
-    }
+    for (int k = 0; k < 4; ++k) c[k] = bf_lo(w[k]), s[k] = bf_hi(w[k]);
   }
 }
 
@@ -95,7 +93,7 @@ __device__ __forceinline__ float group_sum(float x) {
 
 template <int D, bool F32>
 __global__ void __launch_bounds__(THREADS, 1) qk_norm_rope_bwd_kernel(const Args a) {
-  constexpr int LANES = D / 16, HEADS = 32 / LANES, H2 = D / 2;  // lanes of a head, heads of a warp
+  constexpr int LANES = D / 8, HEADS = 32 / LANES, H2 = D / 2;  // lanes of a head, heads of a warp
   constexpr int ITEM = PIECE / D;                                // heads of an item
   constexpr uint32_t TABLE = D * (F32 ? 4 : 2);                  // bytes of a position's table entries
   extern __shared__ __align__(128) uint8_t smem[];
@@ -105,6 +103,13 @@ __global__ void __launch_bounds__(THREADS, 1) qk_norm_rope_bwd_kernel(const Args
   float* weights = reinterpret_cast<float*>(smem + WEIGHTS);  // [q, k][2][D]
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + BARS) + warp * SLOTS;
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + BARS + 8 * WARPS * SLOTS);
+  const int begin = int(int64_t(a.T) * blockIdx.x / a.ctas), end = int(int64_t(a.T) * (blockIdx.x + 1) / a.ctas);
+  const int32_t* perm = reinterpret_cast<const int32_t*>(a.ws + perm_offset());
+  if (begin + threadIdx.x < end) {  // the first rows' numbers and positions into the caches while the header is read
+    const int row = perm[begin + threadIdx.x];
+    if (row >= 0 && row < a.T) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.pos + row));
+  }
+  const float weight = threadIdx.x < 4 * D ? bf_to_f((threadIdx.x < 2 * D ? a.qw : a.kw)[threadIdx.x % (2 * D)]) : 0.0f;
   const PlanHeader* hdr = reinterpret_cast<const PlanHeader*>(a.ws);
   if (hdr->magic != kPlanMagic || hdr->T != a.T) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, MOT_DEV_PLAN_MISMATCH);
@@ -118,20 +123,19 @@ __global__ void __launch_bounds__(THREADS, 1) qk_norm_rope_bwd_kernel(const Args
     fence_proxy_async_smem();
   }
   if (threadIdx.x == 0) *abort_flag = 0u;
-  if (threadIdx.x < 4 * D) weights[threadIdx.x] = bf_to_f((threadIdx.x < 2 * D ? a.qw : a.kw)[threadIdx.x % (2 * D)]);
+  static_assert(4 * D <= THREADS, "a thread a weight");
+  if (threadIdx.x < 4 * D) weights[threadIdx.x] = weight;
   __syncthreads();
-  const int32_t* perm = reinterpret_cast<const int32_t*>(a.ws + perm_offset());
   const int nqk = a.Hq + a.Hkv, n_heads = nqk + a.Hkv;
   // items of a row: the normed heads, and, where the result is elsewhere, the value heads to copy
   const int normed = (nqk + ITEM - 1) / ITEM, items = normed + (a.dx != a.d ? (a.Hkv + ITEM - 1) / ITEM : 0);
-  const int begin = int(int64_t(a.T) * blockIdx.x / a.ctas), end = int(int64_t(a.T) * (blockIdx.x + 1) / a.ctas);
   int issued = 0, taken = 0;  // of all this warp's items
   bool ok = true;
   for (int e = 0; e < 2; ++e) {
     const int lo = e == 0 ? begin : max(begin, count0), hi = e == 0 ? min(end, count0) : end;
-    float acc[2][2][8] = {};  // [q, k][half][column]
+    float acc[2][2][4] = {};  // [q, k][half][column]
     const int all = hi > lo ? (hi - lo) * items : 0;                 // less than 2^26
-    const int n = all > warp ? (all - warp + WARPS - 1) / WARPS : 0;  // this warp's items: warp, warp + WARPS, ...
+    const int n = ok && all > warp ? (all - warp + WARPS - 1) / WARPS : 0;  // this warp's items: warp, warp + WARPS, ...
     int my_row = 0, my_pos = 0;                                      // of its items that a lane looks up, 32 at once
     int next_item = warp % items, this_item = next_item;             // of the row: the next one to issue, and to take
     auto issue = [&](int j) {
@@ -178,46 +182,41 @@ __global__ void __launch_bounds__(THREADS, 1) qk_norm_rope_bwd_kernel(const Args
         for (int i = lane; i < pieces; i += 32) to[i] = reinterpret_cast<const uint4*>(slot)[i];
         continue;
       }
-      float c[8], sn[8];
-      load_table<F32>(slot + 4 * PIECE, 8 * sub, c, sn);
+      float c[4], sn[4];
+      load_table<F32>(slot + 4 * PIECE, 4 * sub, c, sn);
 #pragma unroll 1
       for (int h0 = item * ITEM; h0 < min((item + 1) * ITEM, nqk); h0 += HEADS) {
-        const int h = h0 + grp, at = (h - item * ITEM) * D + 8 * sub;  // a head past the last reads what was in the slot
+        const int h = h0 + grp, at = (h - item * ITEM) * D + 4 * sub;  // a head past the last reads what was in the slot
         const bool has = h < nqk, key = h >= a.Hq;
-        float d0[8], d1[8], x0[8], x1[8], w0[8], w1[8];
+        float d0[4], d1[4], x0[4], x1[4];
         const uint16_t* ds = reinterpret_cast<const uint16_t*>(slot) + at;
-        unpack8(*reinterpret_cast<const uint4*>(ds), d0);
-        unpack8(*reinterpret_cast<const uint4*>(ds + H2), d1);
-        unpack8(*reinterpret_cast<const uint4*>(ds + PIECE), x0);
-        unpack8(*reinterpret_cast<const uint4*>(ds + PIECE + H2), x1);
-        const float* w = weights + ((key ? 2 : 0) + e) * D + 8 * sub;
-        *reinterpret_cast<float4*>(w0) = *reinterpret_cast<const float4*>(w);
-        *reinterpret_cast<float4*>(w0 + 4) = *reinterpret_cast<const float4*>(w + 4);
-        *reinterpret_cast<float4*>(w1) = *reinterpret_cast<const float4*>(w + H2);
-        *reinterpret_cast<float4*>(w1 + 4) = *reinterpret_cast<const float4*>(w + H2 + 4);
-        float ss = 0.0f, p0[8], p1[8];
-        mul8(x0, x0, p0);
-        mul8(x1, x1, p1);
+        unpack4(*reinterpret_cast<const uint2*>(ds), d0);
+        unpack4(*reinterpret_cast<const uint2*>(ds + H2), d1);
+        unpack4(*reinterpret_cast<const uint2*>(ds + PIECE), x0);
+        unpack4(*reinterpret_cast<const uint2*>(ds + PIECE + H2), x1);
+        float ss = 0.0f, p0[4], p1[4];
+        mul_each(x0, x0, p0);
+        mul_each(x1, x1, p1);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) ss = __fadd_rn(ss, __fadd_rn(p0[k], p1[k]));
+        for (int k = 0; k < 4; ++k) ss = __fadd_rn(ss, __fadd_rn(p0[k], p1[k]));
         const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fmul_rn(group_sum<LANES>(ss), 1.0f / D), a.eps)));
-        float u0[8], u1[8], dot = 0.0f;
-        mul8(d0, c, u0);
-        mul8(d1, sn, p0);
-        mul8(d1, c, u1);
-        mul8(d0, sn, p1);
+        float u0[4], u1[4], dot = 0.0f;
+        mul_each(d0, c, u0);
+        mul_each(d1, sn, p0);
+        mul_each(d1, c, u1);
+        mul_each(d0, sn, p1);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 4; ++k) {
           u0[k] = __fadd_rn(u0[k], p0[k]);
           u1[k] = __fsub_rn(u1[k], p1[k]);
         }
-        mul8(x0, rstd, x0);
-        mul8(x1, rstd, x1);
-        mul8(u0, x0, p0);
-        mul8(u1, x1, p1);
+        mul_each(x0, rstd, x0);
+        mul_each(x1, rstd, x1);
+        mul_each(u0, x0, p0);
+        mul_each(u1, x1, p1);
         if (!__all_sync(0xffffffffu, has)) {  // heads past the last add zero
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 0; k < 4; ++k) {
             p0[k] = has ? p0[k] : 0.0f;
             p1[k] = has ? p1[k] : 0.0f;
           }
@@ -225,39 +224,43 @@ __global__ void __launch_bounds__(THREADS, 1) qk_norm_rope_bwd_kernel(const Args
         // q's heads, k's, or some of both
         if (__all_sync(0xffffffffu, !key)) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 0; k < 4; ++k) {
             acc[0][0][k] = __fadd_rn(acc[0][0][k], p0[k]);
             acc[0][1][k] = __fadd_rn(acc[0][1][k], p1[k]);
           }
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 0; k < 4; ++k) {
             acc[0][0][k] = __fadd_rn(acc[0][0][k], key ? 0.0f : p0[k]);
             acc[0][1][k] = __fadd_rn(acc[0][1][k], key ? 0.0f : p1[k]);
             acc[1][0][k] = __fadd_rn(acc[1][0][k], key ? p0[k] : 0.0f);
             acc[1][1][k] = __fadd_rn(acc[1][1][k], key ? p1[k] : 0.0f);
           }
         }
-        mul8(u0, w0, u0);
-        mul8(u1, w1, u1);
-        mul8(u0, x0, p0);
-        mul8(u1, x1, p1);
+        const float* w = weights + ((key ? 2 : 0) + e) * D + 4 * sub;
+        float w0[4], w1[4];
+        *reinterpret_cast<float4*>(w0) = *reinterpret_cast<const float4*>(w);
+        *reinterpret_cast<float4*>(w1) = *reinterpret_cast<const float4*>(w + H2);
+        mul_each(u0, w0, u0);
+        mul_each(u1, w1, u1);
+        mul_each(u0, x0, p0);
+        mul_each(u1, x1, p1);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) dot = __fadd_rn(dot, __fadd_rn(p0[k], p1[k]));
+        for (int k = 0; k < 4; ++k) dot = __fadd_rn(dot, __fadd_rn(p0[k], p1[k]));
         const float mean = __fmul_rn(group_sum<LANES>(dot), 1.0f / D);  // D is a power of two
-        mul8(x0, mean, x0);
-        mul8(x1, mean, x1);
+        mul_each(x0, mean, x0);
+        mul_each(x1, mean, x1);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 4; ++k) {
           d0[k] = __fsub_rn(u0[k], x0[k]);
           d1[k] = __fsub_rn(u1[k], x1[k]);
         }
-        mul8(d0, rstd, d0);
-        mul8(d1, rstd, d1);
+        mul_each(d0, rstd, d0);
+        mul_each(d1, rstd, d1);
         if (has) {
-          uint16_t* to = a.dx + (row * n_heads + h) * D + 8 * sub;
-          *reinterpret_cast<uint4*>(to) = pack8(d0);
-          *reinterpret_cast<uint4*>(to + H2) = pack8(d1);
+          uint16_t* to = a.dx + (row * n_heads + h) * D + 4 * sub;
+          *reinterpret_cast<uint2*>(to) = pack4(d0);
+          *reinterpret_cast<uint2*>(to + H2) = pack4(d1);
         }
       }
     }
@@ -270,11 +273,11 @@ __global__ void __launch_bounds__(THREADS, 1) qk_norm_rope_bwd_kernel(const Args
 #pragma unroll
       for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           float v = acc[kind][half][i];
 #pragma unroll
           for (int off = LANES; off < 32; off <<= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));
-          if (grp == 0 && ok) sums[(warp * 2 + kind) * D + half * H2 + 8 * sub + i] = v;
+          if (grp == 0 && ok) sums[(warp * 2 + kind) * D + half * H2 + 4 * sub + i] = v;
         }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * D; i += THREADS) {
@@ -292,17 +295,18 @@ __global__ void __launch_bounds__(THREADS, 1) qk_norm_rope_bwd_kernel(const Args
 }
 
 // Adds the CTAs' sums: a CTA takes 32 columns of one kind and set, warp k the runs k, k + 8, ..., eight reads at once.
-constexpr int FOLD_WARPS = 8, FOLD_THREADS = 32 * FOLD_WARPS;
+constexpr int FOLD_WARPS = 32, FOLD_THREADS = 32 * FOLD_WARPS;
 
 template <int D>
 __global__ void __launch_bounds__(FOLD_THREADS) qk_dweight_fold_kernel(const Args a) {
   __shared__ float sums[FOLD_WARPS][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = int(blockIdx.x) / (D / 32), col = int(blockIdx.x) % (D / 32) * 32 + lane;  // kind * 2 + set
-  pdl_wait();  // also where nothing is written: this grid ends after the one before it
-  if (((a.sets >> (group & 1)) & 1) == 0) return;
+  // the plan is older than the grid before this one
   const PlanHeader* hdr = reinterpret_cast<const PlanHeader*>(a.ws);
-  if (hdr->magic != kPlanMagic || hdr->T != a.T || hdr->count[0] + hdr->count[1] != a.T) return;
+  const bool plan = hdr->magic == kPlanMagic && hdr->T == a.T && hdr->count[0] + hdr->count[1] == a.T;
+  pdl_wait();  // also where nothing is written: this grid ends after the one before it
+  if (((a.sets >> (group & 1)) & 1) == 0 || !plan) return;
   float v = 0.0f;
 #pragma unroll 8
   for (int i = warp; i < a.ctas; i += FOLD_WARPS) v = __fadd_rn(v, __ldcg(a.part + (int64_t(i) * 4 + group) * D + col));
