@@ -7,7 +7,10 @@
 // a step would stay where it is, for its neighbours are 6 to 12 % away.
 //
 // Every element is read and written once: 30 bytes with fp32 states, fp32 gradients and the bf16 copy, 16.06 with 8-bit states
-// and bf16 gradients. The bound is memory.
+// and bf16 gradients. The bound is memory. fp32 states reach a plain copy's rate and more (985 us for 233 million elements, 30 bytes
+// each). 8-bit ones take 73 instructions an element, so that a warp's loads have to come while others compute: 233 million
+// elements in 599 us, 93% of the copy's rate, with the next block's lines asked for ahead and 32 warps an SM (without the
+// first 701 us, with 24 warps 654, with neither 789 and more).
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -300,6 +303,19 @@ __device__ __forceinline__ void warp_block(const Table& a, const Hyper& h, const
   }
 }
 
+// The lines of a whole block with 8-bit states into L2, one a lane.
+template <bool BF16>
+__device__ __forceinline__ void prefetch_block(const mot_adamw_tensor& t, int64_t block, int lane) {
+  constexpr int G = BF16 ? 4 : 8;  // lines of the gradient
+  const int64_t e = block * BLOCK;
+  const uint8_t* at = nullptr;
+  if (lane < 8) at = reinterpret_cast<const uint8_t*>(t.p + e) + 128 * lane;
+  else if (lane < 8 + G) at = static_cast<const uint8_t*>(t.g) + e * (BF16 ? 2 : 4) + 128 * (lane - 8);
+  else if (lane < 10 + G) at = static_cast<const uint8_t*>(t.m) + e + 128 * (lane - 8 - G);
+  else if (lane < 12 + G) at = static_cast<const uint8_t*>(t.v) + e + 128 * (lane - 10 - G);
+  if (at != nullptr) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+}
+
 template <bool BF16, bool E4M3>
 __device__ __forceinline__ void warp_blocks(const Table& a, const Hyper& h, const mot_adamw_tensor& t, int id, int64_t block,
                                             int lane) {
@@ -307,6 +323,7 @@ __device__ __forceinline__ void warp_blocks(const Table& a, const Hyper& h, cons
 #pragma unroll 1
   for (int i = 0; i < a.blocks; ++i, block += WARPS) {
     if ((block + 1) * BLOCK <= t.n) {
+      if (E4M3 && i + 1 < a.blocks && (block + WARPS + 1) * BLOCK <= t.n) prefetch_block<BF16>(t, block + WARPS, lane);
       warp_block<true, BF16, E4M3>(a, h, t, wl, id, block, lane);
     } else {
       if (block * BLOCK < t.n) warp_block<false, BF16, E4M3>(a, h, t, wl, id, block, lane);
@@ -315,9 +332,9 @@ __device__ __forceinline__ void warp_blocks(const Table& a, const Hyper& h, cons
   }
 }
 
-// E4M3 false: no tensor has 8-bit states, whose registers would leave the others with fewer warps.
+// E4M3 false: no tensor has 8-bit states.
 template <bool E4M3>
-__global__ void __launch_bounds__(THREADS, E4M3 ? 3 : 4) adamw_kernel(const __grid_constant__ Table a) {
+__global__ void __launch_bounds__(THREADS, 4) adamw_kernel(const __grid_constant__ Table a) {
   Hyper h;
   if (!load_hyper(a.hyper, h)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, MOT_DEV_BAD_HYPER);
@@ -446,9 +463,11 @@ extern "C" int mot_adamw_step(const mot_adamw_tensor* tensors, int n_tensors, co
   a.hyper = hyper;
   uint32_t k0 = uint32_t(seed), k1 = uint32_t(seed >> 32);
   for (int i = 0; i < adamw::ROUNDS; ++i, k0 += 0x9E3779B9u, k1 += 0xBB67AE85u) a.key[2 * i] = k0, a.key[2 * i + 1] = k1;
-  // 8-bit states are bound by instructions, and a warp's setting up (the step's numbers, its tensor) costs about an eighth of a
-  // block: several blocks a warp once every SM has eight CTAs without. (fp32 states, bound by memory, lose by it: 1019 us for 987.)
-  a.blocks = e4m3 && all >= int64_t(sm_count(dev)) * 8 * adamw::WARPS * 4 ? 4 : 1;
+  // With 8-bit states a warp takes several blocks, whose lines come ahead but for the first's, and its setting up (the step's numbers,
+  // its tensor) costs about an eighth of a block: up to 16 a warp, as long as every SM has eight CTAs (4 a warp 706 us for 656, 32
+  // a warp 666). fp32 states, bound by memory, lose by it: 1019 us for 987.
+  const int64_t waves = all / (int64_t(sm_count(dev)) * 8 * adamw::WARPS);
+  a.blocks = e4m3 && waves > 1 ? int(waves < 16 ? waves : 16) : 1;
   const int64_t per = int64_t(a.blocks) * adamw::WARPS * adamw::BLOCK;
   a.err = &static_cast<PlanHeader*>(ws)->error;
   for (int i = 0; i < n_tensors;) {
