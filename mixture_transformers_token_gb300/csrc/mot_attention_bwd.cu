@@ -14,25 +14,37 @@
 //
 //   stats_kernel  -delta and -lse / scale of every row and head, [Hq][T] (reads dout and out once); its first CTA makes the
 //                 lists of work.
-//   grad_kernel   first the CTAs of dK and dV, one per (tile of keys, KV head, share of the blocks). The borders of the
-//                 sequences' key ranges cut the pack's rows into runs that the same sequences see, and a tile is 128 rows of a
-//                 run or what is left of it. So nothing that a sequence holds reaches the sums of rows that are not its keys, as
-//                 it would through 0 NaN in a tile of two sequences. Over the sequences that see these rows, the group's heads
-//                 and the share's blocks of 128 queries: S' = K Q' and dP' = V dO' (keys in the rows), P' and dS' as bf16 into
-//                 tensor memory in the places of S' and dP', dV += P' dO, dK += dS' Q with A from tensor memory. Each share's
-//                 sums go to the workspace, and the share that comes last adds them up, in the order of the shares.
-//                 (With the shares in a cluster, added up through its shared memory, a CTA spent 20000 of 120000 cycles in that
-//                 and a twentieth of the SMs had no cluster.)
-//                 Then the CTAs of dQ, one per (128 queries of a sequence, head), which fill the SMs as the others end: over
-//                 the blocks of 128 keys, S = Q K', dP = dO V', dS as bf16 into tensor memory in the place of S, dQ += dS K.
+//   grad_kernel   one CTA an SM, which draws pieces of work until there are none left. First those of dK and dV: (tile of keys, KV
+//                 head, share of the blocks). The borders of the sequences' key ranges cut the pack's rows into runs that the same
+//                 sequences see, and a tile is 128 rows of a run or what is left of it. So nothing that a sequence holds reaches
+//                 the sums of rows that are not its keys, as it would through 0 NaN in a tile of two sequences. Over the sequences
+//                 that see these rows, the group's heads and the share's blocks of 128 queries: S' = K Q' and dP' = V dO' (keys in
+//                 the rows), P' and dS' as bf16 into tensor memory in the places of S' and dP', dV += P' dO, dK += dS' Q with A
+//                 from tensor memory. Each share's sums go to the workspace, and the share that comes last adds them up, in the
+//                 order of the shares. Then the pieces of dQ: (128 queries of a sequence, head). Over the blocks of 128 keys, S =
+//                 Q K', dP = dO V', dS as bf16 into tensor memory in the place of S, dQ += dS K.
 //
 // For dK and dV, lse and delta belong to the columns. They are subtracted by the products themselves: one more step of K, whose A
 // is ones and whose B holds the value as three bf16 (24 bits), so that no thread reads them from shared memory, which the products
 // keep busy.
 //
-// A block's tiles are copied by TMA (128-byte swizzle) two or three blocks ahead; one warp copies, one issues the products, and
-// sixteen compute (each thread a quarter of the 128 columns of one row). Rows past a sequence's end inside its last block are other
-// sequences' rows: they are zeroed in shared memory where they would be summed over, and masked where they are columns.
+// A block's tiles are copied by TMA (128-byte swizzle) one to three blocks ahead; one warp draws the work and copies, one issues the
+// products, and sixteen compute (each thread a quarter of the 128 columns of one row). Rows past a sequence's end inside its last
+// block are other sequences' rows: they are zeroed in shared memory where they would be summed over, and masked where they are
+// columns.
+//
+// What bounds it: at D = 128 a block's seven products take 3700 cycles of the tensor cores, which are busy 65% of the time. Tensor
+// memory is full (S', dP', dV and dK are 128 columns each), so a block's S' waits for the dV of the block before, which waits for
+// its P', and dP' likewise: two chains that alternate, each with the latencies of its barriers. 4096 rows of 28/4 heads of 128 (70%
+// of them causal): 357 us, 915 TFLOP/s of the five products that cannot be done without; a pack of twelve sequences of 2900 to 3000
+// rows 2.50 ms, one of 37 of up to 700 rows with 8/8 heads of 64 100 us. A wait's instructions and size count, as three kinds of
+// warps share the instruction cache: with the limit's code in line at every wait these were 369 us, 2.59 ms and 109 us. Measured on
+// the first and not taken:
+//   shares in a cluster, added up through its shared memory (20000 of a CTA's 120000 cycles, and a twentieth of the SMs without one);
+//   halves of 64 queries with a chain each (products of 64 columns take 48 cycles for 32: 3350 cycles a block for 3120);
+//   a warp for each chain's products (394 us for 369); dP of the next block before dQ (2270 cycles for 1975);
+//   dQ's S and dP across the border of two pieces (371 for 356 us);
+//   every wait but one ahead of P' and dS' in the issuing warp (375 for 369 us).
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -102,7 +114,7 @@ struct StatsArgs {
   uint32_t* err;
 };
 
-constexpr int STATS_THREADS = 256;
+constexpr int STATS_THREADS = 128;
 
 // Query blocks [first, end) of a sequence that see a key of the tile from row `row` on: causal query i sees keys up to nk - nq + i.
 __device__ __forceinline__ void query_blocks(const int (&s)[5], int row, int& first, int& end) {
@@ -366,9 +378,9 @@ __device__ void make_work(const StatsArgs& a, int* room) {
   }
 }
 
-// A CTA takes STATS_ROWS rows and 32 heads; D / 8 lanes a row and head, the sums through shared memory into rows of [Hq][T]. (32
-// rows a CTA left a 4096-row pack with 129 CTAs and took 51 us.)
-constexpr int STATS_ROWS = 8;
+// A CTA takes STATS_ROWS rows and 32 heads; D / 8 lanes a row and head, the sums through shared memory into rows of [Hq][T]. (17 us
+// for 4096 rows of 28 heads of 128, cold; 32 rows a CTA left it 129 CTAs and took 51 us, 8 rows took 4 us more on shorter rows.)
+constexpr int STATS_ROWS = 4;
 
 template <int D>
 __global__ void __launch_bounds__(STATS_THREADS) stats_kernel(const StatsArgs a) {
@@ -568,12 +580,34 @@ struct Drawn {
 // Warps that wait for a piece of work: those that issue products and those that compute.
 constexpr int TAKERS = 1 + COMPUTE_WARPS;
 
+// Whether a wait that began at t0 (0: now) may go on: its beginning, or GIVE_UP after the limit or another warp's timeout. Out of
+// line: in line at every wait it filled the instruction cache that three kinds of warps share.
+constexpr uint64_t GIVE_UP = ~uint64_t(0);
+__device__ __noinline__ uint64_t still_waiting(uint64_t t0, volatile uint32_t* abort_flag, uint32_t* err) {
+  if (*abort_flag) return GIVE_UP;
+  const uint64_t now = global_timer_ns();
+  if (t0 == 0) return now;
+  if (now - t0 <= kWaitLimitNs) return t0;
+  *abort_flag = 1u;
+  if (err != nullptr) atomicOr(err, MOT_DEV_TIMEOUT);
+  return GIVE_UP;
+}
+
 // A wait by a whole warp.
 struct Waits {
   volatile uint32_t* abort_flag;
   uint32_t* err;
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t phase) const {
-    return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase & 1u, abort_flag, err));
+    const uint32_t at = smem_u32(bar);
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 1; !__all_sync(0xffffffffu, mbar_try_wait(at, phase & 1u)); ++i) {
+      if (__builtin_expect((i & 255u) == 0, 0)) {
+        t0 = still_waiting(t0, abort_flag, err);
+        if (__any_sync(0xffffffffu, t0 == GIVE_UP)) return false;
+      }
+    }
+    return true;
   }
 };
 
@@ -1225,7 +1259,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (uint64_t* b : {&sh.kv.p_full, &sh.kv.ds_full, &sh.kv.meet, &sh.q.ds_full}) init(*b, COMPUTE_WARPS);
     for (int i = 0; i < 4; ++i) {
       for (uint64_t* b : {&sh.kv.q_full[i], &sh.kv.do_full[i]}) init(*b, 2);  // the tile, and its stats
-      for (uint64_t* b : {&sh.kv.q_empty[i], &sh.kv.do_empty[i], &sh.kv.edges[i], &sh.q.k_full[i], &sh.q.k_empty[i], &sh.q.v_full[i], &sh.q.v_empty[i]})
+      for (uint64_t* b : {&sh.kv.q_empty[i], &sh.kv.do_empty[i], &sh.kv.edges[i], &sh.q.k_full[i], &sh.q.k_empty[i],
+                          &sh.q.v_full[i], &sh.q.v_empty[i]})
         init(*b, 1);
     }
     for (int i = 0; i < 2; ++i) {
