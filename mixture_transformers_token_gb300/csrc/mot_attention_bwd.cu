@@ -36,10 +36,10 @@
 // What bounds it: at D = 128 a block's seven products take 3700 cycles of the tensor cores, which are busy 65% of the time. Tensor
 // memory is full (S', dP', dV and dK are 128 columns each), so a block's S' waits for the dV of the block before, which waits for
 // its P', and dP' likewise: two chains that alternate, each with the latencies of its barriers. 4096 rows of 28/4 heads of 128 (70%
-// of them causal): 357 us, 915 TFLOP/s of the five products that cannot be done without; a pack of twelve sequences of 2900 to 3000
-// rows 2.50 ms, one of 37 of up to 700 rows with 8/8 heads of 64 100 us. A wait's instructions and size count, as three kinds of
-// warps share the instruction cache: with the limit's code in line at every wait these were 369 us, 2.59 ms and 109 us. Measured on
-// the first and not taken:
+// of them causal): 346 us, 950 TFLOP/s of the five products that cannot be done without; a pack of twelve sequences of 2900 to 3000
+// rows 2.48 ms, one of 37 of up to 700 rows with 8/8 heads of 64 100 us. A wait's instructions and size count, as three kinds of
+// warps share the instruction cache: with the limit's code in line at every wait the first took 369 us for 357, the second 2.59 ms
+// for 2.50. Measured on the first and not taken:
 //   shares in a cluster, added up through its shared memory (20000 of a CTA's 120000 cycles, and a twentieth of the SMs without one);
 //   halves of 64 queries with a chain each (products of 64 columns take 48 cycles for 32: 3350 cycles a block for 3120);
 //   a warp for each chain's products (394 us for 369); dP of the next block before dQ (2270 cycles for 1975);
@@ -378,7 +378,7 @@ __device__ void make_work(const StatsArgs& a, int* room) {
   }
 }
 
-// A CTA takes STATS_ROWS rows and 32 heads; D / 8 lanes a row and head, the sums through shared memory into rows of [Hq][T]. (17 us
+// A CTA takes STATS_ROWS rows and 32 heads; D / 8 lanes a row and head, the sums through shared memory into rows of [Hq][T]. (14 us
 // for 4096 rows of 28 heads of 128, cold; 32 rows a CTA left it 129 CTAs and took 51 us, 8 rows took 4 us more on shorter rows.)
 constexpr int STATS_ROWS = 4;
 
@@ -404,21 +404,32 @@ __global__ void __launch_bounds__(STATS_THREADS) stats_kernel(const StatsArgs a)
   const int sub = threadIdx.x % LANES, grp = threadIdx.x / LANES;
   const int row0 = int(blockIdx.x - 1) * STATS_ROWS, h0 = int(blockIdx.y) * 32;
   const int nh = a.Hq - h0 < 32 ? a.Hq - h0 : 32;
-#pragma unroll 8
-  for (int i = grp; i < STATS_ROWS * 32; i += GROUPS) {
-    const int r = i >> 5, h = i & 31;
-    float s = 0.0f;
-    if (row0 + r < a.T && h < nh) {
-      const int64_t off = (int64_t(row0 + r) * a.Hq + h0 + h) * D + 8 * sub;
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.dout + off)), y = __ldg(reinterpret_cast<const uint4*>(a.out + off));
-      s = __fadd_rn(__fmul_rn(bf_lo(x.x), bf_lo(y.x)), __fmul_rn(bf_hi(x.x), bf_hi(y.x)));
+  constexpr int BATCH = D == 128 ? 8 : 4;  // rows and heads whose loads are under way at once (one after the other: 18 us)
+  static_assert(STATS_ROWS * 32 % (BATCH * GROUPS) == 0, "whole batches");
+#pragma unroll 1
+  for (int i0 = grp; i0 < STATS_ROWS * 32; i0 += BATCH * GROUPS) {
+    uint4 xs[BATCH], ys[BATCH];
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      const int r = (i0 + u * GROUPS) >> 5, h = (i0 + u * GROUPS) & 31;
+      xs[u] = ys[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (row0 + r < a.T && h < nh) {
+        const int64_t off = (int64_t(row0 + r) * a.Hq + h0 + h) * D + 8 * sub;
+        xs[u] = __ldg(reinterpret_cast<const uint4*>(a.dout + off));
+        ys[u] = __ldg(reinterpret_cast<const uint4*>(a.out + off));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      const uint4 x = xs[u], y = ys[u];
+      float s = __fadd_rn(__fmul_rn(bf_lo(x.x), bf_lo(y.x)), __fmul_rn(bf_hi(x.x), bf_hi(y.x)));
       s = __fadd_rn(s, __fadd_rn(__fmul_rn(bf_lo(x.y), bf_lo(y.y)), __fmul_rn(bf_hi(x.y), bf_hi(y.y))));
       s = __fadd_rn(s, __fadd_rn(__fmul_rn(bf_lo(x.z), bf_lo(y.z)), __fmul_rn(bf_hi(x.z), bf_hi(y.z))));
       s = __fadd_rn(s, __fadd_rn(__fmul_rn(bf_lo(x.w), bf_lo(y.w)), __fmul_rn(bf_hi(x.w), bf_hi(y.w))));
-    }
 #pragma unroll
-    for (int off = LANES / 2; off >= 1; off >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
-    if (sub == 0) room.sums[h][r] = s;
+      for (int off = LANES / 2; off >= 1; off >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
+      if (sub == 0) room.sums[(i0 + u * GROUPS) & 31][(i0 + u * GROUPS) >> 5] = s;
+    }
   }
   __syncthreads();
   const int h = threadIdx.x / STATS_ROWS, r = threadIdx.x % STATS_ROWS;
