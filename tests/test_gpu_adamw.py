@@ -228,3 +228,44 @@ def test_refusals():
     off = mot.AdamWTensors([c.p[0][1:]], [c.g[0][1:]], [c.m[0][1:]], [c.v[0][1:]])
     with pytest.raises(mot.MotError):
         mot.mot_adamw_step(off, _hyper(), _ws())
+
+
+def test_eight_bit_states_past_32_bits(monkeypatch):
+    # the last elements of more than 2^32 codes, whose random words count from the tensor's first element
+    n, tail = 2 ** 32 + 2 ** 8 + 77, 2 ** 8 + 77
+    if torch.cuda.mem_get_info()[0] < 60 * 2 ** 30:
+        pytest.skip("needs 60 GB of free memory")
+    small = Case([tail], state="e4m3", grad="bf16", p16=False, seed=41)
+    p, g = torch.zeros(n, device=DEV), torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+    p[-tail:], g[-tail:] = small.p[0], small.g[0]
+    m, v = (torch.zeros(n, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn) for _ in range(2))
+    scales = torch.zeros((-(-n // 256), 2), device=DEV)
+    ws = _ws()
+    mot.mot_adamw_step(mot.AdamWTensors([p], [g], [m], [v], scales=[scales], weight_decay=0.1), _hyper(3), ws, seed=9)
+    assert mot.mot_device_status(ws) == 0 and (n - tail) % 256 == 0
+
+    def words(count, tensor, step, seed):  # of the elements from n - tail on
+        b = (n - tail) // 4 + np.arange(-(-count // 4), dtype=np.uint64)
+        w = O.philox4x32_7((b & np.uint64(0xFFFFFFFF), b >> np.uint64(32), np.full_like(b, tensor), np.full_like(b, step)), (seed, 0))
+        return np.stack(w, 1).reshape(-1)[:count].astype(np.uint32)
+
+    monkeypatch.setattr(O, "adamw_words", words)
+    zero = np.zeros(tail, np.float32)
+    want = O.e_adamw(small.p[0].cpu().numpy(), small.g[0].float().cpu().numpy(), zero, zero, np.asarray(_hyper(3).cpu())[:9], 0.1, 0,
+                     3, 9, np.zeros((2, 2), np.float32))
+    codes = lambda t: t.view(torch.uint8)[-tail:].view(torch.float8_e4m3fn).float()  # noqa: E731
+    for a, e in zip((p[-tail:], codes(m), codes(v), scales[-2:]), want):
+        assert np.array_equal(a.cpu().numpy(), np.asarray(e, np.float32))
+    assert not scales[:-2].any() and not p[:-tail].any()
+    del p, g, m, v, scales
+    torch.cuda.empty_cache()
+
+
+def test_several_blocks_a_warp():
+    # enough blocks that a warp takes more than one, a rest of them and of a block at each tensor's end
+    c = Case([6_000_001, 300, 257 * 256 + 3, 1], state="e4m3", grad="bf16", seed=43)
+    want = c.want(1, 1.0, 5)
+    mot.mot_adamw_step(c.plan, _hyper(1), _ws(), seed=5)
+    for i, (p, m, v, s) in enumerate(want):
+        for a, e in ((c.p[i], p), (c.m[i].float(), m), (c.v[i].float(), v), (c.scales[i], s)):
+            assert np.array_equal(a.cpu().numpy(), np.asarray(e, np.float32)), i

@@ -336,3 +336,29 @@ def test_default_buffers_and_refusals():
         call(dout=dout.t().contiguous().t())
     with pytest.raises(mot.MotError):
         call(ws=ws[:-16].contiguous())
+
+
+def _room_for(gb):
+    if torch.cuda.mem_get_info()[0] < gb * 2 ** 30:
+        pytest.skip(f"needs {gb} GB of free memory")
+
+
+def test_rows_past_32_bit_offsets():
+    # the last rows of a pack of more than 2^31 values: the same bits as in a pack of their own
+    Hq, Hkv, D, n = 28, 4, 128, 333
+    _room_for(40)
+    T = 2 ** 31 // ((Hq + 2 * Hkv) * D) + 2 * n
+    seqs = [(0, 0, 200, 200, 150), (200, 0, 133, 200, 0)]
+    qkv, dout = _inputs(n, Hq, Hkv, D, seed=23)
+    s, out, lse = _forward(qkv, seqs, Hq, Hkv, D)
+    want = _backward(dout, qkv, out, lse, s, Hq, Hkv, D)
+    big, bd, bo = (torch.zeros((T, x.shape[1]), dtype=torch.bfloat16, device=DEV) for x in (qkv, dout, out))
+    bl = torch.zeros((Hq, T), device=DEV)
+    big[-n:], bd[-n:], bo[-n:], bl[:, -n:] = qkv, dout, out, lse
+    at = T - n
+    ws = _ws(T, Hq, Hkv, D, 2)
+    moved = torch.tensor([(q + at, k + at, *x) for q, k, *x in seqs], dtype=torch.int32, device=DEV)
+    d = mot.mot_joint_attention_backward(bd, big, bo, bl, moved, Hq, Hkv, D, ws, dqkv=torch.full_like(big, 7.0))
+    assert mot.mot_device_status(ws) == 0
+    assert_bitwise(d[-n:], want, "the last rows")
+    assert bool((d[:1000] == 7.0).all()) and bool((d[-n - 1000:-n] == 7.0).all())
