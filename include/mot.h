@@ -324,8 +324,9 @@ int mot_joint_attention_lse(const mot_bf16* qkv, int64_t T, int Hq, int Hkv, int
 
 /*
  * mot_joint_attention_backward_workspace_bytes -- workspace bytes of mot_joint_attention_backward: the
- * 64-byte header (its error word), the row sums and the partial gradients. 0 for a geometry that the
- * call rejects.
+ * 64-byte header (its error word), the row sums, lists of work and, with two query heads a KV head or more,
+ * the shares' sums (8 Hkv D bytes a row and share: 68 MB for 4096 rows of 28/4 heads of 128). 0 for a geometry
+ * that the call rejects.
  */
 size_t mot_joint_attention_backward_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int n_seq);
 
@@ -340,8 +341,9 @@ size_t mot_joint_attention_backward_workspace_bytes(int64_t T, int Hq, int Hkv, 
  *   lse    [Hq][T] fp32               mot_joint_attention_lse's.
  *   seqs, n_seq, scale                the forward's.
  *   ws     at least mot_joint_attention_backward_workspace_bytes(T, Hq, Hkv, D, n_seq) bytes; everything
- *          after its first 64 bytes is scratch that the call overwrites (so not a routing plan in use).
- *          Its error word receives MOT_DEV_BAD_SEQUENCE as in the forward.
+ *          after its first 64 bytes is scratch that the call overwrites (so not a routing plan in use; calls
+ *          that may run at the same time have workspaces of their own). Its error word receives
+ *          MOT_DEV_BAD_SEQUENCE as in the forward.
  *   dqkv   [T][(Hq + 2 Hkv) D] bf16   out: the q columns of rows that are some sequence's query, and the
  *          K and V columns of rows that are some sequence's key, each row written once, whole; all other
  *          columns are left as they were. A row that several sequences see as a key gets the sum over

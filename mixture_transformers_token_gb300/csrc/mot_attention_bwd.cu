@@ -72,7 +72,7 @@ struct alignas(16) Item {
 // Lists in the workspace, made by stats_kernel's first CTA.
 struct Work {
   int4* tiles;    // (first row, rows, first and last sequence that may see them), ascending
-  int4* parts;    // of dK's and dV's CTAs: (tile, share, shares, the tile's first part)
+  int4* parts;    // of dK's and dV's CTAs: (tile, share, shares)
   Item* items;    // of dQ's CTAs
   int32_t* ended; // [tile][Hkv] shares whose sums are there
   int32_t* counts;  // parts, items, the next piece of work to be drawn
@@ -87,7 +87,8 @@ struct Args {
   const int32_t* seqs;  // [n_seq][5]
   int n_seq, T, Hq, Hkv;
   Work work;
-  float* sums;          // [part][Hkv][dV, dK][D / 4][128 rows][4]
+  int most_shares;
+  float* sums;          // of each tile's rows [Hkv][most_shares][dV, dK][D / 4][rows][4]: as many in all, however the pack is cut
   float c, scale;
   const float* nlse;    // [Hq][T] -lse / scale
   const float* ndelta;  // [Hq][T] -delta
@@ -180,7 +181,7 @@ __device__ int make_parts(const StatsArgs& a, int* room, int tiles, const Seq& s
     }
     int total;
     const int at = parts + scan_before(shares, room, total);
-    for (int p = 0; p < shares; ++p) w.parts[at + p] = make_int4(i, p, shares, at);
+    for (int p = 0; p < shares; ++p) w.parts[at + p] = make_int4(i, p, shares, 0);
     parts += total;
   }
   return parts;
@@ -585,7 +586,8 @@ __device__ __forceinline__ void ld_columns(uint32_t taddr, float (&v)[16]) { tme
 struct Drawn {
   int4 info[2];  // of the two rings' places: what the work is
   int4 more[2];
-  int first[2];
+  int share[2];
+  int4 sent[2];  // of every other piece whose sums were sent: tile and KV head, shares, first row, rows
 };
 
 // Warps that wait for a piece of work: those that issue products and those that compute.
@@ -652,10 +654,15 @@ struct KvBars {
   uint64_t drawn[2], taken[2];
 };
 
+// A share's sums of a tile and KV head.
+template <int D>
+__device__ __forceinline__ float* sums_of(const Args& a, int row0, int rows, int g, int share) {
+  return a.sums + ((int64_t(row0) * a.Hkv + int64_t(rows) * g) * a.most_shares + int64_t(rows) * share) * (2 * D);
+}
 // Four fp32 of a row: 32 rows of a warp are 512 consecutive bytes.
 template <int D>
-__device__ __forceinline__ float4* sums_at(float* sums, int m, int piece, int row) {
-  return reinterpret_cast<float4*>(sums) + (m * (D / 4) + piece) * 128 + row;
+__device__ __forceinline__ float4* sums_at(float* sums, int rows, int m, int piece, int row) {
+  return reinterpret_cast<float4*>(sums) + (m * (D / 4) + piece) * rows + row;
 }
 
 // The thread's row of dV and dK as bf16, its quarter of the columns: the sums of the shares in order (of one: from tensor memory).
@@ -674,11 +681,12 @@ __device__ __forceinline__ void add_shares(float* sums, uint32_t at, bool any, i
       if constexpr (SHARES == 1) {
         if (any) tmem_ld16(at + (m ? L::DK : L::DV) + c0, v);
       } else {
-        float4 u[SHARES][4];  // all reads under way at once
+        float4 u[SHARES][4];  // all reads under way at once; rows past the last read that
+        const float4* from = sums_at<D>(sums, rows, m, c0 / 4, row < rows ? row : rows - 1);
 #pragma unroll
         for (int p = 0; p < SHARES; ++p)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) u[p][q] = __ldcg(sums_at<D>(sums + p * int64_t(a.Hkv) * (2 * 128 * D), m, c0 / 4 + q, row));
+          for (int q = 0; q < 4; ++q) u[p][q] = __ldcg(from + (p * (D / 2) + q) * rows);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float4 s = u[0][q];
@@ -742,8 +750,8 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
         blocks += blocks_of_share(share, first, end, G, shares);
       }
       if (lane == 0) {
-        drawn.info[n & 1] = make_int4(blocks, part.x * a.Hkv + g, shares, w);
-        drawn.first[n & 1] = part.w * a.Hkv + g;
+        drawn.info[n & 1] = make_int4(blocks, part.x * a.Hkv + g, shares, 0);
+        drawn.share[n & 1] = share;
         drawn.more[n & 1] = tile;
         mbar_arrive(smem_u32(&B.drawn[n & 1]));
       }
@@ -890,7 +898,7 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
     const unsigned long long c2 = f2_pack(a.c, a.c);
     // A share's sums are sent when its blocks are done, and said to be there after the next piece's first block: by then they have
     // arrived (a fence at once took 3000 cycles). The share that comes last adds them up.
-    int sent = -1, sent_shares = 0, sent_first = 0, sent_row0 = 0, sent_rows = 0, met = 0;
+    int sent = -1, met = 0;  // the place of what was sent and not yet said to be there
     auto meet = [&]() {  // of the warps that compute; like every wait it gives up
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&B.meet));
@@ -901,16 +909,17 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
       __threadfence();
       if (!meet()) return false;  // all warps' sums are there, and *ended of the piece before has been read
       if (warp == 2 && lane == 0) {
-        *ended = atomicAdd(a.work.ended + sent, 1);
+        *ended = atomicAdd(a.work.ended + drawn.sent[sent].x, 1);
         __threadfence();
       }
       if (!meet()) return false;
-      if (*ended == sent_shares - 1) {
+      const int4 s = drawn.sent[sent];
+      if (*ended == s.y - 1) {
         __threadfence();
-        float* sums = a.sums + int64_t(sent_first) * (2 * 128 * D);
-        const int g = sent % a.Hkv;
-        if (sent_shares == 4) add_shares<D, 4>(sums, at, true, part, row, sent_row0, sent_rows, g, a);
-        else add_shares<D, 2>(sums, at, true, part, row, sent_row0, sent_rows, g, a);
+        const int g = s.x % a.Hkv;
+        float* sums = sums_of<D>(a, s.z, s.w, g, 0);
+        if (s.y == 4) add_shares<D, 4>(sums, at, true, part, row, s.z, s.w, g, a);
+        else add_shares<D, 2>(sums, at, true, part, row, s.z, s.w, g, a);
       }
       sent = -1;
       return true;
@@ -920,7 +929,7 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
     for (int n = 0; ok; ++n) {
       if (!(ok = wait(&B.drawn[n & 1], n >> 1))) break;
       const int4 info = drawn.info[n & 1], tile = drawn.more[n & 1];
-      const int first = drawn.first[n & 1];
+      const int share = drawn.share[n & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&B.taken[n & 1]));
       if (info.x < 0) break;
@@ -983,20 +992,20 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
         add_shares<D, 1>(nullptr, at, any, part, row, tile.x, tile.y, info.y % a.Hkv, a);
       } else {
         if (!(ok = publish())) break;  // the piece before's, where this one had no block
-        float* to = a.sums + int64_t(info.w) * (2 * 128 * D);
+        float* to = sums_of<D>(a, tile.x, tile.y, info.y % a.Hkv, share);
 #pragma unroll 1
         for (int m = 0; m < 2; ++m) {
           float v[D / 4] = {};
           if (any) ld_columns(at + (m ? L::DK : L::DV) + part * (D / 4), v);
+          if (row < tile.y) {
+            float4* put = sums_at<D>(to, tile.y, m, part * (D / 16), row);
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-            __stcg(sums_at<D>(to, m, part * (D / 16) + i, row), make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+            for (int i = 0; i < D / 16; ++i)
+              __stcg(put + i * tile.y, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+          }
         }
-        sent = info.y;
-        sent_shares = info.z;
-        sent_first = first;
-        sent_row0 = tile.x;
-        sent_rows = tile.y;
+        sent = n & 1;
+        if (warp == 2 && lane == 0) drawn.sent[sent] = make_int4(info.y, info.z, tile.x, tile.y);
       }
       tc_fence_before();  // dV and dK have been read: the next P' and dS' say so
     }
@@ -1345,7 +1354,7 @@ struct Room {
     border = change + up((T + 1) * 4);
     runs = border + up((T / 32 + 1) * 4);
     sums = runs + up(borders * 4);
-    end = sums + (most > 1 ? int64_t(max_tiles) * Hkv * most * (2 * 128 * D * 4) : 0);
+    end = sums + (most > 1 ? T * Hkv * most * (2 * D * 4) : 0);
     ctas = int64_t(max_tiles) * Hkv * most + int64_t(max_items) * Hq;
   }
 };
@@ -1377,7 +1386,7 @@ static int launch(const uint16_t* dout, const uint16_t* qkv, const uint16_t* out
   st.seqs = a.seqs;
   st.n_seq = a.n_seq;
   st.work = a.work;
-  st.most_shares = most_shares(a.Hq / a.Hkv);
+  st.most_shares = a.most_shares;
   st.err = a.err;
   stats_kernel<D><<<dim3(unsigned((a.T + STATS_ROWS - 1) / STATS_ROWS + 1), unsigned((a.Hq + 31) / 32)), STATS_THREADS, 0, s>>>(st);
   if (cudaGetLastError() != cudaSuccess) return MOT_ERR_CUDA;
@@ -1434,6 +1443,7 @@ extern "C" int mot_joint_attention_backward(const mot_bf16* dout, const mot_bf16
   a.work.items = reinterpret_cast<attnb::Item*>(base + room.items);
   a.work.counts = reinterpret_cast<int32_t*>(base + room.counts);
   a.work.ended = reinterpret_cast<int32_t*>(base + room.ended);
+  a.most_shares = attnb::most_shares(Hq / Hkv);
   a.sums = reinterpret_cast<float*>(base + room.sums);
   a.work.change = reinterpret_cast<int32_t*>(base + room.change);
   a.work.border = reinterpret_cast<uint32_t*>(base + room.border);
