@@ -37,7 +37,7 @@
 // memory is full (S', dP', dV and dK are 128 columns each), so a block's S' waits for the dV of the block before, which waits for
 // its P', and dP' likewise: two chains that alternate, each with the latencies of its barriers. 4096 rows of 28/4 heads of 128 (70%
 // of them causal): 346 us, 950 TFLOP/s of the five products that cannot be done without; a pack of twelve sequences of 2900 to 3000
-// rows 2.48 ms, one of 37 of up to 700 rows with 8/8 heads of 64 100 us. A wait's instructions and size count, as three kinds of
+// rows 2.48 ms, one of 37 of up to 700 rows with 8/8 heads of 64 99 us. A wait's instructions and size count, as three kinds of
 // warps share the instruction cache: with the limit's code in line at every wait the first took 369 us for 357, the second 2.59 ms
 // for 2.50. Measured on the first and not taken:
 //   shares in a cluster, added up through its shared memory (20000 of a CTA's 120000 cycles, and a twentieth of the SMs without one);
@@ -218,19 +218,23 @@ __device__ void make_work_few(const StatsArgs& a, FewRoom& s) {
   }
   // the borders of the key ranges, each once, in ascending order
   constexpr int NONE = 0x7FFFFFFF;
-  const int c = tid & (kSortedSeqs - 1);
-  const bool edge = tid < 2 * kSortedSeqs && s.d[c][3] > 0;
-  const int at = !edge ? NONE : tid < kSortedSeqs ? s.d[c][1] : s.d[c][1] + s.d[c][3];
-  if (tid < 2 * kSortedSeqs) s.edge[tid] = at;
+  static_assert(2 * kSortedSeqs <= STATS_THREADS, "a thread a border");
+  const int edges = 2 * a.n_seq, mine_of = tid >> 1;  // a sequence's first key, and the one behind its last
+  const bool edge = tid < edges && s.d[mine_of][3] > 0;
+  const int at = !edge ? NONE : s.d[mine_of][1] + (tid & 1 ? s.d[mine_of][3] : 0);
+  if (tid < edges) s.edge[tid] = at;
   __syncthreads();
   bool first = edge;
-  if (edge)
-    for (int i = 0; i < tid; ++i) first &= s.edge[i] != at;
-  if (tid < 2 * kSortedSeqs) s.first[tid] = first ? at : NONE;
+  if (edge) {
+#pragma unroll 8
+    for (int i = 0; i < edges; ++i) first &= i >= tid || s.edge[i] != at;
+  }
+  if (tid < edges) s.first[tid] = first ? at : NONE;
   const int n = __syncthreads_count(first ? 1 : 0);
   if (first) {
     int rank = 0;
-    for (int i = 0; i < 2 * kSortedSeqs; ++i) rank += s.first[i] < at ? 1 : 0;
+#pragma unroll 8
+    for (int i = 0; i < edges; ++i) rank += s.first[i] < at ? 1 : 0;
     s.sorted[rank] = at;
   }
   __syncthreads();
@@ -239,11 +243,12 @@ __device__ void make_work_few(const StatsArgs& a, FewRoom& s) {
   if (tid + 1 < n) {
     from = s.sorted[tid];
     to = s.sorted[tid + 1];
-    for (int i = 0; i < a.n_seq; ++i)
-      if (s.d[i][1] <= from && s.d[i][1] + s.d[i][3] > from) {
-        lo = lo < i ? lo : i;
-        hi = i;
-      }
+#pragma unroll 4
+    for (int i = 0; i < a.n_seq; ++i) {
+      const bool sees = s.d[i][1] <= from && s.d[i][1] + s.d[i][3] > from;
+      lo = sees && i < lo ? i : lo;
+      hi = sees ? i : hi;
+    }
   }
   const int mine = hi >= 0 ? (to - from + BK - 1) / BK : 0;
   int tiles;
@@ -258,9 +263,10 @@ __device__ void make_work_few(const StatsArgs& a, FewRoom& s) {
     return d[3] > 0;
   };
   const int parts = make_parts(a, s.scan, tiles, seq);
-  int items = 0;
+  const int c = tid & (kSortedSeqs - 1);
   for (int r = tid / kSortedSeqs; r < s.items[c]; r += STATS_THREADS / kSortedSeqs) {
     int before = 0;
+#pragma unroll 4
     for (int i = 0; i < a.n_seq; ++i) {
       const int k = s.items[i];
       before += k < r ? k : r;
@@ -269,8 +275,9 @@ __device__ void make_work_few(const StatsArgs& a, FewRoom& s) {
     if (before < w.max_items)
       w.items[before] = {s.d[c][0], s.d[c][1], s.d[c][2], s.d[c][3], s.d[c][4], (s.items[c] - 1 - r) * BQ, {0, 0}};
   }
+  int items;  // at most 2^6 2^17
+  scan_before(tid < kSortedSeqs ? s.items[tid] : 0, s.scan, items);
   if (tid == 0) {
-    for (int i = 0; i < a.n_seq; ++i) items += s.items[i];  // at most 2^6 2^17
     w.counts[0] = parts;
     w.counts[1] = items < w.max_items ? items : w.max_items;
     w.counts[2] = 0;
