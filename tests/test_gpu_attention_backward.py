@@ -248,6 +248,35 @@ def test_long_sequences_among_many():
                Hq, Hkv, D)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,n", [(6, 2, 64, 1400), (4, 1, 64, 1250), (2, 2, 128, 1100), (2, 1, 128, 1281)])
+def test_shares_of_long_sequences(Hq, Hkv, D, n):
+    # tiles whose blocks are shared by one, two and four CTAs, of whole and of few rows
+    seqs = [(7, 7, n, n, n - 300), (n + 7, 900, 60, 60, 0)]
+    qkv, dout = _inputs(n + 80, Hq, Hkv, D, seed=n)
+    s, out, lse = _forward(qkv, seqs, Hq, Hkv, D)
+    d = _backward(dout, qkv, out, lse, s, Hq, Hkv, D)
+    _check(d, dout, qkv, out, lse, seqs, Hq, Hkv, D)
+    assert_bitwise(d, _backward(dout, qkv, out, lse, s, Hq, Hkv, D), "again")
+
+
+def test_two_graphs_with_one_workspace():
+    Hq, Hkv, D = 7, 1, 128
+    ws, graphs = _ws(700, Hq, Hkv, D, 70), []
+    for T, seqs in ((700, [(0, 0, 700, 700, 500)]), (210, [(3 * i, 3 * i, 3, 3, 1) for i in range(70)])):
+        qkv, dout = _inputs(T, Hq, Hkv, D, seed=T)
+        s, out, lse = _forward(qkv, seqs, Hq, Hkv, D)
+        want, got, graph = _backward(dout, qkv, out, lse, s, Hq, Hkv, D), torch.full_like(qkv, 7.0), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            mot.mot_joint_attention_backward(dout, qkv, out, lse, s, Hq, Hkv, D, ws, dqkv=got)
+        graphs.append((graph, got, want, (dout, qkv, out, lse, s)))
+    for i in (0, 1, 1, 0, 1):
+        graph, got, want, _ = graphs[i]
+        got.fill_(7.0)
+        graph.replay()
+        assert_bitwise(got, want, f"graph {i}")
+    assert mot.mot_device_status(ws) == 0
+
+
 @pytest.mark.parametrize("n", [63, 64, 65, 128])
 def test_where_the_table_of_sequences_ends(n):
     Hq, Hkv, D = 4, 2, 64
