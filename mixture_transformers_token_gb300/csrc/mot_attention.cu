@@ -87,6 +87,99 @@ struct Args {
 // need no rescaling.
 constexpr float kLazyLog2 = 8.0f;
 
+// The work items of a sequence are its 256-row pairs of query tiles; item r counts from the
+// end (r = 0 is the last pair, which sees the most keys). The grid visits items heaviest
+// first with the heads fastest: all heads of item 0 of every sequence, then item 1 of every
+// sequence, ... (for up to 64 sequences; beyond that, sequence by sequence), so the in-order
+// block dispatch balances the uneven causal work. CTA u takes head u % Hq of item u / Hq.
+// Returns false past the last item; a bad descriptor contributes none.
+__device__ __forceinline__ int seq_items(const Args& a, int s) {
+  const int32_t* d = a.seqs + 5 * s;
+  return bad_seq(d, a.T) ? 0 : (d[2] + TILES * BQ - 1) / (TILES * BQ);
+}
+
+// Finds the item of CTA index k; called by a whole warp, every lane returns the same answer.
+// The lanes fetch the descriptors in parallel (one sequence per lane and round of 32), so the
+// lookup costs a few memory round trips, not one per sequence.
+__device__ bool find_tile(const Args& a, int k, int lane, int4& sq, int& nc, int& i0) {
+  int found_s = -1, r = -1;
+  if (a.n_seq <= kSortedSeqs) {
+    // items of sequences lane and lane + 32; round rr takes every sequence with more than rr
+    // items, in sequence order
+    const int it0 = lane < a.n_seq ? seq_items(a, lane) : 0;
+    const int it1 = lane + 32 < a.n_seq ? seq_items(a, lane + 32) : 0;
+    int most = it0 > it1 ? it0 : it1;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+      const int o = __shfl_xor_sync(0xffffffffu, most, off);
+      most = o > most ? o : most;
+    }
+    int acc = 0;
+    for (int rr = 0; rr < most; ++rr) {
+      const uint32_t m0 = __ballot_sync(0xffffffffu, it0 > rr), m1 = __ballot_sync(0xffffffffu, it1 > rr);
+      const int c0 = __popc(m0), c1 = __popc(m1);
+      if (k < acc + c0 + c1) {
+        const int t = k - acc;  // the t-th sequence (from 0) taking part in this round
+        found_s = t < c0 ? int(__fns(m0, 0, t + 1)) : 32 + int(__fns(m1, 0, t - c0 + 1));
+        r = rr;
+        break;
+      }
+      acc += c0 + c1;
+    }
+    if (found_s < 0) return false;
+  } else {
+    // sequence by sequence: a warp-wide running count over rounds of 32 sequences
+    int acc = 0;
+    for (int s0 = 0; s0 < a.n_seq && found_s < 0; s0 += 32) {
+      const int s = s0 + lane;
+      const int nt = s < a.n_seq ? seq_items(a, s) : 0;
+      int incl = nt;  // inclusive prefix sum over the lanes
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, k < acc + incl && k >= acc + incl - nt);
+      if (hit != 0u) {
+        const int l = __ffs(hit) - 1;
+        found_s = s0 + l;
+        r = k - acc - (__shfl_sync(0xffffffffu, incl, l) - __shfl_sync(0xffffffffu, nt, l));
+      }
+      acc += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (found_s < 0) return false;
+  }
+  const int32_t* d = a.seqs + 5 * found_s;
+  sq = make_int4(d[0], d[1], d[2], d[3]);
+  nc = d[4];
+  i0 = (seq_items(a, found_s) - 1 - r) * (TILES * BQ);
+  return true;
+}
+
+// CTA 0 checks every descriptor, that the query ranges do not overlap (their rows sum to
+// at most T) and that the grid covers every tile; a failure sets MOT_DEV_BAD_SEQUENCE. Called
+// by a whole warp, one sequence per lane and round.
+__device__ void check_sequences(const Args& a, int lane) {
+  int64_t tiles = 0, rows = 0;
+  bool bad = false;
+  for (int s = lane; s < a.n_seq; s += 32) {
+    const int32_t* d = a.seqs + 5 * s;
+    if (bad_seq(d, a.T)) {
+      bad = true;
+      continue;
+    }
+    tiles += (d[2] + TILES * BQ - 1) / (TILES * BQ);
+    rows += d[2];
+  }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) {
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, off);
+    rows += __shfl_xor_sync(0xffffffffu, rows, off);
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  if (lane == 0 && (bad || rows > a.T || tiles * a.Hq > int64_t(gridDim.x))) atomicOr(a.err, MOT_DEV_BAD_SEQUENCE);
+}
+
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
     joint_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
@@ -111,11 +204,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   // warp 0 finds the CTA's work item; the others read it from shared memory
   int* item = reinterpret_cast<int*>(tmem_slot + 2);  // found, q0, k0, nq, nk, n_causal, i0
   if (threadIdx.x < 32) {
-    if (blockIdx.x == 0)
-      check_sequences<TILES * BQ>(a.seqs, a.n_seq, a.T, a.Hq, gridDim.x, a.err, int(threadIdx.x));
+    if (blockIdx.x == 0) check_sequences(a, int(threadIdx.x));
     int4 sq4 = make_int4(0, 0, 0, 0);
     int c4 = 0, i04 = 0;
-    const bool found = find_item<TILES * BQ>(a.seqs, a.n_seq, a.T, int(blockIdx.x) / a.Hq, int(threadIdx.x), sq4, c4, i04);
+    const bool found = find_tile(a, int(blockIdx.x) / a.Hq, int(threadIdx.x), sq4, c4, i04);
     if (threadIdx.x == 0) {
       item[0] = found ? 1 : 0;
       item[1] = sq4.x;
