@@ -353,8 +353,8 @@ size_t mot_joint_attention_backward_workspace_bytes(int64_t T, int Hq, int Hkv, 
  * dS k_j, dk_j = scale sum dS q_i and dv_j = sum P dout_i over the sequences, query heads of the group
  * and queries that see j. S, dP and the three sums in fp32 on the tensor cores; P and dS are formed in
  * fp32 and enter their products as bf16; one cast. For dk and dv, lse / scale and delta are subtracted in the
- * products' own sums, as three bf16 each (24 bits). dk and dv of up to 128 neighbouring keys are summed in one,
- * two or four shares of the queries and heads (by how many see them), joined in order. The order of every sum is
+ * products' own sums, as three bf16 each (24 bits). dk and dv of up to 128 neighbouring keys are summed in one
+ * to sixteen shares of the queries and heads (by how many see them), joined in order. The order of every sum is
  * fixed by the sequences that share a key with the row's own, the head geometry and the order of seqs: a row's
  * bits do not depend on the pack's other sequences or on where its rows lie. Rows of other sequences, whatever they hold, add nothing; a NaN
  * or infinity in a row of a sequence leaves that sequence's gradients undefined. Tensors do not

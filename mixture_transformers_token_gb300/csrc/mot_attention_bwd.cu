@@ -36,8 +36,8 @@
 // What bounds it: at D = 128 a block's seven products take 3700 cycles of the tensor cores, which are busy 65% of the time. Tensor
 // memory is full (S', dP', dV and dK are 128 columns each), so a block's S' waits for the dV of the block before, which waits for
 // its P', and dP' likewise: two chains that alternate, each with the latencies of its barriers. 4096 rows of 28/4 heads of 128 (70%
-// of them causal): 346 us, 950 TFLOP/s of the five products that cannot be done without; a pack of twelve sequences of 2900 to 3000
-// rows 2.48 ms, one of 37 of up to 700 rows with 8/8 heads of 64 99 us. A wait's instructions and size count, as three kinds of
+// of them causal): 345 us, 951 TFLOP/s of the five products that cannot be done without; a pack of twelve sequences of 2900 to 3000
+// rows 2.47 ms, one of 37 of up to 700 rows with 8/8 heads of 64 100 us. A wait's instructions and size count, as three kinds of
 // warps share the instruction cache: with the limit's code in line at every wait the first took 369 us for 357, the second 2.59 ms
 // for 2.50. Measured on the first and not taken:
 //   shares in a cluster, added up through its shared memory (20000 of a CTA's 120000 cycles, and a twentieth of the SMs without one);
@@ -672,10 +672,11 @@ __device__ __forceinline__ float4* sums_at(float* sums, int rows, int m, int pie
   return reinterpret_cast<float4*>(sums) + (m * (D / 4) + piece) * rows + row;
 }
 
-// The thread's row of dV and dK as bf16, its quarter of the columns: the sums of the shares in order (of one: from tensor memory).
-template <int D, int SHARES>
-__device__ __forceinline__ void add_shares(float* sums, uint32_t at, bool any, int part, int row, int row0, int rows, int g,
-                                           const Args& a) {
+// The thread's row of dV and dK as bf16, its quarter of the columns: the sums of the shares in order, BATCH of them read at once (of
+// one: from tensor memory).
+template <int D, int BATCH>
+__device__ __forceinline__ void add_shares(float* sums, int shares, uint32_t at, bool any, int part, int row, int row0, int rows,
+                                           int g, const Args& a) {
   using L = KvLayout<D>;
   const int64_t N = int64_t(a.Hq + 2 * a.Hkv) * D;
   const int lane = row & 31, base = row - lane;  // the warp's first row
@@ -685,23 +686,27 @@ __device__ __forceinline__ void add_shares(float* sums, uint32_t at, bool any, i
     for (int c0 = part * (D / 4); c0 < (part + 1) * (D / 4); c0 += 16) {
       __syncwarp();
       float v[16] = {};
-      if constexpr (SHARES == 1) {
+      if constexpr (BATCH == 1) {
         if (any) tmem_ld16(at + (m ? L::DK : L::DV) + c0, v);
       } else {
-        float4 u[SHARES][4];  // all reads under way at once; rows past the last read that
-        const float4* from = sums_at<D>(sums, rows, m, c0 / 4, row < rows ? row : rows - 1);
+        const float4* from = sums_at<D>(sums, rows, m, c0 / 4, row < rows ? row : rows - 1);  // rows past the last read that
+#pragma unroll 1
+        for (int p0 = 0; p0 < shares; p0 += BATCH) {
+          float4 u[BATCH][4];
 #pragma unroll
-        for (int p = 0; p < SHARES; ++p)
+          for (int p = 0; p < BATCH; ++p)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) u[p][q] = __ldcg(from + (p * (D / 2) + q) * rows);
+            for (int q = 0; q < 4; ++q) u[p][q] = __ldcg(from + (int64_t(p0 + p) * (D / 2) + q) * rows);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float4 s = u[0][q];
+          for (int q = 0; q < 4; ++q)
 #pragma unroll
-          for (int p = 1; p < SHARES; ++p)
-            s = make_float4(__fadd_rn(s.x, u[p][q].x), __fadd_rn(s.y, u[p][q].y), __fadd_rn(s.z, u[p][q].z),
-                            __fadd_rn(s.w, u[p][q].w));
-          v[4 * q] = s.x, v[4 * q + 1] = s.y, v[4 * q + 2] = s.z, v[4 * q + 3] = s.w;
+            for (int p = 0; p < BATCH; ++p) {
+              const bool start = p == 0 && p0 == 0;
+              v[4 * q] = start ? u[p][q].x : __fadd_rn(v[4 * q], u[p][q].x);
+              v[4 * q + 1] = start ? u[p][q].y : __fadd_rn(v[4 * q + 1], u[p][q].y);
+              v[4 * q + 2] = start ? u[p][q].z : __fadd_rn(v[4 * q + 2], u[p][q].z);
+              v[4 * q + 3] = start ? u[p][q].w : __fadd_rn(v[4 * q + 3], u[p][q].w);
+            }
         }
       }
       const float f = m ? a.scale : 1.0f;
@@ -925,8 +930,8 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
         __threadfence();
         const int g = s.x % a.Hkv;
         float* sums = sums_of<D>(a, s.z, s.w, g, 0);
-        if (s.y == 4) add_shares<D, 4>(sums, at, true, part, row, s.z, s.w, g, a);
-        else add_shares<D, 2>(sums, at, true, part, row, s.z, s.w, g, a);
+        if (s.y >= 4) add_shares<D, 4>(sums, s.y, at, true, part, row, s.z, s.w, g, a);
+        else add_shares<D, 2>(sums, s.y, at, true, part, row, s.z, s.w, g, a);
       }
       sent = -1;
       return true;
@@ -996,7 +1001,7 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
       if (any && !(ok = wait(&B.dk_done, t - 1))) break;
       tc_fence_after();
       if (info.z == 1) {
-        add_shares<D, 1>(nullptr, at, any, part, row, tile.x, tile.y, info.y % a.Hkv, a);
+        add_shares<D, 1>(nullptr, 1, at, any, part, row, tile.x, tile.y, info.y % a.Hkv, a);
       } else {
         if (!(ok = publish())) break;  // the piece before's, where this one had no block
         float* to = sums_of<D>(a, tile.x, tile.y, info.y % a.Hkv, share);
@@ -1335,8 +1340,12 @@ inline bool shape_ok(int64_t T, int Hq, int Hkv, int D, int n_seq) {
          Hq % Hkv == 0 && n_seq >= 1 && n_seq <= MOT_MAX_TOKENS;
 }
 
-// The most CTAs that share a tile: with one query head a KV head (or two) there are as many tiles and KV heads for fewer blocks.
-inline int most_shares(int G) { return G >= 4 ? 4 : G >= 2 ? 2 : 1; }
+// The most CTAs that share a tile: with one query head a KV head (or two) there are as many tiles and KV heads for fewer blocks; one
+// or two KV heads make few pieces. (With four for all, 2000 causal rows of 16/1 heads of 128 took 136 us.)
+inline int most_shares(int Hq, int Hkv) {
+  const int G = Hq / Hkv;
+  return G >= 4 ? (Hkv == 1 ? 16 : Hkv == 2 ? 8 : 4) : G >= 2 ? 2 : 1;
+}
 
 constexpr int64_t kMostWork = 1 << 30;  // pieces of work: drawn as 32-bit numbers, some past the last
 
@@ -1345,7 +1354,7 @@ struct Room {
   int64_t nlse, ndelta, tiles, parts, items, counts, ended, change, border, runs, sums, end, ctas;
   int max_tiles, max_items;
   Room(int64_t T, int Hq, int Hkv, int D, int64_t n_seq) {
-    const int64_t most = most_shares(Hq / Hkv);
+    const int64_t most = most_shares(Hq, Hkv);
     auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
     const int64_t borders = 2 * n_seq < T + 1 ? 2 * n_seq : T + 1, blocks = (T + 127) / 128;
     max_tiles = int(blocks + borders < T ? blocks + borders : T);  // a run adds at most one short tile
@@ -1450,7 +1459,7 @@ extern "C" int mot_joint_attention_backward(const mot_bf16* dout, const mot_bf16
   a.work.items = reinterpret_cast<attnb::Item*>(base + room.items);
   a.work.counts = reinterpret_cast<int32_t*>(base + room.counts);
   a.work.ended = reinterpret_cast<int32_t*>(base + room.ended);
-  a.most_shares = attnb::most_shares(Hq / Hkv);
+  a.most_shares = attnb::most_shares(Hq, Hkv);
   a.sums = reinterpret_cast<float*>(base + room.sums);
   a.work.change = reinterpret_cast<int32_t*>(base + room.change);
   a.work.border = reinterpret_cast<uint32_t*>(base + room.border);

@@ -248,9 +248,10 @@ def test_long_sequences_among_many():
                Hq, Hkv, D)
 
 
-@pytest.mark.parametrize("Hq,Hkv,D,n", [(6, 2, 64, 1400), (4, 1, 64, 1250), (2, 2, 128, 1100), (2, 1, 128, 1281)])
+@pytest.mark.parametrize("Hq,Hkv,D,n", [(6, 2, 64, 1400), (4, 1, 64, 1250), (2, 2, 128, 1100), (2, 1, 128, 1281),
+                                         (8, 1, 128, 1500), (12, 1, 64, 1500), (16, 2, 64, 1100)])
 def test_shares_of_long_sequences(Hq, Hkv, D, n):
-    # tiles whose blocks are shared by one, two and four CTAs, of whole and of few rows
+    # tiles whose blocks are shared by one CTA to sixteen, of whole and of few rows
     seqs = [(7, 7, n, n, n - 300), (n + 7, 900, 60, 60, 0)]
     qkv, dout = _inputs(n + 80, Hq, Hkv, D, seed=n)
     s, out, lse = _forward(qkv, seqs, Hq, Hkv, D)
