@@ -36,8 +36,8 @@
 // What bounds it: at D = 128 a block's seven products take 3700 cycles of the tensor cores, which are busy 65% of the time. Tensor
 // memory is full (S', dP', dV and dK are 128 columns each), so a block's S' waits for the dV of the block before, which waits for
 // its P', and dP' likewise: two chains that alternate, each with the latencies of its barriers. 4096 rows of 28/4 heads of 128 (70%
-// of them causal): 345 us, 951 TFLOP/s of the five products that cannot be done without; a pack of twelve sequences of 2900 to 3000
-// rows 2.47 ms, one of 37 of up to 700 rows with 8/8 heads of 64 100 us. A wait's instructions and size count, as three kinds of
+// of them causal): 341 us, 960 TFLOP/s of the five products that cannot be done without; a pack of twelve sequences of 2900 to 3000
+// rows 2.44 ms, one of 37 of up to 700 rows with 8/8 heads of 64 99 us. A wait's instructions and size count, as three kinds of
 // warps share the instruction cache: with the limit's code in line at every wait the first took 369 us for 357, the second 2.59 ms
 // for 2.50. Measured on the first and not taken:
 //   shares in a cluster, added up through its shared memory (20000 of a CTA's 120000 cycles, and a twentieth of the SMs without one);
@@ -1075,6 +1075,7 @@ __device__ __forceinline__ void dq_phase(const CUtensorMap& tm_qkv, const CUtens
       if (w >= n_work) {
         if (lane == 0) {
           drawn.info[n & 1] = make_int4(0, 0, -1, 0);
+          drawn.more[n & 1] = make_int4(0, 0, 0, 0);
           mbar_arrive(smem_u32(&B.drawn[n & 1]));
         }
         break;
@@ -1185,19 +1186,30 @@ __device__ __forceinline__ void dq_phase(const CUtensorMap& tm_qkv, const CUtens
     const uint32_t at = tmem + (uint32_t(quarter * 32) << 16);
     const unsigned long long c2 = f2_pack(a.c, a.c);
     const int64_t N = int64_t(a.Hq + 2 * a.Hkv) * D;
-    bool ok = true;
-    int u = 0;  // blocks so far
-    for (int n = 0; ok; ++n) {
-      if (!(ok = wait(&B.drawn[n & 1], n >> 1))) break;
-      const int4 sq = drawn.info[n & 1], it = drawn.more[n & 1];
+    int4 next_sq, next_it;
+    float next_nl = 0.0f, next_nd = 0.0f;
+    // item n and its row's values, which are on their way while the item before is written
+    auto fetch = [&](int n) {
+      if (!wait(&B.drawn[n & 1], n >> 1)) return false;
+      next_sq = drawn.info[n & 1];
+      next_it = drawn.more[n & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&B.taken[n & 1]));
-      if (sq.z < 0) break;
+      if (next_sq.z >= 0 && next_it.y + row < next_sq.z) {  // past the last item there is no more
+        const int64_t stat = int64_t(next_it.z) * a.T + next_sq.x + next_it.y + row;
+        next_nl = __ldcg(a.nlse + stat);
+        next_nd = __ldcg(a.ndelta + stat);
+      }
+      return true;
+    };
+    bool ok = fetch(0);
+    int u = 0;  // blocks so far
+    for (int n = 1; ok && next_sq.z >= 0; ++n) {
+      const int4 sq = next_sq, it = next_it;
       const int i = it.y + row, h = it.z;
       const bool valid = i < sq.z;
       const int lim = !valid ? 0 : i < it.x ? sq.w - sq.z + i + 1 : sq.w;  // keys [0, lim) are visible
-      const int64_t stat = int64_t(h) * a.T + sq.x + i;
-      const float nl = valid ? __ldcg(a.nlse + stat) : 0.0f, nd = valid ? __ldcg(a.ndelta + stat) : 0.0f;
+      const float nl = valid ? next_nl : 0.0f, nd = valid ? next_nd : 0.0f;
       const unsigned long long nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
       const int from = u;
       for (const int to = u + blocks_of(sq, it.x, it.y); u < to; ++u) {
@@ -1242,7 +1254,7 @@ __device__ __forceinline__ void dq_phase(const CUtensorMap& tm_qkv, const CUtens
       }
       if (!ok) break;
       // the item's last dQ is done: dP of its last block, which these warps have read, came after the dQ before it
-      if (!(ok = wait(&B.dq_done, u - 1))) break;
+      if (!(ok = fetch(n) && wait(&B.dq_done, u - 1))) break;
       tc_fence_after();
       float v[D / 4];
       ld_columns(at + L::DQ + part * (D / 4), v);
