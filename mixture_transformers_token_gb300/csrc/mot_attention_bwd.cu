@@ -164,21 +164,33 @@ __device__ int make_parts(const StatsArgs& a, int* room, int tiles, const Seq& s
   __syncthreads();  // the tiles are there
   int parts = 0;
   for (int i0 = 0; i0 < tiles; i0 += STATS_THREADS) {
-    const int i = i0 + threadIdx.x;
-    int shares = 0;
-    if (i < tiles) {
-      const int4 tile = __ldcg(w.tiles + i);
-      int64_t blocks = 0;
-      int keys = 0, d[5];
-      for (int s = tile.z; s <= tile.w; ++s) {
-        if (!seq(s, d) || d[1] > tile.x || d[1] + d[3] <= tile.x) continue;
+    const int i = i0 + threadIdx.x, lane = threadIdx.x & 31;
+    // query blocks of every `step`-th sequence from `from` on that sees a row, and the most keys of one of them
+    auto count = [&](int row, int from, int last, int step, int& blocks, int& keys) {
+      int d[5];
+      for (int s = from; s <= last; s += step) {
+        if (!seq(s, d) || d[1] > row || d[1] + d[3] <= row) continue;
         int first, end;
-        query_blocks(d, tile.x, first, end);
-        blocks += (end > first ? end - first : 0) * int64_t(a.Hq / a.Hkv);
+        query_blocks(d, row, first, end);
+        blocks += end > first ? end - first : 0;  // at most T of all sequences
         keys = keys > d[3] ? keys : d[3];
       }
-      shares = shares_of(blocks, keys, a.Hkv, a.most_shares);
+    };
+    int4 tile = make_int4(0, 0, 0, -1);
+    if (i < tiles) tile = __ldcg(w.tiles + i);
+    int blocks = 0, keys = 0;
+    const bool wide = tile.w - tile.z >= 32;  // the warp's, a lane a sequence
+    if (!wide) count(tile.x, tile.z, tile.w, 1, blocks, keys);
+    for (uint32_t left = __ballot_sync(0xffffffffu, wide); left != 0u; left &= left - 1) {
+      const int of = __ffs(left) - 1;
+      int b = 0, k = 0;
+      count(__shfl_sync(0xffffffffu, tile.x, of), __shfl_sync(0xffffffffu, tile.z, of) + lane, __shfl_sync(0xffffffffu, tile.w, of), 32,
+            b, k);
+      b = int(__reduce_add_sync(0xffffffffu, unsigned(b)));
+      k = int(__reduce_max_sync(0xffffffffu, unsigned(k)));
+      if (lane == of) blocks = b, keys = k;
     }
+    const int shares = i < tiles ? shares_of(blocks * int64_t(a.Hq / a.Hkv), keys, a.Hkv, a.most_shares) : 0;
     int total;
     const int at = parts + scan_before(shares, room, total);
     for (int p = 0; p < shares; ++p) w.parts[at + p] = make_int4(i, p, shares, 0);
@@ -352,6 +364,7 @@ __device__ void make_work(const StatsArgs& a, int* room) {
     seen += total;
     const int mine = i < n && seers > 0 ? (to - from + BK - 1) / BK : 0;
     const int at = tiles + scan_before(mine, room, total);
+    if (i < n) w.change[from] = at;  // read above, by this thread alone: now the first tile from this border on
     for (int r = 0; r < mine; ++r) {
       const int row = from + r * BK;
       w.tiles[at + r] = make_int4(row, to - row < BK ? to - row : BK, a.n_seq, -1);
@@ -359,19 +372,25 @@ __device__ void make_work(const StatsArgs& a, int* room) {
     tiles += total;
   }
   __syncthreads();
-  // the first and the last sequence of each tile: a warp a sequence, a lane a tile
-  for (int s = tid >> 5; s < a.n_seq; s += STATS_THREADS / 32) {
-    const int32_t* d = a.seqs + 5 * int64_t(s);
-    if (bad_seq(d, a.T)) continue;
-    int lo = 0, hi = tiles;  // the tile that begins with the sequence's first key
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (w.tiles[mid].x <= d[1]) lo = mid;
-      else hi = mid;
+  // the first and the last sequence of each tile: a thread a sequence, or the warp for one of many tiles, a lane a tile
+  for (int s0 = 0; s0 < a.n_seq; s0 += STATS_THREADS) {
+    const int s = s0 + tid, lane = tid & 31;
+    int lo = 0, hi = 0;
+    if (s < a.n_seq) {
+      const int32_t* d = a.seqs + 5 * int64_t(s);
+      if (!bad_seq(d, a.T)) lo = __ldcg(w.change + d[1]), hi = __ldcg(w.change + d[1] + d[3]);  // both are borders
     }
-    for (int i = lo + (tid & 31); i < tiles && w.tiles[i].x < d[1] + d[3]; i += 32) {
+    const bool wide = hi - lo >= 32;
+    for (int i = lo; i < (wide ? lo : hi); ++i) {
       atomicMin(&w.tiles[i].z, s);
       atomicMax(&w.tiles[i].w, s);
+    }
+    for (uint32_t left = __ballot_sync(0xffffffffu, wide); left != 0u; left &= left - 1) {
+      const int of = __ffs(left) - 1, end = __shfl_sync(0xffffffffu, hi, of);
+      for (int i = __shfl_sync(0xffffffffu, lo, of) + lane; i < end; i += 32) {
+        atomicMin(&w.tiles[i].z, s - lane + of);
+        atomicMax(&w.tiles[i].w, s - lane + of);
+      }
     }
   }
   auto seq = [&](int s, int (&d)[5]) {
