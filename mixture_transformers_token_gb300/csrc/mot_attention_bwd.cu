@@ -36,8 +36,8 @@
 // What bounds it: at D = 128 a block's seven products take 3700 cycles of the tensor cores, which are busy 65% of the time. Tensor
 // memory is full (S', dP', dV and dK are 128 columns each), so a block's S' waits for the dV of the block before, which waits for
 // its P', and dP' likewise: two chains that alternate, each with the latencies of its barriers. 4096 rows of 28/4 heads of 128 (70%
-// of them causal): 341 us, 960 TFLOP/s of the five products that cannot be done without; a pack of twelve sequences of 2900 to 3000
-// rows 2.44 ms, one of 37 of up to 700 rows with 8/8 heads of 64 99 us. A wait's instructions and size count, as three kinds of
+// of them causal): 343 us, 956 TFLOP/s of the five products that cannot be done without; a pack of twelve sequences of 2900 to 3000
+// rows 2.46 ms, one of 37 of up to 700 rows with 8/8 heads of 64 98 us. A wait's instructions and size count, as three kinds of
 // warps share the instruction cache: with the limit's code in line at every wait the first took 369 us for 357, the second 2.59 ms
 // for 2.50. Measured on the first and not taken:
 //   shares in a cluster, added up through its shared memory (20000 of a CTA's 120000 cycles, and a twentieth of the SMs without one);
@@ -184,8 +184,8 @@ __device__ int make_parts(const StatsArgs& a, int* room, int tiles, const Seq& s
     for (uint32_t left = __ballot_sync(0xffffffffu, wide); left != 0u; left &= left - 1) {
       const int of = __ffs(left) - 1;
       int b = 0, k = 0;
-      count(__shfl_sync(0xffffffffu, tile.x, of), __shfl_sync(0xffffffffu, tile.z, of) + lane, __shfl_sync(0xffffffffu, tile.w, of), 32,
-            b, k);
+      const int at = __shfl_sync(0xffffffffu, tile.x, of), from = __shfl_sync(0xffffffffu, tile.z, of);
+      count(at, from + lane, __shfl_sync(0xffffffffu, tile.w, of), 32, b, k);
       b = int(__reduce_add_sync(0xffffffffu, unsigned(b)));
       k = int(__reduce_max_sync(0xffffffffu, unsigned(k)));
       if (lane == of) blocks = b, keys = k;
@@ -500,16 +500,12 @@ struct SeqIter {
   }
 };
 
-// A tile's blocks are shared out by (query block + head of the group) mod shares, a power of two: the shares differ by few blocks
-// where the group's heads do not divide evenly, and which share adds a block depends on the sequence and the head alone.
-// How many of the blocks [first, end) of all G heads a share has.
-__device__ __forceinline__ int blocks_of_share(int share, int first, int end, int G, int shares) {
-  int n = 0;
-  for (int hh = 0; hh < G; ++hh) {
-    const int b0 = first + ((share - first - hh) & (shares - 1));  // the head's first one
-    n += b0 < end ? (end - 1 - b0) / shares + 1 : 0;
-  }
-  return n;
+// A tile's blocks are shared out in turn, counted over the sequences that see it, the group's heads and the query blocks, so that the
+// shares (a power of two) differ by one block. (By query block plus head, short sequences left most of sixteen shares without any.)
+// How many of the n blocks from the `at`-th on a share has.
+__device__ __forceinline__ int blocks_of_share(int share, int at, int n, int shares) {
+  const int skip = (share - at) & (shares - 1);
+  return n > skip ? (n - 1 - skip) / shares + 1 : 0;
 }
 
 // Zeroes rows [from, 128) of `tiles` swizzled [128 x 64] tiles that follow one another (a row is 128 consecutive bytes).
@@ -774,11 +770,13 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
       const int4 tile = __ldcg(a.work.tiles + part.x);
       const int row0 = tile.x;
       SeqIter count(a, tile, lane);
-      int s[5], blocks = 0;
+      int s[5], blocks = 0, at = 0;  // at: blocks of the sequences before, mod shares
       while (count.next(s)) {
         int first, end;
         query_blocks(s, row0, first, end);
-        blocks += blocks_of_share(share, first, end, G, shares);
+        const int all = end > first ? (end - first) * G : 0;
+        blocks += blocks_of_share(share, at, all, shares);
+        at = (at + all) & (shares - 1);
       }
       if (lane == 0) {
         drawn.info[n & 1] = make_int4(blocks, part.x * a.Hkv + g, shares, 0);
@@ -798,12 +796,15 @@ __device__ __forceinline__ int dkv_phase(const CUtensorMap& tm_qkv, const CUtens
         load_tile<D>(smem_u32(smem + L::V), &tm_qkv, (a.Hq + a.Hkv + g) * D, row0, smem_u32(&B.v_full));
       }
       SeqIter it(a, tile, lane);
+      at = 0;
       while (ok && it.next(s)) {
         int first, end;
         query_blocks(s, row0, first, end);
         for (int hh = 0; hh < G && ok; ++hh) {
           const int h = g * G + hh;
-          for (int b = first + ((share - first - hh) & (shares - 1)); b < end; b += shares, ++t) {
+          const int skip = (share - at) & (shares - 1);
+          at = (at + (end > first ? end - first : 0)) & (shares - 1);
+          for (int b = first + skip; b < end; b += shares, ++t) {
             const int st = t % STAGES, y = s[0] + b * BQ, have = s[2] - b * BQ < BQ ? s[2] - b * BQ : BQ;
             // dO before Q: its place is free when dV is done, Q's when dK is, and S' wants Q first
 #pragma unroll

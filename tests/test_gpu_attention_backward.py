@@ -260,6 +260,21 @@ def test_shares_of_long_sequences(Hq, Hkv, D, n):
     assert_bitwise(d, _backward(dout, qkv, out, lse, s, Hq, Hkv, D), "again")
 
 
+def test_short_sequences_over_few_keys():
+    # many sequences' queries in one tile of keys: its blocks are shared out over all of them
+    Hq, Hkv, D, keys = 8, 1, 64, 9
+    seqs, at = [(0, 0, keys, keys, keys)], keys
+    for i in range(70):
+        n = 1 + i * 37 % 150
+        seqs.append((at, 0, n, keys, 0))
+        at += n
+    qkv, dout = _inputs(at, Hq, Hkv, D, seed=29)
+    for some in (seqs, seqs[:50]):
+        s, out, lse = _forward(qkv, some, Hq, Hkv, D)
+        d = _backward(dout, qkv, out, lse, s, Hq, Hkv, D)
+        _check(d, dout, qkv, out, lse, some, Hq, Hkv, D)
+
+
 def test_two_graphs_with_one_workspace():
     Hq, Hkv, D = 7, 1, 128
     ws, graphs = _ws(700, Hq, Hkv, D, 70), []
