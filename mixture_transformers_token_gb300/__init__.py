@@ -7,7 +7,9 @@ fallback: a missing or stale library raises, and every nonzero status raises Mot
 
 Functions keep the C names. Tensors are contiguous CUDA tensors: bf16 for activations and
 weights, uint8 for the modality index (0 = und, 1 = gen), int32 for positions, uint8 for
-the workspace.
+the workspace. `stream` (a torch.cuda.Stream or its handle) is the stream that a call is
+launched on, None the current one; buffers that are not given are made on it, and may be used
+on the current stream once that waits for it. The order of given tensors is the caller's.
 """
 
 from __future__ import annotations
@@ -186,6 +188,25 @@ def _stream(t: torch.Tensor, stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _new(make, shape, dtype: torch.dtype, t: torch.Tensor, stream, kept: bool = True) -> torch.Tensor:
+    """A buffer that the caller did not give, made by torch.empty or torch.zeros on t's device. Its memory belongs to the
+    stream that the call is launched on, where it is filled too: made on the current one, its fill and what that stream
+    still does with the memory would not be ordered before the call's kernels, nor the memory's next use after them.
+    What the caller receives (`kept`; else the call's own, let go at its return) may be used on the current stream."""
+    if stream is None or not t.is_cuda:
+        return make(shape, dtype=dtype, device=t.device)
+    current, handle = torch.cuda.current_stream(t.device), _stream(t, stream)
+    if handle == current.cuda_stream:
+        return make(shape, dtype=dtype, device=t.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, device=t.device) if handle else torch.cuda.default_stream(t.device)
+    with torch.cuda.stream(stream):
+        b = make(shape, dtype=dtype, device=t.device)
+    if kept:
+        b.record_stream(current)
+    return b
+
+
 # ---------------------------------------------------------------------------
 # entry points
 # ---------------------------------------------------------------------------
@@ -207,7 +228,7 @@ def mot_route_plan(mod: torch.Tensor, ws: torch.Tensor | None = None, stream=Non
     T = mod.numel()
     _dev(mod, "mod", torch.uint8, 1)
     if ws is None:
-        ws = torch.empty(max(mot_workspace_bytes(T), 16), dtype=torch.uint8, device=mod.device)
+        ws = _new(torch.empty, (max(mot_workspace_bytes(T), 16),), torch.uint8, mod, stream)
     _dev(ws, "ws", torch.uint8, 1)
     _check("mot_route_plan", _lib().mot_route_plan(mod.data_ptr(), T, ws.data_ptr(), ws.numel(), _stream(mod, stream)))
     return ws
@@ -218,9 +239,9 @@ def mot_fused_add_rmsnorm(x, res, w, mod, eps: float, y=None, res_out=None, ws=N
     If `ws` is given, the same launch also writes the routing plan of `mod` into it."""
     T, H = x.shape
     if y is None:
-        y = torch.empty_like(x)
+        y = _new(torch.empty, (T, H), torch.bfloat16, x, stream)
     if res_out is None:
-        res_out = torch.empty_like(res)
+        res_out = _new(torch.empty, (T, H), torch.bfloat16, x, stream)
     for t, n in ((x, "x"), (res, "res"), (y, "y"), (res_out, "res_out")):
         _dev(t, n, torch.bfloat16, 2)
         if tuple(t.shape) != (T, H):
@@ -264,7 +285,7 @@ def mot_routed_qkv_norm_rope(x, w_qkv, q_norm_w, k_norm_w, pos, rope_cs, Hq: int
         if tuple(b_qkv.shape) != (2, N):
             raise ValueError(f"b_qkv must be [2, {N}]")
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+        out = _new(torch.empty, (T, N), torch.bfloat16, x, stream)
     _dev(out, "out", torch.bfloat16, 2)
     name = "mot_routed_qkv_norm_rope_fp32" if fp32 else "mot_routed_qkv_norm_rope"
     _check(name, getattr(_lib(), name)(
@@ -295,7 +316,7 @@ def mot_routed_gemm(a, w, ws, epilogue: int = EPI_CAST, out=None, stream=None):
     N = w.shape[1]
     ncols = N // 2 if (epilogue & 0xFF) == EPI_SWIGLU else N
     if out is None:
-        out = torch.empty((T, ncols), dtype=torch.bfloat16, device=a.device)
+        out = _new(torch.empty, (T, ncols), torch.bfloat16, a, stream)
     _dev(out, "out", torch.bfloat16, 2)
     if tuple(out.shape) != (T, ncols):
         raise ValueError(f"out must be [{T}, {ncols}]")
@@ -319,7 +340,7 @@ def mot_routed_gemm_noalloc(a, w, mod, epilogue: int = EPI_CAST, out=None, devic
     N = w.shape[1]
     ncols = N // 2 if epilogue == EPI_SWIGLU else N
     if out is None:
-        out = torch.empty((T, ncols), dtype=torch.bfloat16, device=a.device)
+        out = _new(torch.empty, (T, ncols), torch.bfloat16, a, stream)
     _dev(out, "out", torch.bfloat16, 2)
     fp = _dev(device_flags, "device_flags", torch.int32, 1) if device_flags is not None else None
     _check("mot_routed_gemm_noalloc", _lib().mot_routed_gemm_noalloc(
@@ -333,7 +354,7 @@ def mot_gather_rows(src, ws, out=None, stream=None):
     _dev(src, "src", torch.bfloat16, 2)
     _dev(ws, "ws", torch.uint8, 1)
     if out is None:
-        out = torch.empty_like(src)
+        out = _new(torch.empty, (T, K), torch.bfloat16, src, stream)
     _dev(out, "out", torch.bfloat16, 2)
     _check("mot_gather_rows", _lib().mot_gather_rows(src.data_ptr(), T, K, ws.data_ptr(), ws.numel(), out.data_ptr(),
                                                      _stream(src, stream)))
@@ -348,7 +369,7 @@ def mot_swiglu_interleave(w_gate, w_up, out=None, stream=None):
     if tuple(w_up.shape) != (2, I, K):
         raise ValueError("w_up must match w_gate")
     if out is None:
-        out = torch.empty((2, 2 * I, K), dtype=torch.bfloat16, device=w_gate.device)
+        out = _new(torch.empty, (2, 2 * I, K), torch.bfloat16, w_gate, stream)
     _dev(out, "out", torch.bfloat16, 3)
     _check("mot_swiglu_interleave", _lib().mot_swiglu_interleave(
         w_gate.data_ptr(), w_up.data_ptr(), I, K, out.data_ptr(), _stream(w_gate, stream)))
@@ -366,7 +387,7 @@ def mot_routed_gemm_dx(dout, w, ws, flags: int = 0, out=None, stream=None):
         raise ValueError(f"w must be [2, {N}, K]")
     K = w.shape[2]
     if out is None:
-        out = torch.empty((T, K), dtype=torch.bfloat16, device=dout.device)
+        out = _new(torch.empty, (T, K), torch.bfloat16, dout, stream)
     _dev(out, "out", torch.bfloat16, 2)
     if tuple(out.shape) != (T, K):
         raise ValueError(f"out must be [{T}, {K}]")
@@ -387,7 +408,7 @@ def mot_routed_gemm_dw(dout, a, ws, expert: int = 1, flags: int = 0, out=None, s
         raise ValueError("dout and a must have the same rows")
     K = a.shape[1]
     if out is None:
-        out = torch.empty((N, K), dtype=torch.float32, device=dout.device)
+        out = _new(torch.empty, (N, K), torch.float32, dout, stream)
     _dev(out, "out", torch.float32, 2)
     if tuple(out.shape) != (N, K):
         raise ValueError(f"out must be [{N}, {K}]")
@@ -411,7 +432,7 @@ def mot_joint_attention(qkv, seqs, Hq: int, Hkv: int, D: int, ws, scale: float |
     if seqs.shape[1] != 5:
         raise ValueError("seqs must be [n_seq, 5]")
     if out is None:
-        out = torch.zeros((T, Hq * D), dtype=torch.bfloat16, device=qkv.device)
+        out = _new(torch.zeros, (T, Hq * D), torch.bfloat16, qkv, stream)
     _dev(out, "out", torch.bfloat16, 2)
     sc = 1.0 / math.sqrt(D) if scale is None else float(scale)
     _check("mot_joint_attention", _lib().mot_joint_attention(
@@ -433,9 +454,9 @@ def mot_joint_attention_lse(qkv, seqs, Hq: int, Hkv: int, D: int, ws, scale: flo
     if seqs.shape[1] != 5:
         raise ValueError("seqs must be [n_seq, 5]")
     if out is None:
-        out = torch.zeros((T, Hq * D), dtype=torch.bfloat16, device=qkv.device)
+        out = _new(torch.zeros, (T, Hq * D), torch.bfloat16, qkv, stream)
     if lse is None:
-        lse = torch.zeros((Hq, T), dtype=torch.float32, device=qkv.device)
+        lse = _new(torch.zeros, (Hq, T), torch.float32, qkv, stream)
     op = _dev(out, "out", torch.bfloat16, 2)
     lp = _dev(lse, "lse", torch.float32, 2)
     if out.shape != (T, Hq * D) or lse.shape != (Hq, T):
@@ -470,7 +491,7 @@ def mot_joint_attention_backward(dout, qkv, out, lse, seqs, Hq: int, Hkv: int, D
     if seqs.shape[1] != 5:
         raise ValueError("seqs must be [n_seq, 5]")
     if dqkv is None:
-        dqkv = torch.zeros_like(qkv)
+        dqkv = _new(torch.zeros, (T, N), torch.bfloat16, qkv, stream)
     gp = _dev(dqkv, "dqkv", torch.bfloat16, 2)
     if dqkv.shape != (T, N):
         raise ValueError(f"dqkv must be [{T}, {N}]")
@@ -507,7 +528,7 @@ def mot_qk_norm_rope_backward(d_out, x, q_norm_w, k_norm_w, pos, rope_cs, Hq: in
     if rope_cs.shape[1:] != (D // 2, 2):
         raise ValueError("rope_cs must be [P, D/2, 2]")
     if dx is None:
-        dx = torch.empty_like(d_out)
+        dx = _new(torch.empty, (T, N), torch.bfloat16, d_out, stream)
     gp = _dev(dx, "dx", torch.bfloat16, 2)
     if dx.shape != (T, N):
         raise ValueError(f"dx must be [{T}, {N}]")
@@ -515,13 +536,13 @@ def mot_qk_norm_rope_backward(d_out, x, q_norm_w, k_norm_w, pos, rope_cs, Hq: in
     sb = 0
     if sets != 0:
         if dw is None:
-            dw = torch.zeros((2, 2, D), dtype=torch.float32, device=d_out.device)
+            dw = _new(torch.zeros, (2, 2, D), torch.float32, d_out, stream)
         wgp = _dev(dw, "dw", torch.float32, 3)
         if dw.shape != (2, 2, D):
             raise ValueError(f"dw must be [2, 2, {D}]")
         if scratch is None:
-            scratch = torch.empty(max(mot_qk_norm_rope_backward_workspace_bytes(T, D), 16), dtype=torch.uint8,
-                                  device=d_out.device)
+            scratch = _new(torch.empty, (max(mot_qk_norm_rope_backward_workspace_bytes(T, D), 16),), torch.uint8, d_out,
+                           stream, kept=False)
         sp = _dev(scratch, "scratch", torch.uint8, 1)
         sb = scratch.numel()
     elif dw is not None:
@@ -692,7 +713,7 @@ def mot_paged_decode_attention(qkv, table, lens, k_cache, v_cache, Hq: int, ws, 
     if table.shape[0] != R or lens.shape[0] != R:
         raise ValueError("table must be [R, max_pages] and lens [R]")
     if out is None:
-        out = torch.empty((R, Hq * D), dtype=torch.bfloat16, device=qkv.device)
+        out = _new(torch.empty, (R, Hq * D), torch.bfloat16, qkv, stream)
     op = _dev(out, "out", torch.bfloat16, 2)
     if out.shape != (R, Hq * D):
         raise ValueError(f"out must be [{R}, {Hq * D}]")
@@ -729,9 +750,9 @@ def mot_add_rmsnorm_backward(dy, s, w, eps: float, ws, d_res_out=None, dx=None, 
             raise ValueError(f"dw_partials must be [{H // 64}, {T}, 64]")
         pp = dw_partials.data_ptr()
     if dx is None:
-        dx = torch.empty((T, H), dtype=torch.bfloat16, device=dy.device)
+        dx = _new(torch.empty, (T, H), torch.bfloat16, dy, stream)
     if rstd is None:
-        rstd = torch.empty((T,), dtype=torch.float32, device=dy.device)
+        rstd = _new(torch.empty, (T,), torch.float32, dy, stream)
     _dev(dx, "dx", torch.bfloat16, 2)
     _dev(rstd, "rstd", torch.float32, 1)
     _check("mot_add_rmsnorm_backward", _lib().mot_add_rmsnorm_backward(
@@ -751,7 +772,7 @@ def mot_rmsnorm_dweight(dw_partials, ws, dw=None, sets: int = SET_BOTH, stream=N
         raise ValueError("dw_partials must be [H/64, T, 64]")
     H = nb * 64
     if dw is None:
-        dw = torch.empty((2, H), dtype=torch.float32, device=dw_partials.device)
+        dw = _new(torch.empty, (2, H), torch.float32, dw_partials, stream)
     _dev(dw, "dw", torch.float32, 2)
     _check("mot_rmsnorm_dweight", _lib().mot_rmsnorm_dweight(
         dw_partials.data_ptr(), T, H, sets, ws.data_ptr(), ws.numel(), dw.data_ptr(), _stream(dw_partials, stream)))
@@ -783,9 +804,9 @@ def mot_flow_schedule_host(n: int, shift: float) -> torch.Tensor:
     return t
 
 
-def _flow_ws(ws, n_req: int, N: int, device) -> torch.Tensor:
+def _flow_ws(ws, n_req: int, N: int, t: torch.Tensor, stream) -> torch.Tensor:
     if ws is None:
-        ws = torch.zeros(max(mot_flow_workspace_bytes(n_req, N), 64), dtype=torch.uint8, device=device)
+        ws = _new(torch.zeros, (max(mot_flow_workspace_bytes(n_req, N), 64),), torch.uint8, t, stream, kept=False)
     _dev(ws, "ws", torch.uint8, 1)
     return ws
 
@@ -806,9 +827,9 @@ def mot_cfg_combine_renorm(v_c, v_tu, v_iu, policy, ws=None, out=None, stream=No
         raise ValueError("the branches must all be [n_req, N]")
     if tuple(policy.shape) != (n_req, 6):
         raise ValueError("policy must be [n_req, 6]")
-    ws = _flow_ws(ws, n_req, N, v_c.device)
+    ws = _flow_ws(ws, n_req, N, v_c, stream)
     if out is None:
-        out = torch.empty((n_req, N), dtype=torch.float32, device=v_c.device)
+        out = _new(torch.empty, (n_req, N), torch.float32, v_c, stream)
     _dev(out, "out", torch.float32, 2)
     _check("mot_cfg_combine_renorm", _lib().mot_cfg_combine_renorm(
         v_c.data_ptr(), v_tu.data_ptr(), ip, n_req, N, policy.data_ptr(), ws.data_ptr(), ws.numel(),
@@ -834,14 +855,14 @@ def mot_flow_sde_step(x, v, z, times, ws=None, x_next=None, logp=None, stream=No
         zp = z.data_ptr()
     elif x_next is None:
         raise ValueError("either z or x_next must be given")
-    ws = _flow_ws(ws, n_req, N, x.device)
+    ws = _flow_ws(ws, n_req, N, x, stream)
     if x_next is None:
-        x_next = torch.empty((n_req, N), dtype=torch.float32, device=x.device)
+        x_next = _new(torch.empty, (n_req, N), torch.float32, x, stream)
     _dev(x_next, "x_next", torch.float32, 2)
     if tuple(x_next.shape) != (n_req, N):
         raise ValueError("x_next must be [n_req, N]")
     if logp is None:
-        logp = torch.empty((n_req,), dtype=torch.float32, device=x.device)
+        logp = _new(torch.empty, (n_req,), torch.float32, x, stream)
     _dev(logp, "logp", torch.float32, 1)
     _check("mot_flow_sde_step", _lib().mot_flow_sde_step(
         x.data_ptr(), v.data_ptr(), zp, x_next.data_ptr(), n_req, N, times.data_ptr(), ws.data_ptr(), ws.numel(),
@@ -878,9 +899,9 @@ def mot_flow_cfg_sde_step(v_c, v_tu, v_iu, policy, x, z, times, ws=None, x_next=
         zp = z.data_ptr()
     elif x_next is None:
         raise ValueError("either z or x_next must be given")
-    ws = _flow_ws(ws, n_req, N, x.device)
+    ws = _flow_ws(ws, n_req, N, x, stream)
     if x_next is None:
-        x_next = torch.empty((n_req, N), dtype=torch.float32, device=x.device)
+        x_next = _new(torch.empty, (n_req, N), torch.float32, x, stream)
     _dev(x_next, "x_next", torch.float32, 2)
     if tuple(x_next.shape) != (n_req, N):
         raise ValueError("x_next must be [n_req, N]")
@@ -891,7 +912,7 @@ def mot_flow_cfg_sde_step(v_c, v_tu, v_iu, policy, x, z, times, ws=None, x_next=
             raise ValueError("v_out must be [n_req, N]")
         vp = v_out.data_ptr()
     if logp is None:
-        logp = torch.empty((n_req,), dtype=torch.float32, device=x.device)
+        logp = _new(torch.empty, (n_req,), torch.float32, x, stream)
     _dev(logp, "logp", torch.float32, 1)
     _check("mot_flow_cfg_sde_step", _lib().mot_flow_cfg_sde_step(
         v_c.data_ptr(), v_tu.data_ptr(), ip, policy.data_ptr(), x.data_ptr(), zp, x_next.data_ptr(), n_req, N,
@@ -905,7 +926,7 @@ def mot_flow_noise(seeds, step: int, N: int, z=None, stream=None):
     _dev(seeds, "seeds", torch.int64, 1)
     n_req = seeds.shape[0]
     if z is None:
-        z = torch.empty((n_req, N), dtype=torch.float32, device=seeds.device)
+        z = _new(torch.empty, (n_req, N), torch.float32, seeds, stream)
     _dev(z, "z", torch.float32, 2)
     if tuple(z.shape) != (n_req, N):
         raise ValueError(f"z must be [{n_req}, {N}]")
