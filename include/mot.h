@@ -634,7 +634,9 @@ int mot_adamw_hyper_host(double lr, double beta1, double beta2, double eps, doub
  * values at random, up with probability equal to its distance from the lower one (to 2^-16 of a step), so
  * that the states' expectations are exact and small changes are not lost; a positive v' whose code would
  * be zero gets the smallest one. a < 2^-100 makes scale and codes zero; a block with an infinity or a NaN
- * gets the scale NaN and codes of zero. The 16 random bits of element e of tensor i (its index in `tensors`) are the low (m)
+ * gets the scale NaN and codes of zero, so that one gradient whose square overflows fp32 makes all 256 weights of its block
+ * NaN in the next step (fp32 states: it leaves that one weight to its decay). The 16 random bits of element e of tensor i
+ * (its index in `tensors`) are the low (m)
  * and high (v) half of word e % 4 of the Philox4x32-7 block (Salmon et al., SC 2011) with counter
  * (e / 4 low, e / 4 high, i, t) and key (seed low, seed high).
  * Geometry: 1 <= n_tensors <= 65536, n in 1 .. 2^40, else MOT_ERR_GEOMETRY; unknown flags or a negative or

@@ -285,13 +285,14 @@ __device__ __forceinline__ void warp_block(const Table& a, const Hyper& h, const
     float least = fminf(fabsf(m[0]), r[0]);
 #pragma unroll
     for (int i = 1; i < 8; ++i) least = fminf(least, fminf(fabsf(m[i]), r[i]));
-    if (__all_sync(0xffffffffu, least >= 0x1p-6f)) {  // few blocks reach 2^-15 below their largest value
+    // few blocks reach 2^-15 below their largest value (`least` is a number also where one state's values are all NaN)
+    if (__all_sync(0xffffffffu, least >= 0x1p-6f && sm.scale < INFINITY && sr.scale < INFINITY)) {
       codes_of<false, false>(m, w, false, v, cm);
       codes_of<false, true>(r, w, false, v, cr);
     } else {
       codes_of<true, false>(m, w, false, v, cm);
       codes_of<true, true>(r, w, sr.scale > 0.0f, v, cr);
-      if (!(sm.scale < INFINITY)) cm[0] = cm[1] = 0u;  // NaN: inv is zero, so `least` is zero or a NaN
+      if (!(sm.scale < INFINITY)) cm[0] = cm[1] = 0u;  // a NaN
       if (!(sr.scale < INFINITY)) cr[0] = cr[1] = 0u;
     }
     store_codes<ALL>(static_cast<uint8_t*>(t.m) + e, have, cm[0], cm[1]);
