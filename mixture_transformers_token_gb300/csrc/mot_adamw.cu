@@ -292,8 +292,8 @@ __device__ __forceinline__ void warp_block(const Table& a, const Hyper& h, const
     } else {
       codes_of<true, false>(m, w, false, v, cm);
       codes_of<true, true>(r, w, sr.scale > 0.0f, v, cr);
-      if (!(sm.scale < INFINITY)) cm[0] = cm[1] = 0u;  // a NaN
-      if (!(sr.scale < INFINITY)) cr[0] = cr[1] = 0u;
+      if (!(sm.scale > 0.0f)) cm[0] = cm[1] = 0u;  // a NaN, or zero, where negative values have become -0
+      if (!(sr.scale > 0.0f)) cr[0] = cr[1] = 0u;
     }
     store_codes<ALL>(static_cast<uint8_t*>(t.m) + e, have, cm[0], cm[1]);
     store_codes<ALL>(static_cast<uint8_t*>(t.v) + e, have, cr[0], cr[1]);

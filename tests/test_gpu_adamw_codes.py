@@ -85,3 +85,14 @@ def test_first_moments_that_are_nan_beside_second_ones_that_are_not():
     c.scales[0][1, 0] = float("nan")
     _steps(c, (1, 2))
     assert np.isnan(c.scales[0].cpu().numpy()[1, 0]) and np.isfinite(c.scales[0].cpu().numpy()[1, 1])
+
+
+def test_blocks_below_the_least_scale():
+    # magnitudes under 2^-100 of either sign: scale and codes are zero
+    c = Case([256 * 3 + 9], "e4m3", seed=10)
+    c.g[0][:256] = -(2.0 ** -105)
+    c.g[0][256:512] *= 2.0 ** -110
+    c.g[0][768:] *= 2.0 ** -120
+    _steps(c, (1, 2))
+    assert not c.scales[0].cpu().numpy()[[0, 1, 3]].any()
+    assert not c.m[0].view(torch.uint8)[:512].any() and not c.m[0].view(torch.uint8)[768:].any()
