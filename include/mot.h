@@ -293,7 +293,9 @@ int mot_rope_table_fill_host_fp32(double theta, int D, int P, float* host_cs);
  *         j <= nk - nq + i (a prompt row); the others see all nk keys (latent rows). Requires
  *         nk >= 1, 0 <= n_causal <= nq, nk >= nq when n_causal > 0, ranges inside [0, T) and
  *         query ranges of different sequences that do not overlap; otherwise
- *         MOT_DEV_BAD_SEQUENCE is set and the bad sequence's rows are not written.
+ *         MOT_DEV_BAD_SEQUENCE is set and the bad sequence's rows are not written. (Of overlapping
+ *         query ranges only those are found that have more than T rows in all; the rows that
+ *         they share are undefined either way.)
  *   scale  softmax scale (1 / sqrt(D) for the standard attention), > 0.
  *   ws    at least 64 bytes (e.g. a routing plan); its error word receives device errors.
  *   out   [T][Hq D] bf16   out: rows that are some sequence's query; other rows untouched.
@@ -347,7 +349,8 @@ size_t mot_joint_attention_backward_workspace_bytes(int64_t T, int Hq, int Hkv, 
  *   dqkv   [T][(Hq + 2 Hkv) D] bf16   out: the q columns of rows that are some sequence's query, and the
  *          K and V columns of rows that are some sequence's key, each row written once, whole; all other
  *          columns are left as they were. A row that several sequences see as a key gets the sum over
- *          them. A bad descriptor contributes nothing.
+ *          them. A bad descriptor contributes nothing; where the query ranges have more than T rows in all
+ *          (they overlap, MOT_DEV_BAD_SEQUENCE) nothing is written.
  * Per query i and key j that it sees, S = q . k: P = exp(scale S - lse), dP = dout_i . v_j,
  * delta_i = sum of dout_i out_i over the head's columns, dS = P (dP - delta_i); then dq_i = scale sum_j
  * dS k_j, dk_j = scale sum dS q_i and dv_j = sum P dout_i over the sequences, query heads of the group

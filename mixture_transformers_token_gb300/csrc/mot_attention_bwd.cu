@@ -199,6 +199,11 @@ __device__ int make_parts(const StatsArgs& a, int* room, int tiles, const Seq& s
   return parts;
 }
 
+// Query ranges that overlap so far that they have more than T rows: there is no work, which would grow with their number.
+__device__ __forceinline__ void no_work(const Work& w) {
+  if (threadIdx.x == 0) w.counts[0] = w.counts[1] = w.counts[2] = 0;
+}
+
 // The lists of work of up to kSortedSeqs sequences, in shared memory. The items come heaviest first: the last run of queries of
 // every sequence, then the last but one of every sequence, ...
 struct FewRoom {
@@ -228,6 +233,7 @@ __device__ void make_work_few(const StatsArgs& a, FewRoom& s) {
   if (__syncthreads_or(bad ? 1 : 0) != 0 || all_rows > a.T) {
     if (tid == 0) atomicOr(a.err, MOT_DEV_BAD_SEQUENCE);
   }
+  if (all_rows > a.T) return no_work(w);
   // the borders of the key ranges, each once, in ascending order
   constexpr int NONE = 0x7FFFFFFF;
   static_assert(2 * kSortedSeqs <= STATS_THREADS, "a thread a border");
@@ -304,7 +310,7 @@ __device__ void make_work(const StatsArgs& a, int* room) {
   for (int i = tid; i <= a.T; i += STATS_THREADS) w.change[i] = 0;
   for (int i = tid; i < words; i += STATS_THREADS) w.border[i] = 0u;
   __syncthreads();
-  // every good descriptor's borders and changes; its items; and that the query ranges do not overlap
+  // every good descriptor's borders and changes; its items; and the rows of all query ranges, at most T if none overlap
   int items = 0;
   int64_t rows = 0;
   bool bad_any = false;
@@ -342,6 +348,7 @@ __device__ void make_work(const StatsArgs& a, int* room) {
     }
     const bool any = __syncthreads_or(bad_any ? 1 : 0) != 0;
     if (tid == 0 && (any || sum > a.T)) atomicOr(a.err, MOT_DEV_BAD_SEQUENCE);
+    if (sum > a.T) return no_work(w);
   }
   // the borders in ascending order
   int n = 0;
