@@ -294,7 +294,8 @@ __global__ void __launch_bounds__(THREADS, 1) qk_norm_rope_bwd_kernel(const Args
     for (int j = taken; j < issued; ++j) mbar_drain(smem_u32(&full[j % SLOTS]), uint32_t(j / SLOTS) & 1u);
 }
 
-// Adds the CTAs' sums: a CTA takes 32 columns of one kind and set, warp k the runs k, k + 8, ..., eight reads at once.
+// Adds the CTAs' sums: a CTA takes 32 columns of one kind and set, warp k the runs k, k + 32, ... (at most five) in ascending
+// order, then the warps' sums in theirs.
 constexpr int FOLD_WARPS = 32, FOLD_THREADS = 32 * FOLD_WARPS;
 
 template <int D>
@@ -308,7 +309,6 @@ __global__ void __launch_bounds__(FOLD_THREADS) qk_dweight_fold_kernel(const Arg
   pdl_wait();  // also where nothing is written: this grid ends after the one before it
   if (((a.sets >> (group & 1)) & 1) == 0 || !plan) return;
   float v = 0.0f;
-#pragma unroll 8
   for (int i = warp; i < a.ctas; i += FOLD_WARPS) v = __fadd_rn(v, __ldcg(a.part + (int64_t(i) * 4 + group) * D + col));
   sums[warp][lane] = v;
   __syncthreads();
