@@ -561,7 +561,9 @@ size_t mot_qk_norm_rope_backward_workspace_bytes(int64_t T, int D);
  *   d_out     [T][N] bf16, N = (Hq + 2 Hkv) D   gradient of qkv_out (mot_joint_attention_backward's dqkv).
  *   x         [T][N] bf16             the projection's rows q = bf16(acc + b) before the norm:
  *                                     mot_routed_gemm(MOT_EPI_CAST) on the same weights gives them bit for
- *                                     bit where there is no bias. V columns are not read.
+ *                                     bit where there is no bias; with one, no call of this library writes
+ *                                     them or forms the bias's gradient (the sums of dx over each set's
+ *                                     rows). V columns are not read.
  *   q_norm_w, k_norm_w, pos, rope_cs, P, eps   the forward's (any position outside [0, P) sets
  *                                     MOT_DEV_BAD_POSITION and is taken as 0, as in the forward).
  *   ws        the routing plan of the forward's mod for this T: each row's weight set, and the error word.

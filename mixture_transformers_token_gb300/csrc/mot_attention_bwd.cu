@@ -1379,8 +1379,12 @@ inline bool shape_ok(int64_t T, int Hq, int Hkv, int D, int n_seq) {
          Hq % Hkv == 0 && n_seq >= 1 && n_seq <= MOT_MAX_TOKENS;
 }
 
-// The most CTAs that share a tile: with one query head a KV head (or two) there are as many tiles and KV heads for fewer blocks; one
-// or two KV heads make few pieces. (With four for all, 2000 causal rows of 16/1 heads of 128 took 136 us.)
+// The most CTAs that share a tile. One or two KV heads make few pieces, so that shares pay where a tile has blocks enough: 2000 causal
+// rows of 16/1 heads of 128 take 96 us, with four 136. Small groups have few blocks a tile, and cut sums cost about four blocks a
+// piece. With the caps of large groups for all (16, 8 and 4 shares for 1, 2 and more KV heads) heads of 128 take, in us, with a
+// group of one 2000 rows of 1/1 heads 46.8 for 43.7, 12 sequences of up to 3000 of 8/8 740 for 712 and 64 of 500 of 4/4 150 for
+// 151; of two 8000 rows of 2/1 146 for 133; of three 12 of up to 3000 of 12/4 1079 for 1050, but 2000 and 8000 rows of 3/1 54.9 for
+// 65.2 and 168 for 182 and 4000 of 6/2 105 for 107.
 inline int most_shares(int Hq, int Hkv) {
   const int G = Hq / Hkv;
   return G >= 4 ? (Hkv == 1 ? 16 : Hkv == 2 ? 8 : 4) : G >= 2 ? 2 : 1;
