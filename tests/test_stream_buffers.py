@@ -255,3 +255,25 @@ def test_results_let_go_while_the_current_stream_reads_them():
     torch.cuda.synchronize()
     _same([copy, other], want)
     del held
+
+
+@pytest.mark.gpu
+def test_captured_on_a_stream_beside_the_capturing_one():
+    need_gpu()
+    s, side, graph = Step(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    want = *s.attention(), *s.norm()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        s.norm(side)  # results that nobody keeps
+        got = *s.attention(side), *s.norm(side)
+        main.wait_stream(side)
+        copies = [t.clone() for t in got]
+    for _ in range(2):
+        for t in (*got, *copies):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        _same(got, want)
+        _same(copies, want)
