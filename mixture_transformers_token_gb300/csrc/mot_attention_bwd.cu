@@ -37,7 +37,7 @@
 // memory is full (S', dP', dV and dK are 128 columns each), so a block's S' waits for the dV of the block before, which waits for
 // its P', and dP' likewise: two chains that alternate, each with the latencies of its barriers. 4096 rows of 28/4 heads of 128 (70%
 // of them causal): 343 us, 956 TFLOP/s of the five products that cannot be done without; a pack of twelve sequences of 2900 to 3000
-// rows 2.46 ms, one of 37 of up to 700 rows with 8/8 heads of 64 98 us. A wait's instructions and size count, as three kinds of
+// rows 2.47 ms, one of 37 of up to 700 rows with 8/8 heads of 64 98 us. A wait's instructions and size count, as three kinds of
 // warps share the instruction cache: with the limit's code in line at every wait the first took 369 us for 357, the second 2.59 ms
 // for 2.50. Measured on the first and not taken:
 //   shares in a cluster, added up through its shared memory (20000 of a CTA's 120000 cycles, and a twentieth of the SMs without one);
